@@ -44,7 +44,7 @@
 extern "C" {
 #endif
 
-#define MOE_ABI_VERSION 5
+#define MOE_ABI_VERSION 6
 
 /* Status codes. */
 enum {
@@ -424,6 +424,63 @@ int moe_grouped_dgrad(const moe_grouped_problem* p, const void* dy, const void* 
  * empty group adds +0.0, which turns -0.0 into +0.0). */
 int moe_grouped_wgrad(const moe_grouped_problem* p, const void* dy, const void* x,
                       const int32_t* group_offsets, float* dw, int accumulate, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The router: scoring and top-k of router logits (the topk_ids and
+ * topk_weights that moe_apply_contiguous takes), and the weights' gradient.
+ *
+ * For one token with logits l_e (MOE_ROUTE_BIAS_LOGIT: l_e + bias_e):
+ *  - an expert whose l_e (or, below, key) is NaN or -inf is never chosen;
+ *    +inf counts as the largest finite float32;
+ *  - its score s_e is the softmax of l over the token's other experts, or
+ *    sigmoid(l_e); its key is l_e, or with MOE_ROUTE_BIAS_SELECT s_e + bias_e,
+ *    or with groups > 1 (and no such bias) s_e; keys are compared in float64;
+ *  - groups > 1: experts [g E/groups, (g+1) E/groups) are group g, scored by
+ *    the sum of its two largest keys (by the one it has); only experts of
+ *    the topk_groups best groups may be chosen;
+ *  - the topk largest keys are chosen, in descending order, ties (of keys
+ *    and of groups) to the lowest index.  A token with fewer than topk
+ *    experts to choose from gets id -1 and weight 0 in its last slots (what
+ *    moe_apply_contiguous skips);
+ *  - w_j = scale * s_j, or with renormalize scale * s_j / sum over the chosen
+ *    of s (0 when that sum is 0), float32.
+ * ------------------------------------------------------------------------- */
+enum { MOE_ROUTE_SOFTMAX = 0, MOE_ROUTE_SIGMOID = 1 };
+enum {
+  MOE_ROUTE_BIAS_NONE = 0,
+  MOE_ROUTE_BIAS_LOGIT = 1,    /* added to the logits                          */
+  MOE_ROUTE_BIAS_SELECT = 2    /* added to the scores for the choice only      */
+};
+
+typedef struct moe_router {
+  int64_t E;             /* experts, 1 .. 2048                                 */
+  int64_t topk;          /* 1 .. min(E, 64)                                    */
+  int64_t groups;        /* 1 .. 64, divides E; 1: no groups                   */
+  int64_t topk_groups;   /* 1 .. groups                                        */
+  int32_t scoring;       /* MOE_ROUTE_SOFTMAX / _SIGMOID                       */
+  int32_t bias_kind;     /* MOE_ROUTE_BIAS_*                                   */
+  int32_t renormalize;   /* 0 or 1                                             */
+  float scale;           /* finite                                             */
+} moe_router;
+
+/* logits: device, M rows of E values, logits_ld elements from row to row
+ * (logits_ld >= E), float32 if dtype == 0, bf16 if dtype == 1, aligned to its
+ * element; bias: device float32 [E], NULL exactly when bias_kind is NONE;
+ * topk_ids: device int32 [M, topk]; topk_weights: device float32 [M, topk].
+ * M = 0 enqueues nothing.  MOE_EINVAL: a bad field, M outside [0, 2^31), a null
+ * or misaligned pointer. */
+int moe_route_topk(const moe_router* r, int64_t M, const void* logits, int dtype, int64_t logits_ld,
+                   const float* bias, int32_t* topk_ids, float* topk_weights, void* stream);
+
+/* dlogits = the gradient of sum_j dweights_j w_j over the logits, the choice
+ * held fixed (with MOE_ROUTE_BIAS_LOGIT the bias's gradient is its column
+ * sum).  topk_ids: as moe_route_topk wrote them (ids outside [0, E) are
+ * skipped); dweights: device float32 [M, topk]; dlogits: device, logits'
+ * dtype, M rows of E values dlogits_ld elements apart, every one written
+ * (elements between the rows untouched).  Errors as for moe_route_topk. */
+int moe_route_topk_backward(const moe_router* r, int64_t M, const void* logits, int dtype, int64_t logits_ld,
+                            const float* bias, const int32_t* topk_ids, const float* dweights, void* dlogits,
+                            int64_t dlogits_ld, void* stream);
 
 #ifdef __cplusplus
 }

@@ -26,9 +26,11 @@ __all__ = [
     "moe_quantize_mxfp8", "moe_pack_mxfp8_scales", "make_problem", "allocate_workspaces", "ws_view", "status_words",
     "check_status",
     "MoeGroupedProblem", "moe_grouped_forward", "moe_grouped_dgrad", "moe_grouped_wgrad",
+    "ROUTE_SOFTMAX", "ROUTE_SIGMOID", "BIAS_NONE", "BIAS_LOGIT", "BIAS_SELECT", "MoeRouter", "make_router",
+    "moe_route_topk", "moe_route_topk_backward",
 ]
 
-ABI_VERSION = 5
+ABI_VERSION = 6
 STATIC_SCRATCH_BYTES = 64 << 20     # MOE_STATIC_SCRATCH_BYTES
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EHIP = 0, 1, 2, 3
 LAYOUT_CONTIGUOUS, LAYOUT_BATCHED = 0, 1
@@ -36,6 +38,8 @@ W_BF16, W_MXFP8, W_MXFP8_GROUPED = 0, 1, 2
 W1_HALVES, W1_INTERLEAVE16 = 0, 1
 VARIANT_AUTO, VARIANT_TILE, VARIANT_STREAM, VARIANT_FUSED = -1, 0, 1, 2
 REDUCE_NOOP, REDUCE_CONTIGUOUS, REDUCE_NAIVE_BATCHED = 0, 1, 2
+ROUTE_SOFTMAX, ROUTE_SIGMOID = 0, 1                  # MOE_ROUTE_SOFTMAX, MOE_ROUTE_SIGMOID
+BIAS_NONE, BIAS_LOGIT, BIAS_SELECT = 0, 1, 2         # MOE_ROUTE_BIAS_*
 
 _i64, _i32, _vp = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p
 
@@ -48,6 +52,11 @@ class MoeProblem(ctypes.Structure):
 
 class MoeGroupedProblem(ctypes.Structure):
     _fields_ = [("R", _i64), ("N", _i64), ("K", _i64), ("E", _i64)]
+
+
+class MoeRouter(ctypes.Structure):
+    _fields_ = [("E", _i64), ("topk", _i64), ("groups", _i64), ("topk_groups", _i64), ("scoring", _i32),
+                ("bias_kind", _i32), ("renormalize", _i32), ("scale", ctypes.c_float)]
 
 
 class MoePlan(ctypes.Structure):
@@ -112,6 +121,8 @@ def load_library() -> ctypes.CDLL:
         "moe_grouped_forward": (_i32, [_vp] * 6),
         "moe_grouped_dgrad": (_i32, [_vp] * 6),
         "moe_grouped_wgrad": (_i32, [_vp] * 5 + [_i32, _vp]),
+        "moe_route_topk": (_i32, [_vp, _i64, _vp, _i32, _i64, _vp, _vp, _vp, _vp]),
+        "moe_route_topk_backward": (_i32, [_vp, _i64, _vp, _i32, _i64, _vp, _vp, _vp, _vp, _i64, _vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -413,3 +424,68 @@ def moe_grouped_wgrad(dy, x, group_offsets, dw, accumulate: bool = False, stream
                                           1 if accumulate else 0, _stream(stream))
     _check("moe_grouped_wgrad", st)
 
+
+
+# --------------------------------------------------------------- router ----
+
+def make_router(E, topk, scoring=ROUTE_SOFTMAX, bias_kind=BIAS_NONE, renormalize=True, scale=1.0, groups=1,
+                topk_groups=1) -> MoeRouter:
+    return MoeRouter(E, topk, groups, topk_groups, scoring, bias_kind, 1 if renormalize else 0, scale)
+
+
+def _device_of(stream, *tensors):
+    """The call's stream, after checking that every tensor lies on the current
+    device (the one the kernels are launched on)."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.is_cuda and t.device.index != dev:
+            raise ValueError(f"tensor on cuda:{t.device.index}, the current device is cuda:{dev}")
+    return _stream(stream)
+
+
+_LOGIT_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _logits(t: torch.Tensor, E: int, name: str):
+    """(pointer, dtype code, row stride) of a [M, E] matrix whose rows are
+    contiguous and may lie apart."""
+    code = _LOGIT_DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected torch.float32 or torch.bfloat16")
+    if t.dim() != 2 or t.shape[1] != E:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [M, {E}]")
+    if not t.is_cuda:
+        raise ValueError("expected a device tensor")
+    M = t.shape[0]
+    if (E > 1 and t.stride(1) != 1) or (M > 1 and t.stride(0) < E):
+        raise ValueError(f"{name}: strides {t.stride()}, expected contiguous rows that do not overlap")
+    return t.data_ptr(), code, (t.stride(0) if M > 1 else E)
+
+
+def moe_route_topk(router: MoeRouter, logits, topk_ids, topk_weights, bias=None, stream=None):
+    """The topk experts of each row of logits [M, E] (float32 or bf16, rows may
+    lie apart) into topk_ids int32 [M, topk] and topk_weights float32 [M, topk]."""
+    ptr, code, ld = _logits(logits, router.E, "logits")
+    M = logits.shape[0]
+    st = load_library().moe_route_topk(
+        ctypes.byref(router), M, ptr, code, ld, _arg(bias, "bias", torch.float32, router.E),
+        _arg(topk_ids, "topk_ids", torch.int32, M * router.topk),
+        _arg(topk_weights, "topk_weights", torch.float32, M * router.topk),
+        _device_of(stream, logits, topk_ids, topk_weights, bias))
+    _check("moe_route_topk", st)
+
+
+def moe_route_topk_backward(router: MoeRouter, logits, topk_ids, dweights, dlogits, bias=None, stream=None):
+    """dlogits [M, E] (the logits' dtype) from the gradient dweights [M, topk]
+    of the weights moe_route_topk gave for topk_ids."""
+    ptr, code, ld = _logits(logits, router.E, "logits")
+    dptr, dcode, dld = _logits(dlogits, router.E, "dlogits")
+    M = logits.shape[0]
+    if dcode != code or dlogits.shape[0] != M:
+        raise ValueError("dlogits: expected the dtype and shape of logits")
+    st = load_library().moe_route_topk_backward(
+        ctypes.byref(router), M, ptr, code, ld, _arg(bias, "bias", torch.float32, router.E),
+        _arg(topk_ids, "topk_ids", torch.int32, M * router.topk),
+        _arg(dweights, "dweights", torch.float32, M * router.topk), dptr, dld,
+        _device_of(stream, logits, topk_ids, dweights, dlogits, bias))
+    _check("moe_route_topk_backward", st)

@@ -201,6 +201,21 @@ hipError_t launch_reduce_csr(const uint16_t* y, const float* w, const int32_t* o
                              const int32_t* rows, uint16_t* out, int64_t n_out, int64_t K,
                              hipStream_t s);
 
+// --------------------------------------------------------------- router ----
+// A validated moe_router (the enum values are the header's).
+struct RouterArgs {
+  int32_t E, topk, groups, topk_groups;
+  int32_t scoring, bias_kind, renormalize;
+  float scale;
+};
+constexpr int kRouterMaxE = 2048, kRouterMaxTopk = 64, kRouterMaxGroups = 64;
+
+hipError_t launch_route_topk(const RouterArgs& r, int64_t M, const void* logits, bool bf16, int64_t ld,
+                             const float* bias, int32_t* ids, float* weights, hipStream_t s);
+hipError_t launch_route_topk_backward(const RouterArgs& r, int64_t M, const void* logits, bool bf16, int64_t ld,
+                                      const float* bias, const int32_t* ids, const float* dw, void* dl,
+                                      int64_t dl_ld, hipStream_t s);
+
 // p[i * stride] = 0 for i < n (a fill kernel, capturable in a graph).
 hipError_t launch_zero_words(int32_t* p, int64_t n, int64_t stride, hipStream_t s);
 

@@ -715,4 +715,54 @@ int moe_grouped_wgrad(const moe_grouped_problem* p, const void* dy, const void* 
   return launch_train(t, (hipStream_t)stream) == hipSuccess ? MOE_OK : MOE_EHIP;
 }
 
+
+// --------------------------------------------------------------- router ----
+
+static bool router_args(const moe_router* r, RouterArgs* a) {
+  if (!r || r->E < 1 || r->E > kRouterMaxE || r->topk < 1 || r->topk > kRouterMaxTopk || r->topk > r->E) return false;
+  if (r->groups < 1 || r->groups > kRouterMaxGroups || r->E % r->groups || r->topk_groups < 1 ||
+      r->topk_groups > r->groups)
+    return false;
+  if (r->scoring != MOE_ROUTE_SOFTMAX && r->scoring != MOE_ROUTE_SIGMOID) return false;
+  if (r->bias_kind < MOE_ROUTE_BIAS_NONE || r->bias_kind > MOE_ROUTE_BIAS_SELECT) return false;
+  if ((r->renormalize != 0 && r->renormalize != 1) || !(r->scale - r->scale == 0.0f)) return false;
+  *a = RouterArgs{(int32_t)r->E, (int32_t)r->topk, (int32_t)r->groups, (int32_t)r->topk_groups,
+                  r->scoring, r->bias_kind, r->renormalize, r->scale};
+  return true;
+}
+
+// Logits or their gradient: M rows, ld elements apart, dtype 0 float32 or 1 bf16.
+static bool logits_ok(const void* p, int dtype, int64_t M, int64_t E, int64_t ld) {
+  if ((dtype != 0 && dtype != 1) || M < 0 || M >= (1ll << 31) || ld < E || ld >= (1ll << 31)) return false;
+  return M == 0 || (p && ((uintptr_t)p & (dtype == 0 ? 3u : 1u)) == 0);
+}
+
+static bool router_bias_ok(const RouterArgs& a, const float* bias) {
+  return a.bias_kind == MOE_ROUTE_BIAS_NONE ? bias == nullptr : aligned4(bias);
+}
+
+int moe_route_topk(const moe_router* r, int64_t M, const void* logits, int dtype, int64_t logits_ld,
+                   const float* bias, int32_t* topk_ids, float* topk_weights, void* stream) {
+  RouterArgs a;
+  if (!router_args(r, &a) || !logits_ok(logits, dtype, M, r->E, logits_ld) || !router_bias_ok(a, bias))
+    return MOE_EINVAL;
+  if (M > 0 && (!aligned4(topk_ids) || !aligned4(topk_weights))) return MOE_EINVAL;
+  hipError_t e = launch_route_topk(a, M, logits, dtype == 1, logits_ld, bias, topk_ids, topk_weights,
+                                   (hipStream_t)stream);
+  return e == hipSuccess ? MOE_OK : MOE_EHIP;
+}
+
+int moe_route_topk_backward(const moe_router* r, int64_t M, const void* logits, int dtype, int64_t logits_ld,
+                            const float* bias, const int32_t* topk_ids, const float* dweights, void* dlogits,
+                            int64_t dlogits_ld, void* stream) {
+  RouterArgs a;
+  if (!router_args(r, &a) || !logits_ok(logits, dtype, M, r->E, logits_ld) || !router_bias_ok(a, bias) ||
+      !logits_ok(dlogits, dtype, M, r->E, dlogits_ld))
+    return MOE_EINVAL;
+  if (M > 0 && (!aligned4(topk_ids) || !aligned4(dweights))) return MOE_EINVAL;
+  hipError_t e = launch_route_topk_backward(a, M, logits, dtype == 1, logits_ld, bias, topk_ids, dweights, dlogits,
+                                            dlogits_ld, (hipStream_t)stream);
+  return e == hipSuccess ? MOE_OK : MOE_EHIP;
+}
+
 }  // extern "C"

@@ -1,0 +1,171 @@
+// The router's scoring and top-k, and the gradient of its weights.
+//
+// For token t with logits l (plus a bias per expert): the topk experts with
+// the largest keys, ties to the lowest expert, and their weights
+//   w_j = scale * s_j          or, renormalised,  scale * s_j / sum_k s_k
+// where s is the softmax over the experts or the sigmoid of each.  The
+// gradient takes d(sum_j dw_j w_j) / dl with the choice held fixed:
+//   softmax, renormalised: dl_j = scale p_j (dw_j - sum_k p_k dw_k) over the
+//     chosen, p their softmax among themselves (the others cancel: 0);
+//   softmax: dl_i = scale p_i (dw_i - sum_k p_k dw_k), dw_i = 0 unless chosen;
+//   sigmoid: dl_j = ds_j s_j (1 - s_j), ds_j = scale dw_j, or renormalised
+//     scale (dw_j - sum_k dw_k s_k / S) / S with S = sum_k s_k.
+//
+// One wave per token, four tokens per workgroup, the token's logits in
+// registers: each is read once and nothing but the result is written, so at
+// 8192 x 128 the bound is the launch and the k rounds of the selection
+// rather than the 4 MB of logits.
+#include "kernels.h"
+#include "route_device.h"
+
+namespace moe {
+namespace {
+
+constexpr int kRouteWaves = 4;
+
+template <bool BF16>
+__device__ __forceinline__ float load_logit(const void* p, int64_t i) {
+  return BF16 ? bf16_to_f32(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
+}
+
+template <int NV, bool BF16>
+__global__ void __launch_bounds__(64 * kRouteWaves) route_topk_kernel(RouterArgs r, int64_t M,
+                                                                     const void* __restrict__ logits, int64_t ld,
+                                                                     const float* __restrict__ bias,
+                                                                     int32_t* __restrict__ ids,
+                                                                     float* __restrict__ weights) {
+  extern __shared__ double s_keys[];   // with groups: E doubles per wave
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave;
+  if (t >= M) return;
+  double l[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int e = lane + 64 * i;
+    double v = -INFINITY;
+    if (e < r.E) {
+      v = load_logit<BF16>(logits, t * ld + e);
+      if (r.bias_kind == 1) v += (double)bias[e];
+    }
+    l[i] = route_logit(v);
+  }
+  int id;
+  float w;
+  route_token<NV>(r, l, bias, s_keys + (r.groups > 1 ? wave * r.E : 0), id, w);
+  if (lane < r.topk) {
+    ids[t * r.topk + lane] = id;
+    weights[t * r.topk + lane] = w;
+  }
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(64 * kRouteWaves) route_topk_backward_kernel(
+    RouterArgs r, int64_t M, const void* __restrict__ logits, int64_t ld, const float* __restrict__ bias,
+    const int32_t* __restrict__ ids, const float* __restrict__ dw, void* __restrict__ dl, int64_t dl_ld) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave;
+  if (t >= M) return;
+  const bool softmax = r.scoring == 0;
+  auto logit = [&](int e) {
+    double v = load_logit<BF16>(logits, t * ld + e);
+    if (r.bias_kind == 1) v += (double)bias[e];
+    return route_logit(v);
+  };
+  // slot j of the token in lane j
+  int id = lane < r.topk ? ids[t * r.topk + lane] : -1;
+  if (id < 0 || id >= r.E) id = -1;
+  const double lj = id >= 0 ? logit(id) : -INFINITY;
+  const bool have = lj > -INFINITY;
+  const double g = have ? (double)dw[t * r.topk + lane] * (double)r.scale : 0.0;
+  double top = -INFINITY, inv = 0.0, dot = 0.0, d = 0.0;
+  const bool dense = softmax && !r.renormalize;   // every expert has a gradient
+  if (dense) {
+    for (int e = lane; e < r.E; e += 64) top = fmax(top, logit(e));
+    top = wave_max_f64(top);
+    float s = 0.f;
+    for (int e = lane; e < r.E; e += 64) {
+      const double v = logit(e);
+      s += v > -INFINITY ? expf((float)(v - top)) : 0.f;
+    }
+    const double total = wave_sum_f64(s);
+    inv = total > 0.0 ? 1.0 / total : 0.0;
+    dot = wave_sum_f64(have ? g * exp(lj - top) * inv : 0.0);
+    d = g;   // of the score
+  } else if (softmax) {
+    const double m = wave_max_f64(lj);
+    const double e = have ? exp(lj - m) : 0.0;
+    const double sum = wave_sum_f64(e);
+    const double p = have ? e / sum : 0.0;
+    d = p * (g - wave_sum_f64(p * g));
+  } else {
+    const double s = have ? sigmoid_f64(lj) : 0.0;
+    d = g;
+    if (r.renormalize) {
+      const double S = wave_sum_f64(s);
+      const double gs = wave_sum_f64(g * s);
+      d = S > 0.0 ? (g - gs / S) / S : 0.0;
+    }
+    d *= have ? s * (1.0 - s) : 0.0;
+  }
+  const float df = (float)d;
+  for (int e = lane; e - lane < r.E; e += 64) {
+    // an expert named in several slots gets the sum of their gradients
+    float v = 0.f;
+    for (int j = 0; j < r.topk; ++j) {
+      const int ej = __builtin_amdgcn_readlane(id, j);
+      const float dj = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(df), j));
+      v += ej == e ? dj : 0.f;
+    }
+    if (e < r.E) {
+      if (dense) {
+        const double le = logit(e);
+        const float p = le > -INFINITY ? expf((float)(le - top)) * (float)inv : 0.f;
+        v = p * (v - (float)dot);
+      }
+      if (BF16)
+        static_cast<uint16_t*>(dl)[t * dl_ld + e] = (uint16_t)f32_to_bf16_rne(v);
+      else
+        static_cast<float*>(dl)[t * dl_ld + e] = v;
+    }
+  }
+}
+
+template <int NV>
+hipError_t launch_topk(const RouterArgs& r, int64_t M, const void* logits, bool bf16, int64_t ld, const float* bias,
+                       int32_t* ids, float* weights, hipStream_t s) {
+  const dim3 grid((unsigned)((M + kRouteWaves - 1) / kRouteWaves)), block(64 * kRouteWaves);
+  const size_t lds = r.groups > 1 ? sizeof(double) * r.E * kRouteWaves : 0;
+  if (bf16)
+    hipLaunchKernelGGL((route_topk_kernel<NV, true>), grid, block, lds, s, r, M, logits, ld, bias, ids, weights);
+  else
+    hipLaunchKernelGGL((route_topk_kernel<NV, false>), grid, block, lds, s, r, M, logits, ld, bias, ids, weights);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_route_topk(const RouterArgs& r, int64_t M, const void* logits, bool bf16, int64_t ld,
+                             const float* bias, int32_t* ids, float* weights, hipStream_t s) {
+  if (M == 0) return hipSuccess;
+  if (r.E <= 64) return launch_topk<1>(r, M, logits, bf16, ld, bias, ids, weights, s);
+  if (r.E <= 128) return launch_topk<2>(r, M, logits, bf16, ld, bias, ids, weights, s);
+  if (r.E <= 256) return launch_topk<4>(r, M, logits, bf16, ld, bias, ids, weights, s);
+  if (r.E <= 512) return launch_topk<8>(r, M, logits, bf16, ld, bias, ids, weights, s);
+  return launch_topk<32>(r, M, logits, bf16, ld, bias, ids, weights, s);
+}
+
+hipError_t launch_route_topk_backward(const RouterArgs& r, int64_t M, const void* logits, bool bf16, int64_t ld,
+                                      const float* bias, const int32_t* ids, const float* dw, void* dl,
+                                      int64_t dl_ld, hipStream_t s) {
+  if (M == 0) return hipSuccess;
+  const dim3 grid((unsigned)((M + kRouteWaves - 1) / kRouteWaves)), block(64 * kRouteWaves);
+  if (bf16)
+    hipLaunchKernelGGL((route_topk_backward_kernel<true>), grid, block, 0, s, r, M, logits, ld, bias, ids, dw, dl,
+                       dl_ld);
+  else
+    hipLaunchKernelGGL((route_topk_backward_kernel<false>), grid, block, 0, s, r, M, logits, ld, bias, ids, dw, dl,
+                       dl_ld);
+  return hipGetLastError();
+}
+
+}  // namespace moe
