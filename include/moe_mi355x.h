@@ -482,6 +482,71 @@ int moe_route_topk_backward(const moe_router* r, int64_t M, const void* logits, 
                             const float* bias, const int32_t* topk_ids, const float* dweights, void* dlogits,
                             int64_t dlogits_ld, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * A whole mixture-of-experts layer for a few tokens (decode batches, M <= 64)
+ * in two launches: the router's projection and routing, the experts, the
+ * weighted sum and any shared experts.
+ *
+ *   logits = x router_w^T, (ids, w) = moe_route_topk's choice of them
+ *   out[t] = bf16(sum_j w[t,j] W2_e(silu(W1g_e x[t]) * W1u_e x[t]), e = ids[t,j]
+ *                 + the same with weight 1 for each shared expert)
+ *
+ * bf16 x bf16 products summed in float32 in a fixed order (the same bits on
+ * every run); the intermediate, its weight included, is rounded to bf16 once;
+ * the sum over the experts is rounded once.  MXFP8 weights are decoded exactly
+ * (the activations stay bf16, unlike moe_apply_contiguous, which quantises
+ * them), values below bf16's normal range excepted, which may count as 0.
+ * A token without an expert to choose gets only the shared experts, or +0.0.
+ * ------------------------------------------------------------------------- */
+typedef struct moe_layer_problem {
+  int64_t M;               /* tokens, 1 .. 64                                  */
+  int64_t K;               /* hidden size, a multiple of 128                   */
+  int64_t I;               /* intermediate size, a multiple of 128             */
+  int64_t shared_experts;  /* 0 .. 16 experts every token takes, behind the
+                              router's E in the weight arrays                  */
+  moe_router router;       /* E <= 512, topk <= 32                             */
+  int32_t w_dtype;         /* MOE_W_BF16 or MOE_W_MXFP8                        */
+  int32_t w1_order;        /* MOE_W1_*                                         */
+} moe_layer_problem;
+
+typedef struct moe_layer_plan {
+  moe_layer_problem prob;
+  int32_t abi_version;
+  int32_t splits;          /* workgroups that share 16 columns of the output   */
+  int64_t max_slots;       /* experts that can hold a token, shared included   */
+  int64_t rows;            /* rows of the intermediate: M (topk + shared)      */
+  int64_t ws_bytes;        /* size of the workspace                            */
+  /* byte offsets in the workspace (opaque but for the status word) */
+  int64_t off_sync, off_status, off_logits, off_slots, off_rows, off_row_weights, off_z, off_partial;
+  char reason[192];        /* why unsupported                                  */
+} moe_layer_plan;
+
+/* sizeof(moe_router), sizeof(moe_layer_problem) and sizeof(moe_layer_plan) as
+ * compiled into the library (each pointer may be NULL). */
+void moe_layer_struct_sizes(int64_t* router, int64_t* problem, int64_t* plan);
+
+/* Validate `prob` (host) and fill `plan` (host).  MOE_EINVAL: null pointers,
+ * a bad router, non-positive sizes, bad enums.  MOE_EUNSUPPORTED (reason set):
+ * M > 64, E > 512, topk > 32, shared_experts > 16, K or I not a multiple of
+ * 128, other weight types, or one expert's W1 or the intermediate at or past
+ * 2^31 bytes. */
+int moe_layer_plan_init(moe_layer_plan* plan, const moe_layer_problem* prob);
+
+/* x: device bf16 [M, K]; router_w: device bf16 [E, K]; router_bias: device
+ * float32 [E] (NULL exactly when bias_kind is NONE); w: host struct of device
+ * pointers, W1 [E + shared, 2I, K], W2 [E + shared, K, I] and their scales as
+ * for moe_apply_contiguous (expert_map must be NULL); out: device bf16 [M, K];
+ * topk_ids: device int32 [M, topk] and topk_weights: device float32 [M, topk],
+ * written; ws: device, plan->ws_bytes, 16-byte aligned, zero-filled before
+ * its first call.  Each call leaves it ready for the next; calls that share a
+ * workspace must not overlap.  The first launch waits in the kernel for the
+ * routing, for about a second at most: the int32 at off_status counts waits
+ * that gave up, summed over calls (non-zero: some call's outputs are
+ * undefined, and the workspace must be zero-filled again). */
+int moe_layer_apply(const moe_layer_plan* plan, const void* x, const void* router_w, const float* router_bias,
+                    const moe_weights* w, void* out, int32_t* topk_ids, float* topk_weights, void* ws,
+                    void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -28,6 +28,8 @@ __all__ = [
     "MoeGroupedProblem", "moe_grouped_forward", "moe_grouped_dgrad", "moe_grouped_wgrad",
     "ROUTE_SOFTMAX", "ROUTE_SIGMOID", "BIAS_NONE", "BIAS_LOGIT", "BIAS_SELECT", "MoeRouter", "make_router",
     "moe_route_topk", "moe_route_topk_backward",
+    "MoeLayerProblem", "MoeLayerPlan", "make_layer_problem", "moe_layer_plan_init", "allocate_layer_workspace",
+    "moe_layer_apply", "check_layer_status",
 ]
 
 ABI_VERSION = 6
@@ -57,6 +59,18 @@ class MoeGroupedProblem(ctypes.Structure):
 class MoeRouter(ctypes.Structure):
     _fields_ = [("E", _i64), ("topk", _i64), ("groups", _i64), ("topk_groups", _i64), ("scoring", _i32),
                 ("bias_kind", _i32), ("renormalize", _i32), ("scale", ctypes.c_float)]
+
+
+class MoeLayerProblem(ctypes.Structure):
+    _fields_ = [("M", _i64), ("K", _i64), ("I", _i64), ("shared_experts", _i64), ("router", MoeRouter),
+                ("w_dtype", _i32), ("w1_order", _i32)]
+
+
+class MoeLayerPlan(ctypes.Structure):
+    _fields_ = [("prob", MoeLayerProblem), ("abi_version", _i32), ("splits", _i32), ("max_slots", _i64),
+                ("rows", _i64), ("ws_bytes", _i64), ("off_sync", _i64), ("off_status", _i64), ("off_logits", _i64),
+                ("off_slots", _i64), ("off_rows", _i64), ("off_row_weights", _i64), ("off_z", _i64),
+                ("off_partial", _i64), ("reason", ctypes.c_char * 192)]
 
 
 class MoePlan(ctypes.Structure):
@@ -121,6 +135,9 @@ def load_library() -> ctypes.CDLL:
         "moe_grouped_forward": (_i32, [_vp] * 6),
         "moe_grouped_dgrad": (_i32, [_vp] * 6),
         "moe_grouped_wgrad": (_i32, [_vp] * 5 + [_i32, _vp]),
+        "moe_layer_struct_sizes": (None, [_vp, _vp, _vp]),
+        "moe_layer_plan_init": (_i32, [_vp, _vp]),
+        "moe_layer_apply": (_i32, [_vp] * 10),
         "moe_route_topk": (_i32, [_vp, _i64, _vp, _i32, _i64, _vp, _vp, _vp, _vp]),
         "moe_route_topk_backward": (_i32, [_vp, _i64, _vp, _i32, _i64, _vp, _vp, _vp, _vp, _i64, _vp]),
     }
@@ -134,6 +151,10 @@ def load_library() -> ctypes.CDLL:
     sizes = [ctypes.c_int64() for _ in range(3)]
     lib.moe_struct_sizes(*[ctypes.byref(s) for s in sizes])
     want = [ctypes.sizeof(MoeProblem), ctypes.sizeof(MoePlan), ctypes.sizeof(MoeWeights)]
+    if [s.value for s in sizes] != want:
+        raise RuntimeError(f"struct layout mismatch: library {[s.value for s in sizes]}, binding {want}")
+    lib.moe_layer_struct_sizes(*[ctypes.byref(s) for s in sizes])
+    want = [ctypes.sizeof(MoeRouter), ctypes.sizeof(MoeLayerProblem), ctypes.sizeof(MoeLayerPlan)]
     if [s.value for s in sizes] != want:
         raise RuntimeError(f"struct layout mismatch: library {[s.value for s in sizes]}, binding {want}")
     _LIB = lib
@@ -489,3 +510,55 @@ def moe_route_topk_backward(router: MoeRouter, logits, topk_ids, dweights, dlogi
         _arg(dweights, "dweights", torch.float32, M * router.topk), dptr, dld,
         _device_of(stream, logits, topk_ids, dweights, dlogits, bias))
     _check("moe_route_topk_backward", st)
+
+
+# ---------------------------------------------------------------- layer ----
+
+def make_layer_problem(M, K, I, router: MoeRouter, shared_experts=0, w_dtype=W_BF16,
+                       w1_order=W1_HALVES) -> MoeLayerProblem:
+    return MoeLayerProblem(M, K, I, shared_experts, router, w_dtype, w1_order)
+
+
+def moe_layer_plan_init(prob: MoeLayerProblem) -> MoeLayerPlan:
+    plan = MoeLayerPlan()
+    st = load_library().moe_layer_plan_init(ctypes.byref(plan), ctypes.byref(prob))
+    _check("moe_layer_plan_init", st, plan)
+    return plan
+
+
+def allocate_layer_workspace(plan: MoeLayerPlan, device="cuda") -> torch.Tensor:
+    """The layer's workspace, zero-filled (its counters start at zero)."""
+    return torch.zeros(plan.ws_bytes, dtype=torch.uint8, device=device)
+
+
+def check_layer_status(plan: MoeLayerPlan, ws: torch.Tensor):
+    """Raise MoeError when a call on this workspace gave up its bounded wait
+    (its outputs are undefined).  Synchronises with the device."""
+    timeouts = int(ws_view(ws, plan.off_status, 1).cpu()[0])
+    if timeouts:
+        raise MoeError("moe_layer_apply", MOE_EHIP, f"{timeouts} bounded waits timed out; outputs undefined")
+
+
+def moe_layer_apply(plan: MoeLayerPlan, x, router_w, w1, w2, out, topk_ids, topk_weights, ws, router_bias=None,
+                    w1_scale=None, w2_scale=None, stream=None):
+    """out [M, K] = the whole layer on x [M, K] (bf16); also the router's choice
+    (topk_ids int32, topk_weights float32, [M, topk]).  ws: from
+    allocate_layer_workspace; calls that share it must not overlap."""
+    p = plan.prob
+    r = p.router
+    mx = p.w_dtype == W_MXFP8
+    wt = torch.uint8 if mx else torch.bfloat16
+    n1 = (r.E + p.shared_experts) * 2 * p.I * p.K
+    n2 = n1 // 2
+    if mx and (w1_scale is None or w2_scale is None):
+        raise ValueError("MXFP8 weights need w1_scale and w2_scale")
+    w = MoeWeights(_arg(w1, "w1", wt, n1), _arg(w1_scale, "w1_scale", torch.uint8, n1 // 32 if mx else 0),
+                   _arg(w2, "w2", wt, n2), _arg(w2_scale, "w2_scale", torch.uint8, n2 // 32 if mx else 0), None)
+    st = load_library().moe_layer_apply(
+        ctypes.byref(plan), _arg(x, "x", torch.bfloat16, p.M * p.K),
+        _arg(router_w, "router_w", torch.bfloat16, r.E * p.K),
+        _arg(router_bias, "router_bias", torch.float32, r.E), ctypes.byref(w),
+        _arg(out, "out", torch.bfloat16, p.M * p.K), _arg(topk_ids, "topk_ids", torch.int32, p.M * r.topk),
+        _arg(topk_weights, "topk_weights", torch.float32, p.M * r.topk), _ws(ws, "ws", plan.ws_bytes),
+        _device_of(stream, x, router_w, w1, w2, out, topk_ids, topk_weights, ws, router_bias, w1_scale, w2_scale))
+    _check("moe_layer_apply", st)

@@ -216,6 +216,56 @@ hipError_t launch_route_topk_backward(const RouterArgs& r, int64_t M, const void
                                       const float* bias, const int32_t* ids, const float* dw, void* dl,
                                       int64_t dl_ld, hipStream_t s);
 
+// ---------------------------------------------------------------- layer ----
+// The whole layer for a few tokens (layer.hip).
+constexpr int kLayerMaxM = 64;           // a token is a bit of a 64-bit mask
+constexpr int kLayerMaxE = 512;          // one expert per thread of the routing workgroup
+constexpr int kLayerMaxTopk = 32;
+constexpr int kLayerMaxShared = 16;
+constexpr int kLayerMaxRoutes = kLayerMaxM * kLayerMaxTopk;
+// the sync area, int32 words, one 128-byte line per counter that many
+// workgroups touch at once; then one word per strip of the second launch
+enum { kLayerClaim = 0, kLayerArrived = kSyncLine, kLayerRouted = 2 * kSyncLine, kLayerNumSlots = 2 * kSyncLine + 1,
+       kLayerDone = 3 * kSyncLine, kLayerStrips = 4 * kSyncLine };
+
+struct alignas(16) LayerSlot {
+  int32_t e, cnt, pos0, pad;   // expert, its tokens, their first row of z
+  uint64_t mask;               // its tokens
+  uint64_t pad2;
+};
+
+struct LayerArgs {
+  RouterArgs r;
+  int32_t M, K, I, S, w1_order;
+  const uint16_t* x;           // [M, K]
+  const uint16_t* wr;          // [E, K]
+  const float* rbias;          // [E] or null
+  const void* w1;              // [E + S, 2I, K]
+  const uint8_t* w1s;
+  const void* w2;              // [E + S, K, I]
+  const uint8_t* w2s;
+  uint16_t* out;               // [M, K]
+  int32_t* ids;                // [M, topk]
+  float* wts;
+  // workspace
+  int32_t* sync;               // [kLayerStrips + K / 16]
+  int32_t* status;             // [1] waits that timed out
+  float* logits;               // [rsplit][M][logit_ld] partial sums
+  LayerSlot* slots;            // [max_slots]
+  int32_t* rows;               // [cap] token of each row of z
+  float* roww;                 // [cap] its weight
+  uint16_t* z;                 // [cap, I]
+  float* part;                 // [K / 16][splits][M][16]
+  int32_t logit_ld, max_slots, cap;
+  // set by the launcher
+  int32_t rsplit, runits;      // K splits and units of the router
+  int32_t splits, ks;          // workgroups per strip of W2; waves per operand of a W1 strip
+};
+
+int32_t layer_splits(int64_t K);
+int32_t layer_router_splits(int64_t K);
+hipError_t launch_layer(LayerArgs g, bool mxfp8, hipStream_t s);
+
 // p[i * stride] = 0 for i < n (a fill kernel, capturable in a graph).
 hipError_t launch_zero_words(int32_t* p, int64_t n, int64_t stride, hipStream_t s);
 

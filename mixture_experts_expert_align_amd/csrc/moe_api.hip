@@ -765,4 +765,103 @@ int moe_route_topk_backward(const moe_router* r, int64_t M, const void* logits, 
   return e == hipSuccess ? MOE_OK : MOE_EHIP;
 }
 
+// ---------------------------------------------------------------- layer ----
+
+void moe_layer_struct_sizes(int64_t* router, int64_t* problem, int64_t* plan) {
+  if (router) *router = sizeof(moe_router);
+  if (problem) *problem = sizeof(moe_layer_problem);
+  if (plan) *plan = sizeof(moe_layer_plan);
+}
+
+static int layer_fail(moe_layer_plan* plan, int code, const char* msg) {
+  snprintf(plan->reason, sizeof(plan->reason), "%s", msg);
+  return code;
+}
+
+int moe_layer_plan_init(moe_layer_plan* plan, const moe_layer_problem* prob) {
+  if (!plan || !prob) return MOE_EINVAL;
+  memset(plan, 0, sizeof(*plan));
+  plan->prob = *prob;
+  const moe_layer_problem& P = *prob;
+  RouterArgs r;
+  if (!router_args(&P.router, &r)) return layer_fail(plan, MOE_EINVAL, "bad router");
+  if (P.M <= 0 || P.K <= 0 || P.I <= 0 || P.shared_experts < 0)
+    return layer_fail(plan, MOE_EINVAL, "M, K and I must be positive, shared_experts not negative");
+  if (P.w_dtype != MOE_W_BF16 && P.w_dtype != MOE_W_MXFP8 && P.w_dtype != MOE_W_MXFP8_GROUPED)
+    return layer_fail(plan, MOE_EINVAL, "unknown weight dtype");
+  if (P.w1_order != MOE_W1_HALVES && P.w1_order != MOE_W1_INTERLEAVE16)
+    return layer_fail(plan, MOE_EINVAL, "unknown W1 row order");
+  if (P.w_dtype == MOE_W_MXFP8_GROUPED)
+    return layer_fail(plan, MOE_EUNSUPPORTED, "the layer reads row-major MXFP8 scales");
+  if (P.M > kLayerMaxM || r.E > kLayerMaxE || r.topk > kLayerMaxTopk || P.shared_experts > kLayerMaxShared)
+    return layer_fail(plan, MOE_EUNSUPPORTED, "the layer takes M <= 64, E <= 512, topk <= 32, shared_experts <= 16");
+  if (P.K % 128 || P.I % 128) return layer_fail(plan, MOE_EUNSUPPORTED, "the layer needs K % 128 == 0 and I % 128 == 0");
+  const int64_t rows = P.M * (r.topk + P.shared_experts);
+  // 32-bit buffer offsets: one expert's W1, x, the router's weights, z
+  if (P.K >= (1ll << 29) || P.I >= (1ll << 29) || 4 * P.I * P.K >= (1ll << 31) || 2 * P.M * P.K >= (1ll << 31) ||
+      2ll * r.E * P.K >= (1ll << 31) || 2 * rows * P.I >= (1ll << 31))
+    return layer_fail(plan, MOE_EUNSUPPORTED, "the layer addresses one expert and the intermediate with 32-bit offsets");
+  plan->abi_version = MOE_ABI_VERSION;
+  plan->splits = layer_splits(P.K);
+  plan->max_slots = (r.E < P.M * r.topk ? r.E : P.M * r.topk) + P.shared_experts;
+  plan->rows = rows;
+  int64_t o = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t at = o;
+    o = up(o + bytes, kAlign);
+    return at;
+  };
+  plan->off_sync = take(4 * (kLayerStrips + P.K / 16));
+  plan->off_status = take(4);
+  plan->off_logits = take(4 * layer_router_splits(P.K) * P.M * up(r.E, 16));
+  plan->off_slots = take((int64_t)sizeof(LayerSlot) * plan->max_slots);
+  plan->off_rows = take(4 * rows);
+  plan->off_row_weights = take(4 * rows);
+  plan->off_z = take(2 * rows * P.I);
+  plan->off_partial = take(plan->splits > 1 ? 4 * plan->splits * P.M * P.K : 0);
+  plan->ws_bytes = o;
+  return MOE_OK;
+}
+
+int moe_layer_apply(const moe_layer_plan* plan, const void* x, const void* router_w, const float* router_bias,
+                    const moe_weights* w, void* out, int32_t* topk_ids, float* topk_weights, void* ws,
+                    void* stream) {
+  if (!plan || plan->abi_version != MOE_ABI_VERSION || !w) return MOE_EINVAL;
+  const moe_layer_problem& P = plan->prob;
+  const bool mx = P.w_dtype == MOE_W_MXFP8;
+  LayerArgs g{};
+  if (!router_args(&P.router, &g.r) || !router_bias_ok(g.r, router_bias)) return MOE_EINVAL;
+  if (!aligned16(x) || !aligned16(router_w) || !aligned16(w->w1) || !aligned16(w->w2) || !aligned16(out) ||
+      !aligned4(topk_ids) || !aligned4(topk_weights) || !aligned16(ws) || w->expert_map)
+    return MOE_EINVAL;
+  if (mx && (!aligned4(w->w1_scale) || !aligned4(w->w2_scale))) return MOE_EINVAL;
+  g.M = (int32_t)P.M;
+  g.K = (int32_t)P.K;
+  g.I = (int32_t)P.I;
+  g.S = (int32_t)P.shared_experts;
+  g.w1_order = P.w1_order;
+  g.x = static_cast<const uint16_t*>(x);
+  g.wr = static_cast<const uint16_t*>(router_w);
+  g.rbias = router_bias;
+  g.w1 = w->w1;
+  g.w1s = w->w1_scale;
+  g.w2 = w->w2;
+  g.w2s = w->w2_scale;
+  g.out = static_cast<uint16_t*>(out);
+  g.ids = topk_ids;
+  g.wts = topk_weights;
+  g.sync = at<int32_t>(ws, plan->off_sync);
+  g.status = at<int32_t>(ws, plan->off_status);
+  g.logits = at<float>(ws, plan->off_logits);
+  g.slots = at<LayerSlot>(ws, plan->off_slots);
+  g.rows = at<int32_t>(ws, plan->off_rows);
+  g.roww = at<float>(ws, plan->off_row_weights);
+  g.z = at<uint16_t>(ws, plan->off_z);
+  g.part = at<float>(ws, plan->off_partial);
+  g.logit_ld = (int32_t)up(g.r.E, 16);
+  g.max_slots = (int32_t)plan->max_slots;
+  g.cap = (int32_t)plan->rows;
+  return launch_layer(g, mx, (hipStream_t)stream) == hipSuccess ? MOE_OK : MOE_EHIP;
+}
+
 }  // extern "C"
