@@ -547,6 +547,58 @@ int moe_layer_apply(const moe_layer_plan* plan, const void* x, const void* route
                     const moe_weights* w, void* out, int32_t* topk_ids, float* topk_weights, void* ws,
                     void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Low-rank adapters of many requests at once beside a shared projection, and
+ * their gradients: row r of R takes adapter g = adapter[r], in any order (an
+ * id outside [0, G), such as -1: none).
+ *
+ *   s_r = scale[g] A[g] x_r          y_r  = W x_r + B[g] s_r
+ *   t_r = scale[g] B[g]^T dy_r       dx_r = W^T dy_r + A[g]^T t_r
+ *   dA[g] = sum over g's rows of t_r x_r^T,   dB[g] = sum of dy_r s_r^T
+ *
+ * x, dx [R, K], dy, y [R, N], W [N, K], A [G, rank, K], B [G, N, rank]: device
+ * bf16; scale: device float32 [G]; adapter: device int32 [R]; dA [G, rank, K],
+ * dB [G, N, rank]: device float32.  Products of bf16 values summed in float32
+ * in a fixed order (the same bits on every run); s and t are kept to float32
+ * precision, y and dx rounded to bf16 once.  W is shared by all rows and
+ * frozen here (its own gradient is moe_grouped_wgrad with one group).  Row
+ * adapters may name (request, expert) pairs as well as requests.
+ *
+ * `low` (device, moe_lora_low_bytes, 16-byte aligned) receives s or t in the
+ * library's own form; moe_lora_wgrad reads the one that moe_lora_forward
+ * wrote for x and the one that moe_lora_dgrad wrote for dy.  Every call only
+ * enqueues kernels; outputs must not overlap inputs.  With R = 0 the row
+ * matrices, adapter and low may be NULL.  Errors: MOE_EINVAL (null or
+ * misaligned pointer: 16 bytes for matrices and low and ws, 4 for scale and
+ * adapter; R outside [0, 2^31), N, K, G or rank not positive), MOE_EUNSUPPORTED
+ * (N or K not a multiple of 64; rank not a multiple of 8 or past 128; G past
+ * 4096; R max(N, K), N K, G rank max(N, K) or 3 R rank elements of 2 bytes at
+ * or past 2^31 bytes), MOE_EHIP.
+ * ------------------------------------------------------------------------- */
+typedef struct moe_lora_problem {
+  int64_t R;      /* rows                                                      */
+  int64_t N;      /* output features                                           */
+  int64_t K;      /* input features                                            */
+  int64_t G;      /* adapters                                                  */
+  int64_t rank;   /* of every adapter                                          */
+} moe_lora_problem;
+
+/* Bytes of `low` and of moe_lora_wgrad's workspace; -1 for a problem the calls
+ * refuse. */
+int64_t moe_lora_low_bytes(const moe_lora_problem* p);
+int64_t moe_lora_ws_bytes(const moe_lora_problem* p);
+
+int moe_lora_forward(const moe_lora_problem* p, const void* x, const void* w, const void* a, const void* b,
+                     const float* scale, const int32_t* adapter, void* y, void* low, void* stream);
+
+int moe_lora_dgrad(const moe_lora_problem* p, const void* dy, const void* w, const void* a, const void* b,
+                   const float* scale, const int32_t* adapter, void* dx, void* low, void* stream);
+
+/* accumulate = 0 writes dA and dB (+0.0 for an adapter without rows), 1 adds
+ * the finished sums, as moe_grouped_wgrad does. */
+int moe_lora_wgrad(const moe_lora_problem* p, const void* x, const void* dy, const void* low_x, const void* low_dy,
+                   const int32_t* adapter, float* da, float* db, int accumulate, void* ws, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

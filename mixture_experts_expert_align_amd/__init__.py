@@ -30,6 +30,8 @@ __all__ = [
     "moe_route_topk", "moe_route_topk_backward",
     "MoeLayerProblem", "MoeLayerPlan", "make_layer_problem", "moe_layer_plan_init", "allocate_layer_workspace",
     "moe_layer_apply", "check_layer_status",
+    "MoeLoraProblem", "moe_lora_low_bytes", "moe_lora_ws_bytes", "allocate_lora_low", "allocate_lora_workspace",
+    "moe_lora_forward", "moe_lora_dgrad", "moe_lora_wgrad",
 ]
 
 ABI_VERSION = 6
@@ -71,6 +73,10 @@ class MoeLayerPlan(ctypes.Structure):
                 ("rows", _i64), ("ws_bytes", _i64), ("off_sync", _i64), ("off_status", _i64), ("off_logits", _i64),
                 ("off_slots", _i64), ("off_rows", _i64), ("off_row_weights", _i64), ("off_z", _i64),
                 ("off_partial", _i64), ("reason", ctypes.c_char * 192)]
+
+
+class MoeLoraProblem(ctypes.Structure):
+    _fields_ = [("R", _i64), ("N", _i64), ("K", _i64), ("G", _i64), ("rank", _i64)]
 
 
 class MoePlan(ctypes.Structure):
@@ -138,6 +144,11 @@ def load_library() -> ctypes.CDLL:
         "moe_layer_struct_sizes": (None, [_vp, _vp, _vp]),
         "moe_layer_plan_init": (_i32, [_vp, _vp]),
         "moe_layer_apply": (_i32, [_vp] * 10),
+        "moe_lora_low_bytes": (_i64, [_vp]),
+        "moe_lora_ws_bytes": (_i64, [_vp]),
+        "moe_lora_forward": (_i32, [_vp] * 10),
+        "moe_lora_dgrad": (_i32, [_vp] * 10),
+        "moe_lora_wgrad": (_i32, [_vp] * 8 + [_i32, _vp, _vp]),
         "moe_route_topk": (_i32, [_vp, _i64, _vp, _i32, _i64, _vp, _vp, _vp, _vp]),
         "moe_route_topk_backward": (_i32, [_vp, _i64, _vp, _i32, _i64, _vp, _vp, _vp, _vp, _i64, _vp]),
     }
@@ -562,3 +573,81 @@ def moe_layer_apply(plan: MoeLayerPlan, x, router_w, w1, w2, out, topk_ids, topk
         _arg(topk_weights, "topk_weights", torch.float32, p.M * r.topk), _ws(ws, "ws", plan.ws_bytes),
         _device_of(stream, x, router_w, w1, w2, out, topk_ids, topk_weights, ws, router_bias, w1_scale, w2_scale))
     _check("moe_layer_apply", st)
+
+
+# ----------------------------------------------------------------- lora ----
+
+def _lora_bytes(fn: str, R, N, K, G, rank) -> int:
+    v = getattr(load_library(), fn)(ctypes.byref(MoeLoraProblem(R, N, K, G, rank)))
+    if v < 0:
+        raise MoeError(fn, MOE_EINVAL)
+    return v
+
+
+def moe_lora_low_bytes(R, N, K, G, rank) -> int:
+    return _lora_bytes("moe_lora_low_bytes", R, N, K, G, rank)
+
+
+def moe_lora_ws_bytes(R, N, K, G, rank) -> int:
+    return _lora_bytes("moe_lora_ws_bytes", R, N, K, G, rank)
+
+
+def allocate_lora_low(R, rank, device="cuda") -> torch.Tensor:
+    """The narrow products of R rows, as moe_lora_forward and moe_lora_dgrad
+    write them (moe_lora_low_bytes)."""
+    return torch.empty(max(moe_lora_low_bytes(R, 64, 64, 1, rank), 16), dtype=torch.uint8, device=device)
+
+
+def allocate_lora_workspace(R, N, K, G, rank, device="cuda") -> torch.Tensor:
+    """moe_lora_wgrad's workspace (moe_lora_ws_bytes)."""
+    return torch.empty(max(moe_lora_ws_bytes(R, N, K, G, rank), 16), dtype=torch.uint8, device=device)
+
+
+def _lora_project(fn, v, C, w, a, b, scale, adapter, out, out_cols, low, stream):
+    if w.dim() != 2 or a.dim() != 3 or b.dim() != 3:
+        raise ValueError("expected w [N, K], a [G, rank, K], b [G, N, rank]")
+    (N, K), (G, rank) = w.shape, a.shape[:2]
+    if a.shape[2] != K or tuple(b.shape) != (G, N, rank):
+        raise ValueError(f"w {tuple(w.shape)}, a {tuple(a.shape)}, b {tuple(b.shape)}: "
+                         "expected [N, K], [G, rank, K], [G, N, rank]")
+    R = v.shape[0]
+    if v.shape[1:] != w.shape[C:C + 1] or tuple(out.shape) != (R, w.shape[out_cols]):
+        raise ValueError(f"rows {tuple(v.shape)} and {tuple(out.shape)} do not fit w {tuple(w.shape)}")
+    p = MoeLoraProblem(R, N, K, G, rank)
+    st = getattr(load_library(), fn)(
+        ctypes.byref(p), _arg(v, "rows", torch.bfloat16, 0), _arg(w, "w", torch.bfloat16, 0),
+        _arg(a, "a", torch.bfloat16, 0), _arg(b, "b", torch.bfloat16, 0), _arg(scale, "scale", torch.float32, G),
+        _arg(adapter, "adapter", torch.int32, R), _arg(out, "output rows", torch.bfloat16, 0),
+        _ws(low, "low", 6 * R * rank), _device_of(stream, v, w, a, b, scale, adapter, out, low))
+    _check(fn, st)
+
+
+def moe_lora_forward(x, w, a, b, scale, adapter, y, low, stream=None):
+    """y [R, N] = x [R, K] W^T + scale_g (x A_g^T) B_g^T, g = adapter[r] (int32
+    [R], -1: none); w [N, K], a [G, rank, K], b [G, N, rank], scale float32 [G];
+    low: from allocate_lora_low, read again by moe_lora_wgrad."""
+    _lora_project("moe_lora_forward", x, 1, w, a, b, scale, adapter, y, 0, low, stream)
+
+
+def moe_lora_dgrad(dy, w, a, b, scale, adapter, dx, low, stream=None):
+    """dx [R, K] = dy [R, N] W + scale_g (dy B_g) A_g."""
+    _lora_project("moe_lora_dgrad", dy, 0, w, a, b, scale, adapter, dx, 1, low, stream)
+
+
+def moe_lora_wgrad(x, dy, low_x, low_dy, adapter, da, db, ws, accumulate: bool = False, stream=None):
+    """da [G, rank, K] and db [G, N, rank] (float32, written, or added to when
+    ``accumulate``) from the forward's low (of x) and the dgrad's (of dy)."""
+    (R, K), N = x.shape, dy.shape[1]
+    G, rank = da.shape[:2]
+    if dy.shape[0] != R or da.shape[2] != K or tuple(db.shape) != (G, N, rank):
+        raise ValueError(f"x {tuple(x.shape)}, dy {tuple(dy.shape)}, da {tuple(da.shape)}, db {tuple(db.shape)} "
+                         "do not fit")
+    p = MoeLoraProblem(R, N, K, G, rank)
+    low = 6 * R * rank
+    st = load_library().moe_lora_wgrad(
+        ctypes.byref(p), _arg(x, "x", torch.bfloat16, 0), _arg(dy, "dy", torch.bfloat16, 0), _ws(low_x, "low_x", low),
+        _ws(low_dy, "low_dy", low), _arg(adapter, "adapter", torch.int32, R), _arg(da, "da", torch.float32, 0),
+        _arg(db, "db", torch.float32, 0), 1 if accumulate else 0,
+        _ws(ws, "ws", max(load_library().moe_lora_ws_bytes(ctypes.byref(p)), 0)),
+        _device_of(stream, x, dy, low_x, low_dy, adapter, da, db, ws))
+    _check("moe_lora_wgrad", st)

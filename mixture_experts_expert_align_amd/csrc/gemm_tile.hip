@@ -56,7 +56,9 @@ namespace tile {
 // pieces of 32 rows per store instruction.
 // ROUTES: the launch may take the contiguous format, whose W2 rows go to the
 // routes' (token, slot) rows (false for the rows layout of training).
-template <int EPI, int BM, int BN, int WN, int WM, int NT, int TW, int TX, bool ROUTES>
+// EDGE: the last weight tile may reach past the output's nfeat columns, which
+// are a multiple of 8 (a chunk is all inside or all outside).
+template <int EPI, int BM, int BN, int WN, int WM, int NT, int TW, int TX, bool ROUTES, bool EDGE = false>
 __device__ __forceinline__ void tile_epilogue(const GemmArgs& g, const TileCoord& tc,
                                               const f32x16 (&acc)[TW][TX], int wn, int wm, int lane,
                                               uint16_t* stage) {
@@ -114,6 +116,7 @@ __device__ __forceinline__ void tile_epilogue(const GemmArgs& g, const TileCoord
   const int col = EPI == kEpiGateUp ? tc.col0 / 2 : tc.col0;
   const int c = threadIdx.x % NCH;
   auto put = [&](int m, int64_t orow) {
+    if (EDGE && col + 8 * c >= g.nfeat) return;
     *reinterpret_cast<i32x4*>(out + orow * g.out_ld + col + 8 * c) =
         *reinterpret_cast<const i32x4*>(stage + chunk_at(m, c));
   };
@@ -238,11 +241,118 @@ struct SplitRing {
   static constexpr int Elems = WS * WSLOT + RS * RSLOT;   // uint16 elements of LDS
 };
 
+// The adapters' part of a tile (see lora_slices).
+struct NoExt {
+  static constexpr bool kOn = false;
+};
+struct LoraExt {
+  static constexpr bool kOn = true;
+  LoraArgs a;
+  const uint16_t* m;   // [G, nfeat, rank], with WT [G, rank, nfeat]
+};
+
+// The adapters' part of a tile of a shared projection is more of the same
+// contraction: for each adapter d among the tile's rows, 2 rank further
+// positions hold the first two bf16 pieces of the narrow product in that
+// adapter's rows (zeros in the others) against M_g, once per piece.  (Two
+// pieces, 16 bits, leave an error of 2^-17 of that part beside y's own 2^-8.)
+// After the projection's slices the staging ring is free: the adapters are
+// listed, then each slice of BK positions is loaded into the first slot of
+// either operand, every 16-byte chunk (8 positions, of one adapter and piece
+// since rank is a multiple of 8) from where it lies or, masked, as zeros.
+// compute(): multiplies the slice in those slots.
+template <int BM, int BN, int BK, int NW, bool WT, typename Compute>
+__device__ __forceinline__ void lora_slices(const LoraExt& x, const GemmArgs& g, const TileCoord& tc, uint16_t* wslot,
+                                            uint16_t* rslot, int* list, Compute compute) {
+  constexpr int CH = BK / 8, RPB = 64 / CH, RPW = 256 / (BK * 2) > 0 ? 256 / (BK * 2) : 1;
+  constexpr int LW = BN / RPB / NW, LX = BM / RPB / NW;
+  constexpr uint32_t kPast = 0x80000000u;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rank = x.a.rank, span = 2 * rank;
+  int* const slot_of = list + BM;   // [BM] the row's adapter's place in the list, or -1
+  int* const count = list + 2 * BM;
+  if (wave == 0) {
+    constexpr int V = BM / 64;
+    int ad[V], place[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int m = lane + 64 * i;
+      int v = m >= tc.mlo && m < tc.nvalid ? x.a.adapter[tc.row0 + m] : -1;
+      if (v < 0 || v >= x.a.G) v = -1;
+      ad[i] = v;
+      place[i] = -1;
+    }
+    int n = 0;
+    for (;;) {
+      int g0 = -1;
+#pragma unroll
+      for (int i = V - 1; i >= 0; --i) {
+        const uint64_t left = __ballot(ad[i] >= 0 && place[i] < 0);
+        if (left) g0 = __builtin_amdgcn_readlane(ad[i], __ffsll((unsigned long long)left) - 1);
+      }
+      if (g0 < 0) break;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (ad[i] == g0) place[i] = n;
+      if (lane == 0) list[n] = g0;
+      ++n;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) slot_of[lane + 64 * i] = place[i];
+    if (lane == 0) *count = n;
+  }
+  lds_barrier();
+  const int len = __builtin_amdgcn_readfirstlane(*count) * span;
+  int mine[LX];   // the list places of the rows this lane loads
+#pragma unroll
+  for (int i = 0; i < LX; ++i) mine[i] = slot_of[(wave + NW * i) * RPB + lane / CH];
+  const __amdgpu_buffer_rsrc_t mr = buffer_rsrc(x.m, (int64_t)x.a.G * g.nfeat * rank * 2);
+  const __amdgpu_buffer_rsrc_t lr = buffer_rsrc(x.a.low, x.a.R * kLoraPieces * rank * 2);
+  for (int c0 = 0; c0 < len; c0 += BK) {
+    if (WT) {
+#pragma unroll
+      for (int i = 0; i < LW; ++i) {
+        const int r = 2 * (wave + NW * i) + lane / 32;   // position c0 + r: a row of M_g
+        const int col = tc.col0 + 8 * wt_logical(r, lane % 32);
+        const int p = c0 + r, q = p / span;
+        uint32_t o = kPast;
+        if (p < len && col < g.nfeat)
+          o = (uint32_t)((((int64_t)list[q] * rank + (p - q * span) % rank) * g.nfeat + col) * 2);
+        lds_load16(mr, wslot + (wave + NW * i) * RPB * BK, o, 0);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < LW; ++i) {
+        const int n = (wave + NW * i) * RPB + lane / CH;
+        const int p = c0 + 8 * ((lane % CH) ^ ((n / RPW) & (CH - 1))), q = p / span;
+        uint32_t o = kPast;
+        if (p < len && tc.col0 + n < g.nfeat)
+          o = (uint32_t)((((int64_t)list[q] * g.nfeat + tc.col0 + n) * rank + (p - q * span) % rank) * 2);
+        lds_load16(mr, wslot + (wave + NW * i) * RPB * BK, o, 0);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < LX; ++i) {
+      const int m = (wave + NW * i) * RPB + lane / CH;
+      const int p = c0 + 8 * ((lane % CH) ^ ((m / RPW) & (CH - 1))), q = p / span;
+      const uint32_t o =
+          p < len && mine[i] == q ? (uint32_t)(((tc.row0 + m) * kLoraPieces * rank + (p - q * span)) * 2) : kPast;
+      lds_load16(lr, rslot + (wave + NW * i) * RPB * BK, o, 0);
+    }
+    wait_vm<0>();
+    lds_barrier();
+    compute();
+    lds_barrier();
+  }
+}
+
 // One tile: BN weight rows from tc.col0 times the route rows [mlo, nvalid)
 // of the BM from tc.row0, through the epilogue.  smem: SplitRing::Elems
 // elements; the caller meets a barrier before it reuses them.
-template <int EPI, int BM, int BN, int BK, int WN, int WM, bool WT = false, bool ROUTES = true>
-__device__ __forceinline__ void split_tile(const GemmArgs& g, const TileCoord& tc, uint16_t* smem) {
+template <int EPI, int BM, int BN, int BK, int WN, int WM, bool WT = false, bool ROUTES = true, typename Ext = NoExt>
+__device__ __forceinline__ void split_tile(const GemmArgs& g, const TileCoord& tc, uint16_t* smem,
+                                           const Ext& ext = Ext()) {
   constexpr int NW = WN * WM;
   constexpr int CH = BK / 8;
   constexpr int RPB = 64 / CH;
@@ -391,13 +501,25 @@ __device__ __forceinline__ void split_tile(const GemmArgs& g, const TileCoord& t
   // a wave whose route rows all lie outside the tile's valid rows holds only
   // padding: it loads and meets the barriers but computes nothing (its
   // accumulators stay 0, what zero-filled padding rows would give)
-  if (wm * (BM / WM) < tc.nvalid && (wm + 1) * (BM / WM) > tc.mlo) run(std::true_type());
+  const bool live = wm * (BM / WM) < tc.nvalid && (wm + 1) * (BM / WM) > tc.mlo;
+  if (live) run(std::true_type());
   else run(std::false_type());
 
   wait_vm<0>();
   lds_barrier();
+  if constexpr (Ext::kOn) {
+    static_assert(BM * 2 + 1 <= WSLOT / 2, "the adapter list fits a slot");
+    lora_slices<BM, BN, BK, NW, WT>(ext, g, tc, wbase, rbase, reinterpret_cast<int*>(wbase + WSLOT), [&]() {
+      if (!live) return;
+#pragma unroll
+      for (int s = 0; s < NSTEP; ++s) {
+        fload(s & 1, 0, s);
+        mma(s & 1);
+      }
+    });
+  }
   static_assert(BM * (EPI == kEpiGateUp ? BN / 2 : BN) <= Ring::Elems, "epilogue tile fits the LDS");
-  tile_epilogue<EPI, BM, BN, WN, WM, 64 * WN * WM, TW, TX, ROUTES>(g, tc, acc, wn, wm, lane, smem);
+  tile_epilogue<EPI, BM, BN, WN, WM, 64 * WN * WM, TW, TX, ROUTES, Ext::kOn>(g, tc, acc, wn, wm, lane, smem);
 }
 
 template <int EPI, int BM, int BN, int BK, int WN, int WM, int OCC, int ORDER>
@@ -493,6 +615,29 @@ __global__ void __launch_bounds__(64 * WN * WM, OCC) gemm_tile_rows_kernel(GemmA
   }
 }
 
+// A shared projection with per-row adapters: one group of all R rows, the
+// same block order, the adapters' slices after the projection's.
+template <int BM, int BN, int BK, int WN, int WM, int OCC, bool WT>
+__global__ void __launch_bounds__(64 * WN * WM, OCC) gemm_tile_lora_kernel(GemmArgs g, LoraExt x, int64_t nrt,
+                                                                          int64_t nct) {
+  __shared__ __attribute__((aligned(1024))) uint16_t smem[SplitRing<BM, BN, BK>::Elems];
+  const int64_t b = blockIdx.x;
+  const int64_t k = b / NXCD;
+  const int64_t chunk = (k / kXcdChunk) * NXCD + b % NXCD;
+  const int t = (int)(k % kXcdChunk);
+  const int64_t ncb = (nct + kColBlock - 1) / kColBlock;
+  const int64_t rt = (chunk / ncb) * kRowBlock + t / kColBlock;
+  const int64_t ct = (chunk % ncb) * kColBlock + t % kColBlock;
+  if (rt >= nrt || ct >= nct) return;
+  TileCoord tc;
+  tc.expert = 0;
+  tc.col0 = (int)ct * BN;
+  tc.row0 = rt * BM;
+  tc.mlo = 0;
+  tc.nvalid = (int)min<int64_t>(BM, x.a.R - tc.row0);
+  split_tile<kEpiDown, BM, BN, BK, WN, WM, WT, false, LoraExt>(g, tc, smem, x);
+}
+
 // 256 rows x 256 weight rows per tile (W1: 128 features of gate and up)
 constexpr int kRowsBM = 256, kRowsBN = 256;
 
@@ -544,6 +689,38 @@ hipError_t launch_tile_rows_bf16(const GemmArgs& g, const int32_t* offsets, int6
   if (g.epi != kEpiDown) return hipErrorInvalidValue;
   const RowGroups grp{offsets, g.E, R};
   return wt ? launch_rows<kEpiDown, true>(g, grp, s) : launch_rows<kEpiDown, false>(g, grp, s);
+}
+
+hipError_t launch_tile_lora_bf16(const LoraArgs& a, const uint16_t* v, const uint16_t* w, const uint16_t* m,
+                                 uint16_t* out, int kdim, int nfeat, bool wt, hipStream_t s) {
+  using namespace tile;
+  if (kdim % 64 || nfeat % 8) return hipErrorInvalidValue;
+  if (a.R == 0) return hipSuccess;
+  GemmArgs g = {};
+  g.epi = kEpiDown;
+  g.rows.layout = 2;
+  g.act = v;
+  g.act_ld = kdim;
+  g.act_bytes = a.R * kdim * 2;
+  g.w = w;
+  g.w_expert_stride = (int64_t)kdim * nfeat;
+  g.kdim = kdim;
+  g.nfeat = nfeat;
+  g.E = 1;
+  g.out = out;
+  g.out_ld = nfeat;
+  constexpr int BM = kRowsBM, BN = kRowsBN;
+  const int64_t nrt = (a.R + BM - 1) / BM, nct = (nfeat + BN - 1) / BN;
+  const int64_t nchunk = (nrt + kRowBlock - 1) / kRowBlock * ((nct + kColBlock - 1) / kColBlock);
+  const int64_t grid = (nchunk + NXCD - 1) / NXCD * NXCD * kXcdChunk;
+  const LoraExt x{a, m};
+  if (wt)
+    hipLaunchKernelGGL((gemm_tile_lora_kernel<BM, BN, 64, 4, 4, 4, true>), dim3((unsigned)grid), dim3(1024), 0, s, g, x,
+                       nrt, nct);
+  else
+    hipLaunchKernelGGL((gemm_tile_lora_kernel<BM, BN, 64, 4, 4, 4, false>), dim3((unsigned)grid), dim3(1024), 0, s, g,
+                       x, nrt, nct);
+  return hipGetLastError();
 }
 
 hipError_t launch_gemm_tile_bf16(const GemmArgs& g, hipStream_t s) {

@@ -266,6 +266,46 @@ int32_t layer_splits(int64_t K);
 int32_t layer_router_splits(int64_t K);
 hipError_t launch_layer(LayerArgs g, bool mxfp8, hipStream_t s);
 
+// ----------------------------------------------------------------- lora ----
+// Low-rank adapters beside a shared projection (lora.hip).
+constexpr int kLoraPieces = 3;           // bf16 pieces of a narrow product
+constexpr int kLoraMaxRank = 128;
+constexpr int kLoraStreamRows = 64;      // rows up to which the projection streams W
+
+struct LoraArgs {
+  const float* scale;          // [G]
+  const int32_t* adapter;      // [R]; outside [0, G): none
+  uint16_t* low;               // [R][kLoraPieces][rank]
+  int64_t R;
+  int32_t G, rank;
+};
+
+struct LoraGradArgs {
+  const uint16_t* x;           // [R, K]
+  const uint16_t* dy;          // [R, N]
+  const uint16_t* low_x;       // s, as the forward left it
+  const uint16_t* low_dy;      // t, as the dgrad left it
+  const int32_t* counts;       // rows of each adapter, sorted by it
+  const int32_t* offsets;
+  const int32_t* sorted;
+  float* da;                   // [G, rank, K]
+  float* db;                   // [G, N, rank]
+  float* part;                 // [shares][G rank (K + N)]
+  int64_t R;
+  int32_t N, K, G, rank, accumulate;
+};
+
+hipError_t launch_lora_forward(const LoraArgs& a, const uint16_t* x, const uint16_t* w, const uint16_t* am,
+                               const uint16_t* b, uint16_t* y, int N, int K, hipStream_t s);
+hipError_t launch_lora_dgrad(const LoraArgs& a, const uint16_t* dy, const uint16_t* w, const uint16_t* am,
+                             const uint16_t* b, uint16_t* dx, int N, int K, hipStream_t s);
+int32_t lora_wgrad_shares(int64_t R, int64_t N, int64_t K, int64_t G);
+hipError_t launch_lora_wgrad(const LoraGradArgs& a, int32_t shares, hipStream_t s);
+// The projection on the tiles: out[r] = W v_r (wt: W^T v_r) + M_g low_r, for
+// v [R, kdim] and out [R, nfeat]; m: [G, nfeat, rank] (wt: [G, rank, nfeat]).
+hipError_t launch_tile_lora_bf16(const LoraArgs& a, const uint16_t* v, const uint16_t* w, const uint16_t* m,
+                                 uint16_t* out, int kdim, int nfeat, bool wt, hipStream_t s);
+
 // p[i * stride] = 0 for i < n (a fill kernel, capturable in a graph).
 hipError_t launch_zero_words(int32_t* p, int64_t n, int64_t stride, hipStream_t s);
 

@@ -1,0 +1,422 @@
+// Low-rank adapters of many requests at once beside a shared projection, and
+// their gradients.  Row r takes adapter g = adapter[r] (or none):
+//   s_r = scale_g A_g x_r         y_r  = W x_r + B_g s_r
+//   t_r = scale_g B_g^T dy_r      dx_r = W^T dy_r + A_g^T t_r
+//   dA_g = sum over its rows of t_r x_r^T      dB_g = sum of dy_r s_r^T
+// with x [R, K], W [N, K], A [G, rank, K], B [G, N, rank].
+//
+// The rows may come in any order of adapters.  The narrow products s and t
+// come first (shrink); the projection's kernels then treat the adapters'
+// part as more of the same contraction.  s and t are kept to float32
+// precision as three bf16 pieces, hi + mid + lo (3 x 8 significand bits): the
+// matrix units take bf16 operands, and one piece alone would put an error of
+// 2^-8 into dA and dB, which are float32, and a second rounding of the size
+// of y's own into y.
+#include "kernels.h"
+#include "tile_common.h"
+
+namespace moe {
+namespace {
+
+constexpr uint32_t kPast = 0x80000000u;   // an offset past every buffer: loads give 0
+constexpr int kPieces = kLoraPieces;
+
+__device__ __forceinline__ int row_adapter(const int32_t* adapter, int64_t r, int64_t R, int G) {
+  if (r >= R) return -1;
+  const int g = adapter[r];
+  return g >= 0 && g < G ? g : -1;
+}
+
+// The three bf16 pieces of a float32.
+__device__ __forceinline__ void split3(float v, uint32_t (&p)[3]) {
+  p[0] = f32_to_bf16_rne(v);
+  const float r1 = v - bf16_to_f32(p[0]);
+  p[1] = f32_to_bf16_rne(r1);
+  p[2] = f32_to_bf16_rne(r1 - bf16_to_f32(p[1]));
+  if (!(v - v == 0.0f)) p[1] = p[2] = 0;   // inf, NaN: the first piece says it
+}
+
+typedef short v4i16 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
+
+// MFMA operand fragment (16 outputs x 8 contraction rows a lane group) of a
+// row-major LDS block whose rows are the contraction: lane (l16, q) gets
+// column col0 + l16 of rows 8 q .. 8 q + 7, by two transposing reads whose
+// lane L of each group of 16 points at row 8 q + L / 4 (+ 4), columns
+// col0 + 4 (L % 4) .. + 3.  off(row, col): element offset, 4 columns together.
+template <typename Off>
+__device__ __forceinline__ bf16x8 col_frag(const uint16_t* base, int col0, int lane, Off off) {
+  const int q = lane >> 4, L = lane & 15;
+  const int r = 8 * q + (L >> 2), c = col0 + 4 * (L & 3);
+  const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(base + off(r, c)));
+  const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(base + off(r + 4, c)));
+  const v4i16 v8[2] = {lo, hi};
+  return __builtin_bit_cast(bf16x8, v8);
+}
+
+// ---------------------------------------------------------------- shrink --
+// low[r] = scale_g M_g v_r for 16 rows a workgroup: the rows in the MFMA
+// column operand, 16 of the rank's outputs per row tile (JT tiles), the
+// contraction split over the 8 waves, whose sums meet in LDS in wave order.
+// One pass per adapter among the 16 rows; each pass writes its own rows.
+//   T = false: M = A [rank, C], contraction contiguous, loaded as it is;
+//   T = true:  M = B^T, B [C, rank]: 32 of the contraction's rows at a time
+//              go through a part of LDS of the wave's own and are read
+//              transposed.
+// Grid (row blocks, passes in flight): with few row blocks the adapters of
+// one block go to different workgroups.
+constexpr int kShrinkWaves = 8;
+
+template <int JT, bool T>
+__global__ void __launch_bounds__(64 * kShrinkWaves) lora_shrink_kernel(LoraArgs a, const uint16_t* __restrict__ v,
+                                                                       const uint16_t* __restrict__ m, int C) {
+  // the waves' sums; with T before that a [32][rank] block per wave (and the
+  // columns a partial last row tile reads past it)
+  constexpr int kBlock = 32 * 16 * JT + 16;
+  constexpr int kRed = kShrinkWaves * JT * 64 * 16, kT = T ? kShrinkWaves * kBlock * 2 : 0;
+  __shared__ __attribute__((aligned(16))) char smem[kRed > kT ? kRed : kT];
+  const int lane = threadIdx.x & 63, q = lane >> 4, l16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t r0 = (int64_t)blockIdx.x * 16;
+  const int rank = a.rank;
+  const int mine = row_adapter(a.adapter, r0 + l16, a.R, a.G);
+  const __amdgpu_buffer_rsrc_t vr = buffer_rsrc(v + r0 * C, min<int64_t>(16, a.R - r0) * C * 2);
+  const uint32_t vo = r0 + l16 < a.R ? (uint32_t)(l16 * C * 2 + 16 * q) : kPast;
+  f32x4* red = reinterpret_cast<f32x4*>(smem);
+  uint16_t* blk = reinterpret_cast<uint16_t*>(smem) + wave * kBlock;
+
+  if (blockIdx.y == 0) {   // rows without an adapter: zeros
+    for (int i = threadIdx.x; i < 16 * kPieces * rank; i += 64 * kShrinkWaves) {
+      const int64_t r = r0 + i / (kPieces * rank);
+      if (r < a.R && row_adapter(a.adapter, r, a.R, a.G) < 0) a.low[r0 * kPieces * rank + i] = 0;
+    }
+  }
+
+  uint32_t left = (uint32_t)__ballot(mine >= 0) & 0xffffu;
+  for (int pass = 0; left; ++pass) {
+    const int g = __builtin_amdgcn_readlane(mine, __ffs(left) - 1);
+    left &= ~((uint32_t)__ballot(mine == g) & 0xffffu);
+    if (pass % gridDim.y != blockIdx.y) continue;
+    const __amdgpu_buffer_rsrc_t mr = buffer_rsrc(m + (int64_t)g * rank * C, (int64_t)rank * C * 2);
+    f32x4 acc[JT];
+#pragma unroll
+    for (int j = 0; j < JT; ++j) acc[j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    for (int c0 = 32 * wave; c0 < C; c0 += 32 * kShrinkWaves) {
+      const i32x4 x = __builtin_amdgcn_raw_buffer_load_b128(vr, vo, 2 * c0, 0);
+      if (T) {
+        // rows c0 .. c0 + 31 of B: 32 rank elements in a row
+        for (int i = lane; i < 4 * rank; i += 64)
+          *reinterpret_cast<i32x4*>(blk + 8 * i) = __builtin_amdgcn_raw_buffer_load_b128(mr, 16 * i, 2 * c0 * rank, 0);
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int j = 0; j < JT; ++j) {
+          const bf16x8 f = col_frag(blk, 16 * j, lane, [&](int r, int c) { return r * rank + c; });
+          acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, as_bf16x8(x), acc[j], 0, 0, 0);
+        }
+        __builtin_amdgcn_wave_barrier();
+      } else {
+#pragma unroll
+        for (int j = 0; j < JT; ++j) {
+          const int o = 16 * j + l16;
+          const i32x4 w = __builtin_amdgcn_raw_buffer_load_b128(
+              mr, o < rank ? (uint32_t)(o * C * 2 + 16 * q) : kPast, 2 * c0, 0);
+          acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(w), as_bf16x8(x), acc[j], 0, 0, 0);
+        }
+      }
+    }
+    __syncthreads();   // every wave is done with its block
+#pragma unroll
+    for (int j = 0; j < JT; ++j) red[(wave * JT + j) * 64 + lane] = acc[j];
+    __syncthreads();
+    // row tile j: wave j; sum[r]: output 16 j + 4 q + r, row l16
+    if (wave < JT) {
+      f32x4 sum = red[wave * 64 + lane];
+      for (int w = 1; w < kShrinkWaves; ++w) sum += red[(w * JT + wave) * 64 + lane];
+      const int o = 16 * wave + 4 * q;
+      if (mine == g && o < rank) {
+        const float sc = a.scale[g];
+        uint32_t p[4][3];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) split3(sc * sum[r], p[r]);
+        uint16_t* dst = a.low + (r0 + l16) * kPieces * rank + o;
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k)
+          *reinterpret_cast<uint2*>(dst + k * rank) =
+              make_uint2(p[0][k] | (p[1][k] << 16), p[2][k] | (p[3][k] << 16));
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// ----------------------------------------------------- few rows: streaming --
+// y of 16 output features for up to 16 CT rows: W's rows stream from memory
+// into the MFMA row operand, the contraction split over the waves; the
+// adapters' part is added to the finished sums, each row with its own B_g.
+constexpr int kStreamWaves = 16;
+
+template <int CT>
+__global__ void __launch_bounds__(64 * kStreamWaves) lora_stream_kernel(LoraArgs a, const uint16_t* __restrict__ x,
+                                                                       const uint16_t* __restrict__ w,
+                                                                       const uint16_t* __restrict__ b,
+                                                                       uint16_t* __restrict__ y, int N, int K) {
+  __shared__ f32x4 red[kStreamWaves * CT * 64];
+  const int lane = threadIdx.x & 63, q = lane >> 4, l16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n0 = 16 * blockIdx.x;
+  const int64_t r0 = (int64_t)blockIdx.y * 16 * CT;
+  const __amdgpu_buffer_rsrc_t wr = buffer_rsrc(w + (int64_t)n0 * K, 16ll * K * 2);
+  const __amdgpu_buffer_rsrc_t xr = buffer_rsrc(x + r0 * K, min<int64_t>(16 * CT, a.R - r0) * K * 2);
+  const uint32_t wo = (uint32_t)(l16 * K * 2 + 16 * q);
+  f32x4 acc[CT];
+#pragma unroll
+  for (int c = 0; c < CT; ++c) acc[c] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  for (int k0 = 64 * wave; k0 < K; k0 += 64 * kStreamWaves) {
+    i32x4 f[2], e[2][CT];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      f[j] = __builtin_amdgcn_raw_buffer_load_b128(wr, wo + 64 * j, 2 * k0, 0);
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+        e[j][c] = __builtin_amdgcn_raw_buffer_load_b128(
+            xr, r0 + 16 * c + l16 < a.R ? (uint32_t)((16 * c + l16) * K * 2 + 16 * q + 64 * j) : kPast, 2 * k0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+        acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(f[j]), as_bf16x8(e[j][c]), acc[c], 0, 0, 0);
+  }
+#pragma unroll
+  for (int c = 0; c < CT; ++c) red[(wave * CT + c) * 64 + lane] = acc[c];
+  __syncthreads();
+  if (wave >= CT) return;
+  f32x4 sum = red[wave * 64 + lane];
+  for (int k = 1; k < kStreamWaves; ++k) sum += red[(k * CT + wave) * 64 + lane];
+  const int64_t r = r0 + 16 * wave + l16;
+  if (r >= a.R) return;
+  const int g = row_adapter(a.adapter, r, a.R, a.G);
+  const int n = n0 + 4 * q;      // sum[i]: feature n + i
+  if (g >= 0) {
+    const uint16_t* low = a.low + r * kPieces * a.rank;
+    const uint16_t* bg = b + ((int64_t)g * N + n) * a.rank;
+    for (int j = 0; j < a.rank; j += 8) {
+      float s[8];
+      i32x4 p[kPieces];
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) p[k] = *reinterpret_cast<const i32x4*>(low + k * a.rank + j);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        s[i] = 0.f;
+#pragma unroll
+        for (int k = kPieces - 1; k >= 0; --k) s[i] += bf16_to_f32(((uint32_t)p[k][i / 2] >> (16 * (i & 1))) & 0xffffu);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const i32x4 bv = *reinterpret_cast<const i32x4*>(bg + i * a.rank + j);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) sum[i] += s[u] * bf16_to_f32(((uint32_t)bv[u / 2] >> (16 * (u & 1))) & 0xffffu);
+      }
+    }
+  }
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = f32_to_bf16_rne(sum[i]);
+  *reinterpret_cast<uint2*>(y + r * N + n) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+}
+
+// ----------------------------------------------------------------- wgrad --
+// One workgroup: one adapter, 256 columns of x (for dA) or of dy (for dB) and
+// a share of the adapter's rows, taken from the rows sorted by adapter.  64
+// rows at a time are staged in LDS (the columns through the transposed slot
+// layout of the tiles, the pieces of t or s beside them) and both operands
+// are read transposed, the rows being the contraction; the three pieces add
+// into the same accumulators.  With more than one share the sums go to the
+// workspace and a second launch adds them in order.
+constexpr int kWgCols = 256, kWgRows = 64, kWgWaves = 8;
+
+template <int JT>
+__global__ void __launch_bounds__(64 * kWgWaves) lora_wgrad_kernel(LoraGradArgs a) {
+  extern __shared__ __attribute__((aligned(1024))) uint16_t s_ext[];
+  uint16_t* const cols = s_ext;                         // [64][256] swizzled
+  uint16_t* const low = s_ext + kWgRows * kWgCols;      // [64][3 rank]
+  const int lane = threadIdx.x & 63, q = lane >> 4, l16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = blockIdx.y;
+  const int kt = (a.K + kWgCols - 1) / kWgCols;
+  const bool is_a = (int)blockIdx.x < kt;
+  const int c0 = (is_a ? blockIdx.x : blockIdx.x - kt) * kWgCols;
+  const int C = is_a ? a.K : a.N;
+  const uint16_t* v = is_a ? a.x : a.dy;
+  const uint16_t* lo = is_a ? a.low_dy : a.low_x;
+  const int rank = a.rank, pr = kPieces * rank;
+  const int cnt = a.counts[g];
+  const int32_t* rows = a.sorted + a.offsets[g];
+  const int i0 = (int)((int64_t)cnt * blockIdx.z / gridDim.z), i1 = (int)((int64_t)cnt * (blockIdx.z + 1) / gridDim.z);
+  const __amdgpu_buffer_rsrc_t vr = buffer_rsrc(v, a.R * C * 2);
+  const __amdgpu_buffer_rsrc_t lr = buffer_rsrc(lo, a.R * pr * 2);
+  f32x4 acc[JT][2];
+#pragma unroll
+  for (int j = 0; j < JT; ++j)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) acc[j][h] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  const int cpr = pr / 8;                               // 16-byte pieces of a row of low
+  for (int i = i0; i < i1; i += kWgRows) {
+    // columns: a load fills two rows of 512 bytes
+#pragma unroll
+    for (int b = 0; b < kWgRows / 2 / kWgWaves; ++b) {
+      const int r = 2 * (wave + kWgWaves * b) + lane / 32;
+      const int c = c0 + 8 * tile::wt_logical(r, lane % 32);
+      const uint32_t o = i + r < i1 && c < C ? (uint32_t)((int64_t)rows[i + r] * C + c) * 2u : kPast;
+      lds_load16(vr, cols + (wave + kWgWaves * b) * 512, o, 0);
+    }
+    for (int b = wave; b < kWgRows * cpr / 64; b += kWgWaves) {
+      const int e = 64 * b + lane, r = e / cpr;
+      const uint32_t o = i + r < i1 ? (uint32_t)(((int64_t)rows[i + r] * cpr + e % cpr) * 16) : kPast;
+      lds_load16(lr, low + b * 512, o, 0);
+    }
+    wait_vm<0>();
+    lds_barrier();
+#pragma unroll
+    for (int s = 0; s < kWgRows / 32; ++s) {
+      bf16x8 f[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        f[h] = col_frag(cols, 32 * wave + 16 * h, lane,
+                        [&](int r, int c) { return tile::wt_off(32 * s + r, c); });
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p)
+#pragma unroll
+        for (int j = 0; j < JT; ++j) {
+          const bf16x8 t = col_frag(low, p * rank + 16 * j, lane, [&](int r, int c) { return (32 * s + r) * pr + c; });
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            acc[j][h] = is_a ? __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[h], t, acc[j][h], 0, 0, 0)
+                             : __builtin_amdgcn_mfma_f32_16x16x32_bf16(t, f[h], acc[j][h], 0, 0, 0);
+        }
+    }
+    lds_barrier();
+  }
+  // dA [G, rank, K]: lane: output 16 j + l16, columns 4 q ..; dB [G, N, rank]:
+  // lane: column l16, outputs 16 j + 4 q ..
+  const int64_t na = (int64_t)a.G * rank * a.K, nb = (int64_t)a.G * rank * a.N;
+  float* out = gridDim.z > 1 ? a.part + blockIdx.z * (na + nb) + (is_a ? 0 : na) : is_a ? a.da : a.db;
+  const bool add = gridDim.z == 1 && a.accumulate;
+#pragma unroll
+  for (int j = 0; j < JT; ++j)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int col = c0 + 32 * wave + 16 * h + (is_a ? 4 * q : l16);
+      const int o = 16 * j + (is_a ? l16 : 4 * q);
+      if (col >= C || o >= rank) continue;
+      f32x4* dst = reinterpret_cast<f32x4*>(out + (is_a ? ((int64_t)g * rank + o) * a.K + col
+                                                        : ((int64_t)g * a.N + col) * rank + o));
+      f32x4 r = acc[j][h];
+      if (add) {
+        const f32x4 old = *dst;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) r[u] = old[u] + r[u];
+      }
+      *dst = r;
+    }
+}
+
+// dA and dB from the shares' sums, four values a thread.
+__global__ void __launch_bounds__(256) lora_wgrad_join_kernel(LoraGradArgs a, int shares) {
+  const int64_t na = (int64_t)a.G * a.rank * a.K, n = na + (int64_t)a.G * a.rank * a.N;
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  f32x4 s = *reinterpret_cast<const f32x4*>(a.part + i);
+  for (int k = 1; k < shares; ++k) s += *reinterpret_cast<const f32x4*>(a.part + k * n + i);
+  f32x4* dst = reinterpret_cast<f32x4*>(i < na ? a.da + i : a.db + (i - na));
+  if (a.accumulate) {
+    const f32x4 old = *dst;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) s[u] = old[u] + s[u];
+  }
+  *dst = s;
+}
+
+template <int JT>
+hipError_t launch_shrink(const LoraArgs& a, const uint16_t* v, const uint16_t* m, int C, bool t, dim3 grid,
+                         hipStream_t s) {
+  if (t)
+    hipLaunchKernelGGL((lora_shrink_kernel<JT, true>), grid, dim3(64 * kShrinkWaves), 0, s, a, v, m, C);
+  else
+    hipLaunchKernelGGL((lora_shrink_kernel<JT, false>), grid, dim3(64 * kShrinkWaves), 0, s, a, v, m, C);
+  return hipGetLastError();
+}
+
+// low[r] = scale_g (T ? B_g^T : A_g) v_r, contraction C.
+hipError_t shrink(const LoraArgs& a, const uint16_t* v, const uint16_t* m, int C, bool t, hipStream_t s) {
+  const int64_t blocks = (a.R + 15) / 16;
+  int64_t passes = 1024 / blocks;
+  passes = passes < 1 ? 1 : passes > 16 ? 16 : passes;
+  const dim3 grid((unsigned)blocks, (unsigned)passes);
+  if (a.rank <= 16) return launch_shrink<1>(a, v, m, C, t, grid, s);
+  if (a.rank <= 32) return launch_shrink<2>(a, v, m, C, t, grid, s);
+  if (a.rank <= 64) return launch_shrink<4>(a, v, m, C, t, grid, s);
+  return launch_shrink<8>(a, v, m, C, t, grid, s);
+}
+
+template <int JT>
+hipError_t launch_wgrad(const LoraGradArgs& a, dim3 grid, size_t lds, hipStream_t s) {
+  if (lds > 64 * 1024) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&lora_wgrad_kernel<JT>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((lora_wgrad_kernel<JT>), grid, dim3(64 * kWgWaves), lds, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_lora_forward(const LoraArgs& a, const uint16_t* x, const uint16_t* w, const uint16_t* am,
+                               const uint16_t* b, uint16_t* y, int N, int K, hipStream_t s) {
+  if (a.R == 0) return hipSuccess;
+  hipError_t e = shrink(a, x, am, K, false, s);
+  if (e != hipSuccess) return e;
+  if (a.R <= kLoraStreamRows) {
+    const int ct = a.R <= 16 ? 1 : a.R <= 32 ? 2 : 4;
+    const dim3 grid(N / 16, (unsigned)((a.R + 16 * ct - 1) / (16 * ct))), block(64 * kStreamWaves);
+    if (ct == 1) hipLaunchKernelGGL((lora_stream_kernel<1>), grid, block, 0, s, a, x, w, b, y, N, K);
+    else if (ct == 2) hipLaunchKernelGGL((lora_stream_kernel<2>), grid, block, 0, s, a, x, w, b, y, N, K);
+    else hipLaunchKernelGGL((lora_stream_kernel<4>), grid, block, 0, s, a, x, w, b, y, N, K);
+    return hipGetLastError();
+  }
+  return launch_tile_lora_bf16(a, x, w, b, y, K, N, false, s);
+}
+
+hipError_t launch_lora_dgrad(const LoraArgs& a, const uint16_t* dy, const uint16_t* w, const uint16_t* am,
+                             const uint16_t* b, uint16_t* dx, int N, int K, hipStream_t s) {
+  if (a.R == 0) return hipSuccess;
+  hipError_t e = shrink(a, dy, b, N, true, s);
+  if (e != hipSuccess) return e;
+  return launch_tile_lora_bf16(a, dy, w, am, dx, N, K, true, s);
+}
+
+int32_t lora_wgrad_shares(int64_t R, int64_t N, int64_t K, int64_t G) {
+  const int64_t wgs = G * ((K + kWgCols - 1) / kWgCols + (N + kWgCols - 1) / kWgCols);
+  int64_t n = (512 + wgs - 1) / wgs;                  // two workgroups per CU
+  const int64_t most = (R + 4 * kWgRows - 1) / (4 * kWgRows);
+  if (n > most) n = most;
+  return (int32_t)(n < 1 ? 1 : n > 16 ? 16 : n);
+}
+
+hipError_t launch_lora_wgrad(const LoraGradArgs& a, int32_t shares, hipStream_t s) {
+  const dim3 grid((unsigned)((a.K + kWgCols - 1) / kWgCols + (a.N + kWgCols - 1) / kWgCols), (unsigned)a.G,
+                  (unsigned)shares);
+  // the transposed reads of a partial last tile of outputs run past a row
+  const size_t lds = 2 * (kWgRows * kWgCols + kWgRows * kPieces * a.rank + 16);
+  hipError_t e = a.rank <= 16   ? launch_wgrad<1>(a, grid, lds, s)
+                 : a.rank <= 32 ? launch_wgrad<2>(a, grid, lds, s)
+                 : a.rank <= 64 ? launch_wgrad<4>(a, grid, lds, s)
+                                : launch_wgrad<8>(a, grid, lds, s);
+  if (e != hipSuccess || shares == 1) return e;
+  const int64_t n = (int64_t)a.G * a.rank * (a.K + a.N) / 4;
+  hipLaunchKernelGGL(lora_wgrad_join_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a, shares);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -864,4 +864,118 @@ int moe_layer_apply(const moe_layer_plan* plan, const void* x, const void* route
   return launch_layer(g, mx, (hipStream_t)stream) == hipSuccess ? MOE_OK : MOE_EHIP;
 }
 
+// ----------------------------------------------------------------- lora ----
+
+static int lora_ok(const moe_lora_problem* p) {
+  if (!p || p->R < 0 || p->R >= (1ll << 31) || p->N <= 0 || p->K <= 0 || p->G <= 0 || p->rank <= 0) return MOE_EINVAL;
+  if (p->N % 64 || p->K % 64 || p->rank % 8 || p->rank > kLoraMaxRank || p->G > 4096) return MOE_EUNSUPPORTED;
+  const int64_t wide = p->N > p->K ? p->N : p->K, lim = 1ll << 30;   // elements of 2 bytes
+  if (wide >= lim || p->N >= lim / p->K + (lim % p->K != 0) || wide * p->R >= lim || p->G * p->rank >= lim / wide + 1 ||
+      p->G * p->rank * wide >= lim || kLoraPieces * p->R * p->rank >= lim)
+    return MOE_EUNSUPPORTED;
+  return MOE_OK;
+}
+
+static LoraArgs lora_args(const moe_lora_problem* p, const float* scale, const int32_t* adapter, void* low) {
+  LoraArgs a{};
+  a.scale = scale;
+  a.adapter = adapter;
+  a.low = static_cast<uint16_t*>(low);
+  a.R = p->R;
+  a.G = (int32_t)p->G;
+  a.rank = (int32_t)p->rank;
+  return a;
+}
+
+int64_t moe_lora_low_bytes(const moe_lora_problem* p) {
+  return lora_ok(p) == MOE_OK ? 2 * kLoraPieces * p->R * p->rank : -1;
+}
+
+static AlignLayout lora_layout(const moe_lora_problem* p) {
+  return layout_align(0, p->G, p->R, p->R, p->G < p->R ? p->G : p->R, align_nblocks(p->R));
+}
+
+int64_t moe_lora_ws_bytes(const moe_lora_problem* p) {
+  if (lora_ok(p) != MOE_OK) return -1;
+  const int64_t shares = lora_wgrad_shares(p->R, p->N, p->K, p->G);
+  return lora_layout(p).end + (shares > 1 ? 4 * shares * p->G * p->rank * (p->N + p->K) : 0);
+}
+
+static int lora_project(const moe_lora_problem* p, bool dgrad, const void* in, const void* w, const void* a,
+                        const void* b, const float* scale, const int32_t* adapter, void* out, void* low,
+                        void* stream) {
+  const int st = lora_ok(p);
+  if (st != MOE_OK) return st;
+  if (!aligned16(w) || !aligned16(a) || !aligned16(b) || !aligned4(scale)) return MOE_EINVAL;
+  if (p->R > 0 && (!aligned16(in) || !aligned4(adapter) || !aligned16(out) || !aligned16(low))) return MOE_EINVAL;
+  const LoraArgs l = lora_args(p, scale, adapter, low);
+  auto u16 = [](const void* q) { return static_cast<const uint16_t*>(q); };
+  const hipError_t e =
+      dgrad ? launch_lora_dgrad(l, u16(in), u16(w), u16(a), u16(b), static_cast<uint16_t*>(out), (int)p->N, (int)p->K,
+                                (hipStream_t)stream)
+            : launch_lora_forward(l, u16(in), u16(w), u16(a), u16(b), static_cast<uint16_t*>(out), (int)p->N,
+                                  (int)p->K, (hipStream_t)stream);
+  return e == hipSuccess ? MOE_OK : MOE_EHIP;
+}
+
+int moe_lora_forward(const moe_lora_problem* p, const void* x, const void* w, const void* a, const void* b,
+                     const float* scale, const int32_t* adapter, void* y, void* low, void* stream) {
+  return lora_project(p, false, x, w, a, b, scale, adapter, y, low, stream);
+}
+
+int moe_lora_dgrad(const moe_lora_problem* p, const void* dy, const void* w, const void* a, const void* b,
+                   const float* scale, const int32_t* adapter, void* dx, void* low, void* stream) {
+  return lora_project(p, true, dy, w, a, b, scale, adapter, dx, low, stream);
+}
+
+int moe_lora_wgrad(const moe_lora_problem* p, const void* x, const void* dy, const void* low_x, const void* low_dy,
+                   const int32_t* adapter, float* da, float* db, int accumulate, void* ws, void* stream) {
+  const int st = lora_ok(p);
+  if (st != MOE_OK) return st;
+  if (!aligned16(da) || !aligned16(db) || !aligned16(ws) || (accumulate != 0 && accumulate != 1)) return MOE_EINVAL;
+  if (p->R > 0 &&
+      (!aligned16(x) || !aligned16(dy) || !aligned16(low_x) || !aligned16(low_dy) || !aligned4(adapter)))
+    return MOE_EINVAL;
+  // the rows of each adapter, in row order
+  const AlignLayout L = lora_layout(p);
+  AlignArgs al{};
+  al.keys = adapter;
+  al.R = p->R;
+  al.nb = (int32_t)p->G;
+  al.B = 1;
+  al.counts = at<int32_t>(ws, L.counts);
+  al.offsets = at<int32_t>(ws, L.offsets);
+  al.sorted = at<int32_t>(ws, L.sorted);
+  al.block_bucket = at<int32_t>(ws, L.block_bucket);
+  al.num_post = at<int32_t>(ws, L.num_post);
+  al.active = at<int32_t>(ws, L.active);
+  al.status = at<int32_t>(ws, L.status);
+  al.block_hist = at<int32_t>(ws, L.scratch);
+  al.capacity = p->R;
+  al.max_tiles = p->R;
+  al.max_active = p->G < p->R ? p->G : p->R;
+  al.sentinel = (int32_t)p->R;
+  al.nblocks = (int32_t)align_nblocks(p->R);
+  if (launch_align(al, (hipStream_t)stream) != hipSuccess) return MOE_EHIP;
+  LoraGradArgs g{};
+  g.x = static_cast<const uint16_t*>(x);
+  g.dy = static_cast<const uint16_t*>(dy);
+  g.low_x = static_cast<const uint16_t*>(low_x);
+  g.low_dy = static_cast<const uint16_t*>(low_dy);
+  g.counts = al.counts;
+  g.offsets = al.offsets;
+  g.sorted = al.sorted;
+  g.da = da;
+  g.db = db;
+  g.part = at<float>(ws, L.end);
+  g.R = p->R;
+  g.N = (int32_t)p->N;
+  g.K = (int32_t)p->K;
+  g.G = (int32_t)p->G;
+  g.rank = (int32_t)p->rank;
+  g.accumulate = accumulate;
+  return launch_lora_wgrad(g, lora_wgrad_shares(p->R, p->N, p->K, p->G), (hipStream_t)stream) == hipSuccess ? MOE_OK
+                                                                                                            : MOE_EHIP;
+}
+
 }  // extern "C"
