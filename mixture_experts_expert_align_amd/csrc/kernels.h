@@ -226,7 +226,8 @@ constexpr int kLayerMaxRoutes = kLayerMaxM * kLayerMaxTopk;
 // the sync area, int32 words, one 128-byte line per counter that many
 // workgroups touch at once; then one word per strip of the second launch
 enum { kLayerClaim = 0, kLayerArrived = kSyncLine, kLayerRouted = 2 * kSyncLine, kLayerNumSlots = 2 * kSyncLine + 1,
-       kLayerDone = 3 * kSyncLine, kLayerStrips = 4 * kSyncLine };
+       kLayerNumRows = 2 * kSyncLine + 2,
+       kLayerDone = 3 * kSyncLine, kLayerItems = 4 * kSyncLine, kLayerStrips = 5 * kSyncLine };
 
 struct alignas(16) LayerSlot {
   int32_t e, cnt, pos0, pad;   // expert, its tokens, their first row of z
@@ -259,7 +260,7 @@ struct LayerArgs {
   int32_t logit_ld, max_slots, cap;
   // set by the launcher
   int32_t rsplit, runits;      // K splits and units of the router
-  int32_t splits, ks;          // workgroups per strip of W2; waves per operand of a W1 strip
+  int32_t splits, ks;          // workgroups per strip of W2; waves of a W1 strip
 };
 
 int32_t layer_splits(int64_t K);

@@ -40,7 +40,7 @@ constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kSpinLimit = 1 << 20;   // polls, each a round trip to memory
 constexpr uint32_t kPast = 0x80000000u;   // an offset past every buffer: loads give 0
-constexpr int kUnitSteps = kWaves;    // 128-wide steps per router unit, one per wave
+constexpr int kUnitSteps = kWaves;    // 128-wide blocks of K per router unit, one per wave
 
 __device__ __forceinline__ int load_relaxed(const int32_t* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -69,47 +69,84 @@ __device__ __forceinline__ int phase_thread() {
 }
 
 // ------------------------------------------------------------ the stream --
-// One 128-wide step of 16 weight rows.  bf16: piece j of lane (row l16,
-// group q) holds k = 32 j + 8 q .. +7.  MXFP8: piece p holds the codes of
-// k = 64 p + 16 q .. +15, half h of it feeds MFMA 2 p + h; the lane's block
-// scale is byte 2 p + q / 2 of the row's 4 scale bytes of the step.
-template <bool MX>
-struct WStep {
-  i32x4 w[MX ? 2 : 4];
-  uint32_t s;
+// The weight rows are read in pieces of 16 bytes a lane: 32 of the contraction
+// for bf16 (lane group q holds k = 8 q .. +7), 64 for MXFP8 (k = 16 q .. +15,
+// all of one 32-wide block), P pieces a step, D steps in flight; the
+// activations of CT column tiles come along in the same order of k (CT = 0:
+// they are in LDS).  NT: row tiles that share the activations (gate and up).
+// Steps past the end are loaded from past the buffers, as zeros: every load in
+// the loop is unconditional, so the waits count exactly the loads they need.
+//
+// MXFP8 scales: a 128-wide block has 4 scale bytes a row.  One load gives
+// each row's words of 4 blocks, one to each lane group, and each step takes
+// its own from the lane that holds it.  A load of its word by every step
+// (16 separate lines a load) cost 15% of the first launch and 17% of the
+// second at K = 6144, I = 2048 and 33 experts.  (The half-block steps of the
+// slots with more than 16 tokens keep that form: they are bound elsewhere, and
+// the group's registers would spill.)
+template <bool MX, int NT, int CT, int P>
+struct Step {
+  i32x4 w[NT][P];
+  i32x4 a[CT ? CT : 1][P][MX ? 2 : 1];
 };
 
 template <bool MX>
-__device__ __forceinline__ void load_w(WStep<MX>& f, __amdgpu_buffer_rsrc_t wr, __amdgpu_buffer_rsrc_t sr,
-                                       uint32_t wo, uint32_t so, int step) {
-  if (MX) {
-#pragma unroll
-    for (int p = 0; p < 2; ++p) f.w[p] = __builtin_amdgcn_raw_buffer_load_b128(wr, wo + 64 * p, 128 * step, 0);
-    f.s = __builtin_amdgcn_raw_buffer_load_b32(sr, so, 4 * step, 0);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) f.w[j] = __builtin_amdgcn_raw_buffer_load_b128(wr, wo + 64 * j, 256 * step, 0);
-  }
+struct Weights {
+  __amdgpu_buffer_rsrc_t w, s;
+};
+
+// One expert's matrix of `elems` elements.
+template <bool MX>
+__device__ __forceinline__ Weights<MX> expert_weights(const void* w, const uint8_t* ws, int64_t e, int64_t elems) {
+  const int64_t bytes = elems * (MX ? 1 : 2);
+  Weights<MX> r;
+  r.w = buffer_rsrc(static_cast<const uint8_t*>(w) + e * bytes, bytes);
+  r.s = MX ? buffer_rsrc(ws + e * (elems / 32), elems / 32) : r.w;
+  return r;
+}
+// A lane's first byte of a row, of the row's scales and of a row of activations.
+template <bool MX>
+__device__ __forceinline__ uint32_t lane_w(int64_t row, int64_t ld, int q) {
+  return (uint32_t)(row * ld * (MX ? 1 : 2) + 16 * q);
+}
+__device__ __forceinline__ uint32_t lane_s(int64_t row, int64_t ld) { return (uint32_t)(row * (ld / 32)); }
+template <bool MX>
+__device__ __forceinline__ uint32_t lane_a(int64_t row, int64_t ld, int q) {
+  return (uint32_t)(row * ld * 2 + (MX ? 32 : 16) * q);
 }
 
-// The step's activations of one column tile, in the weights' order of k.
-template <bool MX>
-__device__ __forceinline__ void load_a(i32x4 (&a)[4], __amdgpu_buffer_rsrc_t ar, uint32_t ao, int step) {
+// Step `step` of the rows, or zeros when !in.
+template <bool MX, int NT, int CT, int P>
+__device__ __forceinline__ void load_step(Step<MX, NT, CT, P>& f, const Weights<MX>& wr, __amdgpu_buffer_rsrc_t ar,
+                                          const uint32_t (&wo)[NT], const uint32_t (&ao)[CT ? CT : 1], int step,
+                                          bool in) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    a[j] = __builtin_amdgcn_raw_buffer_load_b128(ar, ao + (MX ? 128 * (j >> 1) + 16 * (j & 1) : 64 * j), 256 * step, 0);
+  for (int t = 0; t < NT; ++t) {
+    const uint32_t o = in ? wo[t] : kPast;
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+      f.w[t][p] = __builtin_amdgcn_raw_buffer_load_b128(wr.w, o + 64 * p, 64 * P * step, 0);
+  }
+#pragma unroll
+  for (int c = 0; c < CT; ++c) {
+    const uint32_t o = in ? ao[c] : kPast;
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int h = 0; h < (MX ? 2 : 1); ++h)
+        f.a[c][p][h] =
+            __builtin_amdgcn_raw_buffer_load_b128(ar, o + (MX ? 128 : 64) * p + 16 * h, (MX ? 128 : 64) * P * step, 0);
+  }
+  issue_order();   // steps land in the order they are waited for
 }
-// a lane's first k of a step, in bytes of bf16
-template <bool MX>
-__device__ __forceinline__ int lane_k(int q) { return MX ? 32 * q : 16 * q; }
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
-template <bool MX>
-__device__ __forceinline__ bf16x8 widen(const WStep<MX>& f, int j, int q) {
-  if (!MX) return as_bf16x8(f.w[j]);
-  const float sc = __uint_as_float(((f.s >> (8 * (2 * (j >> 1) + (q >> 1)))) & 0xffu) << 23);
-  const uint32_t lo = (uint32_t)f.w[j >> 1][2 * (j & 1)], hi = (uint32_t)f.w[j >> 1][2 * (j & 1) + 1];
+// Half h of a piece in bf16: the codes times their block's scale, the lowest
+// byte of s.
+__device__ __forceinline__ bf16x8 widen(const i32x4& w, uint32_t s, int h) {
+  const float sc = __uint_as_float((s & 0xffu) << 23);
+  const uint32_t lo = (uint32_t)w[2 * h], hi = (uint32_t)w[2 * h + 1];
   const bf16x2 v[4] = {__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, sc, false),
                        __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, sc, true),
                        __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, sc, false),
@@ -117,13 +154,123 @@ __device__ __forceinline__ bf16x8 widen(const WStep<MX>& f, int j, int q) {
   return __builtin_bit_cast(bf16x8, v);
 }
 
-// Buffers of one expert's weight matrix of `elems` elements.
-template <bool MX>
-__device__ __forceinline__ void expert_rsrc(const void* w, const uint8_t* ws, int64_t e, int64_t elems,
-                                            __amdgpu_buffer_rsrc_t& wr, __amdgpu_buffer_rsrc_t& sr) {
-  const int64_t bytes = elems * (MX ? 1 : 2);
-  wr = buffer_rsrc(static_cast<const uint8_t*>(w) + e * bytes, bytes);
-  sr = MX ? buffer_rsrc(ws + e * (elems / 32), elems / 32) : wr;
+// acc += the nb 128-wide blocks b0, b0 + stride, ... of the rows.  act(i, j):
+// with CT = 0, the activations of MFMA j (of 4) of the i-th block.
+template <bool MX, int NT, int CT, int P, int D, typename Act>
+__device__ __forceinline__ void stream_rows(const Weights<MX>& wr, __amdgpu_buffer_rsrc_t ar, const uint32_t (&wo)[NT],
+                                            const uint32_t (&so)[NT], const uint32_t (&ao)[CT ? CT : 1], int b0,
+                                            int stride, int nb, f32x4 (&acc)[NT][CT ? CT : 1], Act act) {
+  constexpr int kPer = 128 / (P * (MX ? 64 : 32));   // steps of a block
+  const int lane = threadIdx.x & 63, q = lane >> 4, l16 = lane & 15;
+  const int n = nb * kPer;
+  auto at = [&](int i) { return (b0 + i / kPer * stride) * kPer + i % kPer; };
+  Step<MX, NT, CT, P> st[D];
+  // multiplies step i, held in f; sw: the lane's two scale bytes of its block
+  // (0 and 2)
+  auto mma = [&](const Step<MX, NT, CT, P>& f, int i, const uint32_t (&sw)[NT]) {
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int h = 0; h < (MX ? 2 : 1); ++h) {
+        bf16x8 x;
+        if (CT == 0) x = act(min(i, n - 1) / kPer, (MX ? 2 : 1) * (i % kPer * P + p) + h);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const bf16x8 w = MX ? widen(f.w[t][p], sw[t] >> (16 * (i % kPer * P + p)), h) : as_bf16x8(f.w[t][p]);
+#pragma unroll
+          for (int c = 0; c < (CT ? CT : 1); ++c)
+            acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, CT ? as_bf16x8(f.a[c][p][h]) : x, acc[t][c], 0, 0, 0);
+        }
+      }
+    issue_order();
+  };
+  if constexpr (MX && P == 2) {
+    // groups of 4 blocks with one load of scale words each, a group ahead
+    static_assert(4 % D == 0, "a group takes whole rounds of the steps in flight");
+    uint32_t next[NT], words[NT], sw[NT];
+    auto load_words = [&](int b) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        next[t] = __builtin_amdgcn_raw_buffer_load_b32(wr.s, b + q < nb ? so[t] + 4 * (b0 + (b + q) * stride) : kPast, 0, 0);
+      issue_order();
+    };
+    load_words(0);
+#pragma unroll
+    for (int d = 0; d < D; ++d) load_step(st[d], wr, ar, wo, ao, at(d), d < n);
+    for (int it = 0; it < n; it += 4) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) words[t] = next[t];
+      load_words(it + 4);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (it + u >= n) return;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) sw[t] = (uint32_t)__shfl((int)words[t], l16 + 16 * u) >> (8 * (q >> 1));
+        mma(st[u % D], it + u, sw);
+        load_step(st[u % D], wr, ar, wo, ao, at(it + u + D), it + u + D < n);
+      }
+    }
+  } else {
+    uint32_t sw[D][NT];
+    auto load = [&](int d, int i) {
+      if (MX) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          sw[d][t] = __builtin_amdgcn_raw_buffer_load_b32(wr.s, i < n ? so[t] : kPast, 4 * (at(i) / kPer), 0);
+      }
+      load_step(st[d], wr, ar, wo, ao, at(i), i < n);
+    };
+#pragma unroll
+    for (int d = 0; d < D; ++d) load(d, d);
+    for (int it = 0; it < n; it += D)
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        uint32_t s[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) s[t] = MX ? sw[d][t] >> (8 * (q >> 1)) : 0;
+        mma(st[d], it + d, s);
+        load(d, it + d + D);
+      }
+  }
+}
+template <bool MX, int NT, int CT, int P, int D>
+__device__ __forceinline__ void stream_rows(const Weights<MX>& wr, __amdgpu_buffer_rsrc_t ar, const uint32_t (&wo)[NT],
+                                            const uint32_t (&so)[NT], const uint32_t (&ao)[CT], int b0, int stride,
+                                            int nb, f32x4 (&acc)[NT][CT]) {
+  stream_rows<MX, NT, CT, P, D>(wr, ar, wo, so, ao, b0, stride, nb, acc, [](int, int) { return bf16x8{}; });
+}
+
+// The same with the activations of up to 16 tokens in LDS (stage_rows): only
+// the weights go through the vector memory path, one load per KB of them.
+// With a few tokens in the 16 columns, activations read by every step as MFMA
+// operands cost as many load instructions as half the weights.
+template <bool MX, int NT, int P, int D>
+__device__ __forceinline__ void stream_rows_lds(const Weights<MX>& wr, const uint32_t (&wo)[NT],
+                                                const uint32_t (&so)[NT], const char* stage, int quads, int tok, int b0,
+                                                int stride, int nb, f32x4 (&acc)[NT][1]) {
+  const int q = (threadIdx.x & 63) >> 4;
+  const uint32_t none[1] = {0};
+  stream_rows<MX, NT, 0, P, D>(wr, wr.w, wo, so, none, b0, stride, nb, acc, [&](int i, int j) {
+    const int chunk = (MX ? 8 * (j >> 1) + 2 * q + (j & 1) : 4 * j + q) ^ (4 * (tok & 3));
+    return as_bf16x8(*reinterpret_cast<const i32x4*>(stage + (i * quads * 4 + tok) * 256 + 16 * chunk));
+  });
+}
+
+// Blocks b0, b0 + stride, ... (nb of them) of `quads` x 4 rows into the wave's
+// own part of LDS: block i, row r at (i quads 4 + r) 256 bytes, its 16-byte
+// chunks XOR-swizzled by r so that four rows' reads of one chunk spread over
+// the banks.  offset(r): the row's byte offset (rows past the last: any valid
+// row, their columns are not used).
+template <typename Offset>
+__device__ __forceinline__ void stage_rows(char* stage, __amdgpu_buffer_rsrc_t ar, int quads, int b0, int stride, int nb,
+                                           Offset offset) {
+  const int lane = threadIdx.x & 63;
+  for (int j = 0; j < quads; ++j) {
+    const int r = 4 * j + (lane >> 4);
+    const uint32_t o = offset(r) + 16 * ((lane & 15) ^ (4 * (r & 3)));
+    for (int i = 0; i < nb; ++i) lds_load16(ar, stage + (i * quads + j) * 1024, o, 256 * (b0 + i * stride));
+  }
+  wait_vm<0>();
 }
 
 __device__ __forceinline__ uint64_t below(int t) { return t == 0 ? 0ull : (~0ull >> (64 - t)); }
@@ -213,19 +360,13 @@ __device__ __forceinline__ void route(const LayerArgs& g, RouteLds& s, double* k
     g.rows[ct + i] = i % g.M;
     g.roww[ct + i] = 1.0f;
   }
-  if (tid == 0) g.sync[kLayerNumSlots] = nt + g.S;
+  if (tid == 0) {
+    g.sync[kLayerNumSlots] = nt + g.S;
+    g.sync[kLayerNumRows] = ct + g.S * g.M;
+  }
 }
 
 // ---------------------------------------------------------- first launch --
-constexpr int kKeyBytes = kWaves * kLayerMaxE * 8;
-
-template <int CT>
-constexpr int gate_up_lds() {
-  constexpr int red = kWaves * CT * 64 * 16;
-  constexpr int rt = (int)sizeof(RouteLds) + kKeyBytes;
-  return red > rt ? red : rt;
-}
-
 // Partial logits of 16 experts over 1024 of K (one 128-wide step per wave).
 template <int CT>
 __device__ __forceinline__ void router_unit(const LayerArgs& g, int unit, f32x4* red) {
@@ -237,19 +378,19 @@ __device__ __forceinline__ void router_unit(const LayerArgs& g, int unit, f32x4*
 #pragma unroll
   for (int c = 0; c < CT; ++c) acc[c] = (f32x4){0.f, 0.f, 0.f, 0.f};
   if (128 * step < g.K) {
-    const __amdgpu_buffer_rsrc_t wr = buffer_rsrc(g.wr, (int64_t)g.r.E * g.K * 2);
+    Weights<false> wr;
+    wr.w = wr.s = buffer_rsrc(g.wr, (int64_t)g.r.E * g.K * 2);
     const __amdgpu_buffer_rsrc_t ar = buffer_rsrc(g.x, (int64_t)g.M * g.K * 2);
-    WStep<false> w;
-    load_w<false>(w, wr, wr, e0 + l16 < g.r.E ? (uint32_t)((e0 + l16) * g.K * 2 + 16 * q) : kPast, 0, step);
+    const uint32_t wo[1] = {e0 + l16 < g.r.E ? lane_w<false>(e0 + l16, g.K, q) : kPast};
+    uint32_t ao[CT];
 #pragma unroll
-    for (int c = 0; c < CT; ++c) {
-      const int t = 16 * c + l16;
-      i32x4 a[4];
-      load_a<false>(a, ar, t < g.M ? (uint32_t)(t * g.K * 2 + 16 * q) : kPast, step);
+    for (int c = 0; c < CT; ++c) ao[c] = 16 * c + l16 < g.M ? lane_a<false>(16 * c + l16, g.K, q) : kPast;
+    f32x4 sum[1][CT];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(w.w[j]), as_bf16x8(a[j]), acc[c], 0, 0, 0);
-    }
+    for (int c = 0; c < CT; ++c) sum[0][c] = acc[c];
+    stream_rows<false, 1, CT, 4, 1>(wr, ar, wo, wo, ao, step, 1, 1, sum);
+#pragma unroll
+    for (int c = 0; c < CT; ++c) acc[c] = sum[0][c];
   }
 #pragma unroll
   for (int c = 0; c < CT; ++c) red[(wave * CT + c) * 64 + lane] = acc[c];
@@ -267,89 +408,84 @@ __device__ __forceinline__ void router_unit(const LayerArgs& g, int unit, f32x4*
   __syncthreads();
 }
 
-// z of 16 features of one slot: ks waves per operand (gate, up) split K.
-template <bool MX, int CT, int D>
-__device__ __forceinline__ void gate_up_strip(const LayerArgs& g, const LayerSlot& sl, int f0, int kw, int ut,
-                                              bool live, f32x4* red) {
+// What a workgroup keeps of the routing while it streams.
+struct SlotLds {
+  int32_t e[kLayerMaxE + kLayerMaxShared];
+  int32_t pos[kLayerMaxE + kLayerMaxShared + 1];     // first row; the next slot's is one past the last
+  uint8_t tok[kLayerMaxRoutes + kLayerMaxM * kLayerMaxShared];
+};
+constexpr int kStageBytes = 6144;   // a wave's activations in LDS: two workgroups on a CU fit its 160 KB
+
+// z of 16 features of one slot with up to 16 CT tokens: wave kw of ks takes
+// the 128-wide blocks kw, kw + ks, ... of K (the waves together read each
+// weight row in long runs: contiguous parts per wave measured 5% slower) of
+// the gate and up rows.  stage: the wave's activations in LDS, or null.
+template <bool MX, int CT, int P, int D>
+__device__ __forceinline__ void gate_up_strip(const LayerArgs& g, const SlotLds& s, int slot, int f0, int kw, bool live,
+                                              f32x4* red, const char* stage, int quads) {
   const int lane = phase_thread() & 63, q = lane >> 4, l16 = lane & 15;
-  const int ks = g.ks;
-  const int nsteps = g.K / 128;
-  const int s0 = kw * nsteps / ks, n = live ? (kw + 1) * nsteps / ks - s0 : 0;
-  __amdgpu_buffer_rsrc_t wr, sr;
-  expert_rsrc<MX>(g.w1, g.w1s, sl.e, 2ll * g.I * g.K, wr, sr);
-  const __amdgpu_buffer_rsrc_t ar = buffer_rsrc(g.x, (int64_t)g.M * g.K * 2);
-  const int row = w1_row(f0 + l16, ut != 0, g.I, g.w1_order);
-  const uint32_t wo = (uint32_t)row * (uint32_t)g.K * (MX ? 1u : 2u) + 16 * q;
-  const uint32_t so = (uint32_t)row * (uint32_t)(g.K / 32);
-  uint32_t ao[CT];
+  const int e = __builtin_amdgcn_readfirstlane(s.e[slot]);
+  const int pos0 = s.pos[slot], cnt = s.pos[slot + 1] - pos0;
+  const int n = live ? (g.K / 128 - kw + g.ks - 1) / g.ks : 0;
+  const Weights<MX> wr = expert_weights<MX>(g.w1, g.w1s, e, 2ll * g.I * g.K);
+  uint32_t wo[2], so[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int row = w1_row(f0 + l16, t != 0, g.I, g.w1_order);
+    wo[t] = lane_w<MX>(row, g.K, q);
+    so[t] = lane_s(row, g.K);
+  }
   float wt[CT];
+  f32x4 acc[2][CT];
 #pragma unroll
   for (int c = 0; c < CT; ++c) {
-    const int tk = 16 * c + l16;
-    ao[c] = kPast;
-    wt[c] = 0.f;
-    if (live && tk < sl.cnt) {
-      ao[c] = (uint32_t)(load_relaxed(g.rows + sl.pos0 + tk) * g.K * 2 + lane_k<MX>(q));
-      wt[c] = load_relaxed(g.roww + sl.pos0 + tk);
-    }
+    wt[c] = 16 * c + l16 < cnt ? load_relaxed(g.roww + pos0 + 16 * c + l16) : 0.f;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) acc[t][c] = (f32x4){0.f, 0.f, 0.f, 0.f};
   }
-  f32x4 acc[CT];
+  if constexpr (P == 0) {
+    stream_rows_lds<MX, 2, MX ? 2 : 4, D>(wr, wo, so, stage, quads, min(l16, cnt - 1), kw, g.ks, n, acc);
+  } else {
+    const __amdgpu_buffer_rsrc_t ar = buffer_rsrc(g.x, (int64_t)g.M * g.K * 2);
+    uint32_t ao[CT];
 #pragma unroll
-  for (int c = 0; c < CT; ++c) acc[c] = (f32x4){0.f, 0.f, 0.f, 0.f};
-  WStep<MX> w[D];
-  i32x4 a[D][CT][4];
-  auto load = [&](int d, int it) {
-    load_w<MX>(w[d], wr, sr, wo, so, s0 + it);
-#pragma unroll
-    for (int c = 0; c < CT; ++c) load_a<MX>(a[d][c], ar, ao[c], s0 + it);
-  };
-  auto mma = [&](int d) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const bf16x8 wf = widen<MX>(w[d], j, q);
-#pragma unroll
-      for (int c = 0; c < CT; ++c)
-        acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, as_bf16x8(a[d][c][j]), acc[c], 0, 0, 0);
-    }
-  };
-#pragma unroll
-  for (int d = 0; d < D; ++d)
-    if (d < n) load(d, d);
-  for (int it = 0; it < n; it += D) {
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-      if (it + d < n) mma(d);
-      if (it + d + D < n) load(d, it + d + D);
-    }
+    for (int c = 0; c < CT; ++c)
+      ao[c] = 16 * c + l16 < cnt ? lane_a<MX>(s.tok[pos0 + 16 * c + l16], g.K, q) : kPast;
+    stream_rows<MX, 2, CT, P, D>(wr, ar, wo, so, ao, kw, g.ks, n, acc);
   }
-#pragma unroll
-  for (int c = 0; c < CT; ++c) red[((ut * ks + kw) * CT + c) * 64 + lane] = acc[c];
-  __syncthreads();
-  // column tile c of the strip: wave c of its 2 ks waves (or all by the first)
-  const int me = ut * ks + kw;
 #pragma unroll
   for (int c = 0; c < CT; ++c) {
-    if (!live || c % (2 * ks) != me) continue;
-    f32x4 gate = red[c * 64 + lane], up = red[(ks * CT + c) * 64 + lane];
-    for (int k = 1; k < ks; ++k) {
-      gate += red[(k * CT + c) * 64 + lane];
-      up += red[((ks + k) * CT + c) * 64 + lane];
-    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) red[(kw * 2 + t) * 64 + lane] = acc[t][c];
+    __syncthreads();
     const int tk = 16 * c + l16;
-    if (tk < sl.cnt) {
+    if (live && c % g.ks == kw && tk < cnt) {   // column tile c: one of the strip's waves
+      f32x4 gate = red[lane], up = red[64 + lane];
+      for (int k = 1; k < g.ks; ++k) {
+        gate += red[2 * k * 64 + lane];
+        up += red[(2 * k + 1) * 64 + lane];
+      }
       uint32_t h[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) h[r] = f32_to_bf16_rne(wt[c] * (silu_f32(gate[r]) * up[r]));
-      *reinterpret_cast<uint2*>(g.z + (int64_t)(sl.pos0 + tk) * g.I + f0 + 4 * q) =
+      *reinterpret_cast<uint2*>(g.z + (int64_t)(pos0 + tk) * g.I + f0 + 4 * q) =
           make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
     }
+    __syncthreads();
   }
-  __syncthreads();
 }
 
-template <bool MX, int CT, int D, int NV>
-__global__ void __launch_bounds__(kThreads, CT == 4 ? 2 : 4) layer_gate_up_kernel(LayerArgs g) {
-  __shared__ __attribute__((aligned(16))) char smem[gate_up_lds<CT>()];
+// WIDE: M > 16 (a slot may hold up to 64 tokens).  At most 128 registers, so
+// two workgroups share a CU and one's joins overlap the other's streaming.
+template <bool MX, bool WIDE, int NV>
+__global__ void __launch_bounds__(kThreads, 4) layer_gate_up_kernel(LayerArgs g) {
+  constexpr int kRed = kWaves * 2 * 64 * 16 > kWaves * (WIDE ? 4 : 1) * 64 * 16 ? kWaves * 2 * 64 * 16
+                                                                                : kWaves * (WIDE ? 4 : 1) * 64 * 16;
+  constexpr int kRoute = (int)sizeof(RouteLds) + kWaves * 64 * NV * 8;
+  constexpr int kSlots = ((int)sizeof(SlotLds) + 15) / 16 * 16;
+  constexpr int kStream = kWaves * 2 * 64 * 16 + kSlots + kWaves * kStageBytes;
+  __shared__ __attribute__((aligned(16))) char smem[kRoute > kStream ? kRoute : kStream];
+  static_assert(kRed <= kStream, "a router unit's sums fit");
   __shared__ int s_claim, s_last, s_slots;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   f32x4* red = reinterpret_cast<f32x4*>(smem);
@@ -361,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, CT == 4 ? 2 : 4) layer_gate_up_kerne
     __syncthreads();
     const int unit = s_claim;
     if (unit >= g.runits) break;
-    router_unit<CT>(g, unit, red);
+    router_unit<WIDE ? 4 : 1>(g, unit, red);
     wait_memory();
     __syncthreads();
     if (threadIdx.x == 0)
@@ -397,113 +533,176 @@ __global__ void __launch_bounds__(kThreads, CT == 4 ? 2 : 4) layer_gate_up_kerne
   }
   __syncthreads();
   const int nslots = s_slots;
+  SlotLds& s = *reinterpret_cast<SlotLds*>(smem + kWaves * 2 * 64 * 16);
+  {
+    const int tid = phase_thread();
+    const int total = nslots ? load_relaxed(g.sync + kLayerNumRows) : 0;
+    for (int i = tid; i < nslots; i += kThreads) {
+      s.e[i] = load_relaxed(&g.slots[i].e);
+      s.pos[i] = load_relaxed(&g.slots[i].pos0);
+    }
+    if (tid == 0) s.pos[nslots] = total;
+    for (int i = tid; i < total; i += kThreads) {
+      s.tok[i] = (uint8_t)load_relaxed(g.rows + i);
+    }
+  }
+  __syncthreads();
 
-  const int nh = kWaves / (2 * g.ks);             // strips a workgroup takes at once
-  const int h = wave / (2 * g.ks), ut = (wave / g.ks) & 1, kw = wave % g.ks;
+  // Items (slot, nh strips of 16 features): a workgroup starts with its own and
+  // then claims one after another, the last slots first (the shared experts
+  // hold every token and take longest).  With a fixed share each, the
+  // workgroups that got the shared experts' strips ended last by half the
+  // launch; in chunks of several items the ends lay further apart.
+  const int nh = kWaves / g.ks;
+  const int h = wave / g.ks, kw = wave % g.ks;
   const int strips = g.I / 16, per = (strips + nh - 1) / nh;
-  for (int64_t item = blockIdx.x; item < (int64_t)nslots * per; item += gridDim.x) {
-    const int slot = (int)(item / per);
-    const int strip = (int)(item % per) * nh + h;
-    const int32_t* rec = reinterpret_cast<const int32_t*>(g.slots + slot);
-    LayerSlot sl;
-    sl.e = load_relaxed(rec);
-    sl.cnt = load_relaxed(rec + 1);
-    sl.pos0 = load_relaxed(rec + 2);
-    sl.e = __builtin_amdgcn_readfirstlane(sl.e);
-    sl.cnt = __builtin_amdgcn_readfirstlane(sl.cnt);
-    sl.pos0 = __builtin_amdgcn_readfirstlane(sl.pos0);
-    gate_up_strip<MX, CT, D>(g, sl, 16 * strip, kw, ut, strip < strips, red + h * 2 * g.ks * CT * 64);
+  const int items = nslots * per;
+  f32x4* mine = red + h * g.ks * 2 * 64;
+  char* stage = smem + kWaves * 2 * 64 * 16 + kSlots + wave * kStageBytes;
+  const int nb = (g.K / 128 - kw + g.ks - 1) / g.ks;
+  int staged = -1;
+  for (int claim = blockIdx.x; claim < items;) {
+    int next = 0;   // the claim's answer is used an item later
+    if (threadIdx.x == 0)
+      next = __hip_atomic_fetch_add(g.sync + kLayerItems, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const int item = items - 1 - claim;
+    const int slot = item / per;
+    const int strip = item % per * nh + h;
+    const bool live = strip < strips;
+    const int pos0 = s.pos[slot];
+    const int cnt = __builtin_amdgcn_readfirstlane(s.pos[slot + 1] - pos0);
+    const int quads = (cnt + 3) / 4;
+    // the workgroup's waves agree: the first wave has the most blocks
+    if (cnt <= 16 && (g.K / 128 + g.ks - 1) / g.ks * quads * 1024 <= kStageBytes) {
+      if (staged != slot) {
+        const __amdgpu_buffer_rsrc_t ar = buffer_rsrc(g.x, (int64_t)g.M * g.K * 2);
+        stage_rows(stage, ar, quads, kw, g.ks, nb,
+                   [&](int r) { return (uint32_t)s.tok[pos0 + min(r, cnt - 1)] * (uint32_t)g.K * 2u; });
+        staged = slot;
+      }
+      gate_up_strip<MX, 1, 0, 2>(g, s, slot, 16 * strip, kw, live, mine, stage, quads);
+    } else if (!WIDE || cnt <= 16) {
+      gate_up_strip<MX, 1, MX ? 2 : 4, 2>(g, s, slot, 16 * strip, kw, live, mine, nullptr, 0);
+    } else if (cnt <= 32) {
+      gate_up_strip<MX, 2, MX ? 1 : 2, 2>(g, s, slot, 16 * strip, kw, live, mine, nullptr, 0);
+    } else {
+      gate_up_strip<MX, 4, 1, MX ? 1 : 2>(g, s, slot, 16 * strip, kw, live, mine, nullptr, 0);
+    }
+    if (threadIdx.x == 0) s_claim = next;
+    __syncthreads();
+    claim = __builtin_amdgcn_readfirstlane((int)gridDim.x + s_claim);
+    __syncthreads();   // read before the next claim's answer overwrites it
   }
 }
 
 // --------------------------------------------------------- second launch --
-// Workgroup (strip, split): the 16 output features of the strip over its
-// share of the active slots' features, one contiguous run per wave.  The
-// waves' sums meet in LDS in wave order; with more than one split the
-// workgroup that arrives last adds the splits' sums in order.
-template <bool MX, int CT, int D>
-__global__ void __launch_bounds__(kThreads, CT == 4 ? 2 : 4) layer_down_kernel(LayerArgs g) {
-  __shared__ __attribute__((aligned(16))) f32x4 red[kWaves * CT * 64];
+// Workgroup (strip, split): the 32 output features of the strip over its
+// share of the active slots' features, one contiguous run per wave, slot by
+// slot.  Up to 16 tokens the MFMA columns are the tokens and the accumulators
+// run through all slots; beyond, the columns are the slot's own tokens (most
+// slots hold a few of the 64) and each slot's sums are added to the wave's
+// [token][32] tile in LDS.  The waves' sums meet in LDS in wave order; with
+// more than one split the workgroup that arrives last adds the splits' sums
+// in order.
+constexpr int kDownTiles = 2;
+
+template <bool MX, int CT, int P, int D>
+__device__ __forceinline__ void down_run(const LayerArgs& g, const LayerSlot& sl, const uint32_t (&wo)[kDownTiles],
+                                         const uint32_t (&so)[kDownTiles], int b0, int nb, f32x4* tile) {
+  const int lane = threadIdx.x & 63, q = lane >> 4, l16 = lane & 15;
+  const int e = __builtin_amdgcn_readfirstlane(sl.e), cnt = sl.cnt, pos0 = sl.pos0;
+  const Weights<MX> wr = expert_weights<MX>(g.w2, g.w2s, e, (int64_t)g.K * g.I);
+  const __amdgpu_buffer_rsrc_t ar = buffer_rsrc(g.z, (int64_t)g.cap * g.I * 2);
+  uint32_t ao[CT];
+#pragma unroll
+  for (int c = 0; c < CT; ++c) ao[c] = 16 * c + l16 < cnt ? lane_a<MX>(pos0 + 16 * c + l16, g.I, q) : kPast;
+  f32x4 acc[kDownTiles][CT];
+#pragma unroll
+  for (int t = 0; t < kDownTiles; ++t)
+#pragma unroll
+    for (int c = 0; c < CT; ++c) acc[t][c] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  int tok[CT];
+#pragma unroll
+  for (int c = 0; c < CT; ++c) tok[c] = 16 * c + l16 < cnt ? g.rows[pos0 + 16 * c + l16] : -1;
+  stream_rows<MX, kDownTiles, CT, P, D>(wr, ar, wo, so, ao, b0, 1, nb, acc);
+#pragma unroll
+  for (int c = 0; c < CT; ++c)
+    if (tok[c] >= 0) {
+#pragma unroll
+      for (int t = 0; t < kDownTiles; ++t) tile[(tok[c] * kDownTiles + t) * 4 + q] += acc[t][c];
+    }
+}
+
+template <bool MX, bool WIDE>
+__global__ void __launch_bounds__(kThreads, 4) layer_down_kernel(LayerArgs g) {
+  // [wave][token][4 of the 32 features]
+  constexpr int kTok = WIDE ? kLayerMaxM : 16;
+  constexpr int kQ = 4 * kDownTiles;
+  __shared__ __attribute__((aligned(16))) f32x4 red[kWaves * kTok * kQ];
   __shared__ int s_last;
   const int lane = threadIdx.x & 63, q = lane >> 4, l16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int strip = blockIdx.x / g.splits, split = blockIdx.x % g.splits;
   // a first launch that timed out published nothing: no rows to add
   const int nslots = g.sync[kLayerRouted] ? g.sync[kLayerNumSlots] : 0;
-  const int spe = g.I / 128;                             // steps per slot
+  const int spe = g.I / 128;                             // blocks per slot
   const int64_t total = (int64_t)nslots * spe;
   const int parts = g.splits * kWaves, part = split * kWaves + wave;
-  const int64_t s0 = part * total / parts;
-  const int n = (int)((part + 1) * total / parts - s0);
-
-  const __amdgpu_buffer_rsrc_t ar = buffer_rsrc(g.z, (int64_t)g.cap * g.I * 2);
-  const int row = 16 * strip + l16;
-  const uint32_t wo = (uint32_t)row * (uint32_t)g.I * (MX ? 1u : 2u) + 16 * q;
-  const uint32_t so = (uint32_t)row * (uint32_t)(g.I / 32);
-  // cursor of the next step to load
-  int slot = (int)(s0 / spe), step = (int)(s0 % spe);
-  __amdgpu_buffer_rsrc_t wr, sr;
-  uint32_t ao[CT];
-  auto enter = [&]() {
-    const LayerSlot& sl = g.slots[slot];
-    expert_rsrc<MX>(g.w2, g.w2s, sl.e, (int64_t)g.K * g.I, wr, sr);
+  int64_t b = part * total / parts;
+  const int64_t end = (part + 1) * total / parts;
+  uint32_t wo[kDownTiles], so[kDownTiles];
 #pragma unroll
-    for (int c = 0; c < CT; ++c) {
-      const int t = 16 * c + l16;
-      ao[c] = (sl.mask >> t) & 1
-                  ? (uint32_t)(sl.pos0 + __popcll(sl.mask & below(t))) * (uint32_t)g.I * 2u + lane_k<MX>(q)
-                  : kPast;
-    }
-  };
-  f32x4 acc[CT];
-#pragma unroll
-  for (int c = 0; c < CT; ++c) acc[c] = (f32x4){0.f, 0.f, 0.f, 0.f};
-  WStep<MX> w[D];
-  i32x4 a[D][CT][4];
-  auto load = [&](int d) {
-    if (step == spe) {
-      ++slot;
-      step = 0;
-      enter();
-    }
-    load_w<MX>(w[d], wr, sr, wo, so, step);
-#pragma unroll
-    for (int c = 0; c < CT; ++c) load_a<MX>(a[d][c], ar, ao[c], step);
-    ++step;
-  };
-  auto mma = [&](int d) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const bf16x8 wf = widen<MX>(w[d], j, q);
-#pragma unroll
-      for (int c = 0; c < CT; ++c)
-        acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, as_bf16x8(a[d][c][j]), acc[c], 0, 0, 0);
-    }
-  };
-  if (n > 0) enter();
-#pragma unroll
-  for (int d = 0; d < D; ++d)
-    if (d < n) load(d);
-  for (int it = 0; it < n; it += D) {
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-      if (it + d < n) mma(d);
-      if (it + d + D < n) load(d);
-    }
+  for (int t = 0; t < kDownTiles; ++t) {
+    wo[t] = lane_w<MX>(16 * (kDownTiles * strip + t) + l16, g.I, q);
+    so[t] = lane_s(16 * (kDownTiles * strip + t) + l16, g.I);
   }
+  f32x4* tile = red + wave * kTok * kQ;
+
+  if (WIDE) {
 #pragma unroll
-  for (int c = 0; c < CT; ++c) red[(wave * CT + c) * 64 + lane] = acc[c];
+    for (int i = 0; i < kTok * kQ; i += 64) tile[i + lane] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    while (b < end) {
+      const int slot = (int)(b / spe), b0 = (int)(b % spe);
+      const int n = (int)min<int64_t>(spe - b0, end - b);
+      const LayerSlot& sl = g.slots[slot];
+      const int cnt = __builtin_amdgcn_readfirstlane(sl.cnt);
+      if (cnt <= 16) down_run<MX, 1, MX ? 2 : 4, 2>(g, sl, wo, so, b0, n, tile);
+      else if (cnt <= 32) down_run<MX, 2, MX ? 1 : 2, 2>(g, sl, wo, so, b0, n, tile);
+      else down_run<MX, 4, 1, MX ? 1 : 2>(g, sl, wo, so, b0, n, tile);
+      b += n;
+    }
+  } else {
+    const __amdgpu_buffer_rsrc_t ar = buffer_rsrc(g.z, (int64_t)g.cap * g.I * 2);
+    f32x4 acc[kDownTiles][1];
+#pragma unroll
+    for (int t = 0; t < kDownTiles; ++t) acc[t][0] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    while (b < end) {
+      const int slot = (int)(b / spe), b0 = (int)(b % spe);
+      const int n = (int)min<int64_t>(spe - b0, end - b);
+      const LayerSlot& sl = g.slots[slot];
+      const Weights<MX> wr = expert_weights<MX>(g.w2, g.w2s, __builtin_amdgcn_readfirstlane(sl.e), (int64_t)g.K * g.I);
+      const uint32_t ao[1] = {
+          (sl.mask >> l16) & 1 ? lane_a<MX>(sl.pos0 + __popcll(sl.mask & below(l16)), g.I, q) : kPast};
+      stream_rows<MX, kDownTiles, 1, MX ? 2 : 4, 2>(wr, ar, wo, so, ao, b0, 1, n, acc);
+      b += n;
+    }
+#pragma unroll
+    for (int t = 0; t < kDownTiles; ++t) tile[(l16 * kDownTiles + t) * 4 + q] = acc[t][0];
+  }
   __syncthreads();
+  // thread (t, quarter) finishes 4 features of token t
+  const int t = threadIdx.x / kQ, qt = threadIdx.x % kQ;
+  const bool mine = t < g.M;
   f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-  const int t = 16 * wave + l16;           // wave c < CT finishes column tile c
-  if (wave < CT)
-    for (int k = 0; k < kWaves; ++k) sum += red[(k * CT + wave) * 64 + lane];
+  if (mine)
+    for (int k = 0; k < kWaves; ++k) sum += red[(k * kTok + t) * kQ + qt];
+  bool finish = mine;
   if (g.splits > 1) {
-    // [strip][split][token][16] partial sums
-    float* p = g.part + ((int64_t)strip * g.splits * g.M + t) * 16 + 4 * q;
-    if (wave < CT && t < g.M) {
+    // [strip][split][token][32] partial sums
+    float* p = g.part + ((int64_t)strip * g.splits * g.M + t) * (4 * kQ) + 4 * qt;
+    if (mine) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) store_relaxed(p + (int64_t)split * g.M * 16 + r, sum[r]);
+      for (int r = 0; r < 4; ++r) store_relaxed(p + (int64_t)split * g.M * 4 * kQ + r, sum[r]);
     }
     wait_memory();
     __syncthreads();
@@ -511,19 +710,20 @@ __global__ void __launch_bounds__(kThreads, CT == 4 ? 2 : 4) layer_down_kernel(L
       s_last = __hip_atomic_fetch_add(g.sync + kLayerStrips + strip, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
                g.splits - 1;
     __syncthreads();
-    if (s_last && wave < CT && t < g.M) {
+    finish = mine && s_last;
+    if (finish) {
       sum = (f32x4){0.f, 0.f, 0.f, 0.f};
       for (int k = 0; k < g.splits; ++k)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) sum[r] += load_relaxed(p + (int64_t)k * g.M * 16 + r);
+        for (int r = 0; r < 4; ++r) sum[r] += load_relaxed(p + (int64_t)k * g.M * 4 * kQ + r);
     }
     if (s_last && threadIdx.x == 0) store_relaxed(g.sync + kLayerStrips + strip, 0);
   }
-  if (wave < CT && t < g.M && (g.splits == 1 || s_last)) {
+  if (finish) {
     uint32_t h[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) h[r] = f32_to_bf16_rne(sum[r]);
-    *reinterpret_cast<uint2*>(g.out + (int64_t)t * g.K + 16 * strip + 4 * q) =
+    *reinterpret_cast<uint2*>(g.out + (int64_t)t * g.K + 4 * kQ * strip + 4 * qt) =
         make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
   }
   // the last workgroup of the launch clears the first launch's counters
@@ -531,6 +731,7 @@ __global__ void __launch_bounds__(kThreads, CT == 4 ? 2 : 4) layer_down_kernel(L
     const int done = __hip_atomic_fetch_add(g.sync + kLayerDone, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     if (done == (int)gridDim.x - 1) {
       store_relaxed(g.sync + kLayerClaim, 0);
+      store_relaxed(g.sync + kLayerItems, 0);
       store_relaxed(g.sync + kLayerArrived, 0);
       store_relaxed(g.sync + kLayerRouted, 0);
       store_relaxed(g.sync + kLayerDone, 0);
@@ -538,34 +739,30 @@ __global__ void __launch_bounds__(kThreads, CT == 4 ? 2 : 4) layer_down_kernel(L
   }
 }
 
-template <bool MX, int CT, int D>
+template <bool MX, bool WIDE>
 hipError_t launch(const LayerArgs& g, unsigned grid1, hipStream_t s) {
   if (g.r.E <= 64)
-    hipLaunchKernelGGL((layer_gate_up_kernel<MX, CT, D, 1>), dim3(grid1), dim3(kThreads), 0, s, g);
+    hipLaunchKernelGGL((layer_gate_up_kernel<MX, WIDE, 1>), dim3(grid1), dim3(kThreads), 0, s, g);
   else if (g.r.E <= 128)
-    hipLaunchKernelGGL((layer_gate_up_kernel<MX, CT, D, 2>), dim3(grid1), dim3(kThreads), 0, s, g);
+    hipLaunchKernelGGL((layer_gate_up_kernel<MX, WIDE, 2>), dim3(grid1), dim3(kThreads), 0, s, g);
   else
-    hipLaunchKernelGGL((layer_gate_up_kernel<MX, CT, D, 8>), dim3(grid1), dim3(kThreads), 0, s, g);
-  hipError_t e = hipGetLastError();
+    hipLaunchKernelGGL((layer_gate_up_kernel<MX, WIDE, 8>), dim3(grid1), dim3(kThreads), 0, s, g);
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((layer_down_kernel<MX, CT, D>), dim3((unsigned)(g.K / 16 * g.splits)), dim3(kThreads), 0, s, g);
+  hipLaunchKernelGGL((layer_down_kernel<MX, WIDE>), dim3((unsigned)(g.K / (16 * kDownTiles) * g.splits)), dim3(kThreads), 0, s, g);
   return hipGetLastError();
 }
 
 }  // namespace
 
-// Splits of the second launch: with two workgroups per CU the chip holds
-// 512; of 1 .. 8 splits the one whose last round of workgroups is fullest
-// (the fewest splits among equals).
+// Splits of the second launch: the smallest power of two, up to 8, that gives
+// the chip its two workgroups per CU.  K = 6144 (192 strips), MXFP8, 33
+// experts of 2048: 1 / 2 / 4 / 8 splits 127 / 92 / 80 / 101 us (more
+// workgroups than fit pay their start and their join again).
 int32_t layer_splits(int64_t K) {
-  int best = 1;
-  double waste = 1e9;
-  for (int s = 1; s <= 8; ++s) {
-    const int64_t wg = K / 16 * s;
-    const double w = (double)((wg + 511) / 512 * 512) / (double)wg;
-    if (w < waste - 1e-3) { waste = w; best = s; }
-  }
-  return best;
+  int32_t s = 1;
+  while (s < 8 && K / (16 * kDownTiles) * s < 512) s *= 2;
+  return s;
 }
 
 int32_t layer_router_splits(int64_t K) { return (int32_t)((K / 128 + kUnitSteps - 1) / kUnitSteps); }
@@ -574,20 +771,13 @@ hipError_t launch_layer(LayerArgs g, bool mxfp8, hipStream_t s) {
   g.rsplit = layer_router_splits(g.K);
   g.runits = (g.r.E + 15) / 16 * g.rsplit;
   g.splits = layer_splits(g.K);
-  g.ks = g.K >= 512 ? 4 : g.K >= 256 ? 2 : 1;
-  const int nh = kWaves / (2 * g.ks);
+  g.ks = g.K >= 1024 ? 8 : g.K >= 512 ? 4 : g.K >= 256 ? 2 : 1;
+  const int nh = kWaves / g.ks;
   const int64_t items = (int64_t)g.max_slots * ((g.I / 16 + nh - 1) / nh);
   int64_t grid = items > g.runits ? items : g.runits;
   if (grid > 512) grid = 512;
-  const int ct = (g.M + 15) / 16;
-  if (mxfp8) {
-    if (ct == 1) return launch<true, 1, 3>(g, (unsigned)grid, s);
-    if (ct == 2) return launch<true, 2, 2>(g, (unsigned)grid, s);
-    return launch<true, 4, 2>(g, (unsigned)grid, s);
-  }
-  if (ct == 1) return launch<false, 1, 3>(g, (unsigned)grid, s);
-  if (ct == 2) return launch<false, 2, 2>(g, (unsigned)grid, s);
-  return launch<false, 4, 2>(g, (unsigned)grid, s);
+  if (g.M > 16) return mxfp8 ? launch<true, true>(g, (unsigned)grid, s) : launch<false, true>(g, (unsigned)grid, s);
+  return mxfp8 ? launch<true, false>(g, (unsigned)grid, s) : launch<false, false>(g, (unsigned)grid, s);
 }
 
 }  // namespace moe
