@@ -222,12 +222,13 @@ constexpr int kLayerMaxM = 64;           // a token is a bit of a 64-bit mask
 constexpr int kLayerMaxE = 512;          // one expert per thread of the routing workgroup
 constexpr int kLayerMaxTopk = 32;
 constexpr int kLayerMaxShared = 16;
+constexpr int kLayerSoloUnits = 2;       // router units up to which every workgroup routes by itself
 constexpr int kLayerMaxRoutes = kLayerMaxM * kLayerMaxTopk;
 // the sync area, int32 words, one 128-byte line per counter that many
 // workgroups touch at once; then one word per strip of the second launch
 enum { kLayerClaim = 0, kLayerArrived = kSyncLine, kLayerRouted = 2 * kSyncLine, kLayerNumSlots = 2 * kSyncLine + 1,
        kLayerNumRows = 2 * kSyncLine + 2,
-       kLayerDone = 3 * kSyncLine, kLayerItems = 4 * kSyncLine, kLayerStrips = 5 * kSyncLine };
+       kLayerDone = 3 * kSyncLine, kLayerItems = 4 * kSyncLine, kLayerRanked = 5 * kSyncLine, kLayerStrips = 6 * kSyncLine };
 
 struct alignas(16) LayerSlot {
   int32_t e, cnt, pos0, pad;   // expert, its tokens, their first row of z
@@ -260,6 +261,7 @@ struct LayerArgs {
   int32_t logit_ld, max_slots, cap;
   // set by the launcher
   int32_t rsplit, runits;      // K splits and units of the router
+  int32_t solo;                // every workgroup routes by itself
   int32_t splits, ks;          // workgroups per strip of W2; waves of a W1 strip
 };
 

@@ -20,14 +20,15 @@
 // times block scale, exact in bf16), the activations stay bf16.
 //
 // Inside the first launch the router comes before everything else.  Its work
-// (16 experts x 1024 of K per unit) is claimed from a counter by whichever
-// workgroups run, so it never depends on a workgroup that has not started;
-// the workgroup that finishes the last unit adds the partial logits (in
-// order), ranks the tokens, writes the slot list and publishes it; every
-// workgroup then goes through its share of (slot, 16 features) items.  The
-// wait for the list is bounded: after about a second a workgroup gives up,
-// counts a time-out and leaves.  Data that crosses workgroups inside a launch
-// goes through device-coherent accesses (the XCDs' L2s are not coherent).
+// (units of 16 experts x 1024 of K, then of 8 tokens to rank) is claimed from
+// a counter by whichever workgroups run, so a unit only ever waits for units
+// that running workgroups hold; the workgroup that ranks last writes the slot
+// list and publishes it, and every workgroup goes on to claim (slot, 16
+// features) items.  The waits are bounded: after about a second a workgroup
+// gives up, counts a time-out and leaves.  Data that crosses workgroups inside
+// a launch goes through device-coherent accesses (the XCDs' L2s are not
+// coherent).  A small router (solo) is computed by every workgroup on its
+// own, which is faster than passing the result on.
 //
 // Every sum has a fixed order: the bits do not depend on the run.
 #include "kernels.h"
@@ -57,6 +58,18 @@ __device__ __forceinline__ void wait_memory() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_waitcnt(0x0070 | 0x0f00);
   asm volatile("" ::: "memory");
+}
+
+// Polls until *p >= target, or the limit (a time-out is counted).
+__device__ __forceinline__ bool wait_at_least(const int32_t* p, int target, int32_t* timeouts) {
+  for (int n = 0; load_relaxed(p) < target; ++n) {
+    if (n > kSpinLimit) {
+      atomicAdd(timeouts, 1);
+      return false;
+    }
+    __builtin_amdgcn_s_sleep(2);
+  }
+  return true;
 }
 
 // The thread index, opaque to the compiler: what one phase of the first launch
@@ -276,54 +289,85 @@ __device__ __forceinline__ void stage_rows(char* stage, __amdgpu_buffer_rsrc_t a
 __device__ __forceinline__ uint64_t below(int t) { return t == 0 ? 0ull : (~0ull >> (64 - t)); }
 
 // -------------------------------------------------------------- routing --
+constexpr int kSoloRows = kWaves * (kLayerMaxTopk + kLayerMaxShared);
+
+// What a workgroup keeps of the routing while it streams.
+struct SlotLds {
+  int32_t e[kLayerMaxE + kLayerMaxShared];
+  int32_t pos[kLayerMaxE + kLayerMaxShared + 1];     // first row; the next slot's is one past the last
+  float w[kSoloRows];                                 // solo only: the rows' weights
+  uint8_t tok[kLayerMaxRoutes + kLayerMaxM * kLayerMaxShared];
+};
+constexpr int kStageBytes = 6144;   // a wave's activations in LDS: two workgroups on a CU fit its 160 KB
+
 struct RouteLds {
   uint64_t mask[kLayerMaxE];            // tokens of each expert
-  int32_t slot[kLayerMaxE];             // inclusive sums, then slot and first row
-  int32_t pos[kLayerMaxE];
+  int32_t pos[kLayerMaxE];              // their first row
   int32_t id[kLayerMaxRoutes];          // the tokens' choices
   float w[kLayerMaxRoutes];
   int32_t wave_n[kWaves], wave_c[kWaves];
 };
 
-template <int NV>
-__device__ __forceinline__ void rank_tokens(const LayerArgs& g, RouteLds& s, double* keys, int lane, int wave) {
-  const int ep = g.logit_ld;
-  for (int t = wave; t < g.M; t += kWaves) {
-    double l[NV];
+// Ranks tokens t0 .. t0 + 7, one per wave.  partial(n, t, e): the n-th partial
+// logit; all of a lane's are requested before the first is added.
+template <int NV, typename Partial>
+__device__ __forceinline__ void rank_tokens(const LayerArgs& g, int t0, RouteLds& s, double* keys, bool publish,
+                                            Partial partial) {
+  const int tid = phase_thread(), lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int t = t0 + wave;
+  if (t >= g.M) return;
+  float sum[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = lane + 64 * i;
-      double v = -INFINITY;
-      if (e < g.r.E) {
-        float sum = 0.f;
-        for (int n = 0; n < g.rsplit; ++n) sum += load_relaxed(g.logits + ((int64_t)n * g.M + t) * ep + e);
-        v = sum;
-        if (g.r.bias_kind == 1) v += (double)g.rbias[e];
-      }
-      l[i] = route_logit(v);
+  for (int i = 0; i < NV; ++i) sum[i] = 0.f;
+  constexpr int kBatch = 8;
+  for (int n0 = 0; n0 < g.rsplit; n0 += kBatch) {
+    float v[NV][kBatch];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int n = 0; n < kBatch; ++n) v[i][n] = partial(min(n0 + n, g.rsplit - 1), t, min(lane + 64 * i, g.r.E - 1));
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int n = 0; n < kBatch; ++n)
+        if (n0 + n < g.rsplit) sum[i] += v[i][n];
+  }
+  double l[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int e = lane + 64 * i;
+    double v = -INFINITY;
+    if (e < g.r.E) {
+      v = sum[i];
+      if (g.r.bias_kind == 1) v += (double)g.rbias[e];
     }
-    int id;
-    float w;
-    route_token<NV>(g.r, l, g.rbias, keys + (g.r.groups > 1 ? wave * g.r.E : 0), id, w);
-    if (lane < g.r.topk) {
-      g.ids[t * g.r.topk + lane] = id;
-      g.wts[t * g.r.topk + lane] = w;
-      s.id[t * g.r.topk + lane] = id;
-      s.w[t * g.r.topk + lane] = w;
-      if (id >= 0) atomicOr((unsigned long long*)&s.mask[id], 1ull << t);
+    l[i] = route_logit(v);
+  }
+  int id;
+  float w;
+  route_token<NV>(g.r, l, g.rbias, keys + (g.r.groups > 1 ? wave * g.r.E : 0), id, w);
+  if (lane < g.r.topk) {
+    const int i = t * g.r.topk + lane;
+    s.id[i] = id;
+    s.w[i] = w;
+    if (publish) {
+      store_relaxed(g.ids + i, id);
+      store_relaxed(g.wts + i, w);
     }
   }
 }
 
-// The tokens' choices, then the slots: the experts that got a token, in
-// ascending order, each with the rows [pos0, pos0 + cnt) of z for its
-// tokens in ascending order; the shared experts last, with every token.
-template <int NV>
-__device__ __forceinline__ void route(const LayerArgs& g, RouteLds& s, double* keys) {
+// From the tokens' choices (s.id, s.w), the slots: the experts that got a
+// token, in ascending order, each with the rows [pos0, pos0 + cnt) of z for
+// its tokens in ascending order; the shared experts last, with every token.
+// To memory (publish) and, with lds, to the workgroup's own copy.
+__device__ __forceinline__ void build_slots(const LayerArgs& g, RouteLds& s, bool publish, SlotLds* lds) {
   const int tid = phase_thread(), lane = tid & 63, wave = tid >> 6;
   for (int e = tid; e < g.r.E; e += kThreads) s.mask[e] = 0;
   __syncthreads();
-  rank_tokens<NV>(g, s, keys, lane, wave);
+  for (int i = tid; i < g.M * g.r.topk; i += kThreads)
+    if (s.id[i] >= 0) atomicOr((unsigned long long*)&s.mask[s.id[i]], 1ull << (i / g.r.topk));
   __syncthreads();
   // one expert per thread (E <= kThreads): sums of (has tokens, tokens)
   const uint64_t m = tid < g.r.E ? s.mask[tid] : 0;
@@ -346,30 +390,40 @@ __device__ __forceinline__ void route(const LayerArgs& g, RouteLds& s, double* k
   n += n0;
   c += c0;
   if (tid < g.r.E) s.pos[tid] = c - cnt;
-  if (cnt > 0) g.slots[n - 1] = LayerSlot{tid, cnt, c - cnt, 0, m, 0};
-  if (tid < g.S) g.slots[nt + tid] = LayerSlot{g.r.E + tid, g.M, ct + tid * g.M, 0, below(g.M), 0};
+  auto slot = [&](int at, int e, int count, int pos0, uint64_t mask) {
+    if (publish) g.slots[at] = LayerSlot{e, count, pos0, 0, mask, 0};
+    if (lds) { lds->e[at] = e; lds->pos[at] = pos0; }
+  };
+  if (cnt > 0) slot(n - 1, tid, cnt, c - cnt, m);
+  if (tid < g.S) slot(nt + tid, g.r.E + tid, g.M, ct + tid * g.M, below(g.M));
   __syncthreads();
+  auto row = [&](int p, int t, float w) {
+    if (publish) { g.rows[p] = t; g.roww[p] = w; }
+    if (lds) { lds->tok[p] = (uint8_t)t; lds->w[p] = w; }
+  };
   for (int i = tid; i < g.M * g.r.topk; i += kThreads) {
     const int e = s.id[i], t = i / g.r.topk;
-    if (e < 0) continue;
-    const int p = s.pos[e] + __popcll(s.mask[e] & below(t));
-    g.rows[p] = t;
-    g.roww[p] = s.w[i];
+    if (e >= 0) row(s.pos[e] + __popcll(s.mask[e] & below(t)), t, s.w[i]);
   }
-  for (int i = tid; i < g.S * g.M; i += kThreads) {
-    g.rows[ct + i] = i % g.M;
-    g.roww[ct + i] = 1.0f;
-  }
+  for (int i = tid; i < g.S * g.M; i += kThreads) row(ct + i, i % g.M, 1.0f);
   if (tid == 0) {
-    g.sync[kLayerNumSlots] = nt + g.S;
-    g.sync[kLayerNumRows] = ct + g.S * g.M;
+    if (publish) {
+      g.sync[kLayerNumSlots] = nt + g.S;
+      g.sync[kLayerNumRows] = ct + g.S * g.M;
+    }
+    if (lds) {
+      lds->pos[nt + g.S] = ct + g.S * g.M;
+      s.wave_n[0] = nt + g.S;
+    }
   }
+  __syncthreads();
 }
 
 // ---------------------------------------------------------- first launch --
 // Partial logits of 16 experts over 1024 of K (one 128-wide step per wave).
-template <int CT>
-__device__ __forceinline__ void router_unit(const LayerArgs& g, int unit, f32x4* red) {
+// put(n, t, e, v): partial logits e .. e + 3 of token t, split n.
+template <int CT, typename Put>
+__device__ __forceinline__ void router_unit(const LayerArgs& g, int unit, f32x4* red, Put put) {
   const int tid = phase_thread(), lane = tid & 63, q = lane >> 4, l16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int e0 = 16 * (unit / g.rsplit), n = unit % g.rsplit;
@@ -399,22 +453,10 @@ __device__ __forceinline__ void router_unit(const LayerArgs& g, int unit, f32x4*
     f32x4 sum = red[wave * 64 + lane];
     for (int w = 1; w < kWaves; ++w) sum += red[(w * CT + wave) * 64 + lane];
     const int t = 16 * wave + l16;   // sum[r]: expert e0 + 4 q + r, token t
-    if (t < g.M) {
-      float* o = g.logits + ((int64_t)n * g.M + t) * g.logit_ld + e0 + 4 * q;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) store_relaxed(o + r, sum[r]);
-    }
+    if (t < g.M) put(n, t, e0 + 4 * q, sum);
   }
   __syncthreads();
 }
-
-// What a workgroup keeps of the routing while it streams.
-struct SlotLds {
-  int32_t e[kLayerMaxE + kLayerMaxShared];
-  int32_t pos[kLayerMaxE + kLayerMaxShared + 1];     // first row; the next slot's is one past the last
-  uint8_t tok[kLayerMaxRoutes + kLayerMaxM * kLayerMaxShared];
-};
-constexpr int kStageBytes = 6144;   // a wave's activations in LDS: two workgroups on a CU fit its 160 KB
 
 // z of 16 features of one slot with up to 16 CT tokens: wave kw of ks takes
 // the 128-wide blocks kw, kw + ks, ... of K (the waves together read each
@@ -439,7 +481,7 @@ __device__ __forceinline__ void gate_up_strip(const LayerArgs& g, const SlotLds&
   f32x4 acc[2][CT];
 #pragma unroll
   for (int c = 0; c < CT; ++c) {
-    wt[c] = 16 * c + l16 < cnt ? load_relaxed(g.roww + pos0 + 16 * c + l16) : 0.f;
+    wt[c] = 16 * c + l16 >= cnt ? 0.f : g.solo ? s.w[pos0 + 16 * c + l16] : load_relaxed(g.roww + pos0 + 16 * c + l16);
 #pragma unroll
     for (int t = 0; t < 2; ++t) acc[t][c] = (f32x4){0.f, 0.f, 0.f, 0.f};
   }
@@ -479,74 +521,113 @@ __device__ __forceinline__ void gate_up_strip(const LayerArgs& g, const SlotLds&
 // two workgroups share a CU and one's joins overlap the other's streaming.
 template <bool MX, bool WIDE, int NV>
 __global__ void __launch_bounds__(kThreads, 4) layer_gate_up_kernel(LayerArgs g) {
-  constexpr int kRed = kWaves * 2 * 64 * 16 > kWaves * (WIDE ? 4 : 1) * 64 * 16 ? kWaves * 2 * 64 * 16
-                                                                                : kWaves * (WIDE ? 4 : 1) * 64 * 16;
+  // streaming: the strips' sums, the waves' activations, the slots; before
+  // that the routing, in front of the slots
+  constexpr int kSums = kWaves * 2 * 64 * 16;
   constexpr int kRoute = (int)sizeof(RouteLds) + kWaves * 64 * NV * 8;
+  constexpr int kStream = kSums + kWaves * kStageBytes;
   constexpr int kSlots = ((int)sizeof(SlotLds) + 15) / 16 * 16;
-  constexpr int kStream = kWaves * 2 * 64 * 16 + kSlots + kWaves * kStageBytes;
-  __shared__ __attribute__((aligned(16))) char smem[kRoute > kStream ? kRoute : kStream];
-  static_assert(kRed <= kStream, "a router unit's sums fit");
+  static_assert(kRoute <= kStream && kWaves * (WIDE ? 4 : 1) * 64 * 16 <= kStream, "routing and router units fit");
+  __shared__ __attribute__((aligned(16))) char smem[kStream + kSlots];
   __shared__ int s_claim, s_last, s_slots;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   f32x4* red = reinterpret_cast<f32x4*>(smem);
+  RouteLds& rl = *reinterpret_cast<RouteLds*>(smem);
+  double* keys = reinterpret_cast<double*>(smem + sizeof(RouteLds));
+  SlotLds& s = *reinterpret_cast<SlotLds*>(smem + kStream);
+  int nslots;
 
-  // the router's units, until none is left
-  for (;;) {
-    if (threadIdx.x == 0)
-      s_claim = __hip_atomic_fetch_add(g.sync + kLayerClaim, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (NV == 1 && !WIDE && g.solo) {
+    // a small router: every workgroup computes the whole routing by itself
+    constexpr int kLogits = ((int)sizeof(RouteLds) + kWaves * 64 * 8 + 15) / 16 * 16;
+    float* logits = reinterpret_cast<float*>(smem + kLogits);   // [rsplit][8][64]
+    static_assert(kLogits >= kWaves * 64 * 16 && kLogits + kLayerSoloUnits * kWaves * 64 * 4 <= kStream, "logits fit");
+    for (int unit = 0; unit < g.runits; ++unit)
+      router_unit<1>(g, unit, red, [&](int n, int t, int e, f32x4 v) {
+        *reinterpret_cast<f32x4*>(logits + (n * kWaves + t) * 64 + e) = v;
+      });
+    const bool first = blockIdx.x == 0;
+    rank_tokens<NV>(g, 0, rl, keys, first, [&](int n, int t, int e) { return logits[(n * kWaves + t) * 64 + e]; });
     __syncthreads();
-    const int unit = s_claim;
-    if (unit >= g.runits) break;
-    router_unit<WIDE ? 4 : 1>(g, unit, red);
-    wait_memory();
+    build_slots(g, rl, first, &s);
+    nslots = __builtin_amdgcn_readfirstlane(rl.wave_n[0]);
+    if (first && threadIdx.x == 0) g.sync[kLayerRouted] = 1;
     __syncthreads();
-    if (threadIdx.x == 0)
-      s_last = __hip_atomic_fetch_add(g.sync + kLayerArrived, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-               g.runits - 1;
-    __syncthreads();
-    if (s_last) {
-      RouteLds* rl = reinterpret_cast<RouteLds*>(smem);
-      route<NV>(g, *rl, reinterpret_cast<double*>(smem + sizeof(RouteLds)));
-      wait_memory();
-      __syncthreads();
+  } else {
+    // The routing's units, until none is left: the router's, then ranking 8
+    // tokens each.  A ranking unit waits for the router's units, which
+    // running workgroups have claimed before it.
+    const int tunits = (g.M + kWaves - 1) / kWaves;
+    for (;;) {
       if (threadIdx.x == 0)
-        __hip_atomic_store(g.sync + kLayerRouted, 1, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_AGENT);
+        s_claim = __hip_atomic_fetch_add(g.sync + kLayerClaim, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __syncthreads();
+      const int unit = s_claim;
+      if (unit >= g.runits + tunits) break;
+      if (unit < g.runits) {
+        router_unit<WIDE ? 4 : 1>(g, unit, red, [&](int n, int t, int e, f32x4 v) {
+          float* o = g.logits + ((int64_t)n * g.M + t) * g.logit_ld + e;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) store_relaxed(o + r, v[r]);
+        });
+        wait_memory();
+        __syncthreads();
+        if (threadIdx.x == 0)
+          __hip_atomic_fetch_add(g.sync + kLayerArrived, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      } else {
+        if (threadIdx.x == 0) s_last = wait_at_least(g.sync + kLayerArrived, g.runits, g.status);
+        __syncthreads();
+        const bool ready = s_last;
+        __syncthreads();
+        if (ready) {
+          rank_tokens<NV>(g, (unit - g.runits) * kWaves, rl, keys, true, [&](int n, int t, int e) {
+            return load_relaxed(g.logits + ((int64_t)n * g.M + t) * g.logit_ld + e);
+          });
+          wait_memory();
+          __syncthreads();
+          if (threadIdx.x == 0)
+            s_last = tunits == 1 || __hip_atomic_fetch_add(g.sync + kLayerRanked, 1, __ATOMIC_RELAXED,
+                                                           __HIP_MEMORY_SCOPE_AGENT) == tunits - 1;
+          __syncthreads();
+          if (s_last) {   // every token is ranked: the slots
+            if (tunits > 1) {
+              for (int i = phase_thread(); i < g.M * g.r.topk; i += kThreads) {
+                rl.id[i] = load_relaxed(g.ids + i);
+                rl.w[i] = load_relaxed(g.wts + i);
+              }
+            }
+            __syncthreads();
+            build_slots(g, rl, true, nullptr);
+            wait_memory();
+            __syncthreads();
+            if (threadIdx.x == 0)
+              __hip_atomic_store(g.sync + kLayerRouted, 1, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_AGENT);
+          }
+        }
+      }
+      // Keeps this round's work of thread 0 apart from the next claim's: with no
+      // barrier between the two, the compiler may run thread 0 through both
+      // while the other lanes of its wave go round without it, and the
+      // wave's barriers no longer match the other waves'.
+      __syncthreads();
     }
-    // Keeps this round's work of thread 0 apart from the next claim's: with no
-    // barrier between the two, the compiler may run thread 0 through both
-    // while the other lanes of its wave go round without it, and the
-    // wave's barriers no longer match the other waves'.
+
+    if (threadIdx.x == 0)
+      s_slots = wait_at_least(g.sync + kLayerRouted, 1, g.status) ? load_relaxed(g.sync + kLayerNumSlots) : 0;
+    __syncthreads();
+    nslots = s_slots;
+    {
+      const int tid = phase_thread();
+      const int total = nslots ? load_relaxed(g.sync + kLayerNumRows) : 0;
+      for (int i = tid; i < nslots; i += kThreads) {
+        s.e[i] = load_relaxed(&g.slots[i].e);
+        s.pos[i] = load_relaxed(&g.slots[i].pos0);
+      }
+      if (tid == 0) s.pos[nslots] = total;
+      for (int i = tid; i < total; i += kThreads) s.tok[i] = (uint8_t)load_relaxed(g.rows + i);
+    }
     __syncthreads();
   }
-
-  if (threadIdx.x == 0) {
-    int n = 0, ok = 1;
-    while (load_relaxed(g.sync + kLayerRouted) == 0) {
-      if (++n > kSpinLimit) {
-        atomicAdd(g.status, 1);
-        ok = 0;
-        break;
-      }
-      __builtin_amdgcn_s_sleep(2);
-    }
-    s_slots = ok ? load_relaxed(g.sync + kLayerNumSlots) : 0;
-  }
-  __syncthreads();
-  const int nslots = s_slots;
-  SlotLds& s = *reinterpret_cast<SlotLds*>(smem + kWaves * 2 * 64 * 16);
-  {
-    const int tid = phase_thread();
-    const int total = nslots ? load_relaxed(g.sync + kLayerNumRows) : 0;
-    for (int i = tid; i < nslots; i += kThreads) {
-      s.e[i] = load_relaxed(&g.slots[i].e);
-      s.pos[i] = load_relaxed(&g.slots[i].pos0);
-    }
-    if (tid == 0) s.pos[nslots] = total;
-    for (int i = tid; i < total; i += kThreads) {
-      s.tok[i] = (uint8_t)load_relaxed(g.rows + i);
-    }
-  }
-  __syncthreads();
 
   // Items (slot, nh strips of 16 features): a workgroup starts with its own and
   // then claims one after another, the last slots first (the shared experts
@@ -558,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 4) layer_gate_up_kernel(LayerArgs g)
   const int strips = g.I / 16, per = (strips + nh - 1) / nh;
   const int items = nslots * per;
   f32x4* mine = red + h * g.ks * 2 * 64;
-  char* stage = smem + kWaves * 2 * 64 * 16 + kSlots + wave * kStageBytes;
+  char* stage = smem + kSums + wave * kStageBytes;
   const int nb = (g.K / 128 - kw + g.ks - 1) / g.ks;
   int staged = -1;
   for (int claim = blockIdx.x; claim < items;) {
@@ -639,12 +720,17 @@ __global__ void __launch_bounds__(kThreads, 4) layer_down_kernel(LayerArgs g) {
   constexpr int kTok = WIDE ? kLayerMaxM : 16;
   constexpr int kQ = 4 * kDownTiles;
   __shared__ __attribute__((aligned(16))) f32x4 red[kWaves * kTok * kQ];
+  // the slots (dynamic: the launch passes room for the most there can be) are
+  // requested before their number is known
+  extern __shared__ LayerSlot s_slots[];
   __shared__ int s_last;
   const int lane = threadIdx.x & 63, q = lane >> 4, l16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int strip = blockIdx.x / g.splits, split = blockIdx.x % g.splits;
+  for (int i = threadIdx.x; i < g.max_slots; i += kThreads) s_slots[i] = g.slots[i];
   // a first launch that timed out published nothing: no rows to add
   const int nslots = g.sync[kLayerRouted] ? g.sync[kLayerNumSlots] : 0;
+  __syncthreads();
   const int spe = g.I / 128;                             // blocks per slot
   const int64_t total = (int64_t)nslots * spe;
   const int parts = g.splits * kWaves, part = split * kWaves + wave;
@@ -664,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 4) layer_down_kernel(LayerArgs g) {
     while (b < end) {
       const int slot = (int)(b / spe), b0 = (int)(b % spe);
       const int n = (int)min<int64_t>(spe - b0, end - b);
-      const LayerSlot& sl = g.slots[slot];
+      const LayerSlot& sl = s_slots[slot];
       const int cnt = __builtin_amdgcn_readfirstlane(sl.cnt);
       if (cnt <= 16) down_run<MX, 1, MX ? 2 : 4, 2>(g, sl, wo, so, b0, n, tile);
       else if (cnt <= 32) down_run<MX, 2, MX ? 1 : 2, 2>(g, sl, wo, so, b0, n, tile);
@@ -679,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 4) layer_down_kernel(LayerArgs g) {
     while (b < end) {
       const int slot = (int)(b / spe), b0 = (int)(b % spe);
       const int n = (int)min<int64_t>(spe - b0, end - b);
-      const LayerSlot& sl = g.slots[slot];
+      const LayerSlot& sl = s_slots[slot];
       const Weights<MX> wr = expert_weights<MX>(g.w2, g.w2s, __builtin_amdgcn_readfirstlane(sl.e), (int64_t)g.K * g.I);
       const uint32_t ao[1] = {
           (sl.mask >> l16) & 1 ? lane_a<MX>(sl.pos0 + __popcll(sl.mask & below(l16)), g.I, q) : kPast};
@@ -733,6 +819,7 @@ __global__ void __launch_bounds__(kThreads, 4) layer_down_kernel(LayerArgs g) {
       store_relaxed(g.sync + kLayerClaim, 0);
       store_relaxed(g.sync + kLayerItems, 0);
       store_relaxed(g.sync + kLayerArrived, 0);
+      store_relaxed(g.sync + kLayerRanked, 0);
       store_relaxed(g.sync + kLayerRouted, 0);
       store_relaxed(g.sync + kLayerDone, 0);
     }
@@ -749,7 +836,8 @@ hipError_t launch(const LayerArgs& g, unsigned grid1, hipStream_t s) {
     hipLaunchKernelGGL((layer_gate_up_kernel<MX, WIDE, 8>), dim3(grid1), dim3(kThreads), 0, s, g);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((layer_down_kernel<MX, WIDE>), dim3((unsigned)(g.K / (16 * kDownTiles) * g.splits)), dim3(kThreads), 0, s, g);
+  hipLaunchKernelGGL((layer_down_kernel<MX, WIDE>), dim3((unsigned)(g.K / (16 * kDownTiles) * g.splits)), dim3(kThreads),
+                     sizeof(LayerSlot) * g.max_slots, s, g);
   return hipGetLastError();
 }
 
@@ -771,10 +859,12 @@ hipError_t launch_layer(LayerArgs g, bool mxfp8, hipStream_t s) {
   g.rsplit = layer_router_splits(g.K);
   g.runits = (g.r.E + 15) / 16 * g.rsplit;
   g.splits = layer_splits(g.K);
+  g.solo = g.runits <= kLayerSoloUnits && g.M <= kWaves && g.r.E <= 64;
   g.ks = g.K >= 1024 ? 8 : g.K >= 512 ? 4 : g.K >= 256 ? 2 : 1;
   const int nh = kWaves / g.ks;
   const int64_t items = (int64_t)g.max_slots * ((g.I / 16 + nh - 1) / nh);
-  int64_t grid = items > g.runits ? items : g.runits;
+  const int64_t units = g.runits + (g.M + kWaves - 1) / kWaves;
+  int64_t grid = items > units ? items : units;
   if (grid > 512) grid = 512;
   if (g.M > 16) return mxfp8 ? launch<true, true>(g, (unsigned)grid, s) : launch<false, true>(g, (unsigned)grid, s);
   return mxfp8 ? launch<true, false>(g, (unsigned)grid, s) : launch<false, false>(g, (unsigned)grid, s);
