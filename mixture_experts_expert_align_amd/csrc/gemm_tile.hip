@@ -681,6 +681,20 @@ hipError_t launch_layout(const GemmArgs& g, hipStream_t s) {
   return launch_split<EPI, 128, 128, 64, 2, 2, 2, kRouteMajor>(g, s);
 }
 
+template <int BM, int BN, int BK, int WN, int WM, int OCC, bool WT>
+hipError_t launch_lora_tiles(const GemmArgs& g, const LoraExt& x, hipStream_t s) {
+  const int64_t nrt = (x.a.R + BM - 1) / BM, nct = (g.nfeat + BN - 1) / BN;
+  const int64_t nchunk = (nrt + kRowBlock - 1) / kRowBlock * ((nct + kColBlock - 1) / kColBlock);
+  const int64_t grid = (nchunk + NXCD - 1) / NXCD * NXCD * kXcdChunk;
+  hipLaunchKernelGGL((gemm_tile_lora_kernel<BM, BN, BK, WN, WM, OCC, WT>), dim3((unsigned)grid), dim3(64 * WN * WM), 0,
+                     s, g, x, nrt, nct);
+  return hipGetLastError();
+}
+
+// Tiles from which a projection with adapters takes the larger tile size:
+// one for every CU.
+constexpr int64_t kLoraFill = 256;
+
 }  // namespace tile
 
 // 256 rows x 256 features, the contiguous tile shape
@@ -709,18 +723,15 @@ hipError_t launch_tile_lora_bf16(const LoraArgs& a, const uint16_t* v, const uin
   g.E = 1;
   g.out = out;
   g.out_ld = nfeat;
-  constexpr int BM = kRowsBM, BN = kRowsBN;
-  const int64_t nrt = (a.R + BM - 1) / BM, nct = (nfeat + BN - 1) / BN;
-  const int64_t nchunk = (nrt + kRowBlock - 1) / kRowBlock * ((nct + kColBlock - 1) / kColBlock);
-  const int64_t grid = (nchunk + NXCD - 1) / NXCD * NXCD * kXcdChunk;
   const LoraExt x{a, m};
-  if (wt)
-    hipLaunchKernelGGL((gemm_tile_lora_kernel<BM, BN, 64, 4, 4, 4, true>), dim3((unsigned)grid), dim3(1024), 0, s, g, x,
-                       nrt, nct);
-  else
-    hipLaunchKernelGGL((gemm_tile_lora_kernel<BM, BN, 64, 4, 4, 4, false>), dim3((unsigned)grid), dim3(1024), 0, s, g,
-                       x, nrt, nct);
-  return hipGetLastError();
+  const int64_t big = (a.R + 255) / 256 * ((nfeat + 255) / 256);
+  if (wt) return big >= kLoraFill ? launch_lora_tiles<256, 256, 64, 4, 4, 4, true>(g, x, s)
+                                  : launch_lora_tiles<64, 256, 64, 4, 2, 2, true>(g, x, s);
+  if (big >= kLoraFill) return launch_lora_tiles<256, 256, 64, 4, 4, 4, false>(g, x, s);
+  if ((a.R + 127) / 128 * ((nfeat + 127) / 128) >= kLoraFill)
+    return launch_lora_tiles<128, 128, 64, 2, 2, 2, false>(g, x, s);
+  return kdim % 128 == 0 ? launch_lora_tiles<64, 64, 128, 2, 2, 2, false>(g, x, s)
+                         : launch_lora_tiles<64, 64, 64, 2, 2, 2, false>(g, x, s);
 }
 
 hipError_t launch_gemm_tile_bf16(const GemmArgs& g, hipStream_t s) {
