@@ -153,15 +153,16 @@ __device__ __forceinline__ void load_offsets(const GemmArgs& g, const TileCoord&
   const int K = g.kdim;
   if (WT) {
     // weights stored with the output index contiguous: the slot holds BK
-    // contraction rows of BN outputs; block b = rows 2b, 2b+1 (BN = 256:
-    // 512 bytes a row), lane l -> row 2b + l / 32, physical chunk l % 32,
-    // holding logical chunk wt_logical(row, l % 32); the slice's first row
-    // comes in through the instruction offset
-    static_assert(!WT || BN * 2 == 512, "transposed weight rows of 512 bytes");
+    // contraction rows of BN outputs; block b = 512 / BN rows (BN = 256: rows
+    // 2b, 2b+1 of 512 bytes), lane l -> its row l / (BN / 8), physical chunk
+    // l % (BN / 8), holding logical chunk wt_logical(row, that); the slice's
+    // first row comes in through the instruction offset
+    constexpr int CW = BN / 8, RW = 64 / CW;   // chunks per row, rows per block
+    static_assert(!WT || BN == 256 || BN == 128 || BN == 64, "transposed weight rows of 512, 256 or 128 bytes");
 #pragma unroll
     for (int i = 0; i < LW; ++i) {
-      const int r = 2 * (wave + NW * i) + lane / 32;
-      const int c = wt_logical(r, lane % 32);
+      const int r = RW * (wave + NW * i) + lane / CW;
+      const int c = wt_logical_n<BN>(r, lane % CW);
       ow[i] = (uint32_t)(((int64_t)r * g.nfeat + tc.col0 + 8 * c) * 2);
     }
   } else
@@ -257,10 +258,10 @@ struct LoraExt {
 // adapter's rows (zeros in the others) against M_g, once per piece.  (Two
 // pieces, 16 bits, leave an error of 2^-17 of that part beside y's own 2^-8.)
 // After the projection's slices the staging ring is free: the adapters are
-// listed, then each slice of BK positions is loaded into the first slot of
+// listed, then each slice of BK positions is loaded into one of two slots of
 // either operand, every 16-byte chunk (8 positions, of one adapter and piece
 // since rank is a multiple of 8) from where it lies or, masked, as zeros.
-// compute(): multiplies the slice in those slots.
+// compute(i): multiplies the slice in slots i.
 template <int BM, int BN, int BK, int NW, bool WT, typename Compute>
 __device__ __forceinline__ void lora_slices(const LoraExt& x, const GemmArgs& g, const TileCoord& tc, uint16_t* wslot,
                                             uint16_t* rslot, int* list, Compute compute) {
@@ -309,17 +310,22 @@ __device__ __forceinline__ void lora_slices(const LoraExt& x, const GemmArgs& g,
   for (int i = 0; i < LX; ++i) mine[i] = slot_of[(wave + NW * i) * RPB + lane / CH];
   const __amdgpu_buffer_rsrc_t mr = buffer_rsrc(x.m, (int64_t)x.a.G * g.nfeat * rank * 2);
   const __amdgpu_buffer_rsrc_t lr = buffer_rsrc(x.a.low, x.a.R * kLoraPieces * rank * 2);
-  for (int c0 = 0; c0 < len; c0 += BK) {
+  // slice i into slot i % 2 of either operand; every lane loads
+  auto issue = [&](int i) {
+    const int c0 = i * BK;
+    uint16_t* ws = wslot + (i & 1) * BN * BK;
+    uint16_t* rs = rslot + (i & 1) * BM * BK;
     if (WT) {
+      constexpr int CW = BN / 8, RW = 64 / CW;
 #pragma unroll
       for (int i = 0; i < LW; ++i) {
-        const int r = 2 * (wave + NW * i) + lane / 32;   // position c0 + r: a row of M_g
-        const int col = tc.col0 + 8 * wt_logical(r, lane % 32);
+        const int r = RW * (wave + NW * i) + lane / CW;   // position c0 + r: a row of M_g
+        const int col = tc.col0 + 8 * wt_logical_n<BN>(r, lane % CW);
         const int p = c0 + r, q = p / span;
         uint32_t o = kPast;
         if (p < len && col < g.nfeat)
           o = (uint32_t)((((int64_t)list[q] * rank + (p - q * span) % rank) * g.nfeat + col) * 2);
-        lds_load16(mr, wslot + (wave + NW * i) * RPB * BK, o, 0);
+        lds_load16(mr, ws + (wave + NW * i) * RPB * BK, o, 0);
       }
     } else {
 #pragma unroll
@@ -329,7 +335,7 @@ __device__ __forceinline__ void lora_slices(const LoraExt& x, const GemmArgs& g,
         uint32_t o = kPast;
         if (p < len && tc.col0 + n < g.nfeat)
           o = (uint32_t)((((int64_t)list[q] * g.nfeat + tc.col0 + n) * rank + (p - q * span) % rank) * 2);
-        lds_load16(mr, wslot + (wave + NW * i) * RPB * BK, o, 0);
+        lds_load16(mr, ws + (wave + NW * i) * RPB * BK, o, 0);
       }
     }
 #pragma unroll
@@ -338,11 +344,21 @@ __device__ __forceinline__ void lora_slices(const LoraExt& x, const GemmArgs& g,
       const int p = c0 + 8 * ((lane % CH) ^ ((m / RPW) & (CH - 1))), q = p / span;
       const uint32_t o =
           p < len && mine[i] == q ? (uint32_t)(((tc.row0 + m) * kLoraPieces * rank + (p - q * span)) * 2) : kPast;
-      lds_load16(lr, rslot + (wave + NW * i) * RPB * BK, o, 0);
+      lds_load16(lr, rs + (wave + NW * i) * RPB * BK, o, 0);
     }
-    wait_vm<0>();
+    issue_order();
+  };
+  const int ns = (len + BK - 1) / BK;
+  if (ns > 0) issue(0);
+  for (int i = 0; i < ns; ++i) {
+    if (i + 1 < ns) {
+      issue(i + 1);
+      wait_vm<LW + LX>();
+    } else {
+      wait_vm<0>();
+    }
     lds_barrier();
-    compute();
+    compute(i & 1);
     lds_barrier();
   }
 }
@@ -422,7 +438,7 @@ __device__ __forceinline__ void split_tile(const GemmArgs& g, const TileCoord& t
     const int c = 2 * s + (lane >> 5);
 #pragma unroll
     for (int i = 0; i < TW; ++i)
-      fw[fb][i] = WT ? wt_frag(ws, wn * (BN / WN) + 32 * i, 16 * s, lane)
+      fw[fb][i] = WT ? wt_frag<BN>(ws, wn * (BN / WN) + 32 * i, 16 * s, lane)
                      : as_bf16x8(*reinterpret_cast<const i32x4*>(&ws[lds_off<BK>(wrow_l[i], c)]));
 #pragma unroll
     for (int j = 0; j < TX; ++j)
@@ -509,11 +525,11 @@ __device__ __forceinline__ void split_tile(const GemmArgs& g, const TileCoord& t
   lds_barrier();
   if constexpr (Ext::kOn) {
     static_assert(BM * 2 + 1 <= WSLOT / 2, "the adapter list fits a slot");
-    lora_slices<BM, BN, BK, NW, WT>(ext, g, tc, wbase, rbase, reinterpret_cast<int*>(wbase + WSLOT), [&]() {
+    lora_slices<BM, BN, BK, NW, WT>(ext, g, tc, wbase, rbase, reinterpret_cast<int*>(wbase + 2 * WSLOT), [&](int k) {
       if (!live) return;
 #pragma unroll
       for (int s = 0; s < NSTEP; ++s) {
-        fload(s & 1, 0, s);
+        fload(s & 1, k, s);
         mma(s & 1);
       }
     });
@@ -691,9 +707,16 @@ hipError_t launch_lora_tiles(const GemmArgs& g, const LoraExt& x, hipStream_t s)
   return hipGetLastError();
 }
 
-// Tiles from which a projection with adapters takes the larger tile size:
-// one for every CU.
+// The largest tiles that still make one for every CU.
 constexpr int64_t kLoraFill = 256;
+template <bool WT>
+hipError_t launch_lora_size(const GemmArgs& g, const LoraExt& x, hipStream_t s) {
+  auto tiles = [&](int64_t n) { return (x.a.R + n - 1) / n * ((g.nfeat + n - 1) / n); };
+  if (tiles(256) >= kLoraFill) return launch_lora_tiles<256, 256, 64, 4, 4, 4, WT>(g, x, s);
+  if (tiles(128) >= kLoraFill) return launch_lora_tiles<128, 128, 64, 2, 2, 2, WT>(g, x, s);
+  return g.kdim % 128 == 0 ? launch_lora_tiles<64, 64, 128, 2, 2, 2, WT>(g, x, s)
+                           : launch_lora_tiles<64, 64, 64, 2, 2, 2, WT>(g, x, s);
+}
 
 }  // namespace tile
 
@@ -724,14 +747,7 @@ hipError_t launch_tile_lora_bf16(const LoraArgs& a, const uint16_t* v, const uin
   g.out = out;
   g.out_ld = nfeat;
   const LoraExt x{a, m};
-  const int64_t big = (a.R + 255) / 256 * ((nfeat + 255) / 256);
-  if (wt) return big >= kLoraFill ? launch_lora_tiles<256, 256, 64, 4, 4, 4, true>(g, x, s)
-                                  : launch_lora_tiles<64, 256, 64, 4, 2, 2, true>(g, x, s);
-  if (big >= kLoraFill) return launch_lora_tiles<256, 256, 64, 4, 4, 4, false>(g, x, s);
-  if ((a.R + 127) / 128 * ((nfeat + 127) / 128) >= kLoraFill)
-    return launch_lora_tiles<128, 128, 64, 2, 2, 2, false>(g, x, s);
-  return kdim % 128 == 0 ? launch_lora_tiles<64, 64, 128, 2, 2, 2, false>(g, x, s)
-                         : launch_lora_tiles<64, 64, 64, 2, 2, 2, false>(g, x, s);
+  return wt ? launch_lora_size<true>(g, x, s) : launch_lora_size<false>(g, x, s);
 }
 
 hipError_t launch_gemm_tile_bf16(const GemmArgs& g, hipStream_t s) {

@@ -55,90 +55,152 @@ __device__ __forceinline__ bf16x8 col_frag(const uint16_t* base, int col0, int l
 }
 
 // ---------------------------------------------------------------- shrink --
-// low[r] = scale_g M_g v_r for 16 rows a workgroup: the rows in the MFMA
+// low[r] = scale_g M_g v_r for 16 CT rows a workgroup: the rows in the MFMA
 // column operand, 16 of the rank's outputs per row tile (JT tiles), the
-// contraction split over the 8 waves, whose sums meet in LDS in wave order.
-// One pass per adapter among the 16 rows; each pass writes its own rows.
-//   T = false: M = A [rank, C], contraction contiguous, loaded as it is;
-//   T = true:  M = B^T, B [C, rank]: 32 of the contraction's rows at a time
-//              go through a part of LDS of the wave's own and are read
-//              transposed.
-// Grid (row blocks, passes in flight): with few row blocks the adapters of
-// one block go to different workgroups.
-constexpr int kShrinkWaves = 8;
+// contraction split over the 4 waves in steps of 64 (wave w takes steps w,
+// w + 4, ...), whose sums meet in LDS in wave order.  One pass per adapter
+// among the workgroup's rows; each pass reads and writes its own rows.
+//   T = false: M = A [rank, C], contraction contiguous;
+//   T = true:  M = B^T, B [C, rank]: a step's 64 rows are read transposed.
+// Each wave has a ring of D steps in LDS to itself, filled by loads that
+// write LDS (no barrier: it waits for its own loads).  That is for the lines:
+// the MFMA layout wants 16 rows of 64 bytes from a load, which asks the cache
+// for half a line at a time, and a CU got 28 KB/us that way; loads of 8 rows
+// of 128 bytes reach 70.  Chunks are XOR-swizzled so that the 16 rows of a
+// read spread over the banks.
+// Grid (row blocks, passes in flight, row tile groups): with few row blocks
+// the adapters of one block go to different workgroups.
+constexpr int kShrinkWaves = 4;
 
-template <int JT, bool T>
+template <int JT, int CT, bool T, int D>
 __global__ void __launch_bounds__(64 * kShrinkWaves) lora_shrink_kernel(LoraArgs a, const uint16_t* __restrict__ v,
                                                                        const uint16_t* __restrict__ m, int C) {
-  // the waves' sums; with T before that a [32][rank] block per wave (and the
-  // columns a partial last row tile reads past it)
-  constexpr int kBlock = 32 * 16 * JT + 16;
-  constexpr int kRed = kShrinkWaves * JT * 64 * 16, kT = T ? kShrinkWaves * kBlock * 2 : 0;
-  __shared__ __attribute__((aligned(16))) char smem[kRed > kT ? kRed : kT];
+  // a step: 16 CT rows, then 16 JT rows of A or 64 rows of B, 128 bytes of
+  // contraction each (the same size, since rank <= 16 JT)
+  constexpr int kStep = (CT + JT) * 1024;         // elements
+  constexpr int kRing = kStep * D + 16;           // a partial last row tile of B reads past it
+  constexpr int kLoads = 2 * (CT + JT);           // 1 KB each
+  constexpr int kRed = kShrinkWaves * JT * CT * 64 * 16, kRings = kShrinkWaves * kRing * 2;
+  static_assert((D - 1) * kLoads < 64, "wait counts");
+  __shared__ __attribute__((aligned(1024))) char smem[kRed > kRings ? kRed : kRings];
   const int lane = threadIdx.x & 63, q = lane >> 4, l16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t r0 = (int64_t)blockIdx.x * 16;
+  const int64_t r0 = (int64_t)blockIdx.x * 16 * CT;
   const int rank = a.rank;
-  const int mine = row_adapter(a.adapter, r0 + l16, a.R, a.G);
-  const __amdgpu_buffer_rsrc_t vr = buffer_rsrc(v + r0 * C, min<int64_t>(16, a.R - r0) * C * 2);
-  const uint32_t vo = r0 + l16 < a.R ? (uint32_t)(l16 * C * 2 + 16 * q) : kPast;
+  const int j0 = T ? 0 : JT * blockIdx.z;   // first row tile
+  int mine[CT];                             // adapter of row 16 c + l16
+#pragma unroll
+  for (int c = 0; c < CT; ++c) mine[c] = row_adapter(a.adapter, r0 + 16 * c + l16, a.R, a.G);
+  const __amdgpu_buffer_rsrc_t vr = buffer_rsrc(v + r0 * C, min<int64_t>(16 * CT, a.R - r0) * C * 2);
   f32x4* red = reinterpret_cast<f32x4*>(smem);
-  uint16_t* blk = reinterpret_cast<uint16_t*>(smem) + wave * kBlock;
+  uint16_t* ring = reinterpret_cast<uint16_t*>(smem) + wave * kRing;
 
-  if (blockIdx.y == 0) {   // rows without an adapter: zeros
-    for (int i = threadIdx.x; i < 16 * kPieces * rank; i += 64 * kShrinkWaves) {
-      const int64_t r = r0 + i / (kPieces * rank);
-      if (r < a.R && row_adapter(a.adapter, r, a.R, a.G) < 0) a.low[r0 * kPieces * rank + i] = 0;
+  if (blockIdx.y == 0 && blockIdx.z == 0) {   // rows without an adapter: zeros
+    for (int i = threadIdx.x; i < 16 * CT * kPieces * rank / 8; i += 64 * kShrinkWaves) {
+      const int64_t r = r0 + 8 * i / (kPieces * rank);
+      if (r < a.R && row_adapter(a.adapter, r, a.R, a.G) < 0)
+        reinterpret_cast<i32x4*>(a.low + r0 * kPieces * rank)[i] = (i32x4){0, 0, 0, 0};
     }
   }
 
-  uint32_t left = (uint32_t)__ballot(mine >= 0) & 0xffffu;
+  uint64_t left = 0;   // rows whose adapter has not had its pass
+#pragma unroll
+  for (int c = 0; c < CT; ++c) left |= (__ballot(mine[c] >= 0) & 0xffffull) << (16 * c);
   for (int pass = 0; left; ++pass) {
-    const int g = __builtin_amdgcn_readlane(mine, __ffs(left) - 1);
-    left &= ~((uint32_t)__ballot(mine == g) & 0xffffu);
+    const int row = __ffsll((unsigned long long)left) - 1;
+    int g = 0;
+#pragma unroll
+    for (int c = 0; c < CT; ++c)
+      if (row >> 4 == c) g = __builtin_amdgcn_readlane(mine[c], row & 15);
+    uint64_t rows = 0;
+#pragma unroll
+    for (int c = 0; c < CT; ++c) rows |= (__ballot(mine[c] == g) & 0xffffull) << (16 * c);
+    left &= ~rows;
     if (pass % gridDim.y != blockIdx.y) continue;
     const __amdgpu_buffer_rsrc_t mr = buffer_rsrc(m + (int64_t)g * rank * C, (int64_t)rank * C * 2);
-    f32x4 acc[JT];
+    const float sc = a.scale[g];
+    // load i of a step: rows 8 i + lane / 8, physical chunk lane % 8; only
+    // this adapter's rows are read
+    auto chunk = [&](int r) { return 16 * ((lane & 7) ^ ((r >> 1) & 7)); };
+    uint32_t vo[2 * CT], mo[2 * JT];
 #pragma unroll
-    for (int j = 0; j < JT; ++j) acc[j] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    for (int c0 = 32 * wave; c0 < C; c0 += 32 * kShrinkWaves) {
-      const i32x4 x = __builtin_amdgcn_raw_buffer_load_b128(vr, vo, 2 * c0, 0);
-      if (T) {
-        // rows c0 .. c0 + 31 of B: 32 rank elements in a row
-        for (int i = lane; i < 4 * rank; i += 64)
-          *reinterpret_cast<i32x4*>(blk + 8 * i) = __builtin_amdgcn_raw_buffer_load_b128(mr, 16 * i, 2 * c0 * rank, 0);
-        __builtin_amdgcn_wave_barrier();
+    for (int i = 0; i < 2 * CT; ++i) {
+      const int r = 8 * i + (lane >> 3);
+      vo[i] = (rows >> r) & 1 ? (uint32_t)(r * C * 2 + chunk(r)) : kPast;
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * JT; ++i) {
+      const int r = 8 * i + (lane >> 3), e = 64 * i + lane;
+      mo[i] = T ? (e < 8 * rank ? 16 * e : kPast)
+                : (16 * j0 + r < rank ? (uint32_t)((16 * j0 + r) * C * 2 + chunk(r)) : kPast);
+    }
+    f32x4 acc[JT][CT];
+#pragma unroll
+    for (int j = 0; j < JT; ++j)
+#pragma unroll
+      for (int c = 0; c < CT; ++c) acc[j][c] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    const int n = (C / 64 - wave + kShrinkWaves - 1) / kShrinkWaves;
+    auto load = [&](int d, int i) {   // past the end: zeros
+      const int k0 = 64 * (wave + kShrinkWaves * i);
+      const bool in = i < n;
+      uint16_t* s = ring + d * kStep;
+#pragma unroll
+      for (int l = 0; l < 2 * CT; ++l) lds_load16(vr, s + 512 * l, in ? vo[l] : kPast, 2 * k0);
+#pragma unroll
+      for (int l = 0; l < 2 * JT; ++l)
+        lds_load16(mr, s + CT * 1024 + 512 * l, in ? mo[l] : kPast, T ? 2 * k0 * rank : 2 * k0);
+      issue_order();
+    };
+    auto mma = [&](int d) {
+      const uint16_t* s = ring + d * kStep;
+      const uint16_t* sm = s + CT * 1024;
+      auto frag = [&](const uint16_t* p, int t, int h) {   // 16 rows from 16 t, 32 of the step's contraction
+        return as_bf16x8(*reinterpret_cast<const i32x4*>(p + (16 * t + l16) * 64 + 8 * ((4 * h + q) ^ ((l16 >> 1) & 7))));
+      };
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        bf16x8 x[CT];
+#pragma unroll
+        for (int c = 0; c < CT; ++c) x[c] = frag(s, c, h);
 #pragma unroll
         for (int j = 0; j < JT; ++j) {
-          const bf16x8 f = col_frag(blk, 16 * j, lane, [&](int r, int c) { return r * rank + c; });
-          acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, as_bf16x8(x), acc[j], 0, 0, 0);
-        }
-        __builtin_amdgcn_wave_barrier();
-      } else {
+          const bf16x8 w = T ? col_frag(sm, 16 * j, lane, [&](int r, int c) { return (32 * h + r) * rank + c; })
+                             : frag(sm, j, h);
 #pragma unroll
-        for (int j = 0; j < JT; ++j) {
-          const int o = 16 * j + l16;
-          const i32x4 w = __builtin_amdgcn_raw_buffer_load_b128(
-              mr, o < rank ? (uint32_t)(o * C * 2 + 16 * q) : kPast, 2 * c0, 0);
-          acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(w), as_bf16x8(x), acc[j], 0, 0, 0);
+          for (int c = 0; c < CT; ++c) acc[j][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x[c], acc[j][c], 0, 0, 0);
         }
       }
-    }
-    __syncthreads();   // every wave is done with its block
+      issue_order();
+    };
 #pragma unroll
-    for (int j = 0; j < JT; ++j) red[(wave * JT + j) * 64 + lane] = acc[j];
+    for (int d = 0; d < D; ++d) load(d, d);
+    for (int it = 0; it < n; it += D)
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        wait_vm<(D - 1) * kLoads>();
+        mma(d);
+        load(d, it + d + D);
+      }
+    wait_vm<0>();
+    __syncthreads();   // every wave is done with its ring
+#pragma unroll
+    for (int j = 0; j < JT; ++j)
+#pragma unroll
+      for (int c = 0; c < CT; ++c) red[((wave * JT + j) * CT + c) * 64 + lane] = acc[j][c];
     __syncthreads();
-    // row tile j: wave j; sum[r]: output 16 j + 4 q + r, row l16
-    if (wave < JT) {
-      f32x4 sum = red[wave * 64 + lane];
-      for (int w = 1; w < kShrinkWaves; ++w) sum += red[(w * JT + wave) * 64 + lane];
-      const int o = 16 * wave + 4 * q;
-      if (mine == g && o < rank) {
-        const float sc = a.scale[g];
+    // (row tile j, column tile c): one wave; sum[r]: output 16 j + 4 q + r
+#pragma unroll
+    for (int t = 0; t < JT * CT; ++t) {
+      const int j = t / CT, c = t % CT;
+      if (t % kShrinkWaves != wave) continue;
+      f32x4 sum = red[t * 64 + lane];
+      for (int w = 1; w < kShrinkWaves; ++w) sum += red[(w * JT * CT + t) * 64 + lane];
+      const int o = 16 * (j0 + j) + 4 * q;
+      if (mine[c] == g && o < rank) {
         uint32_t p[4][3];
 #pragma unroll
         for (int r = 0; r < 4; ++r) split3(sc * sum[r], p[r]);
-        uint16_t* dst = a.low + (r0 + l16) * kPieces * rank + o;
+        uint16_t* dst = a.low + (r0 + 16 * c + l16) * kPieces * rank + o;
 #pragma unroll
         for (int k = 0; k < kPieces; ++k)
           *reinterpret_cast<uint2*>(dst + k * rank) =
@@ -337,26 +399,31 @@ __global__ void __launch_bounds__(256) lora_wgrad_join_kernel(LoraGradArgs a, in
   *dst = s;
 }
 
-template <int JT>
-hipError_t launch_shrink(const LoraArgs& a, const uint16_t* v, const uint16_t* m, int C, bool t, dim3 grid,
-                         hipStream_t s) {
+template <int JT, int CT, int D>
+hipError_t launch_shrink(const LoraArgs& a, const uint16_t* v, const uint16_t* m, int C, bool t, hipStream_t s) {
+  const int64_t blocks = (a.R + 16 * CT - 1) / (16 * CT);
+  int64_t passes = 1024 / blocks;
+  passes = passes < 1 ? 1 : passes > 16 * CT ? 16 * CT : passes;
+  const dim3 block(64 * kShrinkWaves);
   if (t)
-    hipLaunchKernelGGL((lora_shrink_kernel<JT, true>), grid, dim3(64 * kShrinkWaves), 0, s, a, v, m, C);
+    hipLaunchKernelGGL((lora_shrink_kernel<JT, CT, true, D>), dim3((unsigned)blocks, (unsigned)passes), block, 0, s, a,
+                       v, m, C);
   else
-    hipLaunchKernelGGL((lora_shrink_kernel<JT, false>), grid, dim3(64 * kShrinkWaves), 0, s, a, v, m, C);
+    hipLaunchKernelGGL((lora_shrink_kernel<JT, CT, false, D>),
+                       dim3((unsigned)blocks, (unsigned)passes, (unsigned)((a.rank + 16 * JT - 1) / (16 * JT))), block, 0,
+                       s, a, v, m, C);
   return hipGetLastError();
 }
 
-// low[r] = scale_g (T ? B_g^T : A_g) v_r, contraction C.
+// low[r] = scale_g (T ? B_g^T : A_g) v_r, contraction C.  With few rows each
+// 16 of the rank's outputs go to a workgroup of their own.  (Blocks of 32 rows
+// read each adapter's matrix half as often but put one workgroup on a CU: 24
+// against 17 us at 8192 x 4096, rank 16, no difference at rank 64.)
 hipError_t shrink(const LoraArgs& a, const uint16_t* v, const uint16_t* m, int C, bool t, hipStream_t s) {
-  const int64_t blocks = (a.R + 15) / 16;
-  int64_t passes = 1024 / blocks;
-  passes = passes < 1 ? 1 : passes > 16 ? 16 : passes;
-  const dim3 grid((unsigned)blocks, (unsigned)passes);
-  if (a.rank <= 16) return launch_shrink<1>(a, v, m, C, t, grid, s);
-  if (a.rank <= 32) return launch_shrink<2>(a, v, m, C, t, grid, s);
-  if (a.rank <= 64) return launch_shrink<4>(a, v, m, C, t, grid, s);
-  return launch_shrink<8>(a, v, m, C, t, grid, s);
+  if (a.rank <= 16 || (!t && a.R <= 1024)) return launch_shrink<1, 1, 4>(a, v, m, C, t, s);
+  if (a.rank <= 32) return launch_shrink<2, 1, 3>(a, v, m, C, t, s);
+  if (a.rank <= 64) return launch_shrink<4, 1, 2>(a, v, m, C, t, s);
+  return launch_shrink<8, 1, 2>(a, v, m, C, t, s);
 }
 
 template <int JT>

@@ -39,6 +39,22 @@ __device__ __forceinline__ int wt_logical(int r, int p) {
 }
 __device__ __forceinline__ int wt_off(int r, int col) { return r * 256 + (wt_phys(r, col >> 3) << 3) + (col & 7); }
 
+// The same for slots of BN outputs a row: 256-byte rows (BN = 128) start on
+// the same bank, 128-byte rows (BN = 64) two by two, so the chunk pairs of 4
+// consecutive rows are spread by the row, or by half of it.
+template <int BN>
+__device__ __forceinline__ int wt_phys_n(int r, int c) {
+  return BN == 256 ? wt_phys(r, c) : BN == 128 ? c ^ ((r & 3) << 1) : c ^ (((r >> 1) & 3) << 1);
+}
+template <int BN>
+__device__ __forceinline__ int wt_logical_n(int r, int p) {
+  return BN == 256 ? wt_logical(r, p) : wt_phys_n<BN>(r, p);
+}
+template <int BN>
+__device__ __forceinline__ int wt_off_n(int r, int col) {
+  return r * BN + (wt_phys_n<BN>(r, col >> 3) << 3) + (col & 7);
+}
+
 typedef short v4i16 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
 
@@ -49,12 +65,13 @@ typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
 // lanes a, a+4, a+8 and a+12; source lane L points at row c + L / 4, outputs
 // j + 4 (L % 4) .. +3, so destination lane D holds output j + D at rows
 // c .. c+3.  Two reads give 8 rows.
+template <int BN = 256>
 __device__ __forceinline__ bf16x8 wt_frag(const uint16_t* slot, int j0, int c0, int lane) {
   const int gq = lane >> 4, L = lane & 15;
   const int j = j0 + 16 * (gq & 1) + 4 * (L & 3);
   const int c = c0 + 8 * (gq >> 1) + (L >> 2);
-  const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(slot + wt_off(c, j)));
-  const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(slot + wt_off(c + 4, j)));
+  const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(slot + wt_off_n<BN>(c, j)));
+  const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(slot + wt_off_n<BN>(c + 4, j)));
   const v4i16 v8[2] = {lo, hi};
   return __builtin_bit_cast(bf16x8, v8);
 }
