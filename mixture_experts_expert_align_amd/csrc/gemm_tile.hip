@@ -262,8 +262,12 @@ struct LoraExt {
 // either operand, every 16-byte chunk (8 positions, of one adapter and piece
 // since rank is a multiple of 8) from where it lies or, masked, as zeros.
 // compute(i): multiplies the slice in slots i.
-template <int BM, int BN, int BK, int NW, bool WT, typename Compute>
-__device__ __forceinline__ void lora_slices(const LoraExt& x, const GemmArgs& g, const TileCoord& tc, uint16_t* wslot,
+// ROWS: returns false, with nothing done, for a tile of more than
+// kLoraSliceAdapters adapters.
+constexpr int kLoraSliceAdapters = 8;
+
+template <int BM, int BN, int BK, int NW, bool WT, bool ROWS, typename Compute>
+__device__ __forceinline__ bool lora_slices(const LoraExt& x, const GemmArgs& g, const TileCoord& tc, uint16_t* wslot,
                                             uint16_t* rslot, int* list, Compute compute) {
   constexpr int CH = BK / 8, RPB = 64 / CH, RPW = 256 / (BK * 2) > 0 ? 256 / (BK * 2) : 1;
   constexpr int LW = BN / RPB / NW, LX = BM / RPB / NW;
@@ -304,6 +308,7 @@ __device__ __forceinline__ void lora_slices(const LoraExt& x, const GemmArgs& g,
     if (lane == 0) *count = n;
   }
   lds_barrier();
+  if (ROWS && __builtin_amdgcn_readfirstlane(*count) > kLoraSliceAdapters) return false;
   const int len = __builtin_amdgcn_readfirstlane(*count) * span;
   int mine[LX];   // the list places of the rows this lane loads
 #pragma unroll
@@ -360,6 +365,75 @@ __device__ __forceinline__ void lora_slices(const LoraExt& x, const GemmArgs& g,
     lds_barrier();
     compute(i & 1);
     lds_barrier();
+  }
+  return true;
+}
+
+// The adapters' part of a tile whose rows name many adapters (a decode batch
+// of many requests), where the slices would be mostly zeros: each lane adds
+// to its own outputs, 4 consecutive features at a time, the products of its
+// row's adapter with its row's narrow product (all three pieces).  64 x 64
+// tiles, rank 32, 36 adapters a tile, K = 4096: the tile kernel takes MEASURED.
+template <int TW, int TX, bool WT>
+__device__ __forceinline__ void lora_rows(const LoraExt& x, const GemmArgs& g, const TileCoord& tc, int row0, int col0,
+                                          int lane, f32x16 (&acc)[TW][TX]) {
+  const int rank = x.a.rank;
+#pragma unroll
+  for (int j = 0; j < TX; ++j) {
+    const int m = row0 + 32 * j + (lane & 31);
+    const int ad = m < tc.nvalid ? x.a.adapter[tc.row0 + m] : -1;
+    if (ad < 0 || ad >= x.a.G) continue;
+    const uint16_t* low = x.a.low + (tc.row0 + m) * kLoraPieces * rank;
+    const uint16_t* mg = x.m + (int64_t)ad * rank * g.nfeat;
+    // 32 of the rank at a time (the rest zeros): a lane reads the whole 64
+    // bytes of a row of M_g in a row, while its line is in the L1 cache
+    for (int k0 = 0; k0 < rank; k0 += 32) {
+      float s[32];
+#pragma unroll
+      for (int k = 0; k < 32; k += 8) {
+        i32x4 p[kLoraPieces];
+#pragma unroll
+        for (int c = 0; c < kLoraPieces; ++c)
+          p[c] = k0 + k < rank ? *reinterpret_cast<const i32x4*>(low + c * rank + k0 + k) : (i32x4){0, 0, 0, 0};
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          s[k + u] = 0.f;
+#pragma unroll
+          for (int c = kLoraPieces - 1; c >= 0; --c)
+            s[k + u] += bf16_to_f32(((uint32_t)p[c][u / 2] >> (16 * (u & 1))) & 0xffffu);
+        }
+      }
+      const int kn = min(rank - k0, 32);
+#pragma unroll
+      for (int i = 0; i < TW; ++i)
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const int f = tc.col0 + col0 + 32 * i + 8 * h + 4 * (lane >> 5);
+          if (f >= g.nfeat) continue;
+#pragma unroll
+          for (int k = 0; k < 32; k += 8) {
+            if (k >= kn) break;
+            if (WT) {   // M_g [rank, nfeat]: 4 features of a row at once
+#pragma unroll
+              for (int u = 0; u < 8; ++u) {
+                const uint2 v = *reinterpret_cast<const uint2*>(mg + (int64_t)(k0 + k + u) * g.nfeat + f);
+                acc[i][j][4 * h] += s[k + u] * bf16_to_f32(v.x & 0xffffu);
+                acc[i][j][4 * h + 1] += s[k + u] * bf16_to_f32(v.x >> 16);
+                acc[i][j][4 * h + 2] += s[k + u] * bf16_to_f32(v.y & 0xffffu);
+                acc[i][j][4 * h + 3] += s[k + u] * bf16_to_f32(v.y >> 16);
+              }
+            } else {    // M_g [nfeat, rank]: 8 of a feature's rank at once
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const i32x4 v = *reinterpret_cast<const i32x4*>(mg + (int64_t)(f + r) * rank + k0 + k);
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                  acc[i][j][4 * h + r] += s[k + u] * bf16_to_f32(((uint32_t)v[u / 2] >> (16 * (u & 1))) & 0xffffu);
+              }
+            }
+          }
+        }
+    }
   }
 }
 
@@ -525,14 +599,19 @@ __device__ __forceinline__ void split_tile(const GemmArgs& g, const TileCoord& t
   lds_barrier();
   if constexpr (Ext::kOn) {
     static_assert(BM * 2 + 1 <= WSLOT / 2, "the adapter list fits a slot");
-    lora_slices<BM, BN, BK, NW, WT>(ext, g, tc, wbase, rbase, reinterpret_cast<int*>(wbase + 2 * WSLOT), [&](int k) {
-      if (!live) return;
+    // 64 accumulators a lane and the rows' form do not fit the 128 registers
+    // of the 256 x 256 tiles
+    constexpr bool kRows = BM < 256;
+    const bool done =
+        lora_slices<BM, BN, BK, NW, WT, kRows>(ext, g, tc, wbase, rbase, reinterpret_cast<int*>(wbase + 2 * WSLOT), [&](int k) {
+          if (!live) return;
 #pragma unroll
-      for (int s = 0; s < NSTEP; ++s) {
-        fload(s & 1, k, s);
-        mma(s & 1);
-      }
-    });
+          for (int s = 0; s < NSTEP; ++s) {
+            fload(s & 1, k, s);
+            mma(s & 1);
+          }
+        });
+    if (kRows && !done && live) lora_rows<TW, TX, WT>(ext, g, tc, wm * (BM / WM), wn * (BN / WN), lane, acc);
   }
   static_assert(BM * (EPI == kEpiGateUp ? BN / 2 : BN) <= Ring::Elems, "epilogue tile fits the LDS");
   tile_epilogue<EPI, BM, BN, WN, WM, 64 * WN * WM, TW, TX, ROUTES, Ext::kOn>(g, tc, acc, wn, wm, lane, smem);
