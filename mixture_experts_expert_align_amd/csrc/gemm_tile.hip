@@ -370,40 +370,93 @@ __device__ __forceinline__ bool lora_slices(const LoraExt& x, const GemmArgs& g,
 }
 
 // The adapters' part of a tile whose rows name many adapters (a decode batch
-// of many requests), where the slices would be mostly zeros: each lane adds
-// to its own outputs, 4 consecutive features at a time, the products of its
-// row's adapter with its row's narrow product (all three pieces).  64 x 64
-// tiles, rank 32, 36 adapters a tile, K = 4096: the tile kernel takes MEASURED.
-template <int TW, int TX, bool WT>
-__device__ __forceinline__ void lora_rows(const LoraExt& x, const GemmArgs& g, const TileCoord& tc, int row0, int col0,
-                                          int lane, f32x16 (&acc)[TW][TX]) {
+// of many requests), where the slices would be mostly zeros.  Each wave goes
+// through the adapters of its own 32 rows: M_g straight into the MFMA row
+// operand, the rows' narrow products in the column operand, zeros in the
+// rows of other adapters; kBatch adapters' loads in flight.  64 x 64 tiles,
+// rank 32, 300 rows of 48 adapters, N = K = 4096: the tile kernel takes 47 us
+// with slices, 41 with products lane by lane, 36 like this.
+template <int TW, int TX>
+__device__ __forceinline__ void lora_rows_mfma(const LoraExt& x, const GemmArgs& g, const TileCoord& tc, int row0,
+                                               int col0, int lane, f32x16 (&acc)[TW][TX]) {
+  constexpr int kBatch = 8 / TW;
+  const int rank = x.a.rank, l32 = lane & 31, half = lane >> 5;
+  const __amdgpu_buffer_rsrc_t mr = buffer_rsrc(x.m, (int64_t)x.a.G * g.nfeat * rank * 2);
+  uint32_t fo[TW];   // this lane's feature row, within an adapter's matrix
+#pragma unroll
+  for (int i = 0; i < TW; ++i) {
+    const int f = tc.col0 + col0 + 32 * i + l32;
+    fo[i] = f < g.nfeat ? (uint32_t)(f * rank + 8 * half) * 2u : 0x80000000u;
+  }
+#pragma unroll
+  for (int j = 0; j < TX; ++j) {
+    const int m = row0 + 32 * j + l32;
+    int ad = m >= tc.mlo && m < tc.nvalid ? x.a.adapter[tc.row0 + m] : -1;
+    if (ad >= x.a.G) ad = -1;
+    const uint32_t all = (uint32_t)__ballot(ad >= 0);   // bit r: row r (lanes 0 .. 31)
+    const uint16_t* low = x.a.low + (tc.row0 + (ad >= 0 ? m : 0)) * kLoraPieces * rank;
+    for (int k = 0; k < rank; k += 16) {
+      const bool in = k + 8 * half < rank;
+      i32x4 s[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        s[c] = in && ad >= 0 ? *reinterpret_cast<const i32x4*>(low + c * rank + k + 8 * half) : (i32x4){0, 0, 0, 0};
+      for (uint32_t left = all; left;) {
+        int ga[kBatch];
+        i32x4 w[kBatch][TW];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          ga[u] = left ? __builtin_amdgcn_readlane(ad, __ffs(left) - 1) : -2;
+          left &= ~(uint32_t)__ballot(ad == ga[u]);
+#pragma unroll
+          for (int i = 0; i < TW; ++i)   // no adapter left, or past the rank: zeros
+            w[u][i] = __builtin_amdgcn_raw_buffer_load_b128(
+                mr, ga[u] >= 0 && in ? fo[i] + 2 * k : 0x80000000u, ga[u] >= 0 ? ga[u] * g.nfeat * rank * 2 : 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const bool own = ad == ga[u];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            i32x4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = own ? s[c][e] : 0;
+#pragma unroll
+            for (int i = 0; i < TW; ++i)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(w[u][i]), as_bf16x8(v), acc[i][j], 0, 0, 0);
+          }
+        }
+      }
+    }
+  }
+}
+
+// The same lane by lane, for transposed weights (M_g [rank, nfeat], whose
+// rows are the contraction): each lane adds to its own outputs, 4 consecutive
+// features at a time, the products of its row's adapter with its row's narrow
+// product.
+template <int TW, int TX>
+__device__ __forceinline__ void lora_rows_wt(const LoraExt& x, const GemmArgs& g, const TileCoord& tc, int row0,
+                                             int col0, int lane, f32x16 (&acc)[TW][TX]) {
   const int rank = x.a.rank;
 #pragma unroll
   for (int j = 0; j < TX; ++j) {
     const int m = row0 + 32 * j + (lane & 31);
-    const int ad = m < tc.nvalid ? x.a.adapter[tc.row0 + m] : -1;
+    const int ad = m >= tc.mlo && m < tc.nvalid ? x.a.adapter[tc.row0 + m] : -1;
     if (ad < 0 || ad >= x.a.G) continue;
     const uint16_t* low = x.a.low + (tc.row0 + m) * kLoraPieces * rank;
     const uint16_t* mg = x.m + (int64_t)ad * rank * g.nfeat;
-    // 32 of the rank at a time (the rest zeros): a lane reads the whole 64
-    // bytes of a row of M_g in a row, while its line is in the L1 cache
-    for (int k0 = 0; k0 < rank; k0 += 32) {
-      float s[32];
+    for (int k = 0; k < rank; k += 8) {
+      float s[8];
+      i32x4 p[kLoraPieces];
 #pragma unroll
-      for (int k = 0; k < 32; k += 8) {
-        i32x4 p[kLoraPieces];
+      for (int c = 0; c < kLoraPieces; ++c) p[c] = *reinterpret_cast<const i32x4*>(low + c * rank + k);
 #pragma unroll
-        for (int c = 0; c < kLoraPieces; ++c)
-          p[c] = k0 + k < rank ? *reinterpret_cast<const i32x4*>(low + c * rank + k0 + k) : (i32x4){0, 0, 0, 0};
+      for (int u = 0; u < 8; ++u) {
+        s[u] = 0.f;
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          s[k + u] = 0.f;
-#pragma unroll
-          for (int c = kLoraPieces - 1; c >= 0; --c)
-            s[k + u] += bf16_to_f32(((uint32_t)p[c][u / 2] >> (16 * (u & 1))) & 0xffffu);
-        }
+        for (int c = kLoraPieces - 1; c >= 0; --c) s[u] += bf16_to_f32(((uint32_t)p[c][u / 2] >> (16 * (u & 1))) & 0xffffu);
       }
-      const int kn = min(rank - k0, 32);
 #pragma unroll
       for (int i = 0; i < TW; ++i)
 #pragma unroll
@@ -411,26 +464,12 @@ __device__ __forceinline__ void lora_rows(const LoraExt& x, const GemmArgs& g, c
           const int f = tc.col0 + col0 + 32 * i + 8 * h + 4 * (lane >> 5);
           if (f >= g.nfeat) continue;
 #pragma unroll
-          for (int k = 0; k < 32; k += 8) {
-            if (k >= kn) break;
-            if (WT) {   // M_g [rank, nfeat]: 4 features of a row at once
-#pragma unroll
-              for (int u = 0; u < 8; ++u) {
-                const uint2 v = *reinterpret_cast<const uint2*>(mg + (int64_t)(k0 + k + u) * g.nfeat + f);
-                acc[i][j][4 * h] += s[k + u] * bf16_to_f32(v.x & 0xffffu);
-                acc[i][j][4 * h + 1] += s[k + u] * bf16_to_f32(v.x >> 16);
-                acc[i][j][4 * h + 2] += s[k + u] * bf16_to_f32(v.y & 0xffffu);
-                acc[i][j][4 * h + 3] += s[k + u] * bf16_to_f32(v.y >> 16);
-              }
-            } else {    // M_g [nfeat, rank]: 8 of a feature's rank at once
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const i32x4 v = *reinterpret_cast<const i32x4*>(mg + (int64_t)(f + r) * rank + k0 + k);
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
-                  acc[i][j][4 * h + r] += s[k + u] * bf16_to_f32(((uint32_t)v[u / 2] >> (16 * (u & 1))) & 0xffffu);
-              }
-            }
+          for (int u = 0; u < 8; ++u) {
+            const uint2 v = *reinterpret_cast<const uint2*>(mg + (int64_t)(k + u) * g.nfeat + f);
+            acc[i][j][4 * h] += s[u] * bf16_to_f32(v.x & 0xffffu);
+            acc[i][j][4 * h + 1] += s[u] * bf16_to_f32(v.x >> 16);
+            acc[i][j][4 * h + 2] += s[u] * bf16_to_f32(v.y & 0xffffu);
+            acc[i][j][4 * h + 3] += s[u] * bf16_to_f32(v.y >> 16);
           }
         }
     }
@@ -510,6 +549,9 @@ __device__ __forceinline__ void split_tile(const GemmArgs& g, const TileCoord& t
     const uint16_t* ws = wbase + (kt % WS) * WSLOT;
     const uint16_t* rs = rbase + (kt % RS) * RSLOT;
     const int c = 2 * s + (lane >> 5);
+    if constexpr (WT && Ext::kOn) {
+      wt_frags<BN, TW>(ws, wn * (BN / WN), 16 * s, lane, fw[fb]);
+    } else
 #pragma unroll
     for (int i = 0; i < TW; ++i)
       fw[fb][i] = WT ? wt_frag<BN>(ws, wn * (BN / WN) + 32 * i, 16 * s, lane)
@@ -611,7 +653,12 @@ __device__ __forceinline__ void split_tile(const GemmArgs& g, const TileCoord& t
             mma(s & 1);
           }
         });
-    if (kRows && !done && live) lora_rows<TW, TX, WT>(ext, g, tc, wm * (BM / WM), wn * (BN / WN), lane, acc);
+    if constexpr (kRows) {
+      if (!done && live) {
+        if (WT) lora_rows_wt<TW, TX>(ext, g, tc, wm * (BM / WM), wn * (BN / WN), lane, acc);
+        else lora_rows_mfma<TW, TX>(ext, g, tc, wm * (BM / WM), wn * (BN / WN), lane, acc);
+      }
+    }
   }
   static_assert(BM * (EPI == kEpiGateUp ? BN / 2 : BN) <= Ring::Elems, "epilogue tile fits the LDS");
   tile_epilogue<EPI, BM, BN, WN, WM, 64 * WN * WM, TW, TX, ROUTES, Ext::kOn>(g, tc, acc, wn, wm, lane, smem);

@@ -63,7 +63,9 @@ __device__ __forceinline__ bf16x8 col_frag(const uint16_t* base, int col0, int l
 //   T = false: M = A [rank, C], contraction contiguous;
 //   T = true:  M = B^T, B [C, rank]: a step's 64 rows are read transposed.
 // Each wave has a ring of D steps in LDS to itself, filled by loads that
-// write LDS (no barrier: it waits for its own loads).  That is for the lines:
+// write LDS (no barrier: it waits for its own loads; T: one step in LDS, D on
+// their way in registers, since the compiler waits for every load that writes
+// LDS before a transposing read).  That is for the lines:
 // the MFMA layout wants 16 rows of 64 bytes from a load, which asks the cache
 // for half a line at a time, and a CU got 28 KB/us that way; loads of 8 rows
 // of 128 bytes reach 70.  Chunks are XOR-swizzled so that the 16 rows of a
@@ -78,7 +80,7 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) lora_shrink_kernel(LoraArgs
   // a step: 16 CT rows, then 16 JT rows of A or 64 rows of B, 128 bytes of
   // contraction each (the same size, since rank <= 16 JT)
   constexpr int kStep = (CT + JT) * 1024;         // elements
-  constexpr int kRing = kStep * D + 16;           // a partial last row tile of B reads past it
+  constexpr int kRing = kStep * (T ? 1 : D) + 16;   // a partial last row tile of B reads past it
   constexpr int kLoads = 2 * (CT + JT);           // 1 KB each
   constexpr int kRed = kShrinkWaves * JT * CT * 64 * 16, kRings = kShrinkWaves * kRing * 2;
   static_assert((D - 1) * kLoads < 64, "wait counts");
@@ -140,19 +142,33 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) lora_shrink_kernel(LoraArgs
 #pragma unroll
       for (int c = 0; c < CT; ++c) acc[j][c] = (f32x4){0.f, 0.f, 0.f, 0.f};
     const int n = (C / 64 - wave + kShrinkWaves - 1) / kShrinkWaves;
+    i32x4 reg[T ? D : 1][T ? kLoads : 1];
     auto load = [&](int d, int i) {   // past the end: zeros
       const int k0 = 64 * (wave + kShrinkWaves * i);
       const bool in = i < n;
       uint16_t* s = ring + d * kStep;
 #pragma unroll
-      for (int l = 0; l < 2 * CT; ++l) lds_load16(vr, s + 512 * l, in ? vo[l] : kPast, 2 * k0);
+      for (int l = 0; l < 2 * CT; ++l) {
+        if constexpr (T) reg[d][l] = __builtin_amdgcn_raw_buffer_load_b128(vr, in ? vo[l] : kPast, 2 * k0, 0);
+        else lds_load16(vr, s + 512 * l, in ? vo[l] : kPast, 2 * k0);
+      }
 #pragma unroll
-      for (int l = 0; l < 2 * JT; ++l)
-        lds_load16(mr, s + CT * 1024 + 512 * l, in ? mo[l] : kPast, T ? 2 * k0 * rank : 2 * k0);
+      for (int l = 0; l < 2 * JT; ++l) {
+        if constexpr (T)
+          reg[d][2 * CT + l] = __builtin_amdgcn_raw_buffer_load_b128(mr, in ? mo[l] : kPast, 2 * k0 * rank, 0);
+        else
+          lds_load16(mr, s + CT * 1024 + 512 * l, in ? mo[l] : kPast, 2 * k0);
+      }
       issue_order();
     };
     auto mma = [&](int d) {
-      const uint16_t* s = ring + d * kStep;
+      if constexpr (T) {
+        __builtin_amdgcn_wave_barrier();   // the last step's reads come first
+#pragma unroll
+        for (int l = 0; l < kLoads; ++l) *reinterpret_cast<i32x4*>(ring + 512 * l + 8 * lane) = reg[d][l];
+        __builtin_amdgcn_wave_barrier();
+      }
+      const uint16_t* s = ring + (T ? 0 : d) * kStep;
       const uint16_t* sm = s + CT * 1024;
       auto frag = [&](const uint16_t* p, int t, int h) {   // 16 rows from 16 t, 32 of the step's contraction
         return as_bf16x8(*reinterpret_cast<const i32x4*>(p + (16 * t + l16) * 64 + 8 * ((4 * h + q) ^ ((l16 >> 1) & 7))));
@@ -177,7 +193,7 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) lora_shrink_kernel(LoraArgs
     for (int it = 0; it < n; it += D)
 #pragma unroll
       for (int d = 0; d < D; ++d) {
-        wait_vm<(D - 1) * kLoads>();
+        if constexpr (!T) wait_vm<(D - 1) * kLoads>();
         mma(d);
         load(d, it + d + D);
       }
@@ -289,89 +305,124 @@ __global__ void __launch_bounds__(64 * kStreamWaves) lora_stream_kernel(LoraArgs
 
 // ----------------------------------------------------------------- wgrad --
 // One workgroup: one adapter, 256 columns of x (for dA) or of dy (for dB) and
-// a share of the adapter's rows, taken from the rows sorted by adapter.  64
-// rows at a time are staged in LDS (the columns through the transposed slot
-// layout of the tiles, the pieces of t or s beside them) and both operands
-// are read transposed, the rows being the contraction; the three pieces add
-// into the same accumulators.  With more than one share the sums go to the
-// workspace and a second launch adds them in order.
-constexpr int kWgCols = 256, kWgRows = 64, kWgWaves = 8;
+// a share of the adapter's rows, taken from the rows sorted by adapter.  32
+// rows at a time go through LDS, the next 64 on their way in registers: the
+// columns (512 bytes a row, swizzled) and the pieces of t or s beside them;
+// both operands are read transposed, the rows being the contraction, and the
+// three pieces add into the same accumulators.  A wave owns 64 columns: with
+// 32 the pieces' fragments, which every wave reads, were most of the LDS
+// traffic.  (Through registers, not by loads that write LDS: the compiler
+// waits for all of those before a transposing read, 88 us instead of MEASURED
+// at 8192 rows, K = 6144, N = 4096, 4 adapters of rank 64.)  With more than
+// one share the sums go to the workspace and a second launch adds them in
+// order.
+constexpr int kWgCols = 256, kWgRows = 32, kWgWaves = 4, kWgList = 1024;
 
-template <int JT>
-__global__ void __launch_bounds__(64 * kWgWaves) lora_wgrad_kernel(LoraGradArgs a) {
-  extern __shared__ __attribute__((aligned(1024))) uint16_t s_ext[];
-  uint16_t* const cols = s_ext;                         // [64][256] swizzled
-  uint16_t* const low = s_ext + kWgRows * kWgCols;      // [64][3 rank]
-  const int lane = threadIdx.x & 63, q = lane >> 4, l16 = lane & 15;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+// chunk c of row r: 4 consecutive rows on distinct chunk pairs, rows 8 apart
+// on opposite halves of the banks (its own inverse)
+__device__ __forceinline__ int wg_chunk(int r, int c) { return c ^ ((r & 3) << 1) ^ (((r >> 3) & 1) << 3); }
+
+template <int JT, bool IS_A>
+__device__ __forceinline__ void wgrad_tile(const LoraGradArgs& a, int c0, uint16_t* smem, int32_t* list) {
+  constexpr int NT = 64 * kWgWaves;
+  constexpr int kColLoads = kWgRows * kWgCols / 8 / NT;                // 16-byte chunks a thread
+  constexpr int kLowLoads = (kWgRows * 6 * JT + NT - 1) / NT;          // 32 rows of 3 rank <= 48 JT
+  constexpr int kCols = kWgRows * kWgCols, kBuf = kCols + kLowLoads * NT * 8;   // elements
+  constexpr int D = 2;                                                 // stages on their way
+  const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, l16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = blockIdx.y;
-  const int kt = (a.K + kWgCols - 1) / kWgCols;
-  const bool is_a = (int)blockIdx.x < kt;
-  const int c0 = (is_a ? blockIdx.x : blockIdx.x - kt) * kWgCols;
-  const int C = is_a ? a.K : a.N;
-  const uint16_t* v = is_a ? a.x : a.dy;
-  const uint16_t* lo = is_a ? a.low_dy : a.low_x;
-  const int rank = a.rank, pr = kPieces * rank;
+  const int C = IS_A ? a.K : a.N;
+  const int rank = a.rank, pr = kPieces * rank, cpr = pr / 8;   // chunks of a row of low
   const int cnt = a.counts[g];
   const int32_t* rows = a.sorted + a.offsets[g];
   const int i0 = (int)((int64_t)cnt * blockIdx.z / gridDim.z), i1 = (int)((int64_t)cnt * (blockIdx.z + 1) / gridDim.z);
-  const __amdgpu_buffer_rsrc_t vr = buffer_rsrc(v, a.R * C * 2);
-  const __amdgpu_buffer_rsrc_t lr = buffer_rsrc(lo, a.R * pr * 2);
-  f32x4 acc[JT][2];
+  const __amdgpu_buffer_rsrc_t vr = buffer_rsrc(IS_A ? a.x : a.dy, a.R * C * 2);
+  const __amdgpu_buffer_rsrc_t lr = buffer_rsrc(IS_A ? a.low_dy : a.low_x, a.R * pr * 2);
+  const int ccol = c0 + 8 * (tid & 31);
+  int lrow[kLowLoads], lcol[kLowLoads];   // (row, chunk) of this thread's pieces of low
+#pragma unroll
+  for (int b = 0; b < kLowLoads; ++b) {
+    lrow[b] = (tid + NT * b) / cpr;
+    lcol[b] = tid + NT * b - lrow[b] * cpr;
+  }
+  f32x4 acc[JT][4];
 #pragma unroll
   for (int j = 0; j < JT; ++j)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) acc[j][h] = (f32x4){0.f, 0.f, 0.f, 0.f};
-  const int cpr = pr / 8;                               // 16-byte pieces of a row of low
-  for (int i = i0; i < i1; i += kWgRows) {
-    // columns: a load fills two rows of 512 bytes
+    for (int h = 0; h < 4; ++h) acc[j][h] = (f32x4){0.f, 0.f, 0.f, 0.f};
+
+  for (int base = i0; base < i1; base += kWgList) {
+    const int m = min(kWgList, i1 - base);   // rows of this part of the list
+    for (int i = tid; i < m; i += NT) list[i] = rows[base + i];
+    __syncthreads();
+    i32x4 vc[D][kColLoads], vl[D][kLowLoads];
+    auto load = [&](int d, int st) {   // past the end: zeros
 #pragma unroll
-    for (int b = 0; b < kWgRows / 2 / kWgWaves; ++b) {
-      const int r = 2 * (wave + kWgWaves * b) + lane / 32;
-      const int c = c0 + 8 * tile::wt_logical(r, lane % 32);
-      const uint32_t o = i + r < i1 && c < C ? (uint32_t)((int64_t)rows[i + r] * C + c) * 2u : kPast;
-      lds_load16(vr, cols + (wave + kWgWaves * b) * 512, o, 0);
-    }
-    for (int b = wave; b < kWgRows * cpr / 64; b += kWgWaves) {
-      const int e = 64 * b + lane, r = e / cpr;
-      const uint32_t o = i + r < i1 ? (uint32_t)(((int64_t)rows[i + r] * cpr + e % cpr) * 16) : kPast;
-      lds_load16(lr, low + b * 512, o, 0);
-    }
-    wait_vm<0>();
-    lds_barrier();
+      for (int b = 0; b < kColLoads; ++b) {
+        const int i = st * kWgRows + (tid >> 5) + NT / 32 * b;
+        vc[d][b] = __builtin_amdgcn_raw_buffer_load_b128(
+            vr, i < m && ccol < C ? (uint32_t)(list[min(i, m - 1)] * C + ccol) * 2u : kPast, 0, 0);
+      }
 #pragma unroll
-    for (int s = 0; s < kWgRows / 32; ++s) {
-      bf16x8 f[2];
+      for (int b = 0; b < kLowLoads; ++b) {
+        const int i = st * kWgRows + lrow[b];
+        vl[d][b] = __builtin_amdgcn_raw_buffer_load_b128(
+            lr, lrow[b] < kWgRows && i < m ? (uint32_t)(list[min(i, m - 1)] * cpr + lcol[b]) * 16u : kPast, 0, 0);
+      }
+      issue_order();
+    };
+    const int ns = (m + kWgRows - 1) / kWgRows;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        f[h] = col_frag(cols, 32 * wave + 16 * h, lane,
-                        [&](int r, int c) { return tile::wt_off(32 * s + r, c); });
+    for (int d = 0; d < D; ++d) load(d, d);
+    for (int it = 0; it < ns; it += D) {
 #pragma unroll
-      for (int p = 0; p < kPieces; ++p)
+      for (int d = 0; d < D; ++d) {
+        uint16_t* cols = smem + (d & 1) * kBuf;
+        uint16_t* low = cols + kCols;
 #pragma unroll
-        for (int j = 0; j < JT; ++j) {
-          const bf16x8 t = col_frag(low, p * rank + 16 * j, lane, [&](int r, int c) { return (32 * s + r) * pr + c; });
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            acc[j][h] = is_a ? __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[h], t, acc[j][h], 0, 0, 0)
-                             : __builtin_amdgcn_mfma_f32_16x16x32_bf16(t, f[h], acc[j][h], 0, 0, 0);
+        for (int b = 0; b < kColLoads; ++b) {
+          const int r = (tid >> 5) + NT / 32 * b;
+          *reinterpret_cast<i32x4*>(cols + r * kWgCols + 8 * wg_chunk(r, tid & 31)) = vc[d][b];
         }
+#pragma unroll
+        for (int b = 0; b < kLowLoads; ++b) *reinterpret_cast<i32x4*>(low + 8 * (tid + NT * b)) = vl[d][b];
+        issue_order();
+        load(d, it + d + D);
+        // one barrier a stage: the other buffer's readers have passed it
+        lds_barrier();
+        bf16x8 f[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+          f[h] = col_frag(cols, 64 * wave + 16 * h, lane,
+                          [&](int r, int c) { return r * kWgCols + 8 * wg_chunk(r, c >> 3) + (c & 7); });
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p)
+#pragma unroll
+          for (int j = 0; j < JT; ++j) {
+            const bf16x8 t = col_frag(low, p * rank + 16 * j, lane, [&](int r, int c) { return r * pr + c; });
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+              acc[j][h] = IS_A ? __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[h], t, acc[j][h], 0, 0, 0)
+                               : __builtin_amdgcn_mfma_f32_16x16x32_bf16(t, f[h], acc[j][h], 0, 0, 0);
+          }
+      }
     }
-    lds_barrier();
+    lds_barrier();   // the list and the buffers are read
   }
   // dA [G, rank, K]: lane: output 16 j + l16, columns 4 q ..; dB [G, N, rank]:
   // lane: column l16, outputs 16 j + 4 q ..
   const int64_t na = (int64_t)a.G * rank * a.K, nb = (int64_t)a.G * rank * a.N;
-  float* out = gridDim.z > 1 ? a.part + blockIdx.z * (na + nb) + (is_a ? 0 : na) : is_a ? a.da : a.db;
+  float* out = gridDim.z > 1 ? a.part + blockIdx.z * (na + nb) + (IS_A ? 0 : na) : IS_A ? a.da : a.db;
   const bool add = gridDim.z == 1 && a.accumulate;
 #pragma unroll
   for (int j = 0; j < JT; ++j)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int col = c0 + 32 * wave + 16 * h + (is_a ? 4 * q : l16);
-      const int o = 16 * j + (is_a ? l16 : 4 * q);
+    for (int h = 0; h < 4; ++h) {
+      const int col = c0 + 64 * wave + 16 * h + (IS_A ? 4 * q : l16);
+      const int o = 16 * j + (IS_A ? l16 : 4 * q);
       if (col >= C || o >= rank) continue;
-      f32x4* dst = reinterpret_cast<f32x4*>(out + (is_a ? ((int64_t)g * rank + o) * a.K + col
+      f32x4* dst = reinterpret_cast<f32x4*>(out + (IS_A ? ((int64_t)g * rank + o) * a.K + col
                                                         : ((int64_t)g * a.N + col) * rank + o));
       f32x4 r = acc[j][h];
       if (add) {
@@ -381,6 +432,16 @@ __global__ void __launch_bounds__(64 * kWgWaves) lora_wgrad_kernel(LoraGradArgs 
       }
       *dst = r;
     }
+}
+
+template <int JT>
+__global__ void __launch_bounds__(64 * kWgWaves) lora_wgrad_kernel(LoraGradArgs a) {
+  constexpr int NT = 64 * kWgWaves;
+  __shared__ __attribute__((aligned(16))) uint16_t smem[2 * (kWgRows * kWgCols + (kWgRows * 6 * JT + NT - 1) / NT * NT * 8)];
+  __shared__ int32_t list[kWgList];
+  const int kt = (a.K + kWgCols - 1) / kWgCols;
+  if ((int)blockIdx.x < kt) wgrad_tile<JT, true>(a, blockIdx.x * kWgCols, smem, list);
+  else wgrad_tile<JT, false>(a, (blockIdx.x - kt) * kWgCols, smem, list);
 }
 
 // dA and dB from the shares' sums, four values a thread.
@@ -426,17 +487,6 @@ hipError_t shrink(const LoraArgs& a, const uint16_t* v, const uint16_t* m, int C
   return launch_shrink<8, 1, 2>(a, v, m, C, t, s);
 }
 
-template <int JT>
-hipError_t launch_wgrad(const LoraGradArgs& a, dim3 grid, size_t lds, hipStream_t s) {
-  if (lds > 64 * 1024) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&lora_wgrad_kernel<JT>),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    if (e != hipSuccess) return e;
-  }
-  hipLaunchKernelGGL((lora_wgrad_kernel<JT>), grid, dim3(64 * kWgWaves), lds, s, a);
-  return hipGetLastError();
-}
-
 }  // namespace
 
 hipError_t launch_lora_forward(const LoraArgs& a, const uint16_t* x, const uint16_t* w, const uint16_t* am,
@@ -465,8 +515,8 @@ hipError_t launch_lora_dgrad(const LoraArgs& a, const uint16_t* dy, const uint16
 
 int32_t lora_wgrad_shares(int64_t R, int64_t N, int64_t K, int64_t G) {
   const int64_t wgs = G * ((K + kWgCols - 1) / kWgCols + (N + kWgCols - 1) / kWgCols);
-  int64_t n = (512 + wgs - 1) / wgs;                  // two workgroups per CU
-  const int64_t most = (R + 4 * kWgRows - 1) / (4 * kWgRows);
+  int64_t n = 512 / wgs;                              // at most two workgroups per CU
+  const int64_t most = (R + 255) / 256;
   if (n > most) n = most;
   return (int32_t)(n < 1 ? 1 : n > 16 ? 16 : n);
 }
@@ -474,12 +524,12 @@ int32_t lora_wgrad_shares(int64_t R, int64_t N, int64_t K, int64_t G) {
 hipError_t launch_lora_wgrad(const LoraGradArgs& a, int32_t shares, hipStream_t s) {
   const dim3 grid((unsigned)((a.K + kWgCols - 1) / kWgCols + (a.N + kWgCols - 1) / kWgCols), (unsigned)a.G,
                   (unsigned)shares);
-  // the transposed reads of a partial last tile of outputs run past a row
-  const size_t lds = 2 * (kWgRows * kWgCols + kWgRows * kPieces * a.rank + 16);
-  hipError_t e = a.rank <= 16   ? launch_wgrad<1>(a, grid, lds, s)
-                 : a.rank <= 32 ? launch_wgrad<2>(a, grid, lds, s)
-                 : a.rank <= 64 ? launch_wgrad<4>(a, grid, lds, s)
-                                : launch_wgrad<8>(a, grid, lds, s);
+  const dim3 block(64 * kWgWaves);
+  if (a.rank <= 16) hipLaunchKernelGGL((lora_wgrad_kernel<1>), grid, block, 0, s, a);
+  else if (a.rank <= 32) hipLaunchKernelGGL((lora_wgrad_kernel<2>), grid, block, 0, s, a);
+  else if (a.rank <= 64) hipLaunchKernelGGL((lora_wgrad_kernel<4>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((lora_wgrad_kernel<8>), grid, block, 0, s, a);
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess || shares == 1) return e;
   const int64_t n = (int64_t)a.G * a.rank * (a.K + a.N) / 4;
   hipLaunchKernelGGL(lora_wgrad_join_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a, shares);

@@ -76,6 +76,41 @@ __device__ __forceinline__ bf16x8 wt_frag(const uint16_t* slot, int j0, int c0, 
   return __builtin_bit_cast(bf16x8, v8);
 }
 
+// wt_frag of the tiles j0 and j0 + 32 with the reads, and the wait for them, in
+// one asm statement: before the transposing-read builtin the compiler waits
+// for every load in flight that writes LDS (vmcnt 0), which takes the staging
+// ring's prefetch away.  The caller has waited for the slice, with a barrier.
+template <int BN, int TW>
+__device__ __forceinline__ void wt_frags(const uint16_t* slot, int j0, int c0, int lane, bf16x8 (&f)[TW]) {
+  static_assert(TW == 1 || TW == 2, "one or two tiles");
+  const int gq = lane >> 4, L = lane & 15;
+  const int c = c0 + 8 * (gq >> 1) + (L >> 2);
+  uint32_t a[2 * TW];
+  v4i16 v[2 * TW];
+#pragma unroll
+  for (int i = 0; i < TW; ++i) {
+    const int j = j0 + 32 * i + 16 * (gq & 1) + 4 * (L & 3);
+    a[2 * i] = (uint32_t)(uintptr_t)(lds_v4i16*)(slot + wt_off_n<BN>(c, j));
+    a[2 * i + 1] = (uint32_t)(uintptr_t)(lds_v4i16*)(slot + wt_off_n<BN>(c + 4, j));
+  }
+  if constexpr (TW == 1)
+    asm volatile("ds_read_b64_tr_b16 %0, %2\n\tds_read_b64_tr_b16 %1, %3\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&v"(v[0]), "=&v"(v[1])
+                 : "v"(a[0]), "v"(a[1])
+                 : "memory");
+  else
+    asm volatile("ds_read_b64_tr_b16 %0, %4\n\tds_read_b64_tr_b16 %1, %5\n\tds_read_b64_tr_b16 %2, %6\n\t"
+                 "ds_read_b64_tr_b16 %3, %7\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2 * TW - 2]), "=&v"(v[2 * TW - 1])
+                 : "v"(a[0]), "v"(a[1]), "v"(a[2 * TW - 2]), "v"(a[2 * TW - 1])
+                 : "memory");
+#pragma unroll
+  for (int i = 0; i < TW; ++i) {
+    const v4i16 v8[2] = {v[2 * i], v[2 * i + 1]};
+    f[i] = __builtin_bit_cast(bf16x8, v8);
+  }
+}
+
 // Workgroup -> (expert, first weight row, first route row).
 struct TileCoord {
   int expert, col0;
