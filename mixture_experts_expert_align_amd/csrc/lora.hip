@@ -54,6 +54,15 @@ __device__ __forceinline__ bf16x8 col_frag(const uint16_t* base, int col0, int l
   return __builtin_bit_cast(bf16x8, v8);
 }
 
+// Blocks that are read transposed (rows of `chunks` 16-byte chunks): rows lie
+// an odd multiple of 128 bytes apart, chunk pairs XORed by the row, so that a
+// read's 4 consecutive rows and its lane groups' rows 8 apart fall on
+// different banks.  Pitch and position in chunks.
+__host__ __device__ constexpr int tr_pitch(int chunks) { return ((chunks + 7) / 8 | 1) * 8; }
+__device__ __forceinline__ int tr_at(int r, int c, int pitch) {
+  return r * pitch + (c ^ (((r & 3) ^ ((r >> 3) & 1)) << 1));
+}
+
 // ---------------------------------------------------------------- shrink --
 // low[r] = scale_g M_g v_r for 16 CT rows a workgroup: the rows in the MFMA
 // column operand, 16 of the rank's outputs per row tile (JT tiles), the
@@ -77,10 +86,10 @@ constexpr int kShrinkWaves = 4;
 template <int JT, int CT, bool T, int D>
 __global__ void __launch_bounds__(64 * kShrinkWaves) lora_shrink_kernel(LoraArgs a, const uint16_t* __restrict__ v,
                                                                        const uint16_t* __restrict__ m, int C) {
-  // a step: 16 CT rows, then 16 JT rows of A or 64 rows of B, 128 bytes of
-  // contraction each (the same size, since rank <= 16 JT)
-  constexpr int kStep = (CT + JT) * 1024;         // elements
-  constexpr int kRing = kStep * (T ? 1 : D) + 16;   // a partial last row tile of B reads past it
+  // a step: 16 CT rows, then 16 JT rows of A, of 128 bytes of contraction
+  // each, or 64 rows of B (rank <= 16 JT)
+  constexpr int kStep = CT * 1024 + (T ? 64 * 8 * tr_pitch(2 * JT) : JT * 1024);   // elements
+  constexpr int kRing = kStep * (T ? 1 : D);
   constexpr int kLoads = 2 * (CT + JT);           // 1 KB each
   constexpr int kRed = kShrinkWaves * JT * CT * 64 * 16, kRings = kShrinkWaves * kRing * 2;
   static_assert((D - 1) * kLoads < 64, "wait counts");
@@ -136,6 +145,15 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) lora_shrink_kernel(LoraArgs
       mo[i] = T ? (e < 8 * rank ? 16 * e : kPast)
                 : (16 * j0 + r < rank ? (uint32_t)((16 * j0 + r) * C * 2 + chunk(r)) : kPast);
     }
+    constexpr int kPitch = tr_pitch(2 * JT);
+    int bo[T ? 2 * JT : 1];   // where this lane's chunks of B go
+    if (T) {
+#pragma unroll
+      for (int i = 0; i < 2 * JT; ++i) {
+        const int e = min(64 * i + lane, 8 * rank - 1), r = e / (rank / 8);
+        bo[i] = tr_at(r, e - r * (rank / 8), kPitch);
+      }
+    }
     f32x4 acc[JT][CT];
 #pragma unroll
     for (int j = 0; j < JT; ++j)
@@ -165,7 +183,10 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) lora_shrink_kernel(LoraArgs
       if constexpr (T) {
         __builtin_amdgcn_wave_barrier();   // the last step's reads come first
 #pragma unroll
-        for (int l = 0; l < kLoads; ++l) *reinterpret_cast<i32x4*>(ring + 512 * l + 8 * lane) = reg[d][l];
+        for (int l = 0; l < 2 * CT; ++l) *reinterpret_cast<i32x4*>(ring + 512 * l + 8 * lane) = reg[d][l];
+#pragma unroll
+        for (int l = 0; l < 2 * JT; ++l)
+          if (64 * l + lane < 8 * rank) *reinterpret_cast<i32x4*>(ring + CT * 1024 + 8 * bo[l]) = reg[d][2 * CT + l];
         __builtin_amdgcn_wave_barrier();
       }
       const uint16_t* s = ring + (T ? 0 : d) * kStep;
@@ -180,7 +201,8 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) lora_shrink_kernel(LoraArgs
         for (int c = 0; c < CT; ++c) x[c] = frag(s, c, h);
 #pragma unroll
         for (int j = 0; j < JT; ++j) {
-          const bf16x8 w = T ? col_frag(sm, 16 * j, lane, [&](int r, int c) { return (32 * h + r) * rank + c; })
+          const bf16x8 w = T ? col_frag(sm, 16 * j, lane,
+                                        [&](int r, int c) { return 8 * tr_at(32 * h + r, c >> 3, kPitch) + (c & 7); })
                              : frag(sm, j, h);
 #pragma unroll
           for (int c = 0; c < CT; ++c) acc[j][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x[c], acc[j][c], 0, 0, 0);
@@ -327,7 +349,8 @@ __device__ __forceinline__ void wgrad_tile(const LoraGradArgs& a, int c0, uint16
   constexpr int NT = 64 * kWgWaves;
   constexpr int kColLoads = kWgRows * kWgCols / 8 / NT;                // 16-byte chunks a thread
   constexpr int kLowLoads = (kWgRows * 6 * JT + NT - 1) / NT;          // 32 rows of 3 rank <= 48 JT
-  constexpr int kCols = kWgRows * kWgCols, kBuf = kCols + kLowLoads * NT * 8;   // elements
+  constexpr int kPitch = tr_pitch(6 * JT);                             // chunks
+  constexpr int kCols = kWgRows * kWgCols, kBuf = kCols + kWgRows * 8 * kPitch;   // elements
   constexpr int D = 2;                                                 // stages on their way
   const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, l16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -386,7 +409,8 @@ __device__ __forceinline__ void wgrad_tile(const LoraGradArgs& a, int c0, uint16
           *reinterpret_cast<i32x4*>(cols + r * kWgCols + 8 * wg_chunk(r, tid & 31)) = vc[d][b];
         }
 #pragma unroll
-        for (int b = 0; b < kLowLoads; ++b) *reinterpret_cast<i32x4*>(low + 8 * (tid + NT * b)) = vl[d][b];
+        for (int b = 0; b < kLowLoads; ++b)
+          if (lrow[b] < kWgRows) *reinterpret_cast<i32x4*>(low + 8 * tr_at(lrow[b], lcol[b], kPitch)) = vl[d][b];
         issue_order();
         load(d, it + d + D);
         // one barrier a stage: the other buffer's readers have passed it
@@ -400,7 +424,8 @@ __device__ __forceinline__ void wgrad_tile(const LoraGradArgs& a, int c0, uint16
         for (int p = 0; p < kPieces; ++p)
 #pragma unroll
           for (int j = 0; j < JT; ++j) {
-            const bf16x8 t = col_frag(low, p * rank + 16 * j, lane, [&](int r, int c) { return r * pr + c; });
+            const bf16x8 t = col_frag(low, p * rank + 16 * j, lane,
+                                      [&](int r, int c) { return 8 * tr_at(r, c >> 3, kPitch) + (c & 7); });
 #pragma unroll
             for (int h = 0; h < 4; ++h)
               acc[j][h] = IS_A ? __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[h], t, acc[j][h], 0, 0, 0)
@@ -436,8 +461,7 @@ __device__ __forceinline__ void wgrad_tile(const LoraGradArgs& a, int c0, uint16
 
 template <int JT>
 __global__ void __launch_bounds__(64 * kWgWaves) lora_wgrad_kernel(LoraGradArgs a) {
-  constexpr int NT = 64 * kWgWaves;
-  __shared__ __attribute__((aligned(16))) uint16_t smem[2 * (kWgRows * kWgCols + (kWgRows * 6 * JT + NT - 1) / NT * NT * 8)];
+  __shared__ __attribute__((aligned(16))) uint16_t smem[2 * (kWgRows * kWgCols + kWgRows * 8 * tr_pitch(6 * JT))];
   __shared__ int32_t list[kWgList];
   const int kt = (a.K + kWgCols - 1) / kWgCols;
   if ((int)blockIdx.x < kt) wgrad_tile<JT, true>(a, blockIdx.x * kWgCols, smem, list);
