@@ -85,8 +85,8 @@ __device__ __forceinline__ int phase_thread() {
 // The weight rows are read in pieces of 16 bytes a lane: 32 of the contraction
 // for bf16 (lane group q holds k = 8 q .. +7), 64 for MXFP8 (k = 16 q .. +15,
 // all of one 32-wide block), P pieces a step, D steps in flight; the
-// activations of CT column tiles come along in the same order of k (CT = 0:
-// they are in LDS).  NT: row tiles that share the activations (gate and up).
+// activations of CT column tiles come along in the same order of k.  NT: row
+// tiles that share the activations (gate and up).
 // Steps past the end are loaded from past the buffers, as zeros: every load in
 // the loop is unconditional, so the waits count exactly the loads they need.
 //
@@ -100,7 +100,7 @@ __device__ __forceinline__ int phase_thread() {
 template <bool MX, int NT, int CT, int P>
 struct Step {
   i32x4 w[NT][P];
-  i32x4 a[CT ? CT : 1][P][MX ? 2 : 1];
+  i32x4 a[CT][P][MX ? 2 : 1];
 };
 
 template <bool MX>
@@ -131,7 +131,7 @@ __device__ __forceinline__ uint32_t lane_a(int64_t row, int64_t ld, int q) {
 // Step `step` of the rows, or zeros when !in.
 template <bool MX, int NT, int CT, int P>
 __device__ __forceinline__ void load_step(Step<MX, NT, CT, P>& f, const Weights<MX>& wr, __amdgpu_buffer_rsrc_t ar,
-                                          const uint32_t (&wo)[NT], const uint32_t (&ao)[CT ? CT : 1], int step,
+                                          const uint32_t (&wo)[NT], const uint32_t (&ao)[CT], int step,
                                           bool in) {
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -167,12 +167,11 @@ __device__ __forceinline__ bf16x8 widen(const i32x4& w, uint32_t s, int h) {
   return __builtin_bit_cast(bf16x8, v);
 }
 
-// acc += the nb 128-wide blocks b0, b0 + stride, ... of the rows.  act(i, j):
-// with CT = 0, the activations of MFMA j (of 4) of the i-th block.
-template <bool MX, int NT, int CT, int P, int D, typename Act>
+// acc += the nb 128-wide blocks b0, b0 + stride, ... of the rows.
+template <bool MX, int NT, int CT, int P, int D>
 __device__ __forceinline__ void stream_rows(const Weights<MX>& wr, __amdgpu_buffer_rsrc_t ar, const uint32_t (&wo)[NT],
-                                            const uint32_t (&so)[NT], const uint32_t (&ao)[CT ? CT : 1], int b0,
-                                            int stride, int nb, f32x4 (&acc)[NT][CT ? CT : 1], Act act) {
+                                            const uint32_t (&so)[NT], const uint32_t (&ao)[CT], int b0,
+                                            int stride, int nb, f32x4 (&acc)[NT][CT]) {
   constexpr int kPer = 128 / (P * (MX ? 64 : 32));   // steps of a block
   const int lane = threadIdx.x & 63, q = lane >> 4, l16 = lane & 15;
   const int n = nb * kPer;
@@ -185,14 +184,12 @@ __device__ __forceinline__ void stream_rows(const Weights<MX>& wr, __amdgpu_buff
     for (int p = 0; p < P; ++p)
 #pragma unroll
       for (int h = 0; h < (MX ? 2 : 1); ++h) {
-        bf16x8 x;
-        if (CT == 0) x = act(min(i, n - 1) / kPer, (MX ? 2 : 1) * (i % kPer * P + p) + h);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           const bf16x8 w = MX ? widen(f.w[t][p], sw[t] >> (16 * (i % kPer * P + p)), h) : as_bf16x8(f.w[t][p]);
 #pragma unroll
-          for (int c = 0; c < (CT ? CT : 1); ++c)
-            acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, CT ? as_bf16x8(f.a[c][p][h]) : x, acc[t][c], 0, 0, 0);
+          for (int c = 0; c < CT; ++c)
+            acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, as_bf16x8(f.a[c][p][h]), acc[t][c], 0, 0, 0);
         }
       }
     issue_order();
@@ -246,44 +243,114 @@ __device__ __forceinline__ void stream_rows(const Weights<MX>& wr, __amdgpu_buff
       }
   }
 }
-template <bool MX, int NT, int CT, int P, int D>
-__device__ __forceinline__ void stream_rows(const Weights<MX>& wr, __amdgpu_buffer_rsrc_t ar, const uint32_t (&wo)[NT],
-                                            const uint32_t (&so)[NT], const uint32_t (&ao)[CT], int b0, int stride,
-                                            int nb, f32x4 (&acc)[NT][CT]) {
-  stream_rows<MX, NT, CT, P, D>(wr, ar, wo, so, ao, b0, stride, nb, acc, [](int, int) { return bf16x8{}; });
+// ------------------------------------------------------------- whole lines --
+// Up to 8 tokens.  The form above asks the cache for 16 rows of 64 bytes a
+// load, half a line each, and a CU gets 28 KB/us of such requests, little more
+// than its share of the memory bandwidth and less with the activations'.
+// Here a load covers 8 rows of 128 bytes: row slots 2 r and 2 r + 1 of the
+// MFMA both stand for row r, the even one for the first half of each line (4
+// chunks of 16 bytes, one per lane group), the odd one for the second; column
+// c holds token c at the first half's contraction, column c + 8 at the
+// second's.  Of the products, (even slot, column < 8) and (odd slot, column
+// >= 8) are wanted, and a row's sum is the two together; the rest is not
+// used.  As many matrix instructions per byte of weights as before, and half
+// the activation loads.
+// NR: groups of 8 rows (they share the activations).
+template <bool MX, int NR>
+struct LineStep {
+  i32x4 w[NR][MX ? 1 : 2];   // bf16: two lines of a 128-wide block; MXFP8: one
+  i32x4 a[2];
+};
+// A lane's first byte: of row r of a group (its slot's row is l16 / 2), of
+// the activations (row: of token l16 % 8).
+template <bool MX>
+__device__ __forceinline__ uint32_t line_w(int64_t row, int64_t ld, int l16, int q) {
+  return (uint32_t)(row * ld * (MX ? 1 : 2) + 64 * (l16 & 1) + 16 * q);
+}
+template <bool MX>
+__device__ __forceinline__ uint32_t line_a(int64_t row, int64_t ld, int l16, int q) {
+  return (uint32_t)(row * ld * 2 + (MX ? 2 : 1) * (64 * (l16 >> 3) + 16 * q));
 }
 
-// The same with the activations of up to 16 tokens in LDS (stage_rows): only
-// the weights go through the vector memory path, one load per KB of them.
-// With a few tokens in the 16 columns, activations read by every step as MFMA
-// operands cost as many load instructions as half the weights.
-template <bool MX, int NT, int P, int D>
-__device__ __forceinline__ void stream_rows_lds(const Weights<MX>& wr, const uint32_t (&wo)[NT],
-                                                const uint32_t (&so)[NT], const char* stage, int quads, int tok, int b0,
-                                                int stride, int nb, f32x4 (&acc)[NT][1]) {
-  const int q = (threadIdx.x & 63) >> 4;
-  const uint32_t none[1] = {0};
-  stream_rows<MX, NT, 0, P, D>(wr, wr.w, wo, so, none, b0, stride, nb, acc, [&](int i, int j) {
-    const int chunk = (MX ? 8 * (j >> 1) + 2 * q + (j & 1) : 4 * j + q) ^ (4 * (tok & 3));
-    return as_bf16x8(*reinterpret_cast<const i32x4*>(stage + (i * quads * 4 + tok) * 256 + 16 * chunk));
-  });
-}
-
-// Blocks b0, b0 + stride, ... (nb of them) of `quads` x 4 rows into the wave's
-// own part of LDS: block i, row r at (i quads 4 + r) 256 bytes, its 16-byte
-// chunks XOR-swizzled by r so that four rows' reads of one chunk spread over
-// the banks.  offset(r): the row's byte offset (rows past the last: any valid
-// row, their columns are not used).
-template <typename Offset>
-__device__ __forceinline__ void stage_rows(char* stage, __amdgpu_buffer_rsrc_t ar, int quads, int b0, int stride, int nb,
-                                           Offset offset) {
-  const int lane = threadIdx.x & 63;
-  for (int j = 0; j < quads; ++j) {
-    const int r = 4 * j + (lane >> 4);
-    const uint32_t o = offset(r) + 16 * ((lane & 15) ^ (4 * (r & 3)));
-    for (int i = 0; i < nb; ++i) lds_load16(ar, stage + (i * quads + j) * 1024, o, 256 * (b0 + i * stride));
+// acc += the nb 128-wide blocks b0, b0 + stride, ... of NR groups of 8 rows:
+// group t's begin dr[t] (uniform) after the first's.  so: the scales of the
+// lane's row; one load gives a row's words of 8 blocks, one to each of its
+// lanes.
+template <bool MX, int NR, int D>
+__device__ __forceinline__ void stream_lines(const Weights<MX>& wr, __amdgpu_buffer_rsrc_t ar, uint32_t wo, uint32_t so,
+                                             const int (&dr)[NR], int ld, uint32_t ao, int b0, int stride, int nb,
+                                             f32x4 (&acc)[NR]) {
+  const int lane = threadIdx.x & 63, q = lane >> 4, l16 = lane & 15;
+  LineStep<MX, NR> st[D];
+  auto load = [&](LineStep<MX, NR>& f, int i) {   // past the end: zeros
+    const bool in = i < nb;
+    const int b = b0 + i * stride;
+#pragma unroll
+    for (int t = 0; t < NR; ++t)
+#pragma unroll
+      for (int p = 0; p < (MX ? 1 : 2); ++p)
+        f.w[t][p] = __builtin_amdgcn_raw_buffer_load_b128(wr.w, in ? wo + 128 * p : kPast,
+                                                          (MX ? 1 : 2) * (dr[t] * ld + 128 * b), 0);
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+      f.a[p] = __builtin_amdgcn_raw_buffer_load_b128(ar, in ? ao + (MX ? 16 : 128) * p : kPast, 256 * b, 0);
+    issue_order();
+  };
+  auto mma = [&](const LineStep<MX, NR>& f, const uint32_t (&sw)[NR]) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int t = 0; t < NR; ++t) {
+        const bf16x8 w = MX ? widen(f.w[t][0], sw[t], p) : as_bf16x8(f.w[t][MX ? 0 : p]);
+        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, as_bf16x8(f.a[p]), acc[t], 0, 0, 0);
+      }
+    issue_order();
+  };
+  uint32_t sw[NR];
+#pragma unroll
+  for (int t = 0; t < NR; ++t) sw[t] = 0;
+  if constexpr (MX) {
+    static_assert(8 % D == 0, "8 blocks take whole rounds of the steps in flight");
+    uint32_t next[NR], words[NR];
+    const int mine = 4 * (l16 & 1) + q;   // which of 8 blocks' words this lane holds
+    auto load_words = [&](int b) {
+#pragma unroll
+      for (int t = 0; t < NR; ++t)
+        next[t] = __builtin_amdgcn_raw_buffer_load_b32(wr.s, b + mine < nb ? so + 4 * (b0 + (b + mine) * stride) : kPast,
+                                                       dr[t] * (ld / 32), 0);
+      issue_order();
+    };
+    load_words(0);
+#pragma unroll
+    for (int d = 0; d < D; ++d) load(st[d], d);
+    for (int it = 0; it < nb; it += D) {
+      if (it % 8 == 0) {
+#pragma unroll
+        for (int t = 0; t < NR; ++t) words[t] = next[t];
+        load_words(it + 8);
+      }
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        // block u's word is with the row's lane (parity u / 4, group u % 4);
+        // this lane's chunk is scaled by its byte 2 parity + q / 2
+        const int u = (it + d) % 8, from = ((l16 & ~1) | (u >> 2)) + 16 * (u & 3);
+#pragma unroll
+        for (int t = 0; t < NR; ++t)
+          sw[t] = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * from, (int)words[t]) >> (8 * (2 * (l16 & 1) + (q >> 1)));
+        mma(st[d], sw);
+        load(st[d], it + d + D);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int d = 0; d < D; ++d) load(st[d], d);
+    for (int it = 0; it < nb; it += D)
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        mma(st[d], sw);
+        load(st[d], it + d + D);
+      }
   }
-  wait_vm<0>();
 }
 
 __device__ __forceinline__ uint64_t below(int t) { return t == 0 ? 0ull : (~0ull >> (64 - t)); }
@@ -298,7 +365,6 @@ struct SlotLds {
   float w[kSoloRows];                                 // solo only: the rows' weights
   uint8_t tok[kLayerMaxRoutes + kLayerMaxM * kLayerMaxShared];
 };
-constexpr int kStageBytes = 6144;   // a wave's activations in LDS: two workgroups on a CU fit its 160 KB
 
 struct RouteLds {
   uint64_t mask[kLayerMaxE];            // tokens of each expert
@@ -461,10 +527,10 @@ __device__ __forceinline__ void router_unit(const LayerArgs& g, int unit, f32x4*
 // z of 16 features of one slot with up to 16 CT tokens: wave kw of ks takes
 // the 128-wide blocks kw, kw + ks, ... of K (the waves together read each
 // weight row in long runs: contiguous parts per wave measured 5% slower) of
-// the gate and up rows.  stage: the wave's activations in LDS, or null.
+// the gate and up rows.
 template <bool MX, int CT, int P, int D>
 __device__ __forceinline__ void gate_up_strip(const LayerArgs& g, const SlotLds& s, int slot, int f0, int kw, bool live,
-                                              f32x4* red, const char* stage, int quads) {
+                                              f32x4* red) {
   const int lane = phase_thread() & 63, q = lane >> 4, l16 = lane & 15;
   const int e = __builtin_amdgcn_readfirstlane(s.e[slot]);
   const int pos0 = s.pos[slot], cnt = s.pos[slot + 1] - pos0;
@@ -485,16 +551,12 @@ __device__ __forceinline__ void gate_up_strip(const LayerArgs& g, const SlotLds&
 #pragma unroll
     for (int t = 0; t < 2; ++t) acc[t][c] = (f32x4){0.f, 0.f, 0.f, 0.f};
   }
-  if constexpr (P == 0) {
-    stream_rows_lds<MX, 2, MX ? 2 : 4, D>(wr, wo, so, stage, quads, min(l16, cnt - 1), kw, g.ks, n, acc);
-  } else {
-    const __amdgpu_buffer_rsrc_t ar = buffer_rsrc(g.x, (int64_t)g.M * g.K * 2);
-    uint32_t ao[CT];
+  const __amdgpu_buffer_rsrc_t ar = buffer_rsrc(g.x, (int64_t)g.M * g.K * 2);
+  uint32_t ao[CT];
 #pragma unroll
-    for (int c = 0; c < CT; ++c)
-      ao[c] = 16 * c + l16 < cnt ? lane_a<MX>(s.tok[pos0 + 16 * c + l16], g.K, q) : kPast;
-    stream_rows<MX, 2, CT, P, D>(wr, ar, wo, so, ao, kw, g.ks, n, acc);
-  }
+  for (int c = 0; c < CT; ++c)
+    ao[c] = 16 * c + l16 < cnt ? lane_a<MX>(s.tok[pos0 + 16 * c + l16], g.K, q) : kPast;
+  stream_rows<MX, 2, CT, P, D>(wr, ar, wo, so, ao, kw, g.ks, n, acc);
 #pragma unroll
   for (int c = 0; c < CT; ++c) {
 #pragma unroll
@@ -517,15 +579,59 @@ __device__ __forceinline__ void gate_up_strip(const LayerArgs& g, const SlotLds&
   }
 }
 
-// WIDE: M > 16 (a slot may hold up to 64 tokens).  At most 128 registers, so
+// The same for a slot of up to 8 tokens, by whole lines.
+template <bool MX>
+__device__ __forceinline__ void gate_up_lines(const LayerArgs& g, const SlotLds& s, int slot, int f0, int kw, bool live,
+                                              f32x4* red) {
+  const int lane = phase_thread() & 63, q = lane >> 4, l16 = lane & 15;
+  const int e = __builtin_amdgcn_readfirstlane(s.e[slot]);
+  const int pos0 = s.pos[slot], cnt = s.pos[slot + 1] - pos0;
+  const int n = live ? (g.K / 128 - kw + g.ks - 1) / g.ks : 0;
+  const Weights<MX> wr = expert_weights<MX>(g.w1, g.w1s, e, 2ll * g.I * g.K);
+  const __amdgpu_buffer_rsrc_t ar = buffer_rsrc(g.x, (int64_t)g.M * g.K * 2);
+  // groups: features 0 .. 7 and 8 .. 15 of gate, then of up
+  const int row = w1_row(f0 + (l16 >> 1), 0, g.I, g.w1_order);
+  const int up = __builtin_amdgcn_readfirstlane(w1_row(f0, 1, g.I, g.w1_order) - w1_row(f0, 0, g.I, g.w1_order));
+  const int dr[4] = {0, 8, up, up + 8};
+  const int tk = l16 & 7;
+  const uint32_t ao = tk < cnt ? line_a<MX>(s.tok[pos0 + tk], g.K, l16, q) : kPast;
+  const float wt = tk >= cnt ? 0.f : g.solo ? s.w[pos0 + tk] : load_relaxed(g.roww + pos0 + tk);
+  f32x4 acc[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) acc[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  stream_lines<MX, 4, 2>(wr, ar, line_w<MX>(row, g.K, l16, q), lane_s(row, g.K), dr, g.K, ao, kw, g.ks, n, acc);
+#pragma unroll
+  for (int t = 0; t < 4; ++t) red[(kw * 4 + t) * 64 + lane] = acc[t];
+  __syncthreads();
+  if (live && kw == 0 && tk < cnt) {
+    // lane (token tk, features 8 (l16 / 8) + 2 q, + 1): even slots from the
+    // token's column, odd ones from the column 8 on
+    const int hh = l16 >> 3, at = 16 * q + tk;
+    float v[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+    for (int k = 0; k < g.ks; ++k)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const f32x4 lo = red[(k * 4 + 2 * t + hh) * 64 + at], hi = red[(k * 4 + 2 * t + hh) * 64 + at + 8];
+        v[t][0] += lo[0] + hi[1];
+        v[t][1] += lo[2] + hi[3];
+      }
+    const uint32_t a = f32_to_bf16_rne(wt * (silu_f32(v[0][0]) * v[1][0]));
+    const uint32_t b = f32_to_bf16_rne(wt * (silu_f32(v[0][1]) * v[1][1]));
+    *reinterpret_cast<uint32_t*>(g.z + (int64_t)(pos0 + tk) * g.I + f0 + 8 * hh + 2 * q) = a | (b << 16);
+  }
+  __syncthreads();
+}
+
+// WIDE: M > 8 (a slot may hold up to 64 tokens).  At most 128 registers, so
 // two workgroups share a CU and one's joins overlap the other's streaming.
 template <bool MX, bool WIDE, int NV>
 __global__ void __launch_bounds__(kThreads, 4) layer_gate_up_kernel(LayerArgs g) {
-  // streaming: the strips' sums, the waves' activations, the slots; before
-  // that the routing, in front of the slots
-  constexpr int kSums = kWaves * 2 * 64 * 16;
-  constexpr int kRoute = (int)sizeof(RouteLds) + kWaves * 64 * NV * 8;
-  constexpr int kStream = kSums + kWaves * kStageBytes;
+  // streaming: the strips' sums, the slots; before that the routing, in front
+  // of the slots
+  constexpr int kSums = kWaves * 4 * 64 * 16;
+  constexpr int kRoute = (int)sizeof(RouteLds) + kWaves * 64 * NV * 8 +
+                         (NV == 1 ? 16 + kLayerSoloUnits * kWaves * 64 * 4 : 0);
+  constexpr int kStream = ((kSums > kRoute ? kSums : kRoute) + 15) / 16 * 16;
   constexpr int kSlots = ((int)sizeof(SlotLds) + 15) / 16 * 16;
   static_assert(kRoute <= kStream && kWaves * (WIDE ? 4 : 1) * 64 * 16 <= kStream, "routing and router units fit");
   __shared__ __attribute__((aligned(16))) char smem[kStream + kSlots];
@@ -638,10 +744,7 @@ __global__ void __launch_bounds__(kThreads, 4) layer_gate_up_kernel(LayerArgs g)
   const int h = wave / g.ks, kw = wave % g.ks;
   const int strips = g.I / 16, per = (strips + nh - 1) / nh;
   const int items = nslots * per;
-  f32x4* mine = red + h * g.ks * 2 * 64;
-  char* stage = smem + kSums + wave * kStageBytes;
-  const int nb = (g.K / 128 - kw + g.ks - 1) / g.ks;
-  int staged = -1;
+  f32x4* mine = red + h * g.ks * 4 * 64;
   for (int claim = blockIdx.x; claim < items;) {
     int next = 0;   // the claim's answer is used an item later
     if (threadIdx.x == 0)
@@ -652,23 +755,10 @@ __global__ void __launch_bounds__(kThreads, 4) layer_gate_up_kernel(LayerArgs g)
     const bool live = strip < strips;
     const int pos0 = s.pos[slot];
     const int cnt = __builtin_amdgcn_readfirstlane(s.pos[slot + 1] - pos0);
-    const int quads = (cnt + 3) / 4;
-    // the workgroup's waves agree: the first wave has the most blocks
-    if (cnt <= 16 && (g.K / 128 + g.ks - 1) / g.ks * quads * 1024 <= kStageBytes) {
-      if (staged != slot) {
-        const __amdgpu_buffer_rsrc_t ar = buffer_rsrc(g.x, (int64_t)g.M * g.K * 2);
-        stage_rows(stage, ar, quads, kw, g.ks, nb,
-                   [&](int r) { return (uint32_t)s.tok[pos0 + min(r, cnt - 1)] * (uint32_t)g.K * 2u; });
-        staged = slot;
-      }
-      gate_up_strip<MX, 1, 0, 2>(g, s, slot, 16 * strip, kw, live, mine, stage, quads);
-    } else if (!WIDE || cnt <= 16) {
-      gate_up_strip<MX, 1, MX ? 2 : 4, 2>(g, s, slot, 16 * strip, kw, live, mine, nullptr, 0);
-    } else if (cnt <= 32) {
-      gate_up_strip<MX, 2, MX ? 1 : 2, 2>(g, s, slot, 16 * strip, kw, live, mine, nullptr, 0);
-    } else {
-      gate_up_strip<MX, 4, 1, MX ? 1 : 2>(g, s, slot, 16 * strip, kw, live, mine, nullptr, 0);
-    }
+    if (!WIDE || cnt <= 8) gate_up_lines<MX>(g, s, slot, 16 * strip, kw, live, mine);
+    else if (cnt <= 16) gate_up_strip<MX, 1, MX ? 2 : 4, 2>(g, s, slot, 16 * strip, kw, live, mine);
+    else if (cnt <= 32) gate_up_strip<MX, 2, MX ? 1 : 2, 2>(g, s, slot, 16 * strip, kw, live, mine);
+    else gate_up_strip<MX, 4, 1, MX ? 1 : 2>(g, s, slot, 16 * strip, kw, live, mine);
     if (threadIdx.x == 0) s_claim = next;
     __syncthreads();
     claim = __builtin_amdgcn_readfirstlane((int)gridDim.x + s_claim);
@@ -679,10 +769,9 @@ __global__ void __launch_bounds__(kThreads, 4) layer_gate_up_kernel(LayerArgs g)
 // --------------------------------------------------------- second launch --
 // Workgroup (strip, split): the 32 output features of the strip over its
 // share of the active slots' features, one contiguous run per wave, slot by
-// slot.  Up to 16 tokens the MFMA columns are the tokens and the accumulators
-// run through all slots; beyond, the columns are the slot's own tokens (most
-// slots hold a few of the 64) and each slot's sums are added to the wave's
-// [token][32] tile in LDS.  The waves' sums meet in LDS in wave order; with
+// slot.  Up to 8 tokens the MFMA columns are the tokens; beyond, they are the
+// slot's own (most slots hold a few of the 64).  Each slot's sums are added to
+// the wave's [token][32] tile in LDS.  The waves' sums meet in LDS in wave order; with
 // more than one split the workgroup that arrives last adds the splits' sums
 // in order.
 constexpr int kDownTiles = 2;
@@ -714,10 +803,42 @@ __device__ __forceinline__ void down_run(const LayerArgs& g, const LayerSlot& sl
     }
 }
 
+// The same for a slot of up to 8 tokens, by whole lines: acc[t] += 8 output
+// features of tile t each; down_lines_add puts a slot's (or, up to 8 tokens,
+// all slots') sums into the wave's tile, tok: the token of column l16 % 8.
+constexpr int kDownGroups = 2 * kDownTiles;
+
+template <bool MX>
+__device__ __forceinline__ void down_lines(const LayerArgs& g, int e, int strip, int zrow, int b0, int nb,
+                                           f32x4 (&acc)[kDownGroups]) {
+  const int lane = threadIdx.x & 63, q = lane >> 4, l16 = lane & 15;
+  const Weights<MX> wr = expert_weights<MX>(g.w2, g.w2s, e, (int64_t)g.K * g.I);
+  const __amdgpu_buffer_rsrc_t ar = buffer_rsrc(g.z, (int64_t)g.cap * g.I * 2);
+  const int row = 8 * kDownGroups * strip + (l16 >> 1);
+  int dr[kDownGroups];
+#pragma unroll
+  for (int t = 0; t < kDownGroups; ++t) dr[t] = 8 * t;
+  stream_lines<MX, kDownGroups, 2>(wr, ar, line_w<MX>(row, g.I, l16, q), lane_s(row, g.I), dr, g.I,
+                                   zrow >= 0 ? line_a<MX>(zrow, g.I, l16, q) : kPast, b0, 1, nb, acc);
+}
+__device__ __forceinline__ void down_lines_add(const f32x4 (&acc)[kDownGroups], int tok, f32x4* tile) {
+  const int lane = threadIdx.x & 63, q = lane >> 4, l16 = lane & 15;
+  float* f = reinterpret_cast<float*>(tile);
+#pragma unroll
+  for (int t = 0; t < kDownGroups; ++t) {
+    const float a = acc[t][0] + __shfl_xor(acc[t][1], 8), b = acc[t][2] + __shfl_xor(acc[t][3], 8);
+    if (l16 < 8 && tok >= 0) {
+      float2* dst = reinterpret_cast<float2*>(f + tok * (16 * kDownTiles) + 8 * t + 2 * q);
+      const float2 old = *dst;
+      *dst = make_float2(old.x + a, old.y + b);
+    }
+  }
+}
+
 template <bool MX, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 4) layer_down_kernel(LayerArgs g) {
   // [wave][token][4 of the 32 features]
-  constexpr int kTok = WIDE ? kLayerMaxM : 16;
+  constexpr int kTok = WIDE ? kLayerMaxM : 8;
   constexpr int kQ = 4 * kDownTiles;
   __shared__ __attribute__((aligned(16))) f32x4 red[kWaves * kTok * kQ];
   // the slots (dynamic: the launch passes room for the most there can be) are
@@ -742,38 +863,32 @@ __global__ void __launch_bounds__(kThreads, 4) layer_down_kernel(LayerArgs g) {
     wo[t] = lane_w<MX>(16 * (kDownTiles * strip + t) + l16, g.I, q);
     so[t] = lane_s(16 * (kDownTiles * strip + t) + l16, g.I);
   }
+  const int col = l16 & 7;
   f32x4* tile = red + wave * kTok * kQ;
+#pragma unroll
+  for (int i = 0; i < kTok * kQ; i += 64) tile[i + lane] = (f32x4){0.f, 0.f, 0.f, 0.f};
 
-  if (WIDE) {
+  // A slot's sums are added to its own tokens only: a token takes no part in
+  // other experts' products, not even as a zero, so an infinite weight stays
+  // with the tokens of its expert.
+  while (b < end) {
+    const int slot = (int)(b / spe), b0 = (int)(b % spe);
+    const int n = (int)min<int64_t>(spe - b0, end - b);
+    const LayerSlot& sl = s_slots[slot];
+    const int cnt = __builtin_amdgcn_readfirstlane(sl.cnt);
+    if (!WIDE || cnt <= 8) {
+      // columns: the tokens, or beyond 8 tokens the slot's (listed in rows)
+      const int tok = WIDE ? (col < cnt ? g.rows[sl.pos0 + col] : -1) : ((sl.mask >> col) & 1 ? col : -1);
+      const int zrow = sl.pos0 + (WIDE ? col : __popcll(sl.mask & below(col)));
+      f32x4 acc[kDownGroups];
 #pragma unroll
-    for (int i = 0; i < kTok * kQ; i += 64) tile[i + lane] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    while (b < end) {
-      const int slot = (int)(b / spe), b0 = (int)(b % spe);
-      const int n = (int)min<int64_t>(spe - b0, end - b);
-      const LayerSlot& sl = s_slots[slot];
-      const int cnt = __builtin_amdgcn_readfirstlane(sl.cnt);
-      if (cnt <= 16) down_run<MX, 1, MX ? 2 : 4, 2>(g, sl, wo, so, b0, n, tile);
-      else if (cnt <= 32) down_run<MX, 2, MX ? 1 : 2, 2>(g, sl, wo, so, b0, n, tile);
-      else down_run<MX, 4, 1, MX ? 1 : 2>(g, sl, wo, so, b0, n, tile);
-      b += n;
-    }
-  } else {
-    const __amdgpu_buffer_rsrc_t ar = buffer_rsrc(g.z, (int64_t)g.cap * g.I * 2);
-    f32x4 acc[kDownTiles][1];
-#pragma unroll
-    for (int t = 0; t < kDownTiles; ++t) acc[t][0] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    while (b < end) {
-      const int slot = (int)(b / spe), b0 = (int)(b % spe);
-      const int n = (int)min<int64_t>(spe - b0, end - b);
-      const LayerSlot& sl = s_slots[slot];
-      const Weights<MX> wr = expert_weights<MX>(g.w2, g.w2s, __builtin_amdgcn_readfirstlane(sl.e), (int64_t)g.K * g.I);
-      const uint32_t ao[1] = {
-          (sl.mask >> l16) & 1 ? lane_a<MX>(sl.pos0 + __popcll(sl.mask & below(l16)), g.I, q) : kPast};
-      stream_rows<MX, kDownTiles, 1, MX ? 2 : 4, 2>(wr, ar, wo, so, ao, b0, 1, n, acc);
-      b += n;
-    }
-#pragma unroll
-    for (int t = 0; t < kDownTiles; ++t) tile[(l16 * kDownTiles + t) * 4 + q] = acc[t][0];
+      for (int t = 0; t < kDownGroups; ++t) acc[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+      down_lines<MX>(g, __builtin_amdgcn_readfirstlane(sl.e), strip, tok >= 0 ? zrow : -1, b0, n, acc);
+      down_lines_add(acc, tok, tile);
+    } else if (cnt <= 16) down_run<MX, 1, MX ? 2 : 4, 2>(g, sl, wo, so, b0, n, tile);
+    else if (cnt <= 32) down_run<MX, 2, MX ? 1 : 2, 2>(g, sl, wo, so, b0, n, tile);
+    else down_run<MX, 4, 1, MX ? 1 : 2>(g, sl, wo, so, b0, n, tile);
+    b += n;
   }
   __syncthreads();
   // thread (t, quarter) finishes 4 features of token t
@@ -866,7 +981,7 @@ hipError_t launch_layer(LayerArgs g, bool mxfp8, hipStream_t s) {
   const int64_t units = g.runits + (g.M + kWaves - 1) / kWaves;
   int64_t grid = items > units ? items : units;
   if (grid > 512) grid = 512;
-  if (g.M > 16) return mxfp8 ? launch<true, true>(g, (unsigned)grid, s) : launch<false, true>(g, (unsigned)grid, s);
+  if (g.M > 8) return mxfp8 ? launch<true, true>(g, (unsigned)grid, s) : launch<false, true>(g, (unsigned)grid, s);
   return mxfp8 ? launch<true, false>(g, (unsigned)grid, s) : launch<false, false>(g, (unsigned)grid, s);
 }
 

@@ -238,6 +238,26 @@ def test_layer_ties_and_nan_tokens():
 
 
 @gpu
+@pytest.mark.parametrize("M", [3, 8, 13, 40])
+@pytest.mark.parametrize("w", ["bf16", "mxfp8"])
+def test_layer_infinite_weights_stay_with_their_expert(M, w):
+    """An expert's infinities and NaN reach the tokens routed to it and no other."""
+    c = Case(M=M, K=256, I=256, E=6, topk=2, w=w, seed=M)
+    o = c.outputs()
+    c.call(o)
+    if w == "bf16":
+        c.w1[2, 5], c.w2[2, 7], c.w2[2, 40] = float("inf"), float("inf"), float("nan")
+    else:
+        c.w1[2, 5, :8], c.w2[2, 7, 3], c.w2[2, 40] = 0x7f, 0x7f, 0xff
+    p = c.outputs()
+    c.call(p)
+    hit = (o[1] == 2).any(1)
+    assert 0 < int(hit.sum()) < M
+    assert torch.equal(p[1], o[1]) and torch.equal(p[0][~hit], o[0][~hit])
+    assert p[0][hit].isnan().any(1).all()
+
+
+@gpu
 def test_layer_agrees_with_the_separate_calls():
     """Router projection, moe_route_topk and moe_apply_contiguous, as a user
     would otherwise chain them (their own roundings: z and y to bf16)."""
