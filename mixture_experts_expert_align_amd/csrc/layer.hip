@@ -412,7 +412,7 @@ __device__ __forceinline__ void rank_tokens(const LayerArgs& g, int t0, RouteLds
   }
   int id;
   float w;
-  route_token<NV>(g.r, l, g.rbias, keys + (g.r.groups > 1 ? wave * g.r.E : 0), id, w);
+  route_token<NV>(g.r, l, g.rbias, keys + (g.r.groups > 1 ? wave * (g.r.E + g.r.groups) : 0), id, w);
   if (lane < g.r.topk) {
     const int i = t * g.r.topk + lane;
     s.id[i] = id;
@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 4) layer_gate_up_kernel(LayerArgs g)
   // streaming: the strips' sums, the slots; before that the routing, in front
   // of the slots
   constexpr int kSums = kWaves * 4 * 64 * 16;
-  constexpr int kRoute = (int)sizeof(RouteLds) + kWaves * 64 * NV * 8 +
+  constexpr int kRoute = (int)sizeof(RouteLds) + kWaves * 64 * (NV + 1) * 8 +
                          (NV == 1 ? 16 + kLayerSoloUnits * kWaves * 64 * 4 : 0);
   constexpr int kStream = ((kSums > kRoute ? kSums : kRoute) + 15) / 16 * 16;
   constexpr int kSlots = ((int)sizeof(SlotLds) + 15) / 16 * 16;
@@ -645,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 4) layer_gate_up_kernel(LayerArgs g)
 
   if (NV == 1 && !WIDE && g.solo) {
     // a small router: every workgroup computes the whole routing by itself
-    constexpr int kLogits = ((int)sizeof(RouteLds) + kWaves * 64 * 8 + 15) / 16 * 16;
+    constexpr int kLogits = ((int)sizeof(RouteLds) + kWaves * 64 * 2 * 8 + 15) / 16 * 16;
     float* logits = reinterpret_cast<float*>(smem + kLogits);   // [rsplit][8][64]
     static_assert(kLogits >= kWaves * 64 * 16 && kLogits + kLayerSoloUnits * kWaves * 64 * 4 <= kStream, "logits fit");
     for (int unit = 0; unit < g.runits; ++unit)

@@ -11,10 +11,19 @@
 //   sigmoid: dl_j = ds_j s_j (1 - s_j), ds_j = scale dw_j, or renormalised
 //     scale (dw_j - sum_k dw_k s_k / S) / S with S = sum_k s_k.
 //
-// One wave per token, four tokens per workgroup, the token's logits in
-// registers: each is read once and nothing but the result is written, so at
-// 8192 x 128 the bound is the launch and the k rounds of the selection
-// rather than the 4 MB of logits.
+// Nothing but the logits is read, once, and nothing but the result written, so
+// the memory is never the bound: with few tokens it is one token's latency
+// (the float64 exponentials and divisions of the scores, then k rounds of
+// reductions), with many the instructions issued for that.  Hence two forms.
+// A wave per token: the shortest rounds; 3.3 us for 4 x 64, top-8, 18 us for
+// 4096 x 512 with 16 groups (29 by the other form).  And 16 lanes per token,
+// where a round's reductions serve four tokens at once but a lane has four
+// times the experts to look through: forward beyond 4096 tokens (more than
+// four waves per SIMD of the first form) of up to 256 experts: 8192 x 128
+// 7.5 us against 9.5, 8192 x 256 in 8 groups 16.9 against 18.6, while at 4096
+// tokens they are 7.2 against 6.9 and 16.5 against 12.0; backward, whose rows
+// have no rounds, from 2048 tokens: 8192 x 128 4.3 against 6.9, 2048 x 512 the
+// same 6.4.
 #include "kernels.h"
 #include "route_device.h"
 
@@ -34,7 +43,7 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_topk_kernel(RouterArgs
                                                                      const float* __restrict__ bias,
                                                                      int32_t* __restrict__ ids,
                                                                      float* __restrict__ weights) {
-  extern __shared__ double s_keys[];   // with groups: E doubles per wave
+  extern __shared__ double s_keys[];   // with groups: E + groups doubles per wave
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave;
   if (t >= M) return;
@@ -51,10 +60,37 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_topk_kernel(RouterArgs
   }
   int id;
   float w;
-  route_token<NV>(r, l, bias, s_keys + (r.groups > 1 ? wave * r.E : 0), id, w);
+  route_token<NV>(r, l, bias, s_keys + (r.groups > 1 ? wave * (r.E + r.groups) : 0), id, w);
   if (lane < r.topk) {
     ids[t * r.topk + lane] = id;
     weights[t * r.topk + lane] = w;
+  }
+}
+
+constexpr int kRowWaves = 2;
+constexpr int64_t kRowsForwardTokens = 4097, kRowsBackwardTokens = 2048;
+constexpr int kRowsForwardExperts = 256, kRowsBackwardExperts = 512;
+
+template <int NV, bool BF16>
+__global__ void __launch_bounds__(64 * kRowWaves) route_rows_kernel(RouterArgs r, int64_t M,
+                                                                    const void* __restrict__ logits, int64_t ld,
+                                                                    const float* __restrict__ bias,
+                                                                    int32_t* __restrict__ ids,
+                                                                    float* __restrict__ weights) {
+  extern __shared__ double s_keys[];   // with groups: E + groups doubles per token
+  const int row = threadIdx.x >> 4, c = threadIdx.x & 15;
+  const int64_t t = (int64_t)blockIdx.x * (4 * kRowWaves) + row;
+  const int64_t in = min(t, M - 1);    // past the last token: the last one again, not stored
+  int id;
+  float w;
+  route_row<NV>(r, [&](int e) {
+    double v = load_logit<BF16>(logits, in * ld + e);
+    if (r.bias_kind == 1) v += (double)bias[e];
+    return route_logit(v);
+  }, bias, s_keys + (r.groups > 1 ? row * (r.E + r.groups) : 0), id, w);
+  if (t < M && c < r.topk) {
+    ids[t * r.topk + c] = id;
+    weights[t * r.topk + c] = w;
   }
 }
 
@@ -130,15 +166,118 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_topk_backward_kernel(
   }
 }
 
+// The same, a token per row of 16 lanes.
+template <int NV, bool BF16>
+__global__ void __launch_bounds__(64 * kRowWaves) route_rows_backward_kernel(
+    RouterArgs r, int64_t M, const void* __restrict__ logits, int64_t ld, const float* __restrict__ bias,
+    const int32_t* __restrict__ ids, const float* __restrict__ dw, void* __restrict__ dl, int64_t dl_ld) {
+  const int lane = threadIdx.x & 63, row = threadIdx.x >> 4, c = lane & 15;
+  const int64_t t = (int64_t)blockIdx.x * (4 * kRowWaves) + row;
+  const int64_t in = min(t, M - 1);    // past the last token: the last one again, not stored
+  auto logit = [&](int e) {
+    double v = load_logit<BF16>(logits, in * ld + e);
+    if (r.bias_kind == 1) v += (double)bias[e];
+    return route_logit(v);
+  };
+  int id = c < r.topk ? ids[in * r.topk + c] : -1;
+  if (id < 0 || id >= r.E) id = -1;
+  const double lj = id >= 0 ? logit(id) : -INFINITY;
+  const bool have = lj > -INFINITY;
+  const double g = have ? (double)dw[in * r.topk + c] * (double)r.scale : 0.0;
+  double d = g, dot = 0.0, inv = 0.0;
+  const bool softmax = r.scoring == 0, dense = softmax && !r.renormalize;
+  float p[NV];
+  if (dense) {
+    double top = -INFINITY;
+    double l[NV];
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      l[i] = c + 16 * i < r.E ? logit(c + 16 * i) : -INFINITY;
+      top = fmax(top, l[i]);
+    }
+    top = row_max_f64(top);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      p[i] = l[i] > -INFINITY ? expf((float)(l[i] - top)) : 0.f;
+      s += p[i];
+    }
+    const double total = row_sum_f64(s);
+    inv = total > 0.0 ? 1.0 / total : 0.0;
+    dot = row_sum_f64(have ? g * exp(lj - top) * inv : 0.0);
+  } else if (softmax) {
+    const double m = row_max_f64(lj);
+    const double e = have ? exp(lj - m) : 0.0;
+    const double sum = row_sum_f64(e);
+    const double q = have ? e / sum : 0.0;
+    d = q * (g - row_sum_f64(q * g));
+  } else {
+    const double s = have ? sigmoid_f64(lj) : 0.0;
+    if (r.renormalize) {
+      const double S = row_sum_f64(s);
+      const double gs = row_sum_f64(g * s);
+      d = S > 0.0 ? (g - gs / S) / S : 0.0;
+    }
+    d *= have ? s * (1.0 - s) : 0.0;
+  }
+  const float df = (float)d;
+  float v[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) v[i] = 0.f;
+  for (int j = 0; j < r.topk; ++j) {   // an expert named in several slots gets their sum
+    const int ej = __shfl(id, (lane & 48) | j);
+    const float dj = __shfl(df, (lane & 48) | j);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] += ej == c + 16 * i ? dj : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int e = c + 16 * i;
+    if (dense) v[i] = p[i] * (float)inv * (v[i] - (float)dot);
+    if (t < M && e < r.E) {
+      if (BF16)
+        static_cast<uint16_t*>(dl)[t * dl_ld + e] = (uint16_t)f32_to_bf16_rne(v[i]);
+      else
+        static_cast<float*>(dl)[t * dl_ld + e] = v[i];
+    }
+  }
+}
+
 template <int NV>
 hipError_t launch_topk(const RouterArgs& r, int64_t M, const void* logits, bool bf16, int64_t ld, const float* bias,
                        int32_t* ids, float* weights, hipStream_t s) {
   const dim3 grid((unsigned)((M + kRouteWaves - 1) / kRouteWaves)), block(64 * kRouteWaves);
-  const size_t lds = r.groups > 1 ? sizeof(double) * r.E * kRouteWaves : 0;
+  const size_t lds = r.groups > 1 ? sizeof(double) * (r.E + r.groups) * kRouteWaves : 0;
   if (bf16)
     hipLaunchKernelGGL((route_topk_kernel<NV, true>), grid, block, lds, s, r, M, logits, ld, bias, ids, weights);
   else
     hipLaunchKernelGGL((route_topk_kernel<NV, false>), grid, block, lds, s, r, M, logits, ld, bias, ids, weights);
+  return hipGetLastError();
+}
+
+template <int NV>
+hipError_t launch_rows(const RouterArgs& r, int64_t M, const void* logits, bool bf16, int64_t ld, const float* bias,
+                       int32_t* ids, float* weights, hipStream_t s) {
+  const dim3 grid((unsigned)((M + 4 * kRowWaves - 1) / (4 * kRowWaves))), block(64 * kRowWaves);
+  const size_t lds = r.groups > 1 ? sizeof(double) * (r.E + r.groups) * 4 * kRowWaves : 0;
+  if (bf16)
+    hipLaunchKernelGGL((route_rows_kernel<NV, true>), grid, block, lds, s, r, M, logits, ld, bias, ids, weights);
+  else
+    hipLaunchKernelGGL((route_rows_kernel<NV, false>), grid, block, lds, s, r, M, logits, ld, bias, ids, weights);
+  return hipGetLastError();
+}
+
+template <int NV>
+hipError_t launch_rows_backward(const RouterArgs& r, int64_t M, const void* logits, bool bf16, int64_t ld,
+                                const float* bias, const int32_t* ids, const float* dw, void* dl, int64_t dl_ld,
+                                hipStream_t s) {
+  const dim3 grid((unsigned)((M + 4 * kRowWaves - 1) / (4 * kRowWaves))), block(64 * kRowWaves);
+  if (bf16)
+    hipLaunchKernelGGL((route_rows_backward_kernel<NV, true>), grid, block, 0, s, r, M, logits, ld, bias, ids, dw, dl,
+                       dl_ld);
+  else
+    hipLaunchKernelGGL((route_rows_backward_kernel<NV, false>), grid, block, 0, s, r, M, logits, ld, bias, ids, dw,
+                       dl, dl_ld);
   return hipGetLastError();
 }
 
@@ -147,6 +286,10 @@ hipError_t launch_topk(const RouterArgs& r, int64_t M, const void* logits, bool 
 hipError_t launch_route_topk(const RouterArgs& r, int64_t M, const void* logits, bool bf16, int64_t ld,
                              const float* bias, int32_t* ids, float* weights, hipStream_t s) {
   if (M == 0) return hipSuccess;
+  if (M >= kRowsForwardTokens && r.E <= kRowsForwardExperts && r.topk <= 16 && r.groups <= 16) {
+    if (r.E <= 128) return launch_rows<8>(r, M, logits, bf16, ld, bias, ids, weights, s);
+    return launch_rows<16>(r, M, logits, bf16, ld, bias, ids, weights, s);
+  }
   if (r.E <= 64) return launch_topk<1>(r, M, logits, bf16, ld, bias, ids, weights, s);
   if (r.E <= 128) return launch_topk<2>(r, M, logits, bf16, ld, bias, ids, weights, s);
   if (r.E <= 256) return launch_topk<4>(r, M, logits, bf16, ld, bias, ids, weights, s);
@@ -158,6 +301,11 @@ hipError_t launch_route_topk_backward(const RouterArgs& r, int64_t M, const void
                                       const float* bias, const int32_t* ids, const float* dw, void* dl,
                                       int64_t dl_ld, hipStream_t s) {
   if (M == 0) return hipSuccess;
+  if (M >= kRowsBackwardTokens && r.E <= kRowsBackwardExperts && r.topk <= 16) {
+    if (r.E <= 128) return launch_rows_backward<8>(r, M, logits, bf16, ld, bias, ids, dw, dl, dl_ld, s);
+    if (r.E <= 256) return launch_rows_backward<16>(r, M, logits, bf16, ld, bias, ids, dw, dl, dl_ld, s);
+    return launch_rows_backward<32>(r, M, logits, bf16, ld, bias, ids, dw, dl, dl_ld, s);
+  }
   const dim3 grid((unsigned)((M + kRouteWaves - 1) / kRouteWaves)), block(64 * kRouteWaves);
   if (bf16)
     hipLaunchKernelGGL((route_topk_backward_kernel<true>), grid, block, 0, s, r, M, logits, ld, bias, ids, dw, dl,

@@ -161,8 +161,24 @@ def test_router(scoring, bias_kind, renorm, M, E, topk, groups, tg):
 @gpu
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("bias_kind", ["none", "logit", "select"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("M,E,topk,groups,tg", [(4097, 1, 1, 1, 1), (4101, 65, 3, 1, 1), (4099, 128, 16, 16, 3),
+                                                (4098, 99, 4, 3, 2), (4100, 256, 12, 2, 1), (2049, 512, 8, 16, 4),
+                                                (2051, 300, 16, 1, 1), (4098, 200, 17, 1, 1),
+                                                (4098, 160, 4, 32, 9)])
+def test_router_many_rows(scoring, bias_kind, renorm, M, E, topk, groups, tg):
+    """Enough tokens for several of them to a wave (up to 16 choices and 16 groups)."""
+    rng = np.random.default_rng(E)
+    bias = None if bias_kind == "none" else (0.25 * rng.normal(size=E)).astype(np.float32)
+    dtype = torch.float32 if renorm else torch.bfloat16
+    check(logits(M, E, dtype, M + E), topk, scoring, bias, bias_kind, renorm, 2.5, groups, tg)
+
+
+@gpu
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bias_kind", ["none", "logit", "select"])
 @pytest.mark.parametrize("groups,tg", [(1, 1), (4, 2)])
-def test_router_masks_and_special_values(scoring, bias_kind, groups, tg):
+def test_router_masks_and_special_values(scoring, bias_kind, groups, tg, rows=16):
     E, topk = 64, 6
     l = logits(16, E, torch.float32, 3)
     low = torch.finfo(torch.float32).min
@@ -187,8 +203,17 @@ def test_router_masks_and_special_values(scoring, bias_kind, groups, tg):
         bias[5] = float("-inf")
         bias[6] = float("nan")
         bias[40] = 0.5
+    l = l[torch.arange(rows) % 16].contiguous()
     for renorm in (True, False):
         check(l, topk, scoring, bias, bias_kind, renorm, 1.0, groups, tg)
+
+
+@gpu
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bias_kind", ["none", "logit", "select"])
+@pytest.mark.parametrize("groups,tg", [(1, 1), (4, 2), (16, 5)])
+def test_router_masks_and_special_values_many_rows(scoring, bias_kind, groups, tg):
+    test_router_masks_and_special_values(scoring, bias_kind, groups, tg, rows=4101)
 
 
 @gpu
