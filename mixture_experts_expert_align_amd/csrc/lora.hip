@@ -250,79 +250,131 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) lora_shrink_kernel(LoraArgs
 }
 
 // ----------------------------------------------------- few rows: streaming --
-// y of 16 output features for up to 16 CT rows: W's rows stream from memory
-// into the MFMA row operand, the contraction split over the waves; the
-// adapters' part is added to the finished sums, each row with its own B_g.
+// y of 16 output features for up to 8 CT rows, the contraction split over the
+// waves.  W streams from memory by whole lines: a load covers 8 rows of 128
+// bytes, the row slots 2 f and 2 f + 1 of the MFMA are the two halves of
+// feature f's line, column c holds row c's activations at the first half,
+// column c + 8 at the second, and of the products the matching ones (even
+// slot, column < 8) and (odd slot, column >= 8) are added; the others are not
+// used.  (Loads of 16 rows by 64 bytes, all products used, reach 28 KB/us on a
+// CU; these about 70.)  Wave j also adds the adapters' product of the ranks
+// 8 j .. 8 j + 7 to its sums, each row with its own B_g.
 constexpr int kStreamWaves = 16;
 
-template <int CT>
+__device__ __forceinline__ float ror8(float v) {   // lane c of a row of 16: from lane (c + 8) % 16
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), 0x128, 0xf, 0xf, false));
+}
+
+struct AdapterPart {   // 8 ranks of one row's s and of two features' B rows
+  i32x4 p[kPieces], b[2];
+};
+
+template <int CT, int D>
 __global__ void __launch_bounds__(64 * kStreamWaves) lora_stream_kernel(LoraArgs a, const uint16_t* __restrict__ x,
                                                                        const uint16_t* __restrict__ w,
                                                                        const uint16_t* __restrict__ b,
                                                                        uint16_t* __restrict__ y, int N, int K) {
-  __shared__ f32x4 red[kStreamWaves * CT * 64];
-  const int lane = threadIdx.x & 63, q = lane >> 4, l16 = lane & 15;
+  __shared__ float2 red[kStreamWaves * CT * 64];
+  const int lane = threadIdx.x & 63, q = lane >> 4, l16 = lane & 15, hh = l16 >> 3;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n0 = 16 * blockIdx.x;
-  const int64_t r0 = (int64_t)blockIdx.y * 16 * CT;
+  const int n0 = 16 * blockIdx.x, n = n0 + 8 * hh + 2 * q;   // the lane's features n, n + 1
+  const int row0 = l16 & 7;                                  // of row 8 c + row0
+  const int rank0 = 8 * wave;
+  auto adapter_load = [&](AdapterPart& v, int c) {
+    const int64_t r = 8 * c + row0;
+    const int g = r < a.R ? row_adapter(a.adapter, r, a.R, a.G) : -1;
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) v.p[k] = (i32x4){0, 0, 0, 0};
+    v.b[0] = v.b[1] = (i32x4){0, 0, 0, 0};
+    if (g >= 0) {
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k)
+        v.p[k] = *reinterpret_cast<const i32x4*>(a.low + (r * kPieces + k) * a.rank + rank0);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        v.b[i] = *reinterpret_cast<const i32x4*>(b + ((int64_t)g * N + n + i) * a.rank + rank0);
+    }
+  };
+  auto adapter_add = [&](const AdapterPart& v, float2& sum) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      float s = 0.f;
+#pragma unroll
+      for (int k = kPieces - 1; k >= 0; --k) s += bf16_to_f32(((uint32_t)v.p[k][u / 2] >> (16 * (u & 1))) & 0xffffu);
+      sum.x += s * bf16_to_f32(((uint32_t)v.b[0][u / 2] >> (16 * (u & 1))) & 0xffffu);
+      sum.y += s * bf16_to_f32(((uint32_t)v.b[1][u / 2] >> (16 * (u & 1))) & 0xffffu);
+    }
+  };
+  const bool adds = rank0 < a.rank;
+  // up to two tiles of rows: requested before the projection's loads
+  constexpr int kEarly = CT <= 2 ? CT : 0;
+  AdapterPart part[kEarly ? kEarly : 1];
+#pragma unroll
+  for (int c = 0; c < kEarly; ++c)
+    if (adds) adapter_load(part[c], c);
+
   const __amdgpu_buffer_rsrc_t wr = buffer_rsrc(w + (int64_t)n0 * K, 16ll * K * 2);
-  const __amdgpu_buffer_rsrc_t xr = buffer_rsrc(x + r0 * K, min<int64_t>(16 * CT, a.R - r0) * K * 2);
-  const uint32_t wo = (uint32_t)(l16 * K * 2 + 16 * q);
-  f32x4 acc[CT];
+  const __amdgpu_buffer_rsrc_t xr = buffer_rsrc(x, a.R * K * 2);
+  const uint32_t wo = (uint32_t)((l16 >> 1) * K * 2 + 64 * (l16 & 1) + 16 * q);
+  const uint32_t xo = (uint32_t)(row0 * K * 2 + 64 * hh + 16 * q);
+  f32x4 acc[2][CT];
 #pragma unroll
-  for (int c = 0; c < CT; ++c) acc[c] = (f32x4){0.f, 0.f, 0.f, 0.f};
-  for (int k0 = 64 * wave; k0 < K; k0 += 64 * kStreamWaves) {
-    i32x4 f[2], e[2][CT];
+  for (int t = 0; t < 2; ++t)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      f[j] = __builtin_amdgcn_raw_buffer_load_b128(wr, wo + 64 * j, 2 * k0, 0);
+    for (int c = 0; c < CT; ++c) acc[t][c] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  struct Step {
+    i32x4 w[2], x[CT];
+  } st[D];
+  const int lines = K / 64;
+  auto load = [&](Step& f, int line) {   // past the end: zeros
+    const bool in = line < lines;
 #pragma unroll
-      for (int c = 0; c < CT; ++c)
-        e[j][c] = __builtin_amdgcn_raw_buffer_load_b128(
-            xr, r0 + 16 * c + l16 < a.R ? (uint32_t)((16 * c + l16) * K * 2 + 16 * q + 64 * j) : kPast, 2 * k0, 0);
+    for (int t = 0; t < 2; ++t)
+      f.w[t] = __builtin_amdgcn_raw_buffer_load_b128(wr, in ? wo : kPast, 128 * line + 16 * t * K, 0);
+#pragma unroll
+    for (int c = 0; c < CT; ++c)
+      f.x[c] = __builtin_amdgcn_raw_buffer_load_b128(xr, in && 8 * c + row0 < a.R ? xo : kPast,
+                                                     128 * line + 16 * c * K, 0);
+    issue_order();
+  };
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(st[d], wave + kStreamWaves * d);
+  for (int line = wave; line < lines; line += kStreamWaves * D)
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+          acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(st[d].w[t]), as_bf16x8(st[d].x[c]), acc[t][c], 0, 0, 0);
+      issue_order();
+      load(st[d], line + kStreamWaves * (d + D));
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int c = 0; c < CT; ++c)
-        acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(f[j]), as_bf16x8(e[j][c]), acc[c], 0, 0, 0);
+  for (int c = 0; c < CT; ++c) {
+    // Lanes l16 < 8 take the first 8 features' sums of their row, the others the
+    // second 8.  (Every lane takes part in every exchange.)
+    const float e0 = ror8(acc[1][c][0]), o0 = ror8(acc[0][c][1]), e1 = ror8(acc[1][c][2]), o1 = ror8(acc[0][c][3]);
+    float2 v;
+    v.x = hh ? e0 + acc[1][c][1] : acc[0][c][0] + o0;
+    v.y = hh ? e1 + acc[1][c][3] : acc[0][c][2] + o1;
+    if (adds) {
+      if (!kEarly) adapter_load(part[0], c);
+      adapter_add(part[kEarly ? c : 0], v);
+    }
+    red[(wave * CT + c) * 64 + lane] = v;
   }
-#pragma unroll
-  for (int c = 0; c < CT; ++c) red[(wave * CT + c) * 64 + lane] = acc[c];
   __syncthreads();
   if (wave >= CT) return;
-  f32x4 sum = red[wave * 64 + lane];
-  for (int k = 1; k < kStreamWaves; ++k) sum += red[(k * CT + wave) * 64 + lane];
-  const int64_t r = r0 + 16 * wave + l16;
-  if (r >= a.R) return;
-  const int g = row_adapter(a.adapter, r, a.R, a.G);
-  const int n = n0 + 4 * q;      // sum[i]: feature n + i
-  if (g >= 0) {
-    const uint16_t* low = a.low + r * kPieces * a.rank;
-    const uint16_t* bg = b + ((int64_t)g * N + n) * a.rank;
-    for (int j = 0; j < a.rank; j += 8) {
-      float s[8];
-      i32x4 p[kPieces];
-#pragma unroll
-      for (int k = 0; k < kPieces; ++k) p[k] = *reinterpret_cast<const i32x4*>(low + k * a.rank + j);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        s[i] = 0.f;
-#pragma unroll
-        for (int k = kPieces - 1; k >= 0; --k) s[i] += bf16_to_f32(((uint32_t)p[k][i / 2] >> (16 * (i & 1))) & 0xffffu);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const i32x4 bv = *reinterpret_cast<const i32x4*>(bg + i * a.rank + j);
-#pragma unroll
-        for (int u = 0; u < 8; ++u) sum[i] += s[u] * bf16_to_f32(((uint32_t)bv[u / 2] >> (16 * (u & 1))) & 0xffffu);
-      }
-    }
+  float2 sum = red[wave * 64 + lane];
+  for (int k = 1; k < kStreamWaves; ++k) {
+    const float2 v = red[(k * CT + wave) * 64 + lane];
+    sum.x += v.x;
+    sum.y += v.y;
   }
-  uint32_t h[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = f32_to_bf16_rne(sum[i]);
-  *reinterpret_cast<uint2*>(y + r * N + n) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+  const int64_t r = 8 * wave + row0;
+  if (r >= a.R) return;
+  *reinterpret_cast<uint32_t*>(y + r * N + n) = f32_to_bf16_rne(sum.x) | ((uint32_t)f32_to_bf16_rne(sum.y) << 16);
 }
 
 // ----------------------------------------------------------------- wgrad --
@@ -519,11 +571,12 @@ hipError_t launch_lora_forward(const LoraArgs& a, const uint16_t* x, const uint1
   hipError_t e = shrink(a, x, am, K, false, s);
   if (e != hipSuccess) return e;
   if (a.R <= kLoraStreamRows) {
-    const int ct = a.R <= 16 ? 1 : a.R <= 32 ? 2 : 4;
-    const dim3 grid(N / 16, (unsigned)((a.R + 16 * ct - 1) / (16 * ct))), block(64 * kStreamWaves);
-    if (ct == 1) hipLaunchKernelGGL((lora_stream_kernel<1>), grid, block, 0, s, a, x, w, b, y, N, K);
-    else if (ct == 2) hipLaunchKernelGGL((lora_stream_kernel<2>), grid, block, 0, s, a, x, w, b, y, N, K);
-    else hipLaunchKernelGGL((lora_stream_kernel<4>), grid, block, 0, s, a, x, w, b, y, N, K);
+    static_assert(kLoraStreamRows == 64 && kLoraMaxRank <= 8 * kStreamWaves, "8 tiles of rows, 8 ranks a wave");
+    const dim3 grid(N / 16), block(64 * kStreamWaves);
+    if (a.R <= 8) hipLaunchKernelGGL((lora_stream_kernel<1, 4>), grid, block, 0, s, a, x, w, b, y, N, K);
+    else if (a.R <= 16) hipLaunchKernelGGL((lora_stream_kernel<2, 3>), grid, block, 0, s, a, x, w, b, y, N, K);
+    else if (a.R <= 32) hipLaunchKernelGGL((lora_stream_kernel<4, 2>), grid, block, 0, s, a, x, w, b, y, N, K);
+    else hipLaunchKernelGGL((lora_stream_kernel<8, 1>), grid, block, 0, s, a, x, w, b, y, N, K);
     return hipGetLastError();
   }
   return launch_tile_lora_bf16(a, x, w, b, y, K, N, false, s);
