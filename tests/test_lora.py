@@ -154,6 +154,14 @@ CASES = [
     (100, 64, 64, 7, 72, "mixed"), (255, 320, 448, 300, 8, "mixed"), (300, 512, 256, 48, 32, "mixed"),
     (513, 256, 320, 4, 128, "runs"), (700, 832, 576, 8, 16, "runs"), (1025, 384, 512, 2, 56, "mixed"),
     (40, 256, 256, 4, 16, -1), (300, 256, 256, 4, 16, -1), (300, 128, 256, 1, 16, 0), (9000, 128, 64, 3, 8, "mixed"),
+    # 128 x 64, 128 x 128 and 256 x 256 tiles, of y and of dx; few and many adapters in a tile
+    (1001, 2048, 192, 3, 8, "mixed"), (290, 4160, 128, 48, 32, "mixed"), (1001, 192, 2048, 3, 24, "mixed"),
+    (290, 128, 4160, 48, 8, "mixed"), (2048, 2048, 64, 5, 16, "mixed"), (2040, 2112, 64, 40, 8, "mixed"),
+    (2048, 64, 2048, 8, 64, "mixed"), (2040, 128, 2112, 40, 16, "mixed"), (4096, 4096, 64, 3, 16, "runs"),
+    (4090, 4160, 64, 24, 8, "mixed"), (4096, 64, 4096, 5, 128, "runs"), (4090, 64, 4160, 24, 8, "mixed"),
+    # 9 to 64 rows by whole lines: every count of row tiles, one and many adapters
+    (8, 256, 704, 3, 128, "mixed"), (9, 64, 64, 4, 8, "mixed"), (24, 128, 1088, 30, 16, "mixed"),
+    (32, 192, 4096, 2, 16, "runs"), (47, 64, 2048, 9, 88, "mixed"), (64, 192, 4160, 64, 16, "mixed"),
 ]
 
 
