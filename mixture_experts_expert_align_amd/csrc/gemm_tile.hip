@@ -264,7 +264,68 @@ struct LoraExt {
 // compute(i): multiplies the slice in slots i.
 // ROWS: returns false, with nothing done, for a tile of more than
 // kLoraSliceAdapters adapters.
+//
+// The zeros that keep an adapter from the other adapters' rows keep it out
+// only while it is finite.  So that one request's broken adapter does not
+// reach its neighbours in a tile, elements of M_g that are infinite or NaN
+// are taken out of the fragments (lora_finite), and a tile that met any adds
+// their products afterwards, to the rows that name the adapter
+// (lora_add_nonfinite).
 constexpr int kLoraSliceAdapters = 8;
+
+// Two bf16 in a dword: bits 15 and 31 of the carry out of their exponents.
+__device__ __forceinline__ uint32_t nonfinite_bf16x2(uint32_t v) { return (v & 0x7f807f80u) + 0x00800080u; }
+
+// Zeros in place of a fragment's infinities and NaN; true if some lane had any.
+__device__ __forceinline__ bool lora_finite(bf16x8& f) {
+  i32x4 v = __builtin_bit_cast(i32x4, f);
+  uint32_t bad = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) bad |= nonfinite_bf16x2((uint32_t)v[e]);
+  if (!__any((int)(bad & 0x80008000u))) return false;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t b = (nonfinite_bf16x2((uint32_t)v[e]) >> 15) & 0x00010001u;
+    v[e] = (int)((uint32_t)v[e] & ~(b * 0xffffu));
+  }
+  f = as_bf16x8(v);
+  return true;
+}
+
+// y of the tile's rows, already written, plus the products with the elements
+// of M_g that lora_finite took out.  (Their sum is infinite or NaN, so y's
+// own rounding does not matter.)
+template <int BM, int BN, int THREADS, bool WT>
+__device__ __forceinline__ void lora_add_nonfinite(const LoraExt& x, const GemmArgs& g, const TileCoord& tc) {
+  wait_vm<0>();
+  __syncthreads();
+  uint16_t* out = static_cast<uint16_t*>(g.out);
+  const int rank = x.a.rank;
+  for (int i = threadIdx.x; i < BM * BN; i += THREADS) {
+    const int m = i / BN, f = tc.col0 + i % BN;
+    if (m < tc.mlo || m >= tc.nvalid || f >= g.nfeat) continue;
+    const int64_t r = tc.row0 + m;
+    const int ad = x.a.adapter[r];
+    if (ad < 0 || ad >= x.a.G) continue;
+    const uint16_t* low = x.a.low + r * kLoraPieces * rank;
+    float extra = 0.f;
+    bool any = false;
+    for (int k = 0; k < rank; ++k) {
+      const uint16_t b = x.m[WT ? ((int64_t)ad * rank + k) * g.nfeat + f : ((int64_t)ad * g.nfeat + f) * rank + k];
+      if ((b & 0x7f80u) != 0x7f80u) continue;
+      any = true;
+      float v = 0.f;
+      for (int c = kLoraPieces - 1; c >= 0; --c) v += bf16_to_f32(low[c * rank + k]);
+      extra += v * bf16_to_f32(b);
+    }
+    if (!any) continue;
+    // (read past this CU's cache, which other waves' stores do not update)
+    const int64_t at = r * g.out_ld + f;
+    const uint32_t pair = __hip_atomic_load(reinterpret_cast<const uint32_t*>(out) + at / 2, __ATOMIC_RELAXED,
+                                            __HIP_MEMORY_SCOPE_AGENT);
+    out[at] = (uint16_t)f32_to_bf16_rne(bf16_to_f32((pair >> (16 * (at & 1))) & 0xffffu) + extra);
+  }
+}
 
 template <int BM, int BN, int BK, int NW, bool WT, bool ROWS, typename Compute>
 __device__ __forceinline__ bool lora_slices(const LoraExt& x, const GemmArgs& g, const TileCoord& tc, uint16_t* wslot,
@@ -276,7 +337,7 @@ __device__ __forceinline__ bool lora_slices(const LoraExt& x, const GemmArgs& g,
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rank = x.a.rank, span = 2 * rank;
   int* const slot_of = list + BM;   // [BM] the row's adapter's place in the list, or -1
-  int* const count = list + 2 * BM;
+  int* const count = list + 2 * BM;   // then the flag of a tile with infinities or NaN
   if (wave == 0) {
     constexpr int V = BM / 64;
     int ad[V], place[V];
@@ -305,7 +366,10 @@ __device__ __forceinline__ bool lora_slices(const LoraExt& x, const GemmArgs& g,
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) slot_of[lane + 64 * i] = place[i];
-    if (lane == 0) *count = n;
+    if (lane == 0) {
+      count[0] = n;
+      count[1] = 0;
+    }
   }
   lds_barrier();
   if (ROWS && __builtin_amdgcn_readfirstlane(*count) > kLoraSliceAdapters) return false;
@@ -378,7 +442,7 @@ __device__ __forceinline__ bool lora_slices(const LoraExt& x, const GemmArgs& g,
 // with slices, 41 with products lane by lane, 36 like this.
 template <int TW, int TX>
 __device__ __forceinline__ void lora_rows_mfma(const LoraExt& x, const GemmArgs& g, const TileCoord& tc, int row0,
-                                               int col0, int lane, f32x16 (&acc)[TW][TX]) {
+                                               int col0, int lane, f32x16 (&acc)[TW][TX], int* flag) {
   constexpr int kBatch = 8 / TW;
   const int rank = x.a.rank, l32 = lane & 31, half = lane >> 5;
   const __amdgpu_buffer_rsrc_t mr = buffer_rsrc(x.m, (int64_t)x.a.G * g.nfeat * rank * 2);
@@ -416,6 +480,12 @@ __device__ __forceinline__ void lora_rows_mfma(const LoraExt& x, const GemmArgs&
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
           const bool own = ad == ga[u];
+          bf16x8 wf[TW];
+#pragma unroll
+          for (int i = 0; i < TW; ++i) {
+            wf[i] = as_bf16x8(w[u][i]);
+            if (lora_finite(wf[i])) *flag = 1;
+          }
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             i32x4 v;
@@ -423,7 +493,7 @@ __device__ __forceinline__ void lora_rows_mfma(const LoraExt& x, const GemmArgs&
             for (int e = 0; e < 4; ++e) v[e] = own ? s[c][e] : 0;
 #pragma unroll
             for (int i = 0; i < TW; ++i)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(w[u][i]), as_bf16x8(v), acc[i][j], 0, 0, 0);
+              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wf[i], as_bf16x8(v), acc[i][j], 0, 0, 0);
           }
         }
       }
@@ -639,29 +709,39 @@ __device__ __forceinline__ void split_tile(const GemmArgs& g, const TileCoord& t
 
   wait_vm<0>();
   lds_barrier();
+  bool nonfinite = false;
   if constexpr (Ext::kOn) {
-    static_assert(BM * 2 + 1 <= WSLOT / 2, "the adapter list fits a slot");
+    static_assert(BM * 2 + 2 <= WSLOT / 2, "the adapter list fits a slot");
     // 64 accumulators a lane and the rows' form do not fit the 128 registers
     // of the 256 x 256 tiles
     constexpr bool kRows = BM < 256;
-    const bool done =
-        lora_slices<BM, BN, BK, NW, WT, kRows>(ext, g, tc, wbase, rbase, reinterpret_cast<int*>(wbase + 2 * WSLOT), [&](int k) {
-          if (!live) return;
+    int* const list = reinterpret_cast<int*>(wbase + 2 * WSLOT);
+    int* const flag = list + 2 * BM + 1;
+    const bool done = lora_slices<BM, BN, BK, NW, WT, kRows>(ext, g, tc, wbase, rbase, list, [&](int k) {
+      if (!live) return;
 #pragma unroll
-          for (int s = 0; s < NSTEP; ++s) {
-            fload(s & 1, k, s);
-            mma(s & 1);
-          }
-        });
+      for (int s = 0; s < NSTEP; ++s) {
+        fload(s & 1, k, s);
+#pragma unroll
+        for (int i = 0; i < TW; ++i)
+          if (lora_finite(fw[s & 1][i])) *flag = 1;
+        mma(s & 1);
+      }
+    });
     if constexpr (kRows) {
       if (!done && live) {
         if (WT) lora_rows_wt<TW, TX>(ext, g, tc, wm * (BM / WM), wn * (BN / WN), lane, acc);
-        else lora_rows_mfma<TW, TX>(ext, g, tc, wm * (BM / WM), wn * (BN / WN), lane, acc);
+        else lora_rows_mfma<TW, TX>(ext, g, tc, wm * (BM / WM), wn * (BN / WN), lane, acc, flag);
       }
     }
+    lds_barrier();
+    nonfinite = __builtin_amdgcn_readfirstlane(*flag) != 0;
+    lds_barrier();
   }
   static_assert(BM * (EPI == kEpiGateUp ? BN / 2 : BN) <= Ring::Elems, "epilogue tile fits the LDS");
   tile_epilogue<EPI, BM, BN, WN, WM, 64 * WN * WM, TW, TX, ROUTES, Ext::kOn>(g, tc, acc, wn, wm, lane, smem);
+  if constexpr (Ext::kOn)
+    if (nonfinite) lora_add_nonfinite<BM, BN, 64 * NW, WT>(ext, g, tc);
 }
 
 template <int EPI, int BM, int BN, int BK, int WN, int WM, int OCC, int ORDER>

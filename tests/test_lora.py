@@ -179,6 +179,54 @@ def test_lora(R, N, K, G, rank, order):
 
 
 @gpu
+@pytest.mark.parametrize("R,N,K,G,order", [
+    (7, 128, 256, 4, "mixed"), (50, 128, 256, 4, "mixed"), (100, 192, 320, 4, "mixed"), (130, 320, 256, 60, "mixed"),
+    (2048, 2048, 64, 4, "mixed"), (2048, 64, 2048, 4, "mixed"), (2048, 2048, 64, 40, "mixed"),
+    (2048, 64, 2048, 40, "mixed"), (4096, 4096, 64, 4, "mixed"), (4096, 64, 4096, 4, "mixed"),
+])
+def test_lora_nonfinite_stays_with_its_adapter(R, N, K, G, order):
+    """An adapter's infinities and NaN, and a row's, reach the outputs that the
+    formulas give them to and no other."""
+    c = Case(R, N, K, G, 16, order)
+    c.adapter[3] = -1
+    c.adapter[1], c.adapter[2] = 1, 2
+    o = c.buffers()
+    c.call(o)
+    c.b[1, 5, 3], c.b[1, 40, 0], c.b[1, N - 1, 15] = float("inf"), float("nan"), float("-inf")
+    c.a[2, 4, 7], c.a[2, 15, K - 1] = float("nan"), float("inf")
+    p = c.buffers()
+    c.call(p)
+    one, two = c.adapter == 1, c.adapter == 2
+    # y: B's element reaches its feature; A's reach s, and with it the whole row
+    bad = torch.zeros(R, N, dtype=torch.bool, device="cuda")
+    for f in (5, 40, N - 1):
+        bad[:, f] = one
+    bad |= two[:, None]
+    assert torch.equal(~p["y"].isfinite(), bad) and torch.equal(p["y"][~bad], o["y"][~bad])
+    bad = torch.zeros(R, K, dtype=torch.bool, device="cuda")
+    bad[:, 7] = bad[:, K - 1] = two
+    bad |= one[:, None]
+    assert torch.equal(~p["dx"].isfinite(), bad) and torch.equal(p["dx"][~bad], o["dx"][~bad])
+    # the gradients: t of adapter 1's rows and s of adapter 2's are not finite
+    for k, g in (("da", 1), ("db", 2)):
+        rest = [i for i in range(G) if i != g]
+        assert not p[k][g].isfinite().all() and torch.equal(p[k][rest], o[k][rest])
+    # a row's own infinity: its y, and its adapter's dA
+    c = Case(R, N, K, G, 16, order)
+    c.adapter[1] = 1
+    o = c.buffers()
+    c.call(o)
+    c.x[1, 3] = float("inf")
+    p = c.buffers()
+    c.call(p)
+    rows = [i for i in range(R) if i != 1]
+    rest = [i for i in range(G) if i != 1]
+    assert not p["y"][1].isfinite().any() and torch.equal(p["y"][rows], o["y"][rows])
+    assert torch.equal(p["dx"], o["dx"])
+    assert torch.equal(p["da"][rest], o["da"][rest]) and torch.equal(p["db"][rest], o["db"][rest])
+
+
+@gpu
 def test_lora_ids_outside_mean_no_adapter():
     c = Case(70, 128, 128, 3, 16)
     o, p = c.buffers(), c.buffers()
