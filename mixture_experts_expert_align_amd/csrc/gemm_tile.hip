@@ -276,20 +276,34 @@ constexpr int kLoraSliceAdapters = 8;
 // Two bf16 in a dword: bits 15 and 31 of the carry out of their exponents.
 __device__ __forceinline__ uint32_t nonfinite_bf16x2(uint32_t v) { return (v & 0x7f807f80u) + 0x00800080u; }
 
-// Zeros in place of a fragment's infinities and NaN; true if some lane had any.
-__device__ __forceinline__ bool lora_finite(bf16x8& f) {
-  i32x4 v = __builtin_bit_cast(i32x4, f);
+// Zeros in place of the infinities and NaN in fragments; true if some lane had
+// any (one test for all of them: one per fragment cost 3 of 36 us).
+template <int N>
+__device__ __forceinline__ bool lora_finite(i32x4 (&f)[N]) {
   uint32_t bad = 0;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) bad |= nonfinite_bf16x2((uint32_t)v[e]);
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) bad |= nonfinite_bf16x2((uint32_t)f[i][e]);
   if (!__any((int)(bad & 0x80008000u))) return false;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const uint32_t b = (nonfinite_bf16x2((uint32_t)v[e]) >> 15) & 0x00010001u;
-    v[e] = (int)((uint32_t)v[e] & ~(b * 0xffffu));
-  }
-  f = as_bf16x8(v);
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t b = (nonfinite_bf16x2((uint32_t)f[i][e]) >> 15) & 0x00010001u;
+      f[i][e] = (int)((uint32_t)f[i][e] & ~(b * 0xffffu));
+    }
   return true;
+}
+template <int N>
+__device__ __forceinline__ bool lora_finite(bf16x8 (&f)[N]) {
+  i32x4 v[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = __builtin_bit_cast(i32x4, f[i]);
+  const bool any = lora_finite(v);
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i] = as_bf16x8(v[i]);
+  return any;
 }
 
 // y of the tile's rows, already written, plus the products with the elements
@@ -467,25 +481,20 @@ __device__ __forceinline__ void lora_rows_mfma(const LoraExt& x, const GemmArgs&
         s[c] = in && ad >= 0 ? *reinterpret_cast<const i32x4*>(low + c * rank + k + 8 * half) : (i32x4){0, 0, 0, 0};
       for (uint32_t left = all; left;) {
         int ga[kBatch];
-        i32x4 w[kBatch][TW];
+        i32x4 w[kBatch * TW];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
           ga[u] = left ? __builtin_amdgcn_readlane(ad, __ffs(left) - 1) : -2;
           left &= ~(uint32_t)__ballot(ad == ga[u]);
 #pragma unroll
           for (int i = 0; i < TW; ++i)   // no adapter left, or past the rank: zeros
-            w[u][i] = __builtin_amdgcn_raw_buffer_load_b128(
+            w[u * TW + i] = __builtin_amdgcn_raw_buffer_load_b128(
                 mr, ga[u] >= 0 && in ? fo[i] + 2 * k : 0x80000000u, ga[u] >= 0 ? ga[u] * g.nfeat * rank * 2 : 0, 0);
         }
+        if (lora_finite(w)) *flag = 1;
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
           const bool own = ad == ga[u];
-          bf16x8 wf[TW];
-#pragma unroll
-          for (int i = 0; i < TW; ++i) {
-            wf[i] = as_bf16x8(w[u][i]);
-            if (lora_finite(wf[i])) *flag = 1;
-          }
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             i32x4 v;
@@ -493,7 +502,7 @@ __device__ __forceinline__ void lora_rows_mfma(const LoraExt& x, const GemmArgs&
             for (int e = 0; e < 4; ++e) v[e] = own ? s[c][e] : 0;
 #pragma unroll
             for (int i = 0; i < TW; ++i)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wf[i], as_bf16x8(v), acc[i][j], 0, 0, 0);
+              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(w[u * TW + i]), as_bf16x8(v), acc[i][j], 0, 0, 0);
           }
         }
       }
@@ -722,9 +731,7 @@ __device__ __forceinline__ void split_tile(const GemmArgs& g, const TileCoord& t
 #pragma unroll
       for (int s = 0; s < NSTEP; ++s) {
         fload(s & 1, k, s);
-#pragma unroll
-        for (int i = 0; i < TW; ++i)
-          if (lora_finite(fw[s & 1][i])) *flag = 1;
+        if (lora_finite(fw[s & 1])) *flag = 1;
         mma(s & 1);
       }
     });
