@@ -184,6 +184,13 @@ CASES = [
     dict(M=64, K=128, I=128, E=3, topk=3, shared=16),
     dict(M=61, K=2048, I=128, E=512, topk=32),
     dict(M=2, K=7168, I=128, E=32, topk=8),
+    # long runs of one wave, up to 8 tokens a slot and more, several slots to a wave
+    dict(M=5, K=16384, I=128, E=4, topk=2),
+    dict(M=8, K=256, I=2048, E=64, topk=8),
+    dict(M=9, K=256, I=2048, E=64, topk=8, order="interleave16"),
+    dict(M=20, K=256, I=1152, E=12, topk=8, shared=1),
+    dict(M=8, K=128, I=128, E=20, topk=7, shared=3),
+    dict(M=64, K=256, I=2432, E=48, topk=4, shared=2),
 ]
 
 
@@ -309,6 +316,31 @@ def test_layer_graph_replays(w):
         for a, b, d in zip(ref, o, o2):
             assert torch.equal(a, b) and torch.equal(a, d), i
     c.check(o)
+
+
+@gpu
+def test_layer_two_graphs_share_a_workspace():
+    """Two captured calls of one plan's size on one stream, replayed in any order."""
+    cs = [Case(M=6, K=256, I=256, E=16, topk=4, seed=i) for i in range(2)]
+    outs, graphs = [], []
+    for c in cs:
+        c.ws = cs[0].ws
+        o = c.outputs()
+        c.call(o)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.call(o)
+        outs.append(o)
+        graphs.append(g)
+    for i in (0, 1, 1, 0, 1):
+        cs[i].x.copy_(torch.randn(6, 256, device="cuda"))
+        ref = cs[i].outputs()
+        cs[i].call(ref)
+        outs[i][0].fill_(float("nan"))
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(ref, outs[i]))
+        cs[i].check(outs[i])
 
 
 @gpu

@@ -11,6 +11,7 @@ the sum of magnitudes; their root mean square error is also held to 2^-18 of
 the result's, far below what one bf16 piece would leave (2^-9)."""
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
@@ -386,3 +387,70 @@ def test_lora_projection_then_layer():
             h = w1[e].double() @ x[t]
             want[t] += wt[t, j].double() * (w2[e].double() @ (h[:128] * torch.sigmoid(h[:128]) * h[128:]))
     assert ((out.double() - want).pow(2).mean() / want.pow(2).mean()).sqrt() <= 1.5 * 2 ** 0.5 * 2.0 ** -8 / 3 ** 0.5
+
+
+@gpu
+def test_lora_and_router_training_step():
+    """As used in training: logits from an adapted projection, the router's
+    weights, their gradient back through the router into the adapters; eager
+    and captured, every stage against its formula at the values it was given."""
+    from operator_refs import route_backward, route_topk
+
+    c = Case(200, 64, 128, 3, 8)
+    r = moe.make_router(64, 4, moe.ROUTE_SIGMOID, renormalize=True, scale=2.0)
+    dw = torch.randn(200, 4, device="cuda")
+
+    def buffers():
+        o = c.buffers()
+        o["ids"] = torch.full((200, 4), 99, dtype=torch.int32, device="cuda")
+        o["wt"] = torch.full((200, 4), float("nan"), device="cuda")
+        o["dl"] = torch.full((200, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+        return o
+
+    def step(o):
+        moe.moe_lora_forward(c.x, c.w, c.a, c.b, c.scale, c.adapter, o["y"], o["low"])
+        moe.moe_route_topk(r, o["y"], o["ids"], o["wt"])
+        moe.moe_route_topk_backward(r, o["y"], o["ids"], dw, o["dl"])
+        moe.moe_lora_dgrad(o["dl"], c.w, c.a, c.b, c.scale, c.adapter, o["dx"], o["low_dy"])
+        moe.moe_lora_wgrad(c.x, o["dl"], o["low"], o["low_dy"], c.adapter, o["da"], o["db"], o["ws"])
+
+    ref, o = buffers(), buffers()
+    step(o)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(o)
+    keys = ("y", "ids", "wt", "dl", "dx", "da", "db")
+    for i in range(3):
+        c.x.copy_(torch.randn(200, 128, device="cuda"))
+        c.adapter.copy_(torch.randint(-1, 3, (200,), device="cuda", dtype=torch.int32))
+        step(ref)
+        for k in keys:
+            o[k].fill_(99)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(ref[k], o[k]) for k in keys), i
+    logits = o["y"].float().cpu().numpy()
+    ids, wt = route_topk(logits, 4, "sigmoid", scale=2.0)
+    assert np.array_equal(o["ids"].cpu().numpy(), ids)
+    assert np.all(np.abs(o["wt"].cpu().numpy() - wt) <= 2.0 ** -23 * np.abs(wt))
+    dl, mag = route_backward(logits, ids, dw.cpu().numpy(), "sigmoid", scale=2.0)
+    got = o["dl"].double().cpu().numpy()
+    assert np.all(np.abs(got - dl) <= 2.0 ** -8 * np.abs(dl) + 2.0 ** -23 * mag + 1e-37)
+    c.dy = o["dl"]
+    c.check(o)
+
+
+@gpu
+def test_lora_workspaces_and_ids_in_succession():
+    """One workspace and one narrow-product buffer for problems of different
+    sizes one after another, with nothing cleared in between."""
+    sizes = [(9000, 128, 64, 3, 8), (33, 320, 192, 40, 40), (300, 64, 448, 4096, 8), (1, 64, 64, 1, 128)]
+    cases = [Case(*z) for z in sizes]
+    ws = torch.full((max(moe.moe_lora_ws_bytes(*z) for z in sizes),), 0xff, dtype=torch.uint8, device="cuda")
+    low = [torch.full((max(moe.moe_lora_low_bytes(*z) for z in sizes),), 0xff, dtype=torch.uint8, device="cuda")
+           for _ in range(2)]
+    for c in cases + cases[::-1]:
+        o = c.buffers()
+        o["low"], o["low_dy"], o["ws"] = low[0], low[1], ws
+        c.call(o)
+        c.check(o)
