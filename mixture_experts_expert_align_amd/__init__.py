@@ -466,20 +466,42 @@ def make_router(E, topk, scoring=ROUTE_SOFTMAX, bias_kind=BIAS_NONE, renormalize
     return MoeRouter(E, topk, groups, topk_groups, scoring, bias_kind, 1 if renormalize else 0, scale)
 
 
-def _device_of(stream, *tensors):
-    """The call's stream, after checking that every tensor lies on the current
-    device (the one the kernels are launched on)."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.is_cuda and t.device.index != dev:
-            raise ValueError(f"tensor on cuda:{t.device.index}, the current device is cuda:{dev}")
-    return _stream(stream)
+def _current() -> int:
+    """The device the kernels are launched on (torch.cuda.current_device())."""
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else torch.cuda.current_device()
+
+
+def _device_for(t: torch.Tensor) -> int:
+    """The current device; for a host tensor the refusal comes before CUDA is
+    initialised for it."""
+    return _current() if t.is_cuda else -2
+
+
+def _on(dev: int, t: Optional[torch.Tensor], name: str, dtype, numel: int) -> Optional[int]:
+    """_arg, and that the tensor lies on device ``dev``."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.numel() >= numel:
+        return t.data_ptr()
+    p = _arg(t, name, dtype, numel)   # names what is wrong
+    raise ValueError(f"{name}: tensor on {t.device}, the current device is cuda:{dev} ({p:#x})")
+
+
+def _ws_on(dev: int, t: torch.Tensor, name: str, nbytes: int) -> int:
+    p = _ws(t, name, nbytes)
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: tensor on {t.device}, the current device is cuda:{dev}")
+    return p
+
+
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 _LOGIT_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 
-def _logits(t: torch.Tensor, E: int, name: str):
+def _logits(dev: int, t: torch.Tensor, E: int, name: str):
     """(pointer, dtype code, row stride) of a [M, E] matrix whose rows are
     contiguous and may lie apart."""
     code = _LOGIT_DTYPES.get(t.dtype)
@@ -487,40 +509,45 @@ def _logits(t: torch.Tensor, E: int, name: str):
         raise ValueError(f"{name}: dtype {t.dtype}, expected torch.float32 or torch.bfloat16")
     if t.dim() != 2 or t.shape[1] != E:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [M, {E}]")
-    if not t.is_cuda:
-        raise ValueError("expected a device tensor")
+    if t.get_device() != dev:
+        if not t.is_cuda:
+            raise ValueError("expected a device tensor")
+        raise ValueError(f"{name}: tensor on {t.device}, the current device is cuda:{dev}")
     M = t.shape[0]
-    if (E > 1 and t.stride(1) != 1) or (M > 1 and t.stride(0) < E):
+    ld, one = t.stride()
+    if (E > 1 and one != 1) or (M > 1 and ld < E):
         raise ValueError(f"{name}: strides {t.stride()}, expected contiguous rows that do not overlap")
-    return t.data_ptr(), code, (t.stride(0) if M > 1 else E)
+    return t.data_ptr(), code, (ld if M > 1 else E)
 
 
 def moe_route_topk(router: MoeRouter, logits, topk_ids, topk_weights, bias=None, stream=None):
     """The topk experts of each row of logits [M, E] (float32 or bf16, rows may
     lie apart) into topk_ids int32 [M, topk] and topk_weights float32 [M, topk]."""
-    ptr, code, ld = _logits(logits, router.E, "logits")
+    E, dev = router.E, _device_for(logits)
+    ptr, code, ld = _logits(dev, logits, E, "logits")
     M = logits.shape[0]
+    n = M * router.topk
     st = load_library().moe_route_topk(
-        ctypes.byref(router), M, ptr, code, ld, _arg(bias, "bias", torch.float32, router.E),
-        _arg(topk_ids, "topk_ids", torch.int32, M * router.topk),
-        _arg(topk_weights, "topk_weights", torch.float32, M * router.topk),
-        _device_of(stream, logits, topk_ids, topk_weights, bias))
+        ctypes.byref(router), M, ptr, code, ld, _on(dev, bias, "bias", torch.float32, E),
+        _on(dev, topk_ids, "topk_ids", torch.int32, n), _on(dev, topk_weights, "topk_weights", torch.float32, n),
+        _raw_stream(stream, dev))
     _check("moe_route_topk", st)
 
 
 def moe_route_topk_backward(router: MoeRouter, logits, topk_ids, dweights, dlogits, bias=None, stream=None):
     """dlogits [M, E] (the logits' dtype) from the gradient dweights [M, topk]
     of the weights moe_route_topk gave for topk_ids."""
-    ptr, code, ld = _logits(logits, router.E, "logits")
-    dptr, dcode, dld = _logits(dlogits, router.E, "dlogits")
+    E, dev = router.E, _device_for(logits)
+    ptr, code, ld = _logits(dev, logits, E, "logits")
+    dptr, dcode, dld = _logits(dev, dlogits, E, "dlogits")
     M = logits.shape[0]
+    n = M * router.topk
     if dcode != code or dlogits.shape[0] != M:
         raise ValueError("dlogits: expected the dtype and shape of logits")
     st = load_library().moe_route_topk_backward(
-        ctypes.byref(router), M, ptr, code, ld, _arg(bias, "bias", torch.float32, router.E),
-        _arg(topk_ids, "topk_ids", torch.int32, M * router.topk),
-        _arg(dweights, "dweights", torch.float32, M * router.topk), dptr, dld,
-        _device_of(stream, logits, topk_ids, dweights, dlogits, bias))
+        ctypes.byref(router), M, ptr, code, ld, _on(dev, bias, "bias", torch.float32, E),
+        _on(dev, topk_ids, "topk_ids", torch.int32, n), _on(dev, dweights, "dweights", torch.float32, n), dptr, dld,
+        _raw_stream(stream, dev))
     _check("moe_route_topk_backward", st)
 
 
@@ -564,15 +591,16 @@ def moe_layer_apply(plan: MoeLayerPlan, x, router_w, w1, w2, out, topk_ids, topk
     n2 = n1 // 2
     if mx and (w1_scale is None or w2_scale is None):
         raise ValueError("MXFP8 weights need w1_scale and w2_scale")
-    w = MoeWeights(_arg(w1, "w1", wt, n1), _arg(w1_scale, "w1_scale", torch.uint8, n1 // 32 if mx else 0),
-                   _arg(w2, "w2", wt, n2), _arg(w2_scale, "w2_scale", torch.uint8, n2 // 32 if mx else 0), None)
+    dev = _device_for(x)
+    w = MoeWeights(_on(dev, w1, "w1", wt, n1), _on(dev, w1_scale, "w1_scale", torch.uint8, n1 // 32 if mx else 0),
+                   _on(dev, w2, "w2", wt, n2), _on(dev, w2_scale, "w2_scale", torch.uint8, n2 // 32 if mx else 0), None)
     st = load_library().moe_layer_apply(
-        ctypes.byref(plan), _arg(x, "x", torch.bfloat16, p.M * p.K),
-        _arg(router_w, "router_w", torch.bfloat16, r.E * p.K),
-        _arg(router_bias, "router_bias", torch.float32, r.E), ctypes.byref(w),
-        _arg(out, "out", torch.bfloat16, p.M * p.K), _arg(topk_ids, "topk_ids", torch.int32, p.M * r.topk),
-        _arg(topk_weights, "topk_weights", torch.float32, p.M * r.topk), _ws(ws, "ws", plan.ws_bytes),
-        _device_of(stream, x, router_w, w1, w2, out, topk_ids, topk_weights, ws, router_bias, w1_scale, w2_scale))
+        ctypes.byref(plan), _on(dev, x, "x", torch.bfloat16, p.M * p.K),
+        _on(dev, router_w, "router_w", torch.bfloat16, r.E * p.K),
+        _on(dev, router_bias, "router_bias", torch.float32, r.E), ctypes.byref(w),
+        _on(dev, out, "out", torch.bfloat16, p.M * p.K), _on(dev, topk_ids, "topk_ids", torch.int32, p.M * r.topk),
+        _on(dev, topk_weights, "topk_weights", torch.float32, p.M * r.topk), _ws_on(dev, ws, "ws", plan.ws_bytes),
+        _raw_stream(stream, dev))
     _check("moe_layer_apply", st)
 
 
@@ -614,12 +642,13 @@ def _lora_project(fn, v, C, w, a, b, scale, adapter, out, out_cols, low, stream)
     R = v.shape[0]
     if v.shape[1:] != w.shape[C:C + 1] or tuple(out.shape) != (R, w.shape[out_cols]):
         raise ValueError(f"rows {tuple(v.shape)} and {tuple(out.shape)} do not fit w {tuple(w.shape)}")
-    p = MoeLoraProblem(R, N, K, G, rank)
+    p, dev = MoeLoraProblem(R, N, K, G, rank), _device_for(v)
     st = getattr(load_library(), fn)(
-        ctypes.byref(p), _arg(v, "rows", torch.bfloat16, 0), _arg(w, "w", torch.bfloat16, 0),
-        _arg(a, "a", torch.bfloat16, 0), _arg(b, "b", torch.bfloat16, 0), _arg(scale, "scale", torch.float32, G),
-        _arg(adapter, "adapter", torch.int32, R), _arg(out, "output rows", torch.bfloat16, 0),
-        _ws(low, "low", 6 * R * rank), _device_of(stream, v, w, a, b, scale, adapter, out, low))
+        ctypes.byref(p), _on(dev, v, "rows", torch.bfloat16, 0), _on(dev, w, "w", torch.bfloat16, 0),
+        _on(dev, a, "a", torch.bfloat16, 0), _on(dev, b, "b", torch.bfloat16, 0),
+        _on(dev, scale, "scale", torch.float32, G), _on(dev, adapter, "adapter", torch.int32, R),
+        _on(dev, out, "output rows", torch.bfloat16, 0), _ws_on(dev, low, "low", 6 * R * rank),
+        _raw_stream(stream, dev))
     _check(fn, st)
 
 
@@ -643,12 +672,12 @@ def moe_lora_wgrad(x, dy, low_x, low_dy, adapter, da, db, ws, accumulate: bool =
     if dy.shape[0] != R or da.shape[2] != K or tuple(db.shape) != (G, N, rank):
         raise ValueError(f"x {tuple(x.shape)}, dy {tuple(dy.shape)}, da {tuple(da.shape)}, db {tuple(db.shape)} "
                          "do not fit")
-    p = MoeLoraProblem(R, N, K, G, rank)
+    p, dev = MoeLoraProblem(R, N, K, G, rank), _device_for(x)
     low = 6 * R * rank
     st = load_library().moe_lora_wgrad(
-        ctypes.byref(p), _arg(x, "x", torch.bfloat16, 0), _arg(dy, "dy", torch.bfloat16, 0), _ws(low_x, "low_x", low),
-        _ws(low_dy, "low_dy", low), _arg(adapter, "adapter", torch.int32, R), _arg(da, "da", torch.float32, 0),
-        _arg(db, "db", torch.float32, 0), 1 if accumulate else 0,
-        _ws(ws, "ws", max(load_library().moe_lora_ws_bytes(ctypes.byref(p)), 0)),
-        _device_of(stream, x, dy, low_x, low_dy, adapter, da, db, ws))
+        ctypes.byref(p), _on(dev, x, "x", torch.bfloat16, 0), _on(dev, dy, "dy", torch.bfloat16, 0),
+        _ws_on(dev, low_x, "low_x", low), _ws_on(dev, low_dy, "low_dy", low),
+        _on(dev, adapter, "adapter", torch.int32, R), _on(dev, da, "da", torch.float32, 0),
+        _on(dev, db, "db", torch.float32, 0), 1 if accumulate else 0,
+        _ws_on(dev, ws, "ws", max(load_library().moe_lora_ws_bytes(ctypes.byref(p)), 0)), _raw_stream(stream, dev))
     _check("moe_lora_wgrad", st)
