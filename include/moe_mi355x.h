@@ -497,6 +497,7 @@ int moe_route_topk_backward(const moe_router* r, int64_t M, const void* logits, 
  * (the activations stay bf16, unlike moe_apply_contiguous, which quantises
  * them), values below bf16's normal range excepted, which may count as 0.
  * A token without an expert to choose gets only the shared experts, or +0.0.
+ * Infinite or NaN weights of an expert reach the tokens that chose it only.
  * ------------------------------------------------------------------------- */
 typedef struct moe_layer_problem {
   int64_t M;               /* tokens, 1 .. 64                                  */
@@ -512,7 +513,7 @@ typedef struct moe_layer_problem {
 typedef struct moe_layer_plan {
   moe_layer_problem prob;
   int32_t abi_version;
-  int32_t splits;          /* workgroups that share 16 columns of the output   */
+  int32_t splits;          /* workgroups that share 32 columns of the output   */
   int64_t max_slots;       /* experts that can hold a token, shared included   */
   int64_t rows;            /* rows of the intermediate: M (topk + shared)      */
   int64_t ws_bytes;        /* size of the workspace                            */
@@ -562,7 +563,9 @@ int moe_layer_apply(const moe_layer_plan* plan, const void* x, const void* route
  * in a fixed order (the same bits on every run); s and t are kept to float32
  * precision, y and dx rounded to bf16 once.  W is shared by all rows and
  * frozen here (its own gradient is moe_grouped_wgrad with one group).  Row
- * adapters may name (request, expert) pairs as well as requests.
+ * adapters may name (request, expert) pairs as well as requests.  Infinities
+ * and NaN in one adapter, or in one row, reach that adapter's or that row's
+ * results only.
  *
  * `low` (device, moe_lora_low_bytes, 16-byte aligned) receives s or t in the
  * library's own form; moe_lora_wgrad reads the one that moe_lora_forward

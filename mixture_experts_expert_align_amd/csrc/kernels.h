@@ -257,7 +257,7 @@ struct LayerArgs {
   int32_t* rows;               // [cap] token of each row of z
   float* roww;                 // [cap] its weight
   uint16_t* z;                 // [cap, I]
-  float* part;                 // [K / 16][splits][M][16]
+  float* part;                 // [K / 32][splits][M][32]
   int32_t logit_ld, max_slots, cap;
   // set by the launcher
   int32_t rsplit, runits;      // K splits and units of the router
