@@ -588,39 +588,42 @@ __device__ __forceinline__ void gate_up_strip(const LayerArgs& g, const SlotLds&
   }
 }
 
-// The same for a slot of up to 8 tokens, by whole lines.
-template <bool MX>
+// The same of F features (8 or 16) for a slot of up to 8 tokens, by whole
+// lines.
+template <bool MX, int F>
 __device__ __forceinline__ void gate_up_lines(const LayerArgs& g, const SlotLds& s, int slot, int f0, int kw, bool live,
                                               f32x4* red) {
+  constexpr int H = F / 8, NR = 2 * H;   // groups of 8 rows: the features' gates, then their ups
   const int lane = phase_thread() & 63, q = lane >> 4, l16 = lane & 15;
   const int e = __builtin_amdgcn_readfirstlane(s.e[slot]);
   const int pos0 = s.pos[slot], cnt = s.pos[slot + 1] - pos0;
   const int n = live ? (g.K / 128 - kw + g.ks - 1) / g.ks : 0;
   const Weights<MX> wr = expert_weights<MX>(g.w1, g.w1s, e, 2ll * g.I * g.K);
   const __amdgpu_buffer_rsrc_t ar = buffer_rsrc(g.x, (int64_t)g.M * g.K * 2);
-  // groups: features 0 .. 7 and 8 .. 15 of gate, then of up
   const int row = w1_row(f0 + (l16 >> 1), 0, g.I, g.w1_order);
   const int up = __builtin_amdgcn_readfirstlane(w1_row(f0, 1, g.I, g.w1_order) - w1_row(f0, 0, g.I, g.w1_order));
-  const int dr[4] = {0, 8, up, up + 8};
-  const int tk = l16 & 7;
+  int dr[NR];
+#pragma unroll
+  for (int t = 0; t < NR; ++t) dr[t] = 8 * (t % H) + (t / H) * up;
+  const int tk = l16 & 7, hh = l16 >> 3;
   const uint32_t ao = tk < cnt ? line_a<MX>(s.tok[pos0 + tk], g.K, l16, q) : kPast;
   const float wt = tk >= cnt ? 0.f : g.solo ? s.w[pos0 + tk] : load_relaxed(g.roww + pos0 + tk);
-  f32x4 acc[4];
+  f32x4 acc[NR];
 #pragma unroll
-  for (int t = 0; t < 4; ++t) acc[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
-  stream_lines<MX, 4, 2>(wr, ar, line_w<MX>(row, g.K, l16, q), lane_s(row, g.K), dr, g.K, ao, kw, g.ks, n, acc);
+  for (int t = 0; t < NR; ++t) acc[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  stream_lines<MX, NR, 2>(wr, ar, line_w<MX>(row, g.K, l16, q), lane_s(row, g.K), dr, g.K, ao, kw, g.ks, n, acc);
 #pragma unroll
-  for (int t = 0; t < 4; ++t) red[(kw * 4 + t) * 64 + lane] = acc[t];
+  for (int t = 0; t < NR; ++t) red[(kw * NR + t) * 64 + lane] = acc[t];
   __syncthreads();
-  if (live && kw == 0 && tk < cnt) {
-    // lane (token tk, features 8 (l16 / 8) + 2 q, + 1): even slots from the
-    // token's column, odd ones from the column 8 on
-    const int hh = l16 >> 3, at = 16 * q + tk;
+  if (live && kw == 0 && tk < cnt && hh < H) {
+    // lane (token tk, features 8 hh + 2 q, + 1): even slots from the token's
+    // column, odd ones from the column 8 on
+    const int at = 16 * q + tk;
     float v[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
     for (int k = 0; k < g.ks; ++k)
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const f32x4 lo = red[(k * 4 + 2 * t + hh) * 64 + at], hi = red[(k * 4 + 2 * t + hh) * 64 + at + 8];
+        const f32x4 lo = red[(k * NR + H * t + hh) * 64 + at], hi = red[(k * NR + H * t + hh) * 64 + at + 8];
         v[t][0] += lo[0] + hi[1];
         v[t][1] += lo[2] + hi[3];
       }
@@ -630,6 +633,9 @@ __device__ __forceinline__ void gate_up_lines(const LayerArgs& g, const SlotLds&
   }
   __syncthreads();
 }
+
+// Features of an item of the first launch.
+__host__ __device__ constexpr int item_features(bool mx, bool wide) { return mx || wide ? 16 : 8; }
 
 // WIDE: M > 8 (a slot may hold up to 64 tokens).  At most 128 registers, so
 // two workgroups share a CU and one's joins overlap the other's streaming.
@@ -744,14 +750,19 @@ __global__ void __launch_bounds__(kThreads, 4) layer_gate_up_kernel(LayerArgs g)
     __syncthreads();
   }
 
-  // Items (slot, nh strips of 16 features): a workgroup starts with its own and
+  // Items (slot, nh strips of F features): a workgroup starts with its own and
   // then claims one after another, the last slots first (the shared experts
   // hold every token and take longest).  With a fixed share each, the
   // workgroups that got the shared experts' strips ended last by half the
-  // launch; in chunks of several items the ends lay further apart.
+  // launch; in chunks of several items the ends lay further apart.  bf16 of
+  // few tokens does best with short items (4 tokens, 4096 x 8192: F = 8 583 us,
+  // 16 605); with MXFP8's shorter rows a start and a join for each 8 features
+  // cost more than the closer ends bring (6144 x 2048: 8 185 us, 16 163; the
+  // last item of each workgroup halved, 172).
+  constexpr int F = item_features(MX, WIDE);
   const int nh = kWaves / g.ks;
   const int h = wave / g.ks, kw = wave % g.ks;
-  const int strips = g.I / 16, per = (strips + nh - 1) / nh;
+  const int strips = g.I / F, per = (strips + nh - 1) / nh;
   const int items = nslots * per;
   f32x4* mine = red + h * g.ks * 4 * 64;
   for (int claim = blockIdx.x; claim < items;) {
@@ -764,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 4) layer_gate_up_kernel(LayerArgs g)
     const bool live = strip < strips;
     const int pos0 = s.pos[slot];
     const int cnt = __builtin_amdgcn_readfirstlane(s.pos[slot + 1] - pos0);
-    if (!WIDE || cnt <= 8) gate_up_lines<MX>(g, s, slot, 16 * strip, kw, live, mine);
+    if (!WIDE || cnt <= 8) gate_up_lines<MX, F>(g, s, slot, F * strip, kw, live, mine);
     else if (cnt <= 16) gate_up_strip<MX, 1, MX ? 2 : 4, 2>(g, s, slot, 16 * strip, kw, live, mine);
     else if (cnt <= 32) gate_up_strip<MX, 2, MX ? 1 : 2, 2>(g, s, slot, 16 * strip, kw, live, mine);
     else gate_up_strip<MX, 4, 1, MX ? 1 : 2>(g, s, slot, 16 * strip, kw, live, mine);
@@ -985,8 +996,8 @@ hipError_t launch_layer(LayerArgs g, bool mxfp8, hipStream_t s) {
   g.splits = layer_splits(g.K);
   g.solo = g.runits <= kLayerSoloUnits && g.M <= kWaves && g.r.E <= 64;
   g.ks = g.K >= 1024 ? 8 : g.K >= 512 ? 4 : g.K >= 256 ? 2 : 1;
-  const int nh = kWaves / g.ks;
-  const int64_t items = (int64_t)g.max_slots * ((g.I / 16 + nh - 1) / nh);
+  const int nh = kWaves / g.ks, f = item_features(mxfp8, g.M > 8);
+  const int64_t items = (int64_t)g.max_slots * ((g.I / f + nh - 1) / nh);
   const int64_t units = g.runits + (g.M + kWaves - 1) / kWaves;
   int64_t grid = items > units ? items : units;
   if (grid > 512) grid = 512;
