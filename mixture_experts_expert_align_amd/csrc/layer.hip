@@ -21,10 +21,11 @@
 // scale, exact in bf16), the activations stay bf16.
 //
 // Measured, first launch + second: 4 tokens, 27 of 64 bf16 experts of 8192
-// features, K = 4096: 602 + 309 us for 5.3 GB of weights, 5.9 TB/s; 16
-// tokens, 33 MXFP8 experts of 2048, K = 6144: 161 + 75 us for 1.27 GB, 5.4
-// TB/s; 61 tokens, 128 bf16 experts of 1024 and 2 shared, K = 4096: 386 + 191
-// us for 3.2 GB, 5.6 TB/s; 7 tokens, 9 experts of 512, K = 256: 10.6 + 8.0 us, latency
+// features, K = 4096: 580 + 305 us for 5.4 GB of weights, 6.1 TB/s; 16
+// tokens, 27 of 33 MXFP8 experts of 2048, K = 6144: 161 + 75 us for 1.04 GB,
+// 4.4 TB/s (18 us of routing first, 20 us from the median workgroup's end to
+// the last one's); 61 tokens, 128 bf16 experts of 1024 and 2 shared, K = 4096: 386 + 191
+// us for 3.2 GB, 5.6 TB/s; 7 tokens, 8 experts of 512, K = 256: 9.8 + 8.4 us, latency
 // (launch, router, ranking, two streams' round trips).  What such reads reach
 // at best is 6.0 to 6.2 TB/s.
 //
