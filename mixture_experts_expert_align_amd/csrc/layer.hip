@@ -727,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 4) layer_gate_up_kernel(LayerArgs g)
           }
         }
       }
-      // Keeps this round's work of thread 0 apart from the next claim's: with no
+      // Keeps this unit's work of thread 0 apart from the next claim's: with no
       // barrier between the two, the compiler may run thread 0 through both
       // while the other lanes of its wave go round without it, and the
       // wave's barriers no longer match the other waves'.
