@@ -265,7 +265,7 @@ struct LayerArgs {
   int32_t splits, ks;          // workgroups per strip of W2; waves of a W1 strip
 };
 
-int32_t layer_splits(int64_t K);
+int32_t layer_splits(int64_t K, int64_t blocks);
 int32_t layer_router_splits(int64_t K);
 hipError_t launch_layer(LayerArgs g, bool mxfp8, hipStream_t s);
 

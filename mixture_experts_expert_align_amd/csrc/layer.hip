@@ -980,12 +980,17 @@ hipError_t launch(const LayerArgs& g, unsigned grid1, hipStream_t s) {
 }  // namespace
 
 // Splits of the second launch: the smallest power of two, up to 8, that gives
-// the chip its two workgroups per CU.  K = 6144 (192 strips), MXFP8, 33
-// experts of 2048: 1 / 2 / 4 / 8 splits 127 / 92 / 80 / 101 us (more
-// workgroups than fit pay their start and their join again).
-int32_t layer_splits(int64_t K) {
+// the chip its two workgroups per CU, but not so many that a wave has fewer
+// than 4 blocks of 128 features to read with every slot filled (`blocks` in
+// all).  K = 6144 (192 strips), MXFP8, 33 experts of 2048: 1 / 2 / 4 / 8 splits
+// 127 / 92 / 80 / 101 us (more workgroups than fit pay their start and their
+// join again).  The whole layer, bf16, 1 / 2 / 4 / 8 splits: one token, K =
+// 7168, 2 of 64 experts of 2048 (32 blocks) 48 / 50 / 56 / - us; one, K =
+// 2048, 8 of 64 of 1024 (64) 43 / 42 / 43 / 47; 4 tokens, K = 2048, 27 of 64
+// of 512 (at most 128) 63 / 57 / 55 / 62.
+int32_t layer_splits(int64_t K, int64_t blocks) {
   int32_t s = 1;
-  while (s < 8 && K / (16 * kDownTiles) * s < 512) s *= 2;
+  while (s < 8 && K / (16 * kDownTiles) * s < 512 && blocks >= 2 * s * kWaves * 4) s *= 2;
   return s;
 }
 
@@ -994,7 +999,7 @@ int32_t layer_router_splits(int64_t K) { return (int32_t)((K / 128 + kUnitSteps 
 hipError_t launch_layer(LayerArgs g, bool mxfp8, hipStream_t s) {
   g.rsplit = layer_router_splits(g.K);
   g.runits = (g.r.E + 15) / 16 * g.rsplit;
-  g.splits = layer_splits(g.K);
+  g.splits = layer_splits(g.K, (int64_t)g.max_slots * (g.I / 128));
   g.solo = g.runits <= kLayerSoloUnits && g.M <= kWaves && g.r.E <= 64;
   g.ks = g.K >= 1024 ? 8 : g.K >= 512 ? 4 : g.K >= 256 ? 2 : 1;
   const int nh = kWaves / g.ks, f = item_features(mxfp8, g.M > 8);

@@ -802,8 +802,8 @@ int moe_layer_plan_init(moe_layer_plan* plan, const moe_layer_problem* prob) {
       2ll * r.E * P.K >= (1ll << 31) || 2 * rows * P.I >= (1ll << 31))
     return layer_fail(plan, MOE_EUNSUPPORTED, "the layer addresses one expert and the intermediate with 32-bit offsets");
   plan->abi_version = MOE_ABI_VERSION;
-  plan->splits = layer_splits(P.K);
   plan->max_slots = (r.E < P.M * r.topk ? r.E : P.M * r.topk) + P.shared_experts;
+  plan->splits = layer_splits(P.K, plan->max_slots * (P.I / 128));
   plan->rows = rows;
   int64_t o = 0;
   auto take = [&](int64_t bytes) {
