@@ -982,7 +982,9 @@ hipError_t launch(const LayerArgs& g, unsigned grid1, hipStream_t s) {
 // Splits of the second launch: the smallest power of two, up to 8, that gives
 // the chip its two workgroups per CU, but not so many that a wave has fewer
 // than 4 blocks of 128 features to read with every slot filled (`blocks` in
-// all).  K = 6144 (192 strips), MXFP8, 33 experts of 2048: 1 / 2 / 4 / 8 splits
+// all; 2 while there are fewer than 64 workgroups, where it is the few CUs'
+// loads that take the time: 7 tokens, K = 256, 32 blocks 17.9 us with 2
+// splits, 19.2 with one).  K = 6144 (192 strips), MXFP8, 33 experts of 2048: 1 / 2 / 4 / 8 splits
 // 127 / 92 / 80 / 101 us (more workgroups than fit pay their start and their
 // join again).  The whole layer, bf16, 1 / 2 / 4 / 8 splits: one token, K =
 // 7168, 2 of 64 experts of 2048 (32 blocks) 48 / 50 / 56 / - us; one, K =
@@ -990,7 +992,8 @@ hipError_t launch(const LayerArgs& g, unsigned grid1, hipStream_t s) {
 // of 512 (at most 128) 63 / 57 / 55 / 62.
 int32_t layer_splits(int64_t K, int64_t blocks) {
   int32_t s = 1;
-  while (s < 8 && K / (16 * kDownTiles) * s < 512 && blocks >= 2 * s * kWaves * 4) s *= 2;
+  const int64_t strips = K / (16 * kDownTiles);
+  while (s < 8 && strips * s < 512 && blocks >= 2 * s * kWaves * (strips * s < 64 ? 2 : 4)) s *= 2;
   return s;
 }
 
