@@ -228,21 +228,22 @@ def test_router_ties_go_to_the_lowest():
 
 
 @gpu
+@pytest.mark.parametrize("M", [37, 4103])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-def test_router_row_strides(dtype):
+def test_router_row_strides(dtype, M):
     """Rows inside a wider matrix (at an odd column for the alignment), and the
     gradient into one: the columns between stay as they were."""
-    wide = logits(37, 150, dtype, 9)
+    wide = logits(M, 150, dtype, 9)
     l = wide[:, 3:131]
-    dw = np.random.default_rng(1).normal(size=(37, 8)).astype(np.float32)
+    dw = np.random.default_rng(1).normal(size=(M, 8)).astype(np.float32)
     r = moe.make_router(128, 8, renormalize=False)
     out = {}
     for name, src in (("view", l), ("dense", l.contiguous())):
-        ids = torch.empty(37, 8, dtype=torch.int32, device="cuda")
-        w = torch.empty(37, 8, device="cuda")
+        ids = torch.empty(M, 8, dtype=torch.int32, device="cuda")
+        w = torch.empty(M, 8, device="cuda")
         moe.moe_route_topk(r, src, ids, w)
-        big = torch.full((37, 140), 5.0, dtype=dtype, device="cuda")
-        dl = big[:, 5:133] if name == "view" else torch.empty(37, 128, dtype=dtype, device="cuda")
+        big = torch.full((M, 140), 5.0, dtype=dtype, device="cuda")
+        dl = big[:, 5:133] if name == "view" else torch.empty(M, 128, dtype=dtype, device="cuda")
         moe.moe_route_topk_backward(r, src, ids, torch.from_numpy(dw).cuda(), dl)
         if name == "view":
             assert (big[:, :5] == 5.0).all() and (big[:, 133:] == 5.0).all()
@@ -252,10 +253,11 @@ def test_router_row_strides(dtype):
 
 
 @gpu
-def test_router_backward_skips_bad_slots_and_adds_repeated_ones():
-    l = logits(3, 32, torch.float32, 4)
-    dw = np.random.default_rng(2).normal(size=(3, 4)).astype(np.float32)
-    ids = np.array([[1, -1, 5, 99], [4, 4, 2, 31], [-1, -1, -1, -5]], np.int32)
+@pytest.mark.parametrize("copies", [1, 701])
+def test_router_backward_skips_bad_slots_and_adds_repeated_ones(copies):
+    l = logits(3 * copies, 32, torch.float32, 4)
+    dw = np.random.default_rng(2).normal(size=(3 * copies, 4)).astype(np.float32)
+    ids = np.array([[1, -1, 5, 99], [4, 4, 2, 31], [-1, -1, -1, -5]] * copies, np.int32)
     for scoring in ("softmax", "sigmoid"):
         for renorm in (True, False):
             r = moe.make_router(32, 4, SCORING[scoring], renormalize=renorm)
