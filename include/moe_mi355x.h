@@ -539,8 +539,9 @@ int moe_layer_plan_init(moe_layer_plan* plan, const moe_layer_problem* prob);
  * for moe_apply_contiguous (expert_map must be NULL); out: device bf16 [M, K];
  * topk_ids: device int32 [M, topk] and topk_weights: device float32 [M, topk],
  * written; ws: device, plan->ws_bytes, 16-byte aligned, zero-filled before
- * its first call.  Each call leaves it ready for the next; calls that share a
- * workspace must not overlap.  The first launch waits in the kernel for the
+ * its first call.  Each call leaves it ready for the next, of this plan or of
+ * any other that it is large enough for; calls that share a workspace must not
+ * overlap.  The first launch waits in the kernel for the
  * routing, for about a second at most: the int32 at off_status counts waits
  * that gave up, summed over calls (non-zero: some call's outputs are
  * undefined, and the workspace must be zero-filled again). */

@@ -566,7 +566,8 @@ def moe_layer_plan_init(prob: MoeLayerProblem) -> MoeLayerPlan:
 
 
 def allocate_layer_workspace(plan: MoeLayerPlan, device="cuda") -> torch.Tensor:
-    """The layer's workspace, zero-filled (its counters start at zero)."""
+    """The layer's workspace, zero-filled (its counters start at zero); it also
+    serves any other plan whose ws_bytes it holds."""
     return torch.zeros(plan.ws_bytes, dtype=torch.uint8, device=device)
 
 

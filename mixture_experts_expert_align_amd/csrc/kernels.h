@@ -225,10 +225,12 @@ constexpr int kLayerMaxShared = 16;
 constexpr int kLayerSoloUnits = 2;       // router units up to which every workgroup routes by itself
 constexpr int kLayerMaxRoutes = kLayerMaxM * kLayerMaxTopk;
 // the sync area, int32 words, one 128-byte line per counter that many
-// workgroups touch at once; then one word per strip of the second launch
+// workgroups touch at once, at the same places for every plan; then one word
+// per strip of the second launch, which the first launch clears
 enum { kLayerClaim = 0, kLayerArrived = kSyncLine, kLayerRouted = 2 * kSyncLine, kLayerNumSlots = 2 * kSyncLine + 1,
        kLayerNumRows = 2 * kSyncLine + 2,
-       kLayerDone = 3 * kSyncLine, kLayerItems = 4 * kSyncLine, kLayerRanked = 5 * kSyncLine, kLayerStrips = 6 * kSyncLine };
+       kLayerDone = 3 * kSyncLine, kLayerItems = 4 * kSyncLine, kLayerRanked = 5 * kSyncLine, kLayerStatus = 6 * kSyncLine,
+       kLayerStrips = 8 * kSyncLine };
 
 struct alignas(16) LayerSlot {
   int32_t e, cnt, pos0, pad;   // expert, its tokens, their first row of z
@@ -250,7 +252,7 @@ struct LayerArgs {
   int32_t* ids;                // [M, topk]
   float* wts;
   // workspace
-  int32_t* sync;               // [kLayerStrips + K / 16]
+  int32_t* sync;               // [kLayerStrips + K / 32]
   int32_t* status;             // [1] waits that timed out
   float* logits;               // [rsplit][M][logit_ld] partial sums
   LayerSlot* slots;            // [max_slots]

@@ -52,6 +52,7 @@ constexpr int kThreads = 64 * kWaves;
 constexpr int kSpinLimit = 1 << 20;   // polls, each a round trip to memory
 constexpr uint32_t kPast = 0x80000000u;   // an offset past every buffer: loads give 0
 constexpr int kUnitSteps = kWaves;    // 128-wide blocks of K per router unit, one per wave
+constexpr int kDownTiles = 2;         // tiles of 16 output features per strip of the second launch
 
 __device__ __forceinline__ int load_relaxed(const int32_t* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -659,6 +660,11 @@ __global__ void __launch_bounds__(kThreads, 4) layer_gate_up_kernel(LayerArgs g)
   SlotLds& s = *reinterpret_cast<SlotLds*>(smem + kStream);
   int nslots;
 
+  // The second launch's arrival counters start at 0.  Cleared here and not by
+  // their last reader: a plan with another K has other data at their place.
+  if (g.splits > 1 && blockIdx.x == gridDim.x - 1)
+    for (int i = threadIdx.x; i < g.K / (16 * kDownTiles); i += kThreads) store_relaxed(g.sync + kLayerStrips + i, 0);
+
   if (NV == 1 && !WIDE && g.solo) {
     // a small router: every workgroup computes the whole routing by itself
     constexpr int kLogits = ((int)sizeof(RouteLds) + kWaves * 64 * 2 * 8 + 15) / 16 * 16;
@@ -795,8 +801,6 @@ __global__ void __launch_bounds__(kThreads, 4) layer_gate_up_kernel(LayerArgs g)
 // the wave's [token][32] tile in LDS.  The waves' sums meet in LDS in wave order; with
 // more than one split the workgroup that arrives last adds the splits' sums
 // in order.
-constexpr int kDownTiles = 2;
-
 template <bool MX, int CT, int P, int D>
 __device__ __forceinline__ void down_run(const LayerArgs& g, const LayerSlot& sl, const uint32_t (&wo)[kDownTiles],
                                          const uint32_t (&so)[kDownTiles], int b0, int nb, f32x4* tile) {
@@ -939,7 +943,6 @@ __global__ void __launch_bounds__(kThreads, 4) layer_down_kernel(LayerArgs g) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) sum[r] += load_relaxed(p + (int64_t)k * g.M * 4 * kQ + r);
     }
-    if (s_last && threadIdx.x == 0) store_relaxed(g.sync + kLayerStrips + strip, 0);
   }
   if (finish) {
     uint32_t h[4];

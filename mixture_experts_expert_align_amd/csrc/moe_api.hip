@@ -811,8 +811,8 @@ int moe_layer_plan_init(moe_layer_plan* plan, const moe_layer_problem* prob) {
     o = up(o + bytes, kAlign);
     return at;
   };
-  plan->off_sync = take(4 * (kLayerStrips + P.K / 16));
-  plan->off_status = take(4);
+  plan->off_sync = take(4 * (kLayerStrips + P.K / 32));
+  plan->off_status = plan->off_sync + 4 * kLayerStatus;
   plan->off_logits = take(4 * layer_router_splits(P.K) * P.M * up(r.E, 16));
   plan->off_slots = take((int64_t)sizeof(LayerSlot) * plan->max_slots);
   plan->off_rows = take(4 * rows);

@@ -396,3 +396,26 @@ def test_layer_mxfp8_decodes_every_code_exactly():
             up = decode_mx(c.w1[0], c.s1[0])[I:, k0 + t]
             want = (up * 32).float().bfloat16()
             assert torch.equal(o[0][t, :I], want) or torch.equal(o[0][t, :I] + 0.0, want + 0.0), k0 + t
+
+
+@gpu
+@pytest.mark.parametrize("w", ["bf16", "mxfp8"])
+def test_layer_workspace_serves_plans_of_other_sizes(w):
+    """One workspace, zero-filled once, for plans of different K, E and M in
+    turn (the smallest K first): each call gives the bits of a workspace of its
+    own, and the status word counts nothing."""
+    cs = [Case(w=w, seed=i, **kw) for i, kw in enumerate([
+        dict(M=8, K=256, I=128, E=64, topk=8), dict(M=4, K=6144, I=1024, E=8, topk=2),
+        dict(M=40, K=1024, I=256, E=130, topk=8, shared=1), dict(M=5, K=2048, I=1152, E=8, topk=2)])]
+    assert cs[1].plan.splits > 1 and cs[3].plan.splits > 1
+    refs = []
+    for c in cs:
+        refs.append(c.outputs())
+        c.call(refs[-1])
+        c.check(refs[-1])
+    ws = torch.zeros(max(c.plan.ws_bytes for c in cs), dtype=torch.uint8, device="cuda")
+    for i in (0, 1, 2, 3, 1, 0, 3, 2, 0, 2, 1):
+        o = cs[i].outputs()
+        cs[i].call(o, ws=ws)
+        assert all(torch.equal(a, b) for a, b in zip(o, refs[i])), i
+        moe.check_layer_status(cs[i].plan, ws)
