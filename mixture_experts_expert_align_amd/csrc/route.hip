@@ -281,12 +281,18 @@ hipError_t launch_rows_backward(const RouterArgs& r, int64_t M, const void* logi
   return hipGetLastError();
 }
 
-}  // namespace
+// Tokens of a launch: it takes fewer than 2^32 threads (HIP drops the rest of a
+// larger grid without an error), up to 64 of them to a token.
+constexpr int64_t kLaunchTokens = 1 << 25;
 
-hipError_t launch_route_topk(const RouterArgs& r, int64_t M, const void* logits, bool bf16, int64_t ld,
-                             const float* bias, int32_t* ids, float* weights, hipStream_t s) {
-  if (M == 0) return hipSuccess;
-  if (M >= kRowsForwardTokens && r.E <= kRowsForwardExperts && r.topk <= 16 && r.groups <= 16) {
+const void* token_rows(const void* p, bool bf16, int64_t elements) {
+  return static_cast<const char*>(p) + elements * (bf16 ? 2 : 4);
+}
+
+// many: the call has enough tokens for 16 lanes each
+hipError_t launch_forward(const RouterArgs& r, bool many, int64_t M, const void* logits, bool bf16, int64_t ld,
+                          const float* bias, int32_t* ids, float* weights, hipStream_t s) {
+  if (many && r.E <= kRowsForwardExperts && r.topk <= 16 && r.groups <= 16) {
     if (r.E <= 128) return launch_rows<8>(r, M, logits, bf16, ld, bias, ids, weights, s);
     return launch_rows<16>(r, M, logits, bf16, ld, bias, ids, weights, s);
   }
@@ -297,11 +303,10 @@ hipError_t launch_route_topk(const RouterArgs& r, int64_t M, const void* logits,
   return launch_topk<32>(r, M, logits, bf16, ld, bias, ids, weights, s);
 }
 
-hipError_t launch_route_topk_backward(const RouterArgs& r, int64_t M, const void* logits, bool bf16, int64_t ld,
-                                      const float* bias, const int32_t* ids, const float* dw, void* dl,
-                                      int64_t dl_ld, hipStream_t s) {
-  if (M == 0) return hipSuccess;
-  if (M >= kRowsBackwardTokens && r.E <= kRowsBackwardExperts && r.topk <= 16) {
+hipError_t launch_backward(const RouterArgs& r, bool many, int64_t M, const void* logits, bool bf16, int64_t ld,
+                           const float* bias, const int32_t* ids, const float* dw, void* dl, int64_t dl_ld,
+                           hipStream_t s) {
+  if (many && r.E <= kRowsBackwardExperts && r.topk <= 16) {
     if (r.E <= 128) return launch_rows_backward<8>(r, M, logits, bf16, ld, bias, ids, dw, dl, dl_ld, s);
     if (r.E <= 256) return launch_rows_backward<16>(r, M, logits, bf16, ld, bias, ids, dw, dl, dl_ld, s);
     return launch_rows_backward<32>(r, M, logits, bf16, ld, bias, ids, dw, dl, dl_ld, s);
@@ -314,6 +319,28 @@ hipError_t launch_route_topk_backward(const RouterArgs& r, int64_t M, const void
     hipLaunchKernelGGL((route_topk_backward_kernel<false>), grid, block, 0, s, r, M, logits, ld, bias, ids, dw, dl,
                        dl_ld);
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_route_topk(const RouterArgs& r, int64_t M, const void* logits, bool bf16, int64_t ld,
+                             const float* bias, int32_t* ids, float* weights, hipStream_t s) {
+  hipError_t e = hipSuccess;
+  for (int64_t t = 0; t < M && e == hipSuccess; t += kLaunchTokens)
+    e = launch_forward(r, M >= kRowsForwardTokens, M - t < kLaunchTokens ? M - t : kLaunchTokens,
+                       token_rows(logits, bf16, t * ld), bf16, ld, bias, ids + t * r.topk, weights + t * r.topk, s);
+  return e;
+}
+
+hipError_t launch_route_topk_backward(const RouterArgs& r, int64_t M, const void* logits, bool bf16, int64_t ld,
+                                      const float* bias, const int32_t* ids, const float* dw, void* dl,
+                                      int64_t dl_ld, hipStream_t s) {
+  hipError_t e = hipSuccess;
+  for (int64_t t = 0; t < M && e == hipSuccess; t += kLaunchTokens)
+    e = launch_backward(r, M >= kRowsBackwardTokens, M - t < kLaunchTokens ? M - t : kLaunchTokens,
+                        token_rows(logits, bf16, t * ld), bf16, ld, bias, ids + t * r.topk, dw + t * r.topk,
+                        const_cast<void*>(token_rows(dl, bf16, t * dl_ld)), dl_ld, s);
+  return e;
 }
 
 }  // namespace moe

@@ -321,3 +321,30 @@ def test_router_graph_replays_and_streams():
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(ref, out)), i
+
+
+@gpu
+@pytest.mark.parametrize("M,E,topk", [((1 << 26) + 5, 17, 17), ((1 << 28) + 5, 1, 1)])
+def test_router_tokens_past_one_launch(M, E, topk):
+    """More tokens than the threads of one launch can take (a wave, and 16
+    lanes, to a token); rows at the ends and about every power of two."""
+    l = torch.empty(M, E, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    for i in range(0, M, 1 << 24):
+        l[i:i + (1 << 24)].normal_(generator=g)
+    r = moe.make_router(E, topk, moe.ROUTE_SIGMOID, renormalize=False)
+    ids = torch.full((M, topk), 99, dtype=torch.int32, device="cuda")
+    w = torch.full((M, topk), float("nan"), device="cuda")
+    moe.moe_route_topk(r, l, ids, w)
+    dl = torch.full_like(l, float("nan"))
+    dw = torch.full((M, topk), 0.5, device="cuda")
+    moe.moe_route_topk_backward(r, l, ids, dw, dl)
+    assert bool((ids >= 0).all()) and bool((ids < E).all()) and bool(w.isfinite().all()) and bool(dl.isfinite().all())
+    at = sorted({t for p in range(1, 29) for t in range((1 << p) - 2, (1 << p) + 3) if t < M} | set(range(M - 40, M)))
+    rows = torch.tensor(at, device="cuda")
+    lh = l[rows].float().cpu().numpy()
+    rid, rw = route_topk(lh, topk, "sigmoid", renorm=False)
+    assert np.array_equal(ids[rows].cpu().numpy(), rid)
+    assert np.all(np.abs(w[rows].cpu().numpy() - rw) <= W_EXACT * np.abs(rw))
+    rd, _ = route_backward(lh, rid, np.full(rid.shape, 0.5, np.float32), "sigmoid", renorm=False)
+    assert np.all(np.abs(dl[rows].double().cpu().numpy() - rd) <= (2.0 ** -8 + W_EXACT) * np.abs(rd))
