@@ -27,9 +27,12 @@ __device__ __forceinline__ int row_adapter(const int32_t* adapter, int64_t r, in
   return g >= 0 && g < G ? g : -1;
 }
 
-// The three bf16 pieces of a float32.
+// The three bf16 pieces of a float32.  A finite value past bf16's largest (from
+// 2^128 - 2^119 on the nearest is infinity) has that one as its first piece,
+// and the rest fits the other two.
 __device__ __forceinline__ void split3(float v, uint32_t (&p)[3]) {
   p[0] = f32_to_bf16_rne(v);
+  if ((p[0] & 0x7fffu) == 0x7f80u && v - v == 0.0f) p[0] -= 1;
   const float r1 = v - bf16_to_f32(p[0]);
   p[1] = f32_to_bf16_rne(r1);
   p[2] = f32_to_bf16_rne(r1 - bf16_to_f32(p[1]));

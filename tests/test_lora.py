@@ -454,3 +454,52 @@ def test_lora_workspaces_and_ids_in_succession():
         o["low"], o["low_dy"], o["ws"] = low[0], low[1], ws
         c.call(o)
         c.check(o)
+
+
+@gpu
+@pytest.mark.parametrize("R,G,N,K", [(5, 3, 128, 64), (40, 40, 64, 128), (300, 3, 256, 320), (300, 60, 320, 256),
+                                     (2048, 4, 2048, 64), (2048, 4, 64, 2048), (2048, 40, 2048, 64), (4096, 2, 4096, 64),
+                                     (4096, 2, 64, 4096)])
+def test_lora_narrow_products_near_the_largest_float(R, G, N, K):
+    """s and t up to the largest float32 are finite, and what is made of them
+    is: y = W x + B s with s near 2^128 and B = 2^-20, the same for dx, and the
+    gradients with 2^-20 on their other side.  One product per sum, so y and dx
+    are off by 2^-17 (two pieces) and half a bf16 step, dA and dB by the 3
+    pieces' sums over the adapter's rows."""
+    c = Case(R, N, K, G, 8, "mixed", seed=R)
+    top = float(torch.finfo(torch.float32).max)
+    c.scale[:] = top
+    c.scale[1:] = -3.397e38
+    c.scale[2:] = 3.4e38
+    small = 2.0 ** -20
+
+    def unit(t):
+        t.zero_()
+        t[..., 0] = 1.0
+
+    for side in ("y", "dx"):
+        for t in (c.a, c.b):
+            t.zero_()
+        c.a[:, 0, 0] = 1.0 if side == "y" else small
+        c.b[:, 0, 0] = small if side == "y" else 1.0
+        unit(c.x)
+        unit(c.dy)
+        if side == "y":
+            c.dy.mul_(small)
+        else:
+            c.x.mul_(small)
+        o = c.buffers()
+        c.call(o)
+        on = c.adapter >= 0
+        s = torch.where(on, c.scale.double()[c.adapter.clamp_min(0).long()], 0.0)   # s of side y, t of side dx
+        got = o[side].double()
+        want = s * small
+        bound = (2.0 ** -8 + 2.0 ** -17 + 256 * U) * want.abs() + 16.0              # |W| < 16
+        assert bool(((got[:, 0] - want).abs() <= bound).all()) and bool(got.isfinite().all())
+        # dB[g, 0, 0] = sum dy s (side y), dA[g, 0, 0] = sum t x (side dx); the other one's own product is small^2
+        k = "db" if side == "y" else "da"
+        for g in range(G):
+            n = int((c.adapter == g).sum())
+            want = n * c.scale[g].double().item() * small
+            assert abs(o[k][g, 0, 0].double().item() - want) <= (3 * n + 64) * U * abs(want), (side, g)
+        assert bool(o["da"].isfinite().all()) and bool(o["db"].isfinite().all())
