@@ -7,7 +7,9 @@
 // gradient takes d(sum_j dw_j w_j) / dl with the choice held fixed:
 //   softmax, renormalised: dl_j = scale p_j (dw_j - sum_k p_k dw_k) over the
 //     chosen, p their softmax among themselves (the others cancel: 0);
-//   softmax: dl_i = scale p_i (dw_i - sum_k p_k dw_k), dw_i = 0 unless chosen;
+//   softmax: dl_i = scale p_i (dw_i - sum_k p_k dw_k), dw_i = 0 unless chosen
+//     (in float64 for the chosen: where one of them has nearly all of the
+//     softmax, the difference is a small part of its terms);
 //   sigmoid: dl_j = ds_j s_j (1 - s_j), ds_j = scale dw_j, or renormalised
 //     scale (dw_j - sum_k dw_k s_k / S) / S with S = sum_k s_k.
 //
@@ -94,6 +96,12 @@ __global__ void __launch_bounds__(64 * kRowWaves) route_rows_kernel(RouterArgs r
   }
 }
 
+// e^x to float32 precision: expf of the nearest float32, times e to the rest.
+__device__ __forceinline__ float exp_f32(double x) {
+  const float h = (float)x;
+  return expf(h) * (1.0f + (float)(x - (double)h));
+}
+
 template <bool BF16>
 __global__ void __launch_bounds__(64 * kRouteWaves) route_topk_backward_kernel(
     RouterArgs r, int64_t M, const void* __restrict__ logits, int64_t ld, const float* __restrict__ bias,
@@ -113,20 +121,25 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_topk_backward_kernel(
   const double lj = id >= 0 ? logit(id) : -INFINITY;
   const bool have = lj > -INFINITY;
   const double g = have ? (double)dw[t * r.topk + lane] * (double)r.scale : 0.0;
-  double top = -INFINITY, inv = 0.0, dot = 0.0, d = 0.0;
+  double top = -INFINITY, d = 0.0;
+  float rest = 0.f;   // dense: an unchosen expert's gradient is e^(l - top) rest
   const bool dense = softmax && !r.renormalize;   // every expert has a gradient
   if (dense) {
     for (int e = lane; e < r.E; e += 64) top = fmax(top, logit(e));
     top = wave_max_f64(top);
-    float s = 0.f;
+    double s = 0.0;
     for (int e = lane; e < r.E; e += 64) {
       const double v = logit(e);
-      s += v > -INFINITY ? expf((float)(v - top)) : 0.f;
+      s += v > -INFINITY ? exp(v - top) : 0.0;
     }
     const double total = wave_sum_f64(s);
-    inv = total > 0.0 ? 1.0 / total : 0.0;
-    dot = wave_sum_f64(have ? g * exp(lj - top) * inv : 0.0);
-    d = g;   // of the score
+    const double inv = total > 0.0 ? 1.0 / total : 0.0;
+    const double p = have ? exp(lj - top) * inv : 0.0;
+    const double dot = wave_sum_f64(p * g);
+    double own = 0.0;   // of all slots with this one's expert
+    for (int j = 0; j < r.topk; ++j) own += __builtin_amdgcn_readlane(id, j) == id ? readlane_f64(g, j) : 0.0;
+    d = p * (own - dot);
+    rest = (float)((0.0 - dot) * inv);
   } else if (softmax) {
     const double m = wave_max_f64(lj);
     const double e = have ? exp(lj - m) : 0.0;
@@ -145,19 +158,20 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_topk_backward_kernel(
   }
   const float df = (float)d;
   for (int e = lane; e - lane < r.E; e += 64) {
-    // an expert named in several slots gets the sum of their gradients
+    // an expert named in several slots gets the sum of their gradients (dense:
+    // each of them is that sum already; the unchosen get -p_e dot)
     float v = 0.f;
-    for (int j = 0; j < r.topk; ++j) {
-      const int ej = __builtin_amdgcn_readlane(id, j);
-      const float dj = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(df), j));
-      v += ej == e ? dj : 0.f;
+    auto slot = [&](int j) {
+      return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(df), j));
+    };
+    if (dense) {
+      const double le = e < r.E ? logit(e) : -INFINITY;
+      if (le > -INFINITY) v = exp_f32(le - top) * rest;
+      for (int j = 0; j < r.topk; ++j) v = __builtin_amdgcn_readlane(id, j) == e ? slot(j) : v;
+    } else {
+      for (int j = 0; j < r.topk; ++j) v += __builtin_amdgcn_readlane(id, j) == e ? slot(j) : 0.f;
     }
     if (e < r.E) {
-      if (dense) {
-        const double le = logit(e);
-        const float p = le > -INFINITY ? expf((float)(le - top)) * (float)inv : 0.f;
-        v = p * (v - (float)dot);
-      }
       if (BF16)
         static_cast<uint16_t*>(dl)[t * dl_ld + e] = (uint16_t)f32_to_bf16_rne(v);
       else
@@ -184,13 +198,12 @@ __global__ void __launch_bounds__(64 * kRowWaves) route_rows_backward_kernel(
   const double lj = id >= 0 ? logit(id) : -INFINITY;
   const bool have = lj > -INFINITY;
   const double g = have ? (double)dw[in * r.topk + c] * (double)r.scale : 0.0;
-  double d = g, dot = 0.0, inv = 0.0;
+  double d = g;
   const bool softmax = r.scoring == 0, dense = softmax && !r.renormalize;
-  float p[NV];
+  float p[NV], rest = 0.f;   // dense: an unchosen expert's gradient is p rest
   if (dense) {
-    double top = -INFINITY;
+    double top = -INFINITY, s = 0.0;
     double l[NV];
-    float s = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       l[i] = c + 16 * i < r.E ? logit(c + 16 * i) : -INFINITY;
@@ -199,12 +212,21 @@ __global__ void __launch_bounds__(64 * kRowWaves) route_rows_backward_kernel(
     top = row_max_f64(top);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      p[i] = l[i] > -INFINITY ? expf((float)(l[i] - top)) : 0.f;
-      s += p[i];
+      const double e = l[i] > -INFINITY ? exp(l[i] - top) : 0.0;
+      s += e;
+      p[i] = (float)e;
     }
     const double total = row_sum_f64(s);
-    inv = total > 0.0 ? 1.0 / total : 0.0;
-    dot = row_sum_f64(have ? g * exp(lj - top) * inv : 0.0);
+    const double inv = total > 0.0 ? 1.0 / total : 0.0;
+    const double q = have ? exp(lj - top) * inv : 0.0;
+    const double dot = row_sum_f64(q * g);
+    double own = 0.0;   // of all slots with this one's expert
+    for (int j = 0; j < r.topk; ++j) {
+      const double gj = __shfl(g, (lane & 48) | j);
+      own += __shfl(id, (lane & 48) | j) == id ? gj : 0.0;
+    }
+    d = q * (own - dot);
+    rest = (float)((0.0 - dot) * inv);
   } else if (softmax) {
     const double m = row_max_f64(lj);
     const double e = have ? exp(lj - m) : 0.0;
@@ -222,18 +244,27 @@ __global__ void __launch_bounds__(64 * kRowWaves) route_rows_backward_kernel(
   }
   const float df = (float)d;
   float v[NV];
+  // an expert named in several slots gets their sum (dense: each slot has it)
+  auto slots = [&](auto put) {
+    for (int j = 0; j < r.topk; ++j) {
+      const int ej = __shfl(id, (lane & 48) | j);
+      const float dj = __shfl(df, (lane & 48) | j);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) v[i] = 0.f;
-  for (int j = 0; j < r.topk; ++j) {   // an expert named in several slots gets their sum
-    const int ej = __shfl(id, (lane & 48) | j);
-    const float dj = __shfl(df, (lane & 48) | j);
+      for (int i = 0; i < NV; ++i) v[i] = put(ej == c + 16 * i, v[i], dj);
+    }
+  };
+  if (dense) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] += ej == c + 16 * i ? dj : 0.f;
+    for (int i = 0; i < NV; ++i) v[i] = p[i] * rest;
+    slots([](bool own, float old, float dj) { return own ? dj : old; });
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = 0.f;
+    slots([](bool own, float old, float dj) { return old + (own ? dj : 0.f); });
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int e = c + 16 * i;
-    if (dense) v[i] = p[i] * (float)inv * (v[i] - (float)dot);
     if (t < M && e < r.E) {
       if (BF16)
         static_cast<uint16_t*>(dl)[t * dl_ld + e] = (uint16_t)f32_to_bf16_rne(v[i]);

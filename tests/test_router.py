@@ -348,3 +348,30 @@ def test_router_tokens_past_one_launch(M, E, topk):
     assert np.all(np.abs(w[rows].cpu().numpy() - rw) <= W_EXACT * np.abs(rw))
     rd, _ = route_backward(lh, rid, np.full(rid.shape, 0.5, np.float32), "sigmoid", renorm=False)
     assert np.all(np.abs(dl[rows].double().cpu().numpy() - rd) <= (2.0 ** -8 + W_EXACT) * np.abs(rd))
+
+
+@gpu
+@pytest.mark.parametrize("M", [40, 2053])
+@pytest.mark.parametrize("E,topk", [(64, 4), (100, 8), (300, 1), (500, 16)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_router_gradient_of_confident_tokens(M, E, topk, dtype):
+    """Softmax over all experts, one of which has nearly all of it: its gradient
+    g (1 - p) is small and must come out to the result's own precision.  In
+    float64 (some 2^-46 of the terms, of exponentials and their sum) but for
+    the unchosen's float32 exponential (2^-22) and at most four more float32
+    roundings (2^-24 each), and half a bf16 step."""
+    l = logits(M, E, torch.float32, E + topk)
+    gap = torch.linspace(4.0, 22.0, M, device="cuda")
+    l[torch.arange(M), torch.arange(M) % E] += gap
+    l = l.to(dtype)
+    dw = np.random.default_rng(M).normal(size=(M, topk)).astype(np.float32)
+    r = moe.make_router(E, topk, renormalize=False, scale=1.5)
+    ids = torch.empty(M, topk, dtype=torch.int32, device="cuda")
+    w = torch.empty(M, topk, device="cuda")
+    moe.moe_route_topk(r, l, ids, w)
+    dl = torch.full_like(l, float("nan"))
+    moe.moe_route_topk_backward(r, l, ids, torch.from_numpy(dw).cuda(), dl)
+    rd, mag = route_backward(l.float().cpu().numpy(), ids.cpu().numpy(), dw, renorm=False, scale=1.5)
+    bound = 2.0 ** -21 * np.abs(rd) + 2.0 ** -46 * mag + (2.0 ** -8 * np.abs(rd) if dtype == torch.bfloat16 else 0) + 1e-37
+    d = np.abs(dl.double().cpu().numpy() - rd)
+    assert np.all(d <= bound), (np.nanmax(d / bound), np.argwhere(~(d <= bound))[:3])
