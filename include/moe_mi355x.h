@@ -541,10 +541,11 @@ int moe_layer_plan_init(moe_layer_plan* plan, const moe_layer_problem* prob);
  * written; ws: device, plan->ws_bytes, 16-byte aligned, zero-filled before
  * its first call.  Each call leaves it ready for the next, of this plan or of
  * any other that it is large enough for; calls that share a workspace must not
- * overlap.  The first launch waits in the kernel for the
- * routing, for about a second at most: the int32 at off_status counts waits
- * that gave up, summed over calls (non-zero: some call's outputs are
- * undefined, and the workspace must be zero-filled again). */
+ * overlap.  The first launch waits in the kernel for the routing, for about a
+ * second at most: the int32 at off_status counts waits that gave up, summed
+ * over calls.  The call whose wait gave up, and every later one on that
+ * workspace until it is zero-filled again, writes NaN to all of out (topk_ids
+ * and topk_weights are then undefined). */
 int moe_layer_apply(const moe_layer_plan* plan, const void* x, const void* router_w, const float* router_bias,
                     const moe_weights* w, void* out, int32_t* topk_ids, float* topk_weights, void* ws,
                     void* stream);

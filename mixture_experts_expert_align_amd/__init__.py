@@ -572,11 +572,12 @@ def allocate_layer_workspace(plan: MoeLayerPlan, device="cuda") -> torch.Tensor:
 
 
 def check_layer_status(plan: MoeLayerPlan, ws: torch.Tensor):
-    """Raise MoeError when a call on this workspace gave up its bounded wait
-    (its outputs are undefined).  Synchronises with the device."""
+    """Raise MoeError when a call on this workspace gave up its bounded wait:
+    its ``out`` and every later one's is NaN until the workspace is zero-filled
+    again.  Synchronises with the device."""
     timeouts = int(ws_view(ws, plan.off_status, 1).cpu()[0])
     if timeouts:
-        raise MoeError("moe_layer_apply", MOE_EHIP, f"{timeouts} bounded waits timed out; outputs undefined")
+        raise MoeError("moe_layer_apply", MOE_EHIP, f"{timeouts} bounded waits timed out; out is NaN")
 
 
 def moe_layer_apply(plan: MoeLayerPlan, x, router_w, w1, w2, out, topk_ids, topk_weights, ws, router_bias=None,

@@ -227,10 +227,10 @@ constexpr int kLayerMaxRoutes = kLayerMaxM * kLayerMaxTopk;
 // the sync area, int32 words, one 128-byte line per counter that many
 // workgroups touch at once, at the same places for every plan; then one word
 // per strip of the second launch, which the first launch clears
-enum { kLayerClaim = 0, kLayerArrived = kSyncLine, kLayerRouted = 2 * kSyncLine, kLayerNumSlots = 2 * kSyncLine + 1,
-       kLayerNumRows = 2 * kSyncLine + 2,
-       kLayerDone = 3 * kSyncLine, kLayerItems = 4 * kSyncLine, kLayerRanked = 5 * kSyncLine, kLayerStatus = 6 * kSyncLine,
-       kLayerStrips = 8 * kSyncLine };
+// (status, routed, slots and rows: the four words the second launch starts from)
+enum { kLayerClaim = 0, kLayerArrived = kSyncLine, kLayerStatus = 2 * kSyncLine, kLayerRouted = 2 * kSyncLine + 1,
+       kLayerNumSlots = 2 * kSyncLine + 2, kLayerNumRows = 2 * kSyncLine + 3,
+       kLayerDone = 3 * kSyncLine, kLayerItems = 4 * kSyncLine, kLayerRanked = 5 * kSyncLine, kLayerStrips = 6 * kSyncLine };
 
 struct alignas(16) LayerSlot {
   int32_t e, cnt, pos0, pad;   // expert, its tokens, their first row of z

@@ -874,8 +874,10 @@ __global__ void __launch_bounds__(kThreads, 4) layer_down_kernel(LayerArgs g) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int strip = blockIdx.x / g.splits, split = blockIdx.x % g.splits;
   for (int i = threadIdx.x; i < g.max_slots; i += kThreads) s_slots[i] = g.slots[i];
-  // a first launch that timed out published nothing: no rows to add
-  const int nslots = g.sync[kLayerRouted] ? g.sync[kLayerNumSlots] : 0;
+  // after a wait that gave up: nothing of the first launch is used, out is NaN
+  const int gave_up = g.sync[kLayerStatus], routed = g.sync[kLayerRouted], slots = g.sync[kLayerNumSlots];
+  const bool failed = gave_up != 0 || routed == 0;
+  const int nslots = failed ? 0 : slots;
   __syncthreads();
   const int spe = g.I / 128;                             // blocks per slot
   const int64_t total = (int64_t)nslots * spe;
@@ -947,7 +949,7 @@ __global__ void __launch_bounds__(kThreads, 4) layer_down_kernel(LayerArgs g) {
   if (finish) {
     uint32_t h[4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) h[r] = f32_to_bf16_rne(sum[r]);
+    for (int r = 0; r < 4; ++r) h[r] = failed ? 0x7fc0u : f32_to_bf16_rne(sum[r]);
     *reinterpret_cast<uint2*>(g.out + (int64_t)t * g.K + 4 * kQ * strip + 4 * qt) =
         make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
   }

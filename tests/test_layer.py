@@ -419,3 +419,24 @@ def test_layer_workspace_serves_plans_of_other_sizes(w):
         cs[i].call(o, ws=ws)
         assert all(torch.equal(a, b) for a, b in zip(o, refs[i])), i
         moe.check_layer_status(cs[i].plan, ws)
+
+
+@gpu
+@pytest.mark.parametrize("kw", [dict(M=4, K=256, I=128, E=8, topk=2), dict(M=4, K=256, I=512, E=64, topk=8, shared=1),
+                                dict(M=20, K=256, I=256, E=8, topk=2), dict(M=7, K=2048, I=1152, E=8, topk=2)])
+def test_layer_output_is_nan_after_a_wait_that_gave_up(kw):
+    """A status word that counts a wait given up (set from the host): out is NaN
+    until the workspace is zero-filled again, then right."""
+    c = Case(**kw)
+    moe.ws_view(c.ws, c.plan.off_status, 1).fill_(1)
+    for _ in range(2):
+        o = c.outputs()
+        o[0].zero_()
+        c.call(o)
+        assert o[0].isnan().all()
+        with pytest.raises(moe.MoeError, match="timed out"):
+            moe.check_layer_status(c.plan, c.ws)
+    c.ws.zero_()
+    o = c.outputs()
+    c.call(o)
+    c.check(o)
