@@ -493,9 +493,11 @@ int moe_route_topk_backward(const moe_router* r, int64_t M, const void* logits, 
  *
  * bf16 x bf16 products summed in float32 in a fixed order (the same bits on
  * every run); the intermediate, its weight included, is rounded to bf16 once;
- * the sum over the experts is rounded once.  MXFP8 weights are decoded exactly
+ * the sum over the experts is rounded once.  MXFP8 weights are decoded to bf16
  * (the activations stay bf16, unlike moe_apply_contiguous, which quantises
- * them), values below bf16's normal range excepted, which may count as 0.
+ * them): exactly in its normal range, below it (|code| 2^(s-127) < 2^-126)
+ * rounded to multiples of 2^-133, past its largest value infinite; scale code
+ * 255 makes its block NaN.
  * A token without an expert to choose gets only the shared experts, or +0.0.
  * Infinite or NaN weights of an expert reach the tokens that chose it only.
  * ------------------------------------------------------------------------- */

@@ -440,3 +440,107 @@ def test_layer_output_is_nan_after_a_wait_that_gave_up(kw):
     o = c.outputs()
     c.call(o)
     c.check(o)
+
+
+LONG_RUNS = [
+    # W1 of 5, 6 and 12 blocks to a wave (the scale words come 4 blocks at a time), slots of 9 to 16 tokens
+    dict(M=16, K=6144, I=128, E=4, topk=2, shared=1),
+    dict(M=13, K=5248, I=128, E=2, topk=1, shared=1, order="interleave16"),
+    dict(M=9, K=12288, I=128, E=1, topk=1, shared=1),
+    # W2 of 6 and 7 blocks to a wave, across the slots' borders
+    dict(M=12, K=128, I=16384, E=1, topk=1, shared=2),
+    dict(M=16, K=128, I=17536, E=1, topk=1, shared=2, order="interleave16"),
+    # more than 16 and more than 32 tokens a slot
+    dict(M=27, K=5248, I=256, E=1, topk=1, shared=1),
+    dict(M=50, K=5248, I=256, E=1, topk=1, shared=1),
+]
+
+
+@gpu
+@pytest.mark.parametrize("w", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("kw", LONG_RUNS, ids=[f"m{c['M']}k{c['K']}i{c['I']}" for c in LONG_RUNS])
+def test_layer_long_runs(kw, w):
+    """Long contractions of slots that hold more than 8 tokens."""
+    c = Case(w=w, **kw)
+    o, p = c.outputs(), c.outputs()
+    c.call(o)
+    c.check(o)
+    c.call(p)
+    assert all(torch.equal(a, b) for a, b in zip(o, p))
+
+
+def _one_hot_layer(M, w1_scales, x_value):
+    """An MXFP8 layer of one expert whose token t sees out[t, i] = 32 x_value W1u[i, k_t]:
+    gate 32 from column 0 (silu(32) = 32 in float32), W2 the identity."""
+    K = I = 256
+    c = Case(M=M, K=K, I=I, E=1, topk=1, w="mxfp8")
+    c.w1[0, :I] = 0
+    c.w1[0, :I, 0] = 0x38                       # 1.0
+    c.s1[0, :I] = 127 + 5
+    codes = torch.arange(I, device="cuda").remainder(127)
+    c.w1[0, I:] = torch.where(torch.arange(I, device="cuda") % 2 == 1, codes + 128, codes).to(torch.uint8)[:, None]
+    c.w1[0, I:, 0] = 0
+    c.s1[0, I:] = w1_scales[None, :]
+    c.w2[0] = 0
+    c.w2[0, torch.arange(K), torch.arange(K)] = 0x38
+    c.s2.fill_(127)
+
+    def outputs():
+        """(columns, their out rows [I])"""
+        o = c.outputs()
+        for k0 in range(1, K, M):
+            n = min(M, K - k0)
+            c.x.zero_()
+            c.x[:, 0] = 1
+            c.x[torch.arange(n), k0 + torch.arange(n)] = x_value
+            c.call(o)
+            for t in range(n):
+                yield k0 + t, o[0][t]
+    return c, outputs
+
+
+@gpu
+@pytest.mark.parametrize("M", [4, 12, 30, 64])
+def test_layer_mxfp8_scale_codes_at_the_ends(M):
+    """Scale codes from 0 (2^-127) and up to 254 (2^127): a code times its scale
+    is exact in bf16's normal range, rounded to bf16's subnormals (multiples of
+    2^-133) below and infinite past it.  The test's own factors are powers of two."""
+    tiny, top = 2.0 ** -126, float(torch.finfo(torch.bfloat16).max)
+    for scales, xv in (([0, 1, 2, 3, 5, 8, 9, 16], 1.0), ([230, 240, 246, 247, 248, 250, 253, 254], 2.0 ** -40)):
+        c, outputs = _one_hot_layer(M, torch.tensor(scales, dtype=torch.uint8, device="cuda"), xv)
+        up = decode_mx(c.w1[0], c.s1[0])[256:]
+        c.w1[0, 256:][up.abs() > top] = 0       # (0 x inf of the other rows of W2 would hide the rest)
+        up = decode_mx(c.w1[0], c.s1[0])[256:]
+        seen = 0
+        for k, got in outputs():
+            ok = got.double() == up[:, k].float().bfloat16().double() * 32 * xv
+            assert bool(ok.all()), (k, scales[k // 32], up[:, k][~ok][:4].tolist(), got[~ok][:4].tolist())
+            seen += int((up[:, k].abs() >= tiny).sum())
+        assert seen > 10000
+    # past bf16's largest value: infinite
+    c, outputs = _one_hot_layer(M, torch.full((8,), 254, dtype=torch.uint8, device="cuda"), 2.0 ** -40)
+    for k, got in outputs():
+        assert not got.isfinite().any(), k
+        break
+
+
+@gpu
+@pytest.mark.parametrize("M", [3, 8, 13, 40])
+def test_layer_mxfp8_scale_code_255_is_nan(M):
+    """Scale code 255 (NaN) of an expert's W1 or W2 makes the tokens routed to
+    it NaN and touches no other."""
+    for which in ("s1", "s2"):
+        c = Case(M=M, K=256, I=256, E=6, topk=2, w="mxfp8", seed=M)
+        o, p = c.outputs(), c.outputs()
+        c.call(o)
+        getattr(c, which)[2, 5, 3] = 255
+        c.call(p)
+        hit = (o[1] == 2).any(1)
+        assert 0 < int(hit.sum()) < M
+        assert torch.equal(p[1], o[1]) and torch.equal(p[0][~hit], o[0][~hit])
+        if which == "s1":
+            assert p[0][hit].isnan().all()
+        else:
+            assert p[0][hit][:, 5].isnan().all()
+            rest = torch.arange(256, device="cuda") != 5
+            assert torch.equal(p[0][:, rest], o[0][:, rest])
