@@ -21,11 +21,23 @@
 // 4096 x 512 with 16 groups (29 by the other form).  And 16 lanes per token,
 // where a round's reductions serve four tokens at once but a lane has four
 // times the experts to look through: forward beyond 4096 tokens (more than
-// four waves per SIMD of the first form) of up to 256 experts: 8192 x 128
-// 7.5 us against 9.5, 8192 x 256 in 8 groups 16.9 against 18.6, while at 4096
-// tokens they are 7.2 against 6.9 and 16.5 against 12.0; backward, whose rows
-// have no rounds, from 2048 tokens: 8192 x 128 4.3 against 6.9, 2048 x 512 the
-// same 6.4.
+// four waves per SIMD of the first form) of up to 128 experts, beyond 6144 of
+// up to 256.  Replayed from a graph, a wave / 16 lanes per token, us:
+//   tokens                           4096       5000       6000       8192      16384
+//   128, softmax                   6.5/6.7    7.3/6.7    8.0/6.8    9.4/6.8  15.8/8.9
+//   128 in 8 groups, softmax     10.7/11.3  12.1/11.4  13.5/11.5  16.5/11.5 28.4/17.0
+//   256, softmax                   8.0/9.7    8.9/9.7    9.8/9.9   11.6/9.8 20.0/13.0
+//   256 in 8 groups, sel. bias   12.1/16.4  13.9/16.4  15.7/16.4  19.0/16.3 33.2/23.4
+//   256, sigmoid, sel. bias       9.3/14.0  10.6/14.1  11.8/14.1  14.4/14.2 24.9/20.0
+// Backward, whose rows have no rounds, from 2048 tokens; where every expert has
+// a gradient (softmax, not renormalised) and there are more than 128, whose
+// exponentials a lane then takes 16 or 32 of, from 4097:
+//   tokens                           2048       3000       4096       8192      16384
+//   128, chosen only               4.6/3.7    4.8/3.9    5.4/4.0    7.0/4.3  11.2/5.8
+//   512, chosen only               7.5/6.3    8.2/6.9    9.1/7.2   12.9/8.3 22.0/13.9
+//   128, every expert              6.2/6.0    6.6/6.7    7.3/6.8   10.8/7.2  18.4/9.8
+//   256, every expert              8.4/9.0   9.0/10.1  10.1/10.3  15.5/11.2 26.6/16.4
+//   512, every expert            12.5/15.0  13.9/17.1  16.1/17.4  24.3/20.0 44.3/32.7
 #include "kernels.h"
 #include "route_device.h"
 
@@ -70,7 +82,8 @@ __global__ void __launch_bounds__(64 * kRouteWaves) route_topk_kernel(RouterArgs
 }
 
 constexpr int kRowWaves = 2;
-constexpr int64_t kRowsForwardTokens = 4097, kRowsBackwardTokens = 2048;
+constexpr int64_t kRowsForwardTokens = 4097, kRowsForwardTokens256 = 6145;   // up to 128 experts, up to 256
+constexpr int64_t kRowsBackwardTokens = 2048, kRowsBackwardTokensEvery = 4097;   // chosen or <= 128 experts; others
 constexpr int kRowsForwardExperts = 256, kRowsBackwardExperts = 512;
 
 template <int NV, bool BF16>
@@ -356,19 +369,22 @@ hipError_t launch_backward(const RouterArgs& r, bool many, int64_t M, const void
 
 hipError_t launch_route_topk(const RouterArgs& r, int64_t M, const void* logits, bool bf16, int64_t ld,
                              const float* bias, int32_t* ids, float* weights, hipStream_t s) {
+  const bool many = M >= (r.E <= 128 ? kRowsForwardTokens : kRowsForwardTokens256);
   hipError_t e = hipSuccess;
   for (int64_t t = 0; t < M && e == hipSuccess; t += kLaunchTokens)
-    e = launch_forward(r, M >= kRowsForwardTokens, M - t < kLaunchTokens ? M - t : kLaunchTokens,
-                       token_rows(logits, bf16, t * ld), bf16, ld, bias, ids + t * r.topk, weights + t * r.topk, s);
+    e = launch_forward(r, many, M - t < kLaunchTokens ? M - t : kLaunchTokens, token_rows(logits, bf16, t * ld),
+                       bf16, ld, bias, ids + t * r.topk, weights + t * r.topk, s);
   return e;
 }
 
 hipError_t launch_route_topk_backward(const RouterArgs& r, int64_t M, const void* logits, bool bf16, int64_t ld,
                                       const float* bias, const int32_t* ids, const float* dw, void* dl,
                                       int64_t dl_ld, hipStream_t s) {
+  const bool every = r.scoring == 0 && !r.renormalize && r.E > 128;
+  const bool many = M >= (every ? kRowsBackwardTokensEvery : kRowsBackwardTokens);
   hipError_t e = hipSuccess;
   for (int64_t t = 0; t < M && e == hipSuccess; t += kLaunchTokens)
-    e = launch_backward(r, M >= kRowsBackwardTokens, M - t < kLaunchTokens ? M - t : kLaunchTokens,
+    e = launch_backward(r, many, M - t < kLaunchTokens ? M - t : kLaunchTokens,
                         token_rows(logits, bf16, t * ld), bf16, ld, bias, ids + t * r.topk, dw + t * r.topk,
                         const_cast<void*>(token_rows(dl, bf16, t * dl_ld)), dl_ld, s);
   return e;

@@ -375,3 +375,23 @@ def test_router_gradient_of_confident_tokens(M, E, topk, dtype):
     bound = 2.0 ** -21 * np.abs(rd) + 2.0 ** -46 * mag + (2.0 ** -8 * np.abs(rd) if dtype == torch.bfloat16 else 0) + 1e-37
     d = np.abs(dl.double().cpu().numpy() - rd)
     assert np.all(d <= bound), (np.nanmax(d / bound), np.argwhere(~(d <= bound))[:3])
+
+
+@gpu
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bias_kind", ["none", "logit", "select"])
+@pytest.mark.parametrize("M,E,topk,groups,tg", [(6147, 256, 12, 2, 1), (6145, 129, 16, 1, 1), (6150, 240, 5, 16, 4),
+                                                (6144, 200, 8, 8, 3)])
+def test_router_many_rows_of_more_than_128_experts(scoring, bias_kind, M, E, topk, groups, tg):
+    """On either side of the number of tokens from which several share a wave."""
+    rng = np.random.default_rng(E)
+    bias = None if bias_kind == "none" else (0.25 * rng.normal(size=E)).astype(np.float32)
+    for renorm, dtype in ((True, torch.float32), (False, torch.bfloat16)):
+        check(logits(M, E, dtype, M + E), topk, scoring, bias, bias_kind, renorm, 2.5, groups, tg)
+
+
+@gpu
+@pytest.mark.parametrize("E,topk", [(129, 3), (300, 8), (500, 16)])
+def test_router_gradient_of_confident_tokens_many_rows(E, topk):
+    """The same where several tokens of more than 128 experts share a wave."""
+    test_router_gradient_of_confident_tokens(4101, E, topk, torch.float32)
