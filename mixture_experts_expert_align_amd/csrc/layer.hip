@@ -988,13 +988,15 @@ hipError_t launch(const LayerArgs& g, unsigned grid1, hipStream_t s) {
 // the chip its two workgroups per CU, but not so many that a wave has fewer
 // than 4 blocks of 128 features to read with every slot filled (`blocks` in
 // all; 2 while there are fewer than 64 workgroups, where it is the few CUs'
-// loads that take the time: 7 tokens, K = 256, 32 blocks 17.9 us with 2
-// splits, 19.2 with one).  K = 6144 (192 strips), MXFP8, 33 experts of 2048: 1 / 2 / 4 / 8 splits
-// 127 / 92 / 80 / 101 us (more workgroups than fit pay their start and their
-// join again).  The whole layer, bf16, 1 / 2 / 4 / 8 splits: one token, K =
-// 7168, 2 of 64 experts of 2048 (32 blocks) 48 / 50 / 56 / - us; one, K =
-// 2048, 8 of 64 of 1024 (64) 43 / 42 / 43 / 47; 4 tokens, K = 2048, 27 of 64
-// of 512 (at most 128) 63 / 57 / 55 / 62.
+// loads that take the time).  1 / 2 / 4 / 8 splits, us: the second launch at K =
+// 6144 (192 strips), MXFP8, 33 experts of 2048, 127 / 92 / 80 / 101 (more
+// workgroups than fit pay their start and their join again).  The whole layer,
+// bf16: one token, K = 7168, 2 of 64 experts of 2048 (32 blocks) 48 / 50 / 56 / -;
+// one, K = 2048, 8 of 64 of 1024 (64) 43 / 42 / 43 / 47; 4 tokens, K = 2048, 27 of
+// 64 of 512 (at most 128) 63 / 57 / 55 / 62; with fewer than 64 workgroups, 7
+// tokens, K = 256 (32) 19.2 / 18.1 / 17.9 / 18.3; 4, K = 512 (32) 19.2 / 19.1 /
+// 18.5 / 19.7; 4, K = 512 (128) 33.0 / 29.6 / 27.3 / 27.7; 40, K = 512 (64) 43.0 /
+// 36.9 / 33.8 / 32.9; 8, MXFP8, K = 256 (32) 16.4 / 16.9 / 17.3 / 18.0.
 int32_t layer_splits(int64_t K, int64_t blocks) {
   int32_t s = 1;
   const int64_t strips = K / (16 * kDownTiles);
