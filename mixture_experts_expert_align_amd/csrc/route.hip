@@ -109,8 +109,10 @@ __global__ void __launch_bounds__(64 * kRowWaves) route_rows_kernel(RouterArgs r
   }
 }
 
-// e^x to float32 precision: expf of the nearest float32, times e to the rest.
+// e^x for x <= 0 to float32 precision: expf of the nearest float32, times e to
+// the rest.  (Far below the smallest float32 the rest must not grow with x.)
 __device__ __forceinline__ float exp_f32(double x) {
+  x = fmax(x, -1000.0);
   const float h = (float)x;
   return expf(h) * (1.0f + (float)(x - (double)h));
 }

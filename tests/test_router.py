@@ -395,3 +395,27 @@ def test_router_many_rows_of_more_than_128_experts(scoring, bias_kind, M, E, top
 def test_router_gradient_of_confident_tokens_many_rows(E, topk):
     """The same where several tokens of more than 128 experts share a wave."""
     test_router_gradient_of_confident_tokens(4101, E, topk, torch.float32)
+
+
+@gpu
+@pytest.mark.parametrize("M", [24, 4104])
+@pytest.mark.parametrize("E", [64, 200, 700])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_router_largest_differences_between_logits(M, E, scoring):
+    """A logit that counts as the largest float32 beside ones of the lowest, of
+    every size between, and masked ones: no NaN, and what the formulas give."""
+    l = logits(M, E, torch.float32, E)
+    low, top = torch.finfo(torch.float32).min, torch.finfo(torch.float32).max
+    l[0::8, 1::3] = low
+    l[0::8, 5] = float("inf")
+    l[1::8, ::2] = low
+    l[1::8, 7] = top
+    l[2::8] *= 1e37
+    l[3::8] *= 1e4
+    l[4::8, 9] = 1e30
+    l[5::8, ::5] = -1e30
+    l[6::8, 1:] = float("-inf")
+    l[7::8, :3] = top
+    l[7::8, 4:] = low
+    for renorm in (True, False):
+        check(l, 6, scoring, renorm=renorm)
