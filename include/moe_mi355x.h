@@ -477,7 +477,8 @@ int moe_route_topk(const moe_router* r, int64_t M, const void* logits, int dtype
  * sum).  topk_ids: as moe_route_topk wrote them (ids outside [0, E) are
  * skipped); dweights: device float32 [M, topk]; dlogits: device, logits'
  * dtype, M rows of E values dlogits_ld elements apart, every one written
- * (elements between the rows untouched).  Errors as for moe_route_topk. */
+ * (elements between the rows untouched); must not overlap the inputs.  Errors
+ * as for moe_route_topk. */
 int moe_route_topk_backward(const moe_router* r, int64_t M, const void* logits, int dtype, int64_t logits_ld,
                             const float* bias, const int32_t* topk_ids, const float* dweights, void* dlogits,
                             int64_t dlogits_ld, void* stream);
@@ -547,7 +548,8 @@ int moe_layer_plan_init(moe_layer_plan* plan, const moe_layer_problem* prob);
  * second at most: the int32 at off_status counts waits that gave up, summed
  * over calls.  The call whose wait gave up, and every later one on that
  * workspace until it is zero-filled again, writes NaN to all of out (topk_ids
- * and topk_weights are then undefined). */
+ * and topk_weights are then undefined).  After MOE_EHIP the workspace must be
+ * zero-filled too.  Outputs and ws must not overlap inputs. */
 int moe_layer_apply(const moe_layer_plan* plan, const void* x, const void* router_w, const float* router_bias,
                     const moe_weights* w, void* out, int32_t* topk_ids, float* topk_weights, void* ws,
                     void* stream);
@@ -564,8 +566,12 @@ int moe_layer_apply(const moe_layer_plan* plan, const void* x, const void* route
  * x, dx [R, K], dy, y [R, N], W [N, K], A [G, rank, K], B [G, N, rank]: device
  * bf16; scale: device float32 [G]; adapter: device int32 [R]; dA [G, rank, K],
  * dB [G, N, rank]: device float32.  Products of bf16 values summed in float32
- * in a fixed order (the same bits on every run); s and t are kept to float32
- * precision, y and dx rounded to bf16 once.  W is shared by all rows and
+ * in a fixed order (the same bits on every run); s and t are kept, and enter dA
+ * and dB, to float32 precision.  Their part of y and dx takes at least 16 of
+ * their bits, so it may be off by 2^-17 of |B[g]| |s_r| and |A[g]^T| |t_r|, beside
+ * the one rounding of y and dx to bf16; how many, and the order of the sums,
+ * goes by R and the adapters of the rows near by, so a row's bits may differ
+ * from those it has in another batch.  W is shared by all rows and
  * frozen here (its own gradient is moe_grouped_wgrad with one group).  Row
  * adapters may name (request, expert) pairs as well as requests.  Infinities
  * and NaN in one adapter, or in one row, reach that adapter's or that row's

@@ -8,7 +8,7 @@
 //
 // The weight is folded into z before its rounding to bf16 (one rounding, as
 // without it), so W2 and the weighted sum are one contraction over (expert,
-// feature) pairs: the second kernel gives each 16 output features to the
+// feature) pairs: the second kernel gives each 32 output features to the
 // waves of a few workgroups, whose MFMA accumulators run through all active
 // experts in float32, and no per-route rows are written or re-read.
 //
@@ -21,21 +21,23 @@
 // scale, exact in the normal range of bf16), the activations stay bf16.
 //
 // Measured, first launch + second: 4 tokens, 27 of 64 bf16 experts of 8192
-// features, K = 4096: 580 + 305 us for 5.4 GB of weights, 6.1 TB/s; 16
-// tokens, 27 of 33 MXFP8 experts of 2048, K = 6144: 161 + 75 us for 1.04 GB,
+// features, K = 4096: 581 + 307 us for 5.4 GB of weights, 6.1 TB/s; 16
+// tokens, 27 of 33 MXFP8 experts of 2048, K = 6144: 161 + 74 us for 1.04 GB,
 // 4.4 TB/s (18 us of routing first, 20 us from the median workgroup's end to
-// the last one's); 61 tokens, 128 bf16 experts of 1024 and 2 shared, K = 4096: 386 + 191
-// us for 3.2 GB, 5.6 TB/s; 7 tokens, 8 experts of 512, K = 256: 9.8 + 8.4 us, latency
+// the last one's); 61 tokens, 128 bf16 experts of 1024 and 2 shared, K = 4096: 386 + 192
+// us for 3.2 GB, 5.6 TB/s; 7 tokens, 8 experts of 512, K = 256: 9.8 + 8.6 us, latency
 // (launch, router, ranking, two streams' round trips).  What such reads reach
-// at best is 6.0 to 6.2 TB/s.
+// at best is 6.2 to 6.3 TB/s (W2 and W1 of the two-launch streaming path, which
+// have no routing in front and no other sums to join).
 //
 // Inside the first launch the router comes before everything else.  Its work
 // (units of 16 experts x 1024 of K, then of 8 tokens to rank) is claimed from
 // a counter by whichever workgroups run, so a unit only ever waits for units
 // that running workgroups hold; the workgroup that ranks last writes the slot
-// list and publishes it, and every workgroup goes on to claim (slot, 16
+// list and publishes it, and every workgroup goes on to claim (slot, 8 or 16
 // features) items.  The waits are bounded: after about a second a workgroup
-// gives up, counts a time-out and leaves.  Data that crosses workgroups inside
+// gives up, counts a time-out and leaves, and the second launch, which reads
+// that count, writes NaN.  Data that crosses workgroups inside
 // a launch goes through device-coherent accesses (the XCDs' L2s are not
 // coherent).  A small router (solo) is computed by every workgroup on its
 // own, which is faster than passing the result on.

@@ -16,8 +16,10 @@
 // Nothing but the logits is read, once, and nothing but the result written, so
 // the memory is never the bound: with few tokens it is one token's latency
 // (the float64 exponentials and divisions of the scores, then k rounds of
-// reductions), with many the instructions issued for that.  Hence two forms.
-// A wave per token: the shortest rounds; 3.3 us for 4 x 64, top-8, 18 us for
+// reductions), with many the instructions issued for that (4096 x 512 with 16
+// groups: vector instructions issue in 59 to 68% of the cycles; 8192 x 128, two
+// waves a SIMD: 29 to 38%, the rest is their latency).  Hence two forms.
+// A wave per token: the shortest rounds; 3.3 us for 4 x 64, top-8, 18.8 us for
 // 4096 x 512 with 16 groups (29 by the other form).  And 16 lanes per token,
 // where a round's reductions serve four tokens at once but a lane has four
 // times the experts to look through: forward beyond 4096 tokens (more than
