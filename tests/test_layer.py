@@ -544,3 +544,36 @@ def test_layer_mxfp8_scale_code_255_is_nan(M):
             assert p[0][hit][:, 5].isnan().all()
             rest = torch.arange(256, device="cuda") != 5
             assert torch.equal(p[0][:, rest], o[0][:, rest])
+
+
+@gpu
+@pytest.mark.parametrize("w", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("kw", [dict(M=3, K=(1 << 22) - 128, I=128, E=2, topk=1), dict(M=12, K=(1 << 22) - 128, I=128, E=2, topk=1),
+                                dict(M=3, K=128, I=(1 << 22) - 128, E=2, topk=1), dict(M=12, K=128, I=(1 << 22) - 128, E=2, topk=1),
+                                dict(M=64, K=(1 << 15) - 128, I=(1 << 14) - 128, E=1, topk=1)],
+                         ids=["m3-k", "m12-k", "m3-i", "m12-i", "m64-both"])
+def test_layer_largest_sizes(kw, w):
+    """One expert's W1 just under 2^31 bytes, the longest rows of either side:
+    the choice, and the output's root mean square error as in check()."""
+    c = Case(w=w, **kw)
+    o = c.outputs()
+    c.call(o)
+    moe.check_layer_status(c.plan, c.ws)
+    x = c.x.double()
+    ids = (x @ c.wr.double().t()).argmax(1)
+    assert torch.equal(ids.int(), o[1][:, 0]) and (o[2] == 1).all()
+
+    def times(v, m, s):   # v [n, C] by the rows of m, decoded in pieces
+        n = max(1, (1 << 27) // m.shape[1])
+        piece = lambda i: m[i:i + n].double() if s is None else decode_mx(m[i:i + n], s[i:i + n])
+        return torch.cat([v @ piece(i).t() for i in range(0, m.shape[0], n)], 1)
+
+    want = torch.zeros(c.M, c.K, dtype=torch.float64, device="cuda")
+    for e in range(c.E):
+        rows = torch.nonzero(ids == e)[:, 0]
+        if rows.numel():
+            h = times(x[rows], c.w1[e], None if c.s1 is None else c.s1[e])
+            z = h[:, :c.I] * torch.sigmoid(h[:, :c.I]) * h[:, c.I:]
+            want[rows] = times(z, c.w2[e], None if c.s2 is None else c.s2[e])
+    rms = ((o[0].double() - want).pow(2).mean() / want.pow(2).mean()).sqrt().item()
+    assert rms <= 1.5 * 2 ** 0.5 * 2.0 ** -8 / 3 ** 0.5, rms

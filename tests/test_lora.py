@@ -503,3 +503,71 @@ def test_lora_narrow_products_near_the_largest_float(R, G, N, K):
             want = n * c.scale[g].double().item() * small
             assert abs(o[k][g, 0, 0].double().item() - want) <= (3 * n + 64) * U * abs(want), (side, g)
         assert bool(o["da"].isfinite().all()) and bool(o["db"].isfinite().all())
+
+
+@gpu
+@pytest.mark.parametrize("R,N,K,G,rank", [((1 << 24) - 1, 64, 64, 5, 8), (5, 32704, 32704, 3, 8), (300, 32704, 32704, 40, 8),
+                                          (32768, 32704, 32704, 4, 16), (200, 64, (1 << 22) - 64, 3, 40),
+                                          (40, (1 << 20) - 64, 64, 7, 128), (130, 192, 64, 4096, 128)])
+def test_lora_largest_sizes(R, N, K, G, rank):
+    """Rows, W and the adapters near 2^31 bytes, offsets past 2^30: rows from all
+    over, and the adapters' gradients by their root mean square.  A float32 sum of
+    n terms of random sign, one by one, has partial sums that grow like sqrt(i)
+    and is off by at most half a step of each: 2^-24 sqrt(sum of i / n) =
+    2^-24 sqrt(n / 2) of its size.  For s or t, C / 4 terms to a wave; for dA and
+    dB three pieces of every row; and 2^-23 for the pieces and the last sums."""
+    g = torch.Generator(device="cuda").manual_seed(R)
+
+    def rn(*s, std=1.0):
+        t = torch.empty(*s, dtype=torch.bfloat16, device="cuda")
+        for i in range(0, t.numel(), 1 << 28):
+            t.view(-1)[i:i + (1 << 28)].normal_(0.0, std, generator=g)
+        return t
+
+    c = Case(1, 64, 64, 1, 8)
+    c.R, c.N, c.K, c.G, c.rank = R, N, K, G, rank
+    c.x, c.dy, c.w, c.a, c.b = rn(R, K), rn(R, N), rn(N, K, std=K ** -0.5), rn(G, rank, K, std=K ** -0.5), rn(G, N, rank, std=rank ** -0.5)
+    c.scale = 0.5 + torch.rand(G, generator=g, device="cuda")
+    c.adapter = torch.randint(-1, G, (R,), generator=g, device="cuda", dtype=torch.int32)
+    o = c.buffers()
+    c.call(o)
+    at = torch.unique(torch.cat([torch.arange(2, device="cuda"), torch.arange(R - 3, R, device="cuda"),
+                                 torch.randint(0, R, (40,), generator=g, device="cuda")]))
+
+    def by_rows(rows, m, t):   # rows [n, C] times m's rows (t: columns), m in pieces
+        v, n = rows.double(), (1 << 27) // m.shape[1]
+        if t:
+            out = torch.zeros(v.shape[0], m.shape[1], dtype=torch.float64, device="cuda")
+            for i in range(0, m.shape[0], n):
+                out += v[:, i:i + n] @ m[i:i + n].double()
+            return out
+        return torch.cat([v @ m[i:i + n].double().t() for i in range(0, m.shape[0], n)], 1)
+
+    y, dx = by_rows(c.x[at], c.w, False), by_rows(c.dy[at], c.w, True)
+    for i, r in enumerate(at.tolist()):
+        q = int(c.adapter[r])
+        if q >= 0:
+            y[i] += c.scale[q].double() * (c.b[q].double() @ (c.a[q].double() @ c.x[r].double()))
+            dx[i] += c.scale[q].double() * ((c.dy[r].double() @ c.b[q].double()) @ c.a[q].double())
+    for got, want, n in ((o["y"], y, K), (o["dx"], dx, N)):
+        d = (got[at].double() - want).abs()
+        # n terms of random sign, each of size / sqrt(n): U n of their magnitudes is U sqrt(n) of the size
+        size = want.pow(2).mean().sqrt()
+        assert bool((d <= 2.0 ** -8 * want.abs() + (2.0 ** -15 + 4 * U * n ** 0.5) * size).all()), d.max().item()
+        assert bool(got.isfinite().all())
+    for q in range(0, G, max(G // 5, 1)):
+        rows = torch.nonzero(c.adapter == q)[:, 0]
+        da, db = (torch.zeros(t.shape[1:], dtype=torch.float64, device="cuda") for t in (o["da"], o["db"]))
+        step = max(1, (1 << 27) // (N + K))
+        for i in range(0, rows.numel(), step):
+            k = rows[i:i + step]
+            x, dy = c.x[k].double(), c.dy[k].double()
+            s, t = c.scale[q].double() * (x @ c.a[q].double().t()), c.scale[q].double() * (dy @ c.b[q].double())
+            da += t.t() @ x
+            db += dy.t() @ s
+        for got, want, C in ((o["da"][q], da, N), (o["db"][q], db, K)):
+            if rows.numel() == 0:
+                assert (got == 0).all()
+                continue
+            rms = ((got.double() - want).pow(2).mean() / want.pow(2).mean()).sqrt().item()
+            assert rms <= 2.0 ** -24 * ((C / 8) ** 0.5 + (3 * rows.numel() / 2) ** 0.5 + 2), (q, rms)
