@@ -262,8 +262,18 @@ struct LoraExt {
 // either operand, every 16-byte chunk (8 positions, of one adapter and piece
 // since rank is a multiple of 8) from where it lies or, masked, as zeros.
 // compute(i): multiplies the slice in slots i.
-// ROWS: returns false, with nothing done, for a tile of more than
-// kLoraSliceAdapters adapters.
+// ROWS: returns false, with nothing done, for a tile of more adapters than the
+// slices are the faster form for, kLoraSliceAdapters or, with WT, whose other
+// form goes lane by lane, kLoraSliceAdaptersT.  Whole calls, slices / the other
+// form, us, by the adapters of rows in no order (a tile of 64 or 128 rows names
+// about that many, of 48 about 36 and 43):
+//   adapters                         4          8         16         24         32         48
+//   300 x 4096 x 4096, rank 16  31.9/31.0  34.3/31.8  38.9/34.0  40.9/34.8  44.9/38.5  47.7/39.0
+//     rank 64                   40.2/40.7  50.2/46.5  64.8/55.5  75.7/61.7  84.3/66.7  99.6/69.5
+//   2000 x 2048 x 2048, rank 32 39.3/38.7  49.5/46.3  65.8/58.4  79.2/65.8  92.6/70.8   116/78.2
+//   WT: 300 rows, rank 16       37.3/43.2  39.5/44.7  44.6/46.5  46.6/48.3  51.6/50.4  54.7/51.3
+//     rank 64                   49.2/79.0  58.1/85.7  72.3/89.7  91.3/99.7   100/102    118/107
+//     2000 rows, rank 32        43.4/80.1  53.9/92.9   73.1/104   86.2/109   102/112    126/119
 //
 // The zeros that keep an adapter from the other adapters' rows keep it out
 // only while it is finite.  So that one request's broken adapter does not
@@ -271,7 +281,7 @@ struct LoraExt {
 // are taken out of the fragments (lora_finite), and a tile that met any adds
 // their products afterwards, to the rows that name the adapter
 // (lora_add_nonfinite).
-constexpr int kLoraSliceAdapters = 8;
+constexpr int kLoraSliceAdapters = 8, kLoraSliceAdaptersT = 28;
 
 // Two bf16 in a dword: bits 15 and 31 of the carry out of their exponents.
 __device__ __forceinline__ uint32_t nonfinite_bf16x2(uint32_t v) { return (v & 0x7f807f80u) + 0x00800080u; }
@@ -386,7 +396,7 @@ __device__ __forceinline__ bool lora_slices(const LoraExt& x, const GemmArgs& g,
     }
   }
   lds_barrier();
-  if (ROWS && __builtin_amdgcn_readfirstlane(*count) > kLoraSliceAdapters) return false;
+  if (ROWS && __builtin_amdgcn_readfirstlane(*count) > (WT ? kLoraSliceAdaptersT : kLoraSliceAdapters)) return false;
   const int len = __builtin_amdgcn_readfirstlane(*count) * span;
   int mine[LX];   // the list places of the rows this lane loads
 #pragma unroll

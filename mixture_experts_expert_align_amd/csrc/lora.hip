@@ -85,6 +85,7 @@ __device__ __forceinline__ int tr_at(int r, int c, int pitch) {
 // Grid (row blocks, passes in flight, row tile groups): with few row blocks
 // the adapters of one block go to different workgroups.
 constexpr int kShrinkWaves = 4;
+constexpr int64_t kShrinkSplitRows = 320;
 
 template <int JT, int CT, bool T, int D>
 __global__ void __launch_bounds__(64 * kShrinkWaves) lora_shrink_kernel(LoraArgs a, const uint16_t* __restrict__ v,
@@ -262,6 +263,10 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) lora_shrink_kernel(LoraArgs
 // used.  (Loads of 16 rows by 64 bytes, all products used, reach 28 KB/us on a
 // CU; these about 70.)  Wave j also adds the adapters' product of the ranks
 // 8 j .. 8 j + 7 to its sums, each row with its own B_g.
+// Whole calls by lines / by tiles, us, 1, 16, 32, 48, 64 rows: 4096 x 4096, rank 16
+// 11.1/24.5 16.6/27.2 19.7/29.3 25.7/30.5 29.1/31.5; 2048 x 2048, rank 8 9.0/16.1
+// 11.0/16.8 13.3/17.1 17.0/17.7 19.6/18.0; N = 4096, K = 14336, rank 16 28.2/60.6
+// 33.6/64.7 45.2/65.9 61.7/68.9 71.4/70.9.
 constexpr int kStreamWaves = 16;
 
 __device__ __forceinline__ float ror8(float v) {   // lane c of a row of 16: from lane (c + 8) % 16
@@ -556,11 +561,15 @@ hipError_t launch_shrink(const LoraArgs& a, const uint16_t* v, const uint16_t* m
 }
 
 // low[r] = scale_g (T ? B_g^T : A_g) v_r, contraction C.  With few rows each
-// 16 of the rank's outputs go to a workgroup of their own.  (Blocks of 32 rows
+// 16 of the rank's outputs go to a workgroup of their own (forward of N = 1024, K
+// = 4096, 4 adapters, each on its own / all in one, us: rank 128, 65 rows 39.0 /
+// 46.6, 300 47.1 / 48.7, 512 52.5 / 48.7, 1024 66.6 / 52.3; rank 32, 65 rows 28.6 /
+// 30.3, 300 32.1 / 31.2, 1024 34.3 / 31.4; 300 rows of 48, rank 32, N = K = 4096,
+// 49.2 / 50.0).  (Blocks of 32 rows
 // read each adapter's matrix half as often but put one workgroup on a CU: 24
 // against 17 us at 8192 x 4096, rank 16, no difference at rank 64.)
 hipError_t shrink(const LoraArgs& a, const uint16_t* v, const uint16_t* m, int C, bool t, hipStream_t s) {
-  if (a.rank <= 16 || (!t && a.R <= 1024)) return launch_shrink<1, 1, 4>(a, v, m, C, t, s);
+  if (a.rank <= 16 || (!t && a.R <= kShrinkSplitRows)) return launch_shrink<1, 1, 4>(a, v, m, C, t, s);
   if (a.rank <= 32) return launch_shrink<2, 1, 3>(a, v, m, C, t, s);
   if (a.rank <= 64) return launch_shrink<4, 1, 2>(a, v, m, C, t, s);
   return launch_shrink<8, 1, 2>(a, v, m, C, t, s);
@@ -593,9 +602,15 @@ hipError_t launch_lora_dgrad(const LoraArgs& a, const uint16_t* dy, const uint16
   return launch_tile_lora_bf16(a, dy, w, am, dx, N, K, true, s);
 }
 
+// Shares of each adapter's rows: at most two workgroups per CU, 256 rows of an
+// even split at least.  1 / 2 / 3 / 4 / 8 / 16 shares, whole call, us: 8192 rows of
+// 4, 4096 x 6144, rank 64 (rule: 3) 87 / 73 / 62 / 73 / 84 / 119; 1001 of 3, 2048 x
+// 2048, rank 8 (4) 16.8 / 15.5 / 14.7 / 15.0 / 16.5 / 21.0; 4096 of one, 1024 x 1024,
+// rank 32 (16) 111 / 65 / 50 / 42 / 31 / 29; 300 of 48, 4096 x 4096, rank 32 (1) 26 /
+// 65 / 86 / 107 / 229 / 412.
 int32_t lora_wgrad_shares(int64_t R, int64_t N, int64_t K, int64_t G) {
   const int64_t wgs = G * ((K + kWgCols - 1) / kWgCols + (N + kWgCols - 1) / kWgCols);
-  int64_t n = 512 / wgs;                              // at most two workgroups per CU
+  int64_t n = 512 / wgs;
   const int64_t most = (R + 255) / 256;
   if (n > most) n = most;
   return (int32_t)(n < 1 ? 1 : n > 16 ? 16 : n);

@@ -891,7 +891,9 @@ int64_t moe_lora_low_bytes(const moe_lora_problem* p) {
   return lora_ok(p) == MOE_OK ? 2 * kLoraPieces * p->R * p->rank : -1;
 }
 
-// Chunks of the rows' sort: one workgroup takes 30 us for 8192 rows.
+// Chunks of the rows' sort (the gradients' whole call, 4 adapters of rank 16, N =
+// K = 256, one workgroup / several, us: 1024 rows 14.5 / 17.4, 2048 18.6 / 19.3,
+// 3000 22.0 / 20.5, 8192 38.2 / 23.7).
 static int64_t lora_align_blocks(int64_t R) { return R <= 2 * kAlignChunk ? 0 : align_nblocks_of(R); }
 
 static AlignLayout lora_layout(const moe_lora_problem* p) {
