@@ -44,7 +44,7 @@
 extern "C" {
 #endif
 
-#define MOE_ABI_VERSION 6
+#define MOE_ABI_VERSION 7
 
 /* Status codes. */
 enum {
@@ -611,6 +611,172 @@ int moe_lora_dgrad(const moe_lora_problem* p, const void* dy, const void* w, con
  * the finished sums, as moe_grouped_wgrad does. */
 int moe_lora_wgrad(const moe_lora_problem* p, const void* x, const void* dy, const void* low_x, const void* low_dy,
                    const int32_t* adapter, float* da, float* db, int accumulate, void* ws, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The load balance of a router's choice: counts per expert, the balance loss
+ * of each sequence of a packed batch, and the loss's gradient over the logits.
+ *
+ * Sequence s is the tokens [seq_offsets[s], seq_offsets[s+1]); a token counts
+ * when at least one of its topk ids is in [0, E) (padding tokens carry ids of
+ * -1 only).  With l the logits as moe_route_topk takes them (the bias added
+ * with MOE_ROUTE_BIAS_LOGIT, NaN and -inf never chosen, +inf as the largest
+ * float32) and p_t,e the softmax of l_t, or sigmoid(l_t,e) over their sum (0
+ * for an expert that cannot be chosen):
+ *
+ *   counts[s,e] = routes of s's tokens to e        tokens[s] = T_s, those that count
+ *   probs[s,e]  = P_s,e = sum of p_t,e over the tokens that count / T_s
+ *   loss[s]     = E / (topk T_s) sum_e counts[s,e] P_s,e
+ *   dlogits[t,e] = dloss[s] E / (topk T_s^2) sum_f counts[s,f] dp_t,f / dl_t,e
+ *
+ * and 0 throughout for T_s = 0.  The choice is held fixed: no gradient passes
+ * through the counts.  groups, topk_groups, renormalize, scale and a bias for
+ * the choice only (MOE_ROUTE_BIAS_SELECT: pass bias as for moe_route_topk) play
+ * no part.  Everything is computed in float32, sums over many tokens in
+ * float64, in a fixed order: the same bits on every run.
+ * ------------------------------------------------------------------------- */
+
+/* Bytes of moe_balance_loss's workspace for M tokens in S sequences; -1 for
+ * what it refuses. */
+int64_t moe_balance_ws_bytes(const moe_router* r, int64_t M, int64_t S);
+
+/* logits, dtype, logits_ld, bias, topk_ids: as for moe_route_topk (ids as it
+ * wrote them; ids outside [0, E) are skipped, one that a token holds twice is
+ * counted twice).  seq_offsets: device int32 [S+1], ascending, within [0, M]
+ * (tokens in no sequence are left out); NULL with S = 1: all M tokens.
+ * loss: device float32 [S]; counts: device int32 [S, E]; tokens: device int32
+ * [S]; probs: device float32 [S, E]; ws: device, moe_balance_ws_bytes, 16-byte
+ * aligned, its contents do not matter before or after.  Calls that share a
+ * workspace must not overlap; outputs and ws must not overlap inputs.  With M =
+ * 0 the outputs are written as zeros, and logits and topk_ids may be NULL.
+ * MOE_EINVAL: a bad router field, M outside [0, 2^31), S outside [1, 65536], S >
+ * 1 without seq_offsets, M topk at or past 2^31, a null or misaligned pointer. */
+int moe_balance_loss(const moe_router* r, int64_t M, int64_t S, const void* logits, int dtype, int64_t logits_ld,
+                     const float* bias, const int32_t* topk_ids, const int32_t* seq_offsets, float* loss,
+                     int32_t* counts, int32_t* tokens, float* probs, void* ws, void* stream);
+
+/* dlogits from counts and tokens as moe_balance_loss wrote them for the same
+ * logits, ids and sequences, and dloss, device float32 [S].  accumulate = 0
+ * writes every dlogits[t, e] (0 for tokens that do not count), 1 adds to it
+ * (one rounding; tokens that do not count are left as they are), for instance
+ * to what moe_route_topk_backward wrote.  dlogits: as for
+ * moe_route_topk_backward.  Errors as above. */
+int moe_balance_loss_backward(const moe_router* r, int64_t M, int64_t S, const void* logits, int dtype,
+                              int64_t logits_ld, const float* bias, const int32_t* topk_ids,
+                              const int32_t* seq_offsets, const int32_t* counts, const int32_t* tokens,
+                              const float* dloss, void* dlogits, int64_t dlogits_ld, int accumulate, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The norms around a block: its output, normed and gated, into the residual
+ * stream, and the stream's norm as the next block's input.  For each token
+ *
+ *   u  = block / rms(block) * w_post      (w_post NULL: u = block)
+ *   x' = res_scale x + gate u             (block NULL: x' = x, not written)
+ *   h  = x' / rms(x') * w_pre             (w_pre NULL: no h)
+ *
+ * with rms(v) = sqrt(mean of v^2 + eps), gate none (1), one per channel [K] or
+ * one per token [M].  Computed in float32; x' and h are each rounded once, h
+ * from the x' before its rounding.  (Squares past the largest float32, values
+ * beyond 1.8e19 in magnitude, make a row's rms infinite.)  One call serves the
+ * first norm of a model (block NULL), every junction between two blocks, and
+ * the last block's output (w_pre NULL).
+ * ------------------------------------------------------------------------- */
+enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2 };
+
+typedef struct moe_norm_problem {
+  int64_t M;            /* tokens, 0 .. 2^31 - 1                               */
+  int64_t K;            /* hidden size, a multiple of 8 up to 16384            */
+  int32_t x_dtype;      /* x, x' and their gradients: 0 float32, 1 bf16        */
+  int32_t w_dtype;      /* w_post, w_pre and a gate per channel: 0 float32, 1 bf16 */
+  int32_t gate_kind;    /* MOE_GATE_*                                          */
+  float eps;            /* > 0, finite                                         */
+  float res_scale;      /* finite                                              */
+} moe_norm_problem;
+
+/* sizeof(moe_norm_problem) and sizeof(moe_ortho_problem) as compiled into the
+ * library (each pointer may be NULL). */
+void moe_block_struct_sizes(int64_t* norm, int64_t* ortho);
+
+/* x [M, K]: device, x_dtype; block [M, K]: device bf16 or NULL; w_post [K], NULL
+ * without a norm behind the block; gate: NULL exactly when gate_kind is NONE,
+ * device w_dtype [K] or float32 [M]; w_pre [K] and h [M, K] (device bf16): both
+ * or neither; x_out [M, K]: device, x_dtype, may be x itself, NULL exactly when
+ * block is.  block NULL needs w_pre, no w_post and MOE_GATE_NONE (res_scale is
+ * not applied).  16-byte alignment for all but a gate per token (4).  M = 0
+ * enqueues nothing.  MOE_EINVAL: a bad field, a null or misaligned pointer, a
+ * combination not named here; MOE_EUNSUPPORTED: K not a multiple of 8 or past
+ * 16384. */
+int moe_block_norm(const moe_norm_problem* p, const void* x, const void* block, const void* w_post,
+                   const void* gate, const void* w_pre, void* x_out, void* h, void* stream);
+
+/* Bytes of moe_block_norm_backward's workspace; -1 for a refused problem. */
+int64_t moe_block_norm_ws_bytes(const moe_norm_problem* p);
+
+/* Gradients at the stored x' (x_out as the forward wrote it; block NULL: x):
+ * with dx_out the gradient of x' from what follows (device, x_dtype; NULL: 0)
+ * and dh that of h (device bf16; NULL exactly when w_pre is),
+ *
+ *   d  = dx_out + (w_pre dh - n mean(w_pre dh n)) / rms(x'),   n = x' / rms(x')
+ *   dx = res_scale d,   dblock = the same of gate d through the block's norm
+ *   dw_pre = sum over tokens of dh n,   dw_post = sum of gate d (block / rms(block))
+ *   dgate = sum of d u: over the tokens (per channel), over K (per token)
+ *
+ * dx [M, K]: device, x_dtype, may be dx_out itself; dblock [M, K]: device bf16,
+ * NULL exactly when block is; dw_post, dw_pre: device float32 [K], dgate: device
+ * float32 [K] or [M]; each of the three may be NULL (not wanted) and must be
+ * where its operand is.  accumulate = 0 writes the sums over the tokens (dw_pre,
+ * dw_post, dgate per channel; +0.0 for M = 0), 1 adds the finished sums; a
+ * gate's gradient per token is always written.  Sums in float32 in a fixed
+ * order.  dx_out and w_pre must not both be NULL.  ws: device,
+ * moe_block_norm_ws_bytes, 16-byte aligned, contents of no matter; calls that
+ * share it must not overlap.  Other outputs must not overlap inputs.  Errors as
+ * for moe_block_norm. */
+int moe_block_norm_backward(const moe_norm_problem* p, const void* x_out, const void* block, const void* w_post,
+                            const void* gate, const void* w_pre, const void* dx_out, const void* dh, void* dx,
+                            void* dblock, float* dw_post, float* dgate, float* dw_pre, int accumulate, void* ws,
+                            void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The orthogonalised update of E matrices (the experts' weights, their
+ * gradients or momenta as moe_grouped_wgrad leaves them): Newton-Schulz steps
+ * on each matrix U [N, K],
+ *
+ *   X = U / (|U|_F + eps),   `steps` times with coefficients (a, b, c):
+ *   X <- X (a I + b A + c A^2),  A = X^T X  (N < K: of the transpose)
+ *   out = scale X
+ *
+ * Products of float16 operands summed in float32 in a fixed order (the same
+ * bits on every run).  X is kept in two float16 pieces (22 bits), the
+ * diagonals of A and of b A + c A^2 in float32 beside their float16
+ * off-diagonal parts, all scaled by powers of two to float16's range; the norm
+ * is summed in float64.  With five steps of (3.4445, -4.775, 2.0315) the result
+ * is within 2e-3 of the exact one (2-norm, relative) before its rounding to
+ * bf16 for matrices of Gaussian, low-rank and decaying spectra.  A matrix with
+ * a NaN or an infinity gives NaN in all of its own out; a zero matrix gives
+ * zeros.
+ * ------------------------------------------------------------------------- */
+#define MOE_ORTHO_MAX_STEPS 16
+
+typedef struct moe_ortho_problem {
+  int64_t E, N, K;      /* matrices and their shape, each >= 1                 */
+  int32_t dtype;        /* of the update: 0 float32, 1 bf16                    */
+  int32_t steps;        /* 1 .. MOE_ORTHO_MAX_STEPS                            */
+  float eps;            /* > 0, finite                                         */
+  float scale;          /* finite                                              */
+  float coef[MOE_ORTHO_MAX_STEPS][3];   /* a, b, c of each step                */
+} moe_ortho_problem;
+
+/* Bytes of the workspace; -1 for a refused problem. */
+int64_t moe_ortho_ws_bytes(const moe_ortho_problem* p);
+
+/* update [E, N, K]: device, dtype, aligned to its element; out [E, N, K]: device
+ * bf16, 2-byte aligned, must not overlap update or ws; ws: device, 16-byte
+ * aligned, contents of no matter; calls that share it must not overlap.
+ * MOE_EINVAL: null or misaligned pointer, sizes below 1, bad dtype, steps, eps or
+ * scale; MOE_EUNSUPPORTED: N or K past 32768, E past 65535, a matrix of 2^30
+ * elements or more or 2^36 in all (sides rounded up to multiples of 256),
+ * coefficients that are not finite or let a singular value in [0, 1] grow past
+ * 4096. */
+int moe_orthogonalize(const moe_ortho_problem* p, const void* update, void* out, void* ws, void* stream);
 
 #ifdef __cplusplus
 }

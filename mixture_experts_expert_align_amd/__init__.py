@@ -32,9 +32,14 @@ __all__ = [
     "moe_layer_apply", "check_layer_status",
     "MoeLoraProblem", "moe_lora_low_bytes", "moe_lora_ws_bytes", "allocate_lora_low", "allocate_lora_workspace",
     "moe_lora_forward", "moe_lora_dgrad", "moe_lora_wgrad",
+    "moe_balance_ws_bytes", "allocate_balance_workspace", "moe_balance_loss", "moe_balance_loss_backward",
+    "GATE_NONE", "GATE_CHANNEL", "GATE_TOKEN", "MoeNormProblem", "make_norm_problem", "moe_block_norm_ws_bytes",
+    "allocate_norm_workspace", "moe_block_norm", "moe_block_norm_backward",
+    "ORTHO_MAX_STEPS", "MUON_COEF", "MoeOrthoProblem", "make_ortho_problem", "moe_ortho_ws_bytes",
+    "allocate_ortho_workspace", "moe_orthogonalize",
 ]
 
-ABI_VERSION = 6
+ABI_VERSION = 7
 STATIC_SCRATCH_BYTES = 64 << 20     # MOE_STATIC_SCRATCH_BYTES
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EHIP = 0, 1, 2, 3
 LAYOUT_CONTIGUOUS, LAYOUT_BATCHED = 0, 1
@@ -44,6 +49,9 @@ VARIANT_AUTO, VARIANT_TILE, VARIANT_STREAM, VARIANT_FUSED = -1, 0, 1, 2
 REDUCE_NOOP, REDUCE_CONTIGUOUS, REDUCE_NAIVE_BATCHED = 0, 1, 2
 ROUTE_SOFTMAX, ROUTE_SIGMOID = 0, 1                  # MOE_ROUTE_SOFTMAX, MOE_ROUTE_SIGMOID
 BIAS_NONE, BIAS_LOGIT, BIAS_SELECT = 0, 1, 2         # MOE_ROUTE_BIAS_*
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN = 0, 1, 2        # MOE_GATE_*
+ORTHO_MAX_STEPS = 16                                 # MOE_ORTHO_MAX_STEPS
+MUON_COEF = (3.4445, -4.7750, 2.0315)                # the Muon optimiser's steps
 
 _i64, _i32, _vp = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p
 
@@ -77,6 +85,16 @@ class MoeLayerPlan(ctypes.Structure):
 
 class MoeLoraProblem(ctypes.Structure):
     _fields_ = [("R", _i64), ("N", _i64), ("K", _i64), ("G", _i64), ("rank", _i64)]
+
+
+class MoeNormProblem(ctypes.Structure):
+    _fields_ = [("M", _i64), ("K", _i64), ("x_dtype", _i32), ("w_dtype", _i32), ("gate_kind", _i32),
+                ("eps", ctypes.c_float), ("res_scale", ctypes.c_float)]
+
+
+class MoeOrthoProblem(ctypes.Structure):
+    _fields_ = [("E", _i64), ("N", _i64), ("K", _i64), ("dtype", _i32), ("steps", _i32), ("eps", ctypes.c_float),
+                ("scale", ctypes.c_float), ("coef", (ctypes.c_float * 3) * ORTHO_MAX_STEPS)]
 
 
 class MoePlan(ctypes.Structure):
@@ -150,6 +168,15 @@ def load_library() -> ctypes.CDLL:
         "moe_lora_dgrad": (_i32, [_vp] * 10),
         "moe_lora_wgrad": (_i32, [_vp] * 8 + [_i32, _vp, _vp]),
         "moe_route_topk": (_i32, [_vp, _i64, _vp, _i32, _i64, _vp, _vp, _vp, _vp]),
+        "moe_balance_ws_bytes": (_i64, [_vp, _i64, _i64]),
+        "moe_balance_loss": (_i32, [_vp, _i64, _i64, _vp, _i32, _i64] + [_vp] * 9),
+        "moe_balance_loss_backward": (_i32, [_vp, _i64, _i64, _vp, _i32, _i64] + [_vp] * 7 + [_i64, _i32, _vp]),
+        "moe_block_struct_sizes": (None, [_vp, _vp]),
+        "moe_block_norm": (_i32, [_vp] * 9),
+        "moe_block_norm_ws_bytes": (_i64, [_vp]),
+        "moe_block_norm_backward": (_i32, [_vp] * 13 + [_i32, _vp, _vp]),
+        "moe_ortho_ws_bytes": (_i64, [_vp]),
+        "moe_orthogonalize": (_i32, [_vp] * 5),
         "moe_route_topk_backward": (_i32, [_vp, _i64, _vp, _i32, _i64, _vp, _vp, _vp, _vp, _i64, _vp]),
     }
     for name, (res, args) in sig.items():
@@ -168,6 +195,10 @@ def load_library() -> ctypes.CDLL:
     want = [ctypes.sizeof(MoeRouter), ctypes.sizeof(MoeLayerProblem), ctypes.sizeof(MoeLayerPlan)]
     if [s.value for s in sizes] != want:
         raise RuntimeError(f"struct layout mismatch: library {[s.value for s in sizes]}, binding {want}")
+    lib.moe_block_struct_sizes(*[ctypes.byref(s) for s in sizes[:2]])
+    want = [ctypes.sizeof(MoeNormProblem), ctypes.sizeof(MoeOrthoProblem)]
+    if [s.value for s in sizes[:2]] != want:
+        raise RuntimeError(f"struct layout mismatch: library {[s.value for s in sizes[:2]]}, binding {want}")
     _LIB = lib
     return lib
 
@@ -683,3 +714,175 @@ def moe_lora_wgrad(x, dy, low_x, low_dy, adapter, da, db, ws, accumulate: bool =
         _on(dev, db, "db", torch.float32, 0), 1 if accumulate else 0,
         _ws_on(dev, ws, "ws", max(load_library().moe_lora_ws_bytes(ctypes.byref(p)), 0)), _raw_stream(stream, dev))
     _check("moe_lora_wgrad", st)
+
+
+# -------------------------------------------------------------- balance ----
+
+def moe_balance_ws_bytes(router: MoeRouter, M, S=1) -> int:
+    v = load_library().moe_balance_ws_bytes(ctypes.byref(router), M, S)
+    if v < 0:
+        raise MoeError("moe_balance_ws_bytes", MOE_EINVAL)
+    return v
+
+
+def allocate_balance_workspace(router: MoeRouter, M, S=1, device="cuda") -> torch.Tensor:
+    """moe_balance_loss's workspace for M tokens in S sequences."""
+    return torch.empty(moe_balance_ws_bytes(router, M, S), dtype=torch.uint8, device=device)
+
+
+def _sequences(counts, E: int, seq_offsets) -> int:
+    if counts.dim() != 2 or counts.shape[1] != E:
+        raise ValueError(f"counts: shape {tuple(counts.shape)}, expected [S, {E}]")
+    S = counts.shape[0]
+    if seq_offsets is None and S != 1:
+        raise ValueError(f"counts of {S} sequences need seq_offsets")
+    if seq_offsets is not None and seq_offsets.numel() != S + 1:
+        raise ValueError(f"seq_offsets: {seq_offsets.numel()} elements, expected {S + 1}")
+    return S
+
+
+def moe_balance_loss(router: MoeRouter, logits, topk_ids, loss, counts, tokens, probs, ws, bias=None,
+                     seq_offsets=None, stream=None):
+    """Per sequence s of logits [M, E] (float32 or bf16) and topk_ids int32 [M,
+    topk]: loss [S] float32, counts [S, E] int32 (routes per expert), tokens [S]
+    int32 (those with a route), probs [S, E] float32 (mean scores).  seq_offsets:
+    int32 [S + 1], None for one sequence; ws: from allocate_balance_workspace."""
+    E, dev = router.E, _device_for(logits)
+    ptr, code, ld = _logits(dev, logits, E, "logits")
+    M, S = logits.shape[0], _sequences(counts, E, seq_offsets)
+    lib = load_library()
+    st = lib.moe_balance_loss(
+        ctypes.byref(router), M, S, ptr, code, ld, _on(dev, bias, "bias", torch.float32, E),
+        _on(dev, topk_ids, "topk_ids", torch.int32, M * router.topk),
+        _on(dev, seq_offsets, "seq_offsets", torch.int32, S + 1), _on(dev, loss, "loss", torch.float32, S),
+        _on(dev, counts, "counts", torch.int32, S * E), _on(dev, tokens, "tokens", torch.int32, S),
+        _on(dev, probs, "probs", torch.float32, S * E),
+        _ws_on(dev, ws, "ws", lib.moe_balance_ws_bytes(ctypes.byref(router), M, S)), _raw_stream(stream, dev))
+    _check("moe_balance_loss", st)
+
+
+def moe_balance_loss_backward(router: MoeRouter, logits, topk_ids, counts, tokens, dloss, dlogits, bias=None,
+                              seq_offsets=None, accumulate: bool = False, stream=None):
+    """dlogits [M, E] (the logits' dtype) from dloss [S] float32 and the counts
+    and tokens of moe_balance_loss; written, or added to when ``accumulate``."""
+    E, dev = router.E, _device_for(logits)
+    ptr, code, ld = _logits(dev, logits, E, "logits")
+    dptr, dcode, dld = _logits(dev, dlogits, E, "dlogits")
+    M, S = logits.shape[0], _sequences(counts, E, seq_offsets)
+    if dcode != code or dlogits.shape[0] != M:
+        raise ValueError("dlogits: expected the dtype and shape of logits")
+    st = load_library().moe_balance_loss_backward(
+        ctypes.byref(router), M, S, ptr, code, ld, _on(dev, bias, "bias", torch.float32, E),
+        _on(dev, topk_ids, "topk_ids", torch.int32, M * router.topk),
+        _on(dev, seq_offsets, "seq_offsets", torch.int32, S + 1), _on(dev, counts, "counts", torch.int32, S * E),
+        _on(dev, tokens, "tokens", torch.int32, S), _on(dev, dloss, "dloss", torch.float32, S), dptr, dld,
+        1 if accumulate else 0, _raw_stream(stream, dev))
+    _check("moe_balance_loss_backward", st)
+
+
+# ----------------------------------------------------------------- norm ----
+
+def make_norm_problem(M, K, x_dtype=torch.bfloat16, w_dtype=torch.float32, gate_kind=GATE_NONE, eps=1e-6,
+                      res_scale=1.0) -> MoeNormProblem:
+    """x_dtype: the residual stream's; w_dtype: the norms' weights' and a gate
+    per channel's."""
+    for name, t in (("x_dtype", x_dtype), ("w_dtype", w_dtype)):
+        if t not in _LOGIT_DTYPES:
+            raise ValueError(f"{name}: {t}, expected torch.float32 or torch.bfloat16")
+    return MoeNormProblem(M, K, _LOGIT_DTYPES[x_dtype], _LOGIT_DTYPES[w_dtype], gate_kind, eps, res_scale)
+
+
+_FLOATS = (torch.float32, torch.bfloat16)      # by dtype code
+
+
+def moe_block_norm_ws_bytes(problem: MoeNormProblem) -> int:
+    v = load_library().moe_block_norm_ws_bytes(ctypes.byref(problem))
+    if v < 0:
+        raise MoeError("moe_block_norm_ws_bytes", MOE_EINVAL)
+    return v
+
+
+def allocate_norm_workspace(problem: MoeNormProblem, device="cuda") -> torch.Tensor:
+    """moe_block_norm_backward's workspace."""
+    return torch.empty(max(moe_block_norm_ws_bytes(problem), 16), dtype=torch.uint8, device=device)
+
+
+def _gate(dev: int, p: MoeNormProblem, t, name: str, dtype):
+    if p.gate_kind == GATE_TOKEN:
+        return _on(dev, t, name, torch.float32, p.M)
+    return _on(dev, t, name, dtype, p.K)
+
+
+def moe_block_norm(problem: MoeNormProblem, x, x_out=None, block=None, w_post=None, gate=None, w_pre=None, h=None,
+                   stream=None):
+    """x_out = res_scale x + gate (block normed by w_post), h = x_out normed by
+    w_pre; [M, K] each, h and block bf16.  Without a block: h of x alone; without
+    w_pre: no h."""
+    p, dev = problem, _device_for(x)
+    n, xt, wt = p.M * p.K, _FLOATS[p.x_dtype], _FLOATS[p.w_dtype]
+    st = load_library().moe_block_norm(
+        ctypes.byref(p), _on(dev, x, "x", xt, n), _on(dev, block, "block", torch.bfloat16, n),
+        _on(dev, w_post, "w_post", wt, p.K), _gate(dev, p, gate, "gate", wt), _on(dev, w_pre, "w_pre", wt, p.K),
+        _on(dev, x_out, "x_out", xt, n), _on(dev, h, "h", torch.bfloat16, n), _raw_stream(stream, dev))
+    _check("moe_block_norm", st)
+
+
+def moe_block_norm_backward(problem: MoeNormProblem, x_out, dx_out, dx, ws, block=None, w_post=None, gate=None,
+                            w_pre=None, dh=None, dblock=None, dw_post=None, dgate=None, dw_pre=None,
+                            accumulate: bool = False, stream=None):
+    """dx and dblock [M, K] from dx_out (None: 0) and dh, the gradients of
+    moe_block_norm's x_out and h; dw_post, dw_pre and dgate (float32, each may
+    be None) written, or added to when ``accumulate`` (a gate's per token: always
+    written).  Without a block, x_out is x."""
+    p, dev = problem, _device_for(x_out)
+    n, xt, wt, f32 = p.M * p.K, _FLOATS[p.x_dtype], _FLOATS[p.w_dtype], torch.float32
+    lib = load_library()
+    st = lib.moe_block_norm_backward(
+        ctypes.byref(p), _on(dev, x_out, "x_out", xt, n), _on(dev, block, "block", torch.bfloat16, n),
+        _on(dev, w_post, "w_post", wt, p.K), _gate(dev, p, gate, "gate", wt), _on(dev, w_pre, "w_pre", wt, p.K),
+        _on(dev, dx_out, "dx_out", xt, n), _on(dev, dh, "dh", torch.bfloat16, n), _on(dev, dx, "dx", xt, n),
+        _on(dev, dblock, "dblock", torch.bfloat16, n), _on(dev, dw_post, "dw_post", f32, p.K),
+        _gate(dev, p, dgate, "dgate", f32), _on(dev, dw_pre, "dw_pre", f32, p.K), 1 if accumulate else 0,
+        _ws_on(dev, ws, "ws", max(lib.moe_block_norm_ws_bytes(ctypes.byref(p)), 0)), _raw_stream(stream, dev))
+    _check("moe_block_norm_backward", st)
+
+
+# ---------------------------------------------------------------- ortho ----
+
+def make_ortho_problem(E, N, K, dtype=torch.float32, steps=5, coef=MUON_COEF, eps=1e-7,
+                       scale=1.0) -> MoeOrthoProblem:
+    """E updates [N, K] of dtype float32 or bf16; coef: (a, b, c) of every step,
+    or one such triple a step."""
+    if dtype not in _LOGIT_DTYPES:
+        raise ValueError(f"dtype: {dtype}, expected torch.float32 or torch.bfloat16")
+    p = MoeOrthoProblem(E, N, K, _LOGIT_DTYPES[dtype], steps, eps, scale)
+    rows = [coef] * steps if coef and not hasattr(coef[0], "__len__") else list(coef)
+    if len(rows) != steps or any(len(r) != 3 for r in rows):
+        raise ValueError(f"coef: expected (a, b, c), or {steps} of them")
+    for i, r in enumerate(rows[:ORTHO_MAX_STEPS]):
+        p.coef[i][:] = r
+    return p
+
+
+def moe_ortho_ws_bytes(problem: MoeOrthoProblem) -> int:
+    v = load_library().moe_ortho_ws_bytes(ctypes.byref(problem))
+    if v < 0:
+        raise MoeError("moe_ortho_ws_bytes", MOE_EINVAL)
+    return v
+
+
+def allocate_ortho_workspace(problem: MoeOrthoProblem, device="cuda") -> torch.Tensor:
+    """moe_orthogonalize's workspace."""
+    return torch.empty(moe_ortho_ws_bytes(problem), dtype=torch.uint8, device=device)
+
+
+def moe_orthogonalize(problem: MoeOrthoProblem, update, out, ws, stream=None):
+    """out [E, N, K] (bf16) = scale times the orthogonalised update [E, N, K]
+    (the problem's dtype), each matrix by itself."""
+    p, dev = problem, _device_for(update)
+    n = p.E * p.N * p.K
+    lib = load_library()
+    st = lib.moe_orthogonalize(
+        ctypes.byref(p), _on(dev, update, "update", _FLOATS[p.dtype], n), _on(dev, out, "out", torch.bfloat16, n),
+        _ws_on(dev, ws, "ws", max(lib.moe_ortho_ws_bytes(ctypes.byref(p)), 0)), _raw_stream(stream, dev))
+    _check("moe_orthogonalize", st)

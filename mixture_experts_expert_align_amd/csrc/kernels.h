@@ -316,6 +316,94 @@ hipError_t launch_lora_wgrad(const LoraGradArgs& a, int32_t shares, hipStream_t 
 hipError_t launch_tile_lora_bf16(const LoraArgs& a, const uint16_t* v, const uint16_t* w, const uint16_t* m,
                                  uint16_t* out, int kdim, int nfeat, bool wt, hipStream_t s);
 
+// -------------------------------------------------------------- balance ----
+// Counts, balance loss and its gradient (balance.hip).
+constexpr int kBalanceExperts = 64;      // experts a workgroup of the second launch sums
+
+struct BalanceArgs {
+  int64_t M;
+  int32_t S, E, topk, sigmoid, add_bias;
+  const void* logits;
+  int32_t bf16;
+  int64_t ld;
+  const float* bias;
+  const int32_t* ids;          // [M, topk]
+  const int32_t* offsets;      // [S+1] or null: one sequence of all tokens
+  float* loss;                 // [S]
+  int32_t* counts;             // [S, E]
+  int32_t* tokens;             // [S]
+  float* probs;                // [S, E]
+  // workspace; a slot is a (chunk of tokens, sequence) pair that meet: chunk + sequence
+  int32_t chunk, nchunk;       // tokens of a workgroup of the first launch; their number
+  float* psum;                 // [nchunk + S][E] sums of p
+  int32_t* csum;               // [nchunk + S][E] routes
+  int32_t* tsum;               // [nchunk + S] tokens that count
+  double* lpart;               // [S][blocks of kBalanceExperts]
+  int32_t* done;               // [S]
+  // backward
+  const int32_t* counts_in;
+  const int32_t* tokens_in;
+  const float* dloss;
+  void* dlogits;
+  int64_t dld;
+  int32_t accumulate;
+  int64_t t0;                  // set by the launcher: first token of a launch
+};
+
+int32_t balance_chunk(int64_t M);
+hipError_t launch_balance(const BalanceArgs& a, hipStream_t s);
+hipError_t launch_balance_backward(const BalanceArgs& a, hipStream_t s);
+
+// ----------------------------------------------------------------- norm ----
+// The norms around a block (norm.hip).
+constexpr int kNormMaxK = 16384;
+
+struct NormArgs {
+  int64_t M;
+  int32_t K, xf32, wbf16, gate_kind;
+  float eps, res_scale;
+  const void* x;               // x, or in the backward x'
+  const uint16_t* block;
+  const void* w_post;
+  const void* gate;
+  const void* w_pre;
+  void* x_out;
+  uint16_t* h;
+  // backward
+  const void* dx_out;
+  const uint16_t* dh;
+  void* dx;
+  uint16_t* dblock;
+  float* dw_post;
+  float* dgate;
+  float* dw_pre;
+  int32_t accumulate;
+  float* part;                 // [workgroups][2][K]
+};
+
+int32_t norm_backward_blocks(int64_t M, int64_t K);
+hipError_t launch_block_norm(const NormArgs& a, hipStream_t s);
+hipError_t launch_block_norm_backward(const NormArgs& a, hipStream_t s);
+
+// ---------------------------------------------------------------- ortho ----
+// Newton-Schulz steps (ortho.hip).
+constexpr int kOrthoMaxSteps = 16;
+constexpr int kOrthoNormBlocks = 64;     // partial sums of a matrix's squares
+
+struct OrthoArgs {
+  int32_t E, N, K, bf16, steps;
+  float eps, scale;
+  float coef[kOrthoMaxSteps][3];
+  const void* update;
+  uint16_t* out;
+  void* ws;
+};
+
+int64_t ortho_ws_bytes(int64_t E, int64_t N, int64_t K);
+// The bounds of the steps: false where X, A or B could leave float16's range.
+bool ortho_scales(const OrthoArgs& a, int32_t (*s)[3]);
+hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t s);
+
 // p[i * stride] = 0 for i < n (a fill kernel, capturable in a graph).
 hipError_t launch_zero_words(int32_t* p, int64_t n, int64_t stride, hipStream_t s);
 

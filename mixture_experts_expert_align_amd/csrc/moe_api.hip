@@ -983,4 +983,237 @@ int moe_lora_wgrad(const moe_lora_problem* p, const void* x, const void* dy, con
                                                                                                             : MOE_EHIP;
 }
 
+// -------------------------------------------------------------- balance ----
+
+constexpr int64_t kBalanceMaxS = 65536;
+
+struct BalanceLayout {
+  int64_t psum, csum, tsum, lpart, done, end;
+};
+
+static bool balance_layout(const moe_router* r, int64_t M, int64_t S, BalanceLayout* L) {
+  RouterArgs a;
+  if (!router_args(r, &a) || M < 0 || M * r->topk >= (1ll << 31) || S < 1 || S > kBalanceMaxS) return false;
+  const int64_t chunk = balance_chunk(M), slots = (M + chunk - 1) / chunk + S;
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t o = at;
+    at += up(bytes, 256);
+    return o;
+  };
+  L->lpart = take(8 * S * ((r->E + kBalanceExperts - 1) / kBalanceExperts));
+  L->psum = take(4 * slots * r->E);
+  L->csum = take(4 * slots * r->E);
+  L->tsum = take(4 * slots);
+  L->done = take(4 * S);
+  L->end = at;
+  return true;
+}
+
+int64_t moe_balance_ws_bytes(const moe_router* r, int64_t M, int64_t S) {
+  BalanceLayout L;
+  return M < (1ll << 31) && balance_layout(r, M, S, &L) ? L.end : -1;
+}
+
+static bool balance_args(const moe_router* r, int64_t M, int64_t S, const void* logits, int dtype, int64_t ld,
+                         const float* bias, const int32_t* ids, const int32_t* offsets, BalanceArgs* b) {
+  RouterArgs a;
+  if (!router_args(r, &a) || !logits_ok(logits, dtype, M, r->E, ld) || !router_bias_ok(a, bias)) return false;
+  if (M * r->topk >= (1ll << 31) || S < 1 || S > kBalanceMaxS || (S > 1 && !offsets) || ((uintptr_t)offsets & 3))
+    return false;
+  if (M > 0 && !aligned4(ids)) return false;
+  b->M = M;
+  b->S = (int32_t)S;
+  b->E = a.E;
+  b->topk = a.topk;
+  b->sigmoid = a.scoring;
+  b->add_bias = a.bias_kind == MOE_ROUTE_BIAS_LOGIT;
+  b->logits = logits;
+  b->bf16 = dtype;
+  b->ld = ld;
+  b->bias = bias;
+  b->ids = ids;
+  b->offsets = offsets;
+  return true;
+}
+
+int moe_balance_loss(const moe_router* r, int64_t M, int64_t S, const void* logits, int dtype, int64_t logits_ld,
+                     const float* bias, const int32_t* topk_ids, const int32_t* seq_offsets, float* loss,
+                     int32_t* counts, int32_t* tokens, float* probs, void* ws, void* stream) {
+  BalanceArgs b{};
+  BalanceLayout L;
+  if (!balance_args(r, M, S, logits, dtype, logits_ld, bias, topk_ids, seq_offsets, &b) ||
+      !balance_layout(r, M, S, &L) || !aligned4(loss) || !aligned4(counts) || !aligned4(tokens) || !aligned4(probs) ||
+      !aligned16(ws))
+    return MOE_EINVAL;
+  b.loss = loss;
+  b.counts = counts;
+  b.tokens = tokens;
+  b.probs = probs;
+  b.chunk = balance_chunk(M);
+  b.nchunk = (int32_t)((M + b.chunk - 1) / b.chunk);
+  b.psum = at<float>(ws, L.psum);
+  b.csum = at<int32_t>(ws, L.csum);
+  b.tsum = at<int32_t>(ws, L.tsum);
+  b.lpart = at<double>(ws, L.lpart);
+  b.done = at<int32_t>(ws, L.done);
+  return launch_balance(b, (hipStream_t)stream) == hipSuccess ? MOE_OK : MOE_EHIP;
+}
+
+int moe_balance_loss_backward(const moe_router* r, int64_t M, int64_t S, const void* logits, int dtype,
+                              int64_t logits_ld, const float* bias, const int32_t* topk_ids,
+                              const int32_t* seq_offsets, const int32_t* counts, const int32_t* tokens,
+                              const float* dloss, void* dlogits, int64_t dlogits_ld, int accumulate, void* stream) {
+  BalanceArgs b{};
+  if (!balance_args(r, M, S, logits, dtype, logits_ld, bias, topk_ids, seq_offsets, &b) ||
+      !logits_ok(dlogits, dtype, M, r->E, dlogits_ld) || !aligned4(counts) || !aligned4(tokens) || !aligned4(dloss) ||
+      (accumulate != 0 && accumulate != 1))
+    return MOE_EINVAL;
+  b.counts_in = counts;
+  b.tokens_in = tokens;
+  b.dloss = dloss;
+  b.dlogits = dlogits;
+  b.dld = dlogits_ld;
+  b.accumulate = accumulate;
+  return launch_balance_backward(b, (hipStream_t)stream) == hipSuccess ? MOE_OK : MOE_EHIP;
+}
+
+// ----------------------------------------------------------------- norm ----
+
+void moe_block_struct_sizes(int64_t* norm, int64_t* ortho) {
+  if (norm) *norm = sizeof(moe_norm_problem);
+  if (ortho) *ortho = sizeof(moe_ortho_problem);
+}
+
+static bool finite_f32(float v) { return v - v == 0.0f; }
+
+static int norm_ok(const moe_norm_problem* p) {
+  if (!p || p->M < 0 || p->M >= (1ll << 31) || p->K <= 0) return MOE_EINVAL;
+  if ((p->x_dtype != 0 && p->x_dtype != 1) || (p->w_dtype != 0 && p->w_dtype != 1)) return MOE_EINVAL;
+  if (p->gate_kind < MOE_GATE_NONE || p->gate_kind > MOE_GATE_TOKEN) return MOE_EINVAL;
+  if (!(p->eps > 0.0f) || !finite_f32(p->eps) || !finite_f32(p->res_scale)) return MOE_EINVAL;
+  if (p->K % 8 || p->K > kNormMaxK) return MOE_EUNSUPPORTED;
+  return MOE_OK;
+}
+
+// Null, or 16-byte aligned.
+static bool optional16(const void* q) { return ((uintptr_t)q & 15) == 0; }
+
+// What forward and backward ask of the weights and the gate alike.
+static bool norm_weights(const moe_norm_problem* p, const void* w_post, const void* gate, const void* w_pre) {
+  if (!optional16(w_post) || !optional16(w_pre)) return false;
+  if ((p->gate_kind == MOE_GATE_NONE) != (gate == nullptr)) return false;
+  return ((uintptr_t)gate & (p->gate_kind == MOE_GATE_TOKEN ? 3 : 15)) == 0;
+}
+
+// Without a block there is nothing to norm behind it or to gate.
+static bool norm_block(const void* block, const void* w_post, const void* gate, const void* w_pre) {
+  return block ? optional16(block) : w_pre && !w_post && !gate;
+}
+
+static NormArgs norm_args(const moe_norm_problem* p, const void* x, const void* block, const void* w_post,
+                          const void* gate, const void* w_pre) {
+  NormArgs a{};
+  a.M = p->M;
+  a.K = (int32_t)p->K;
+  a.xf32 = p->x_dtype == 0;
+  a.wbf16 = p->w_dtype;
+  a.gate_kind = p->gate_kind;
+  a.eps = p->eps;
+  a.res_scale = p->res_scale;
+  a.x = x;
+  a.block = static_cast<const uint16_t*>(block);
+  a.w_post = w_post;
+  a.gate = gate;
+  a.w_pre = w_pre;
+  return a;
+}
+
+int moe_block_norm(const moe_norm_problem* p, const void* x, const void* block, const void* w_post,
+                   const void* gate, const void* w_pre, void* x_out, void* h, void* stream) {
+  const int st = norm_ok(p);
+  if (st != MOE_OK) return st;
+  if (p->M == 0) return MOE_OK;
+  if (!norm_weights(p, w_post, gate, w_pre) || !norm_block(block, w_post, gate, w_pre) || !aligned16(x) || !optional16(x_out) ||
+      !optional16(h) || (block != nullptr) != (x_out != nullptr) || (w_pre != nullptr) != (h != nullptr))
+    return MOE_EINVAL;
+  NormArgs a = norm_args(p, x, block, w_post, gate, w_pre);
+  a.x_out = x_out;
+  a.h = static_cast<uint16_t*>(h);
+  return launch_block_norm(a, (hipStream_t)stream) == hipSuccess ? MOE_OK : MOE_EHIP;
+}
+
+int64_t moe_block_norm_ws_bytes(const moe_norm_problem* p) {
+  return norm_ok(p) == MOE_OK ? 8 * (int64_t)norm_backward_blocks(p->M, p->K) * p->K : -1;
+}
+
+int moe_block_norm_backward(const moe_norm_problem* p, const void* x_out, const void* block, const void* w_post,
+                            const void* gate, const void* w_pre, const void* dx_out, const void* dh, void* dx,
+                            void* dblock, float* dw_post, float* dgate, float* dw_pre, int accumulate, void* ws,
+                            void* stream) {
+  const int st = norm_ok(p);
+  if (st != MOE_OK) return st;
+  const bool rows = p->M > 0;
+  if (!norm_weights(p, w_post, gate, w_pre) || (accumulate != 0 && accumulate != 1) || !optional16(dw_post) || !optional16(dw_pre) || !aligned16(ws) ||
+      (dw_post && !w_post) || (dw_pre && !w_pre) || (dgate && !gate) || ((uintptr_t)dgate & 3))
+    return MOE_EINVAL;
+  if (rows && (!norm_block(block, w_post, gate, w_pre) || !aligned16(x_out) || !aligned16(dx) ||
+               !optional16(dblock) || !optional16(dx_out) || !optional16(dh) ||
+               (block != nullptr) != (dblock != nullptr) || (w_pre != nullptr) != (dh != nullptr) ||
+               (!dx_out && !w_pre)))
+    return MOE_EINVAL;
+  NormArgs a = norm_args(p, x_out, block, w_post, gate, w_pre);
+  a.dx_out = dx_out;
+  a.dh = static_cast<const uint16_t*>(dh);
+  a.dx = dx;
+  a.dblock = static_cast<uint16_t*>(dblock);
+  a.dw_post = dw_post;
+  a.dgate = dgate;
+  a.dw_pre = dw_pre;
+  a.accumulate = accumulate;
+  a.part = static_cast<float*>(ws);
+  return launch_block_norm_backward(a, (hipStream_t)stream) == hipSuccess ? MOE_OK : MOE_EHIP;
+}
+
+// ---------------------------------------------------------------- ortho ----
+
+static int ortho_ok(const moe_ortho_problem* p, OrthoArgs* a) {
+  if (!p || p->E < 1 || p->N < 1 || p->K < 1 || (p->dtype != 0 && p->dtype != 1)) return MOE_EINVAL;
+  if (p->steps < 1 || p->steps > MOE_ORTHO_MAX_STEPS || !(p->eps > 0.0f) || !finite_f32(p->eps) ||
+      !finite_f32(p->scale))
+    return MOE_EINVAL;
+  if (p->N > 32768 || p->K > 32768 || p->E > 65535 || up(p->N, 256) * up(p->K, 256) >= (1ll << 30) ||
+      p->E * up(p->N, 256) * up(p->K, 256) >= (1ll << 36))
+    return MOE_EUNSUPPORTED;
+  static_assert(kOrthoMaxSteps == MOE_ORTHO_MAX_STEPS, "steps");
+  a->E = (int32_t)p->E;
+  a->N = (int32_t)p->N;
+  a->K = (int32_t)p->K;
+  a->bf16 = p->dtype;
+  a->steps = p->steps;
+  a->eps = p->eps;
+  a->scale = p->scale;
+  for (int i = 0; i < p->steps; ++i)
+    for (int j = 0; j < 3; ++j) a->coef[i][j] = p->coef[i][j];
+  int32_t s[kOrthoMaxSteps][3];
+  return ortho_scales(*a, s) ? MOE_OK : MOE_EUNSUPPORTED;
+}
+
+int64_t moe_ortho_ws_bytes(const moe_ortho_problem* p) {
+  OrthoArgs a{};
+  return ortho_ok(p, &a) == MOE_OK ? ortho_ws_bytes(a.E, a.N, a.K) : -1;
+}
+
+int moe_orthogonalize(const moe_ortho_problem* p, const void* update, void* out, void* ws, void* stream) {
+  OrthoArgs a{};
+  const int st = ortho_ok(p, &a);
+  if (st != MOE_OK) return st;
+  if (!update || ((uintptr_t)update & (p->dtype == 0 ? 3 : 1)) || !out || ((uintptr_t)out & 1) || !aligned16(ws))
+    return MOE_EINVAL;
+  a.update = update;
+  a.out = static_cast<uint16_t*>(out);
+  a.ws = ws;
+  return launch_orthogonalize(a, (hipStream_t)stream) == hipSuccess ? MOE_OK : MOE_EHIP;
+}
+
 }  // extern "C"
