@@ -38,8 +38,8 @@ __device__ __forceinline__ uint32_t f32_to_f16(float f) {
 __device__ __forceinline__ float f16_to_f32(uint32_t u) {
   return (float)__builtin_bit_cast(_Float16, (uint16_t)u);
 }
-__device__ __forceinline__ float half_of(const uint2& v, int h) {
-  return f16_to_f32((h & 2 ? v.y : v.x) >> (h & 1 ? 16 : 0));
+__device__ __forceinline__ float half_of(const i32x4& v, int h) {   // value h of 8
+  return f16_to_f32((uint32_t)v[h / 2] >> (h & 1 ? 16 : 0));
 }
 
 // 2^s
@@ -147,6 +147,7 @@ struct StepArgs {
   // output
   uint16_t* y;            // bf16 [E, N, K]
   int32_t N, K, wide;
+  int32_t vec;            // rows of y take 16-byte stores
   float scale;
   int32_t chunk;          // consecutive tiles of an XCD
   int64_t total;          // tiles
@@ -169,6 +170,19 @@ struct Shape<64> {
 };
 
 constexpr int kBK = 64;   // contraction of a slice
+constexpr int kBand = 4;  // rows of tiles that are gone through together
+
+// 8 values (or what the row has of them) of output row `row` from column c on.
+__device__ __forceinline__ void store_row(const StepArgs& a, int64_t row, int c, const i32x4& s) {
+  uint16_t* o = a.y + row * a.K + c;
+  if (a.vec && c + 8 <= a.K) {
+    *reinterpret_cast<i32x4*>(o) = s;
+    return;
+  }
+#pragma unroll
+  for (int h = 0; h < 8; ++h)
+    if (c + h < a.K) o[h] = (uint16_t)((uint32_t)s[h / 2] >> (h & 1 ? 16 : 0));
+}
 
 template <int T, int MODE>
 __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2 : T == 128 ? 2 : 4)
@@ -192,18 +206,30 @@ __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2
   const int nm = mp / T;
   int e, tp, tq;
   if (MODE == kApply) {
-    const int nn = np / T;
-    e = (int)(tl / ((int64_t)nn * nm));
-    const int r = (int)(tl % ((int64_t)nn * nm));
-    tq = r / nm;
-    tp = r % nm;
+    // bands of kBand rows of tiles, column by column: 32 tiles in a row read 4
+    // row tiles of X and 8 of B
+    const int nn = np / T, per = nn * nm;
+    e = (int)(tl / per);
+    const int r = (int)(tl % per), band = r / (kBand * nm), in = r % (kBand * nm);
+    const int h = min(kBand, nn - band * kBand);
+    tp = in / h;
+    tq = band * kBand + in % h;
   } else {
+    // the same over the tiles tp >= tq: the band from row t has its columns t,
+    // t + 1, ... 1, 2, ... up to h rows high
     const int nt = nm * (nm + 1) / 2;
     e = (int)(tl / nt);
-    int r = (int)(tl % nt);
-    tq = 0;
-    while (r >= nm - tq) r -= nm - tq++;      // row tq holds the tiles tp >= tq
-    tp = tq + r;
+    int r = (int)(tl % nt), t = 0, h = min(kBand, nm);
+    for (;;) {
+      const int in = h * (nm - t) - h * (h - 1) / 2;
+      if (r < in) break;
+      r -= in;
+      t += h;
+      h = min(kBand, nm - t);
+    }
+    tp = t;
+    while (r >= min(h, tp - t + 1)) r -= min(h, tp++ - t + 1);
+    tq = t + r;
   }
   const int p0 = tp * T, q0 = tq * T;
   const int kd = MODE == kGram ? np : mp;     // contraction, also the row length of P and Q
@@ -268,9 +294,9 @@ __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2
     for (int j = 0; j < TJ; ++j)
       fq[fb][j] = *reinterpret_cast<const i32x4*>(qs + tile::lds_off<kBK>((wj * TJ + j) * 32 + (lane & 31), c));
   };
-  auto mma = [&](int fb) {
+  auto mma = [&](int fb, int i0, int i1) {
 #pragma unroll
-    for (int i = 0; i < TI; ++i)
+    for (int i = i0; i < i1; ++i)
 #pragma unroll
       for (int j = 0; j < TJ; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, fp[fb][i]),
@@ -287,6 +313,16 @@ __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2
   else if (nk > 1) wait_vm<L>();
   else wait_vm<0>();
   lds_barrier();
+  // a step's reads for the next step go between its MFMAs, one each
+  auto interleave = [&](auto mfmas) {
+    constexpr int R = TI + TJ, N = decltype(mfmas)::value;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (i < R) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    }
+    if constexpr (R > N) __builtin_amdgcn_sched_group_barrier(0x100, R - N, 0);
+  };
   // slice kt; F 2: slices kt+2 and kt+3 exist, 1: only kt+2, 0: only kt+1, -1:
   // kt is the last
   auto slice = [&](int kt, auto mode) {
@@ -294,17 +330,25 @@ __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2
 #pragma unroll
     for (int st = 0; st + 1 < NSTEP; ++st) {
       fload((st + 1) & 1, kt, st + 1);
-      mma(st & 1);
+      mma(st & 1, 0, TI);
+      interleave(std::integral_constant<int, TI * TJ>());
+      __builtin_amdgcn_sched_barrier(0);
     }
     if (F >= 0) {
+      mma((NSTEP - 1) & 1, 0, TI / 2);
+      __builtin_amdgcn_sched_barrier(0);
       if (F >= 1) wait_vm<L>();   // slice kt+1 is in; P of kt+2 may fly
       else wait_vm<0>();
       lds_barrier();              // nobody reads slice kt's slots any more
       if (F >= 1) issue_q(kt + 2);
       if (F >= 2) issue_p(kt + 3);
       fload(0, kt + 1, 0);
+      mma((NSTEP - 1) & 1, TI / 2, TI);
+      interleave(std::integral_constant<int, (TI - TI / 2) * TJ>());
+      __builtin_amdgcn_sched_barrier(0);
+    } else {
+      mma((NSTEP - 1) & 1, 0, TI);
     }
-    mma((NSTEP - 1) & 1);
   };
   fload(0, 0, 0);
   int kt = 0;
@@ -313,78 +357,134 @@ __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2
   if (kt + 1 < nk) slice(kt++, std::integral_constant<int, 0>());
   slice(kt, std::integral_constant<int, -1>());
 
-  // acc[i][j][4 g + h]: p = p0 + 32 (wi TI + i) + 8 g + 4 (lane / 32) + h,
-  // q = q0 + 32 (wj TJ + j) + lane % 32
+  // Epilogue through LDS, HR rows q of the tile at a time as float32 rows of T:
+  // rows are read back 8 values a thread, finished and stored by whole lines;
+  // where the transpose is stored too, the finished 16-bit values take the place
+  // of the first of their two 16-byte chunks and are read by columns.  A row's
+  // even chunks lie before its odd ones, and chunk i of either at i ^ r ^ (r / 8):
+  // 8 rows of a chunk (the accumulators), 8 chunks of a row, and a column of every
+  // eighth row all lie in different banks.  (With i ^ r alone the columns met in
+  // one, 29000 cycles a tile of 256.)
+  constexpr int NT = 64 * NW;
+  constexpr int HR = T == 256 ? 128 : T;
+  constexpr int CH = T / 4, SW = CH / 2 - 1;
+  static_assert(HR * T * 4 <= 5 * kSlot * 2, "the rows fit the slots");
+  float* const stage = reinterpret_cast<float*>(smem);
+  auto chunk = [&](int r, int c) {
+    return stage + r * T + ((((c >> 1) ^ ((r ^ (r >> 3)) & SW)) + (c & 1) * (CH / 2)) << 2);
+  };
+  const int64_t me = (int64_t)e * mp;
+  const bool turned = MODE == kApply ? !a.last || a.wide : tp != tq;
 #pragma unroll
-  for (int i = 0; i < TI; ++i)
+  for (int hf = 0; hf < T / HR; ++hf) {
+    lds_barrier();
+    // acc[i][j][4 g + h]: p = 32 (wi TI + i) + 8 g + 4 (lane / 32) + h,
+    // q = 32 (wj TJ + j) + lane % 32
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
-      const int q = q0 + 32 * (wj * TJ + j) + (lane & 31);
+      const int r = 32 * (wj * TJ + j) + (lane & 31) - hf * HR;
+      if (32 * (wj * TJ + j) / HR != hf) continue;
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int p = p0 + 32 * (wi * TI + i) + 8 * g + 4 * (lane >> 5);
-        float v[4];
+      for (int i = 0; i < TI; ++i)
 #pragma unroll
-        for (int h = 0; h < 4; ++h) v[h] = acc[i][j][4 * g + h] * a.in;
-        if (MODE == kApply) {
-          const int64_t at = ((int64_t)e * np + q) * mp + p;
-          const uint2 xh = *reinterpret_cast<const uint2*>(M.hi[a.cur] + at);
-          const uint2 xl = *reinterpret_cast<const uint2*>(M.lo[a.cur] + at);
-          const f32x4 d = *reinterpret_cast<const f32x4*>(M.db + (int64_t)e * mp + p);
+        for (int g = 0; g < 4; ++g)
+          *reinterpret_cast<f32x4*>(chunk(r, 8 * (wi * TI + i) + 2 * g + (lane >> 5))) =
+              (f32x4){acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+    }
+    lds_barrier();
+    constexpr int UR = T / 8, U = HR * UR / NT;   // units of a row; of a thread
+    static_assert(U * NT == HR * UR, "units fill the threads");
+    const int u = threadIdx.x % UR, p = p0 + 8 * u;
+    float dp[8];
+    if (MODE != kGram) {
+      const float* D = (MODE == kApply ? M.db : M.da) + me + p;
+#pragma unroll
+      for (int h = 0; h < 8; ++h) dp[h] = D[h];
+    }
+#pragma unroll
+    for (int w = 0; w < U; ++w) {
+      const int r = threadIdx.x / UR + NT / UR * w, q = q0 + hf * HR + r;
+      float v[8];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const f32x4 f = *reinterpret_cast<const f32x4*>(chunk(r, 2 * u + c));
+#pragma unroll
+        for (int h = 0; h < 4; ++h) v[4 * c + h] = f[h] * a.in;
+      }
+      i32x4 s;   // the 8 finished values, 16 bits each
+      if (MODE == kApply) {
+        const int64_t at = ((int64_t)e * np + q) * mp + p;
+        const i32x4 xh = *reinterpret_cast<const i32x4*>(M.hi[a.cur] + at);
+        const i32x4 xl = *reinterpret_cast<const i32x4*>(M.lo[a.cur] + at);
+#pragma unroll
+        for (int h = 0; h < 8; ++h)
+          v[h] += (a.ca + dp[h]) * ((half_of(xh, h) + half_of(xl, h) * (1.0f / kLow)) * a.aux);
+        if (a.last) {
+          // X [n, m] is the output [N, K], or its transpose
 #pragma unroll
           for (int h = 0; h < 4; ++h)
-            v[h] += (a.ca + d[h]) * ((half_of(xh, h) + half_of(xl, h) * (1.0f / kLow)) * a.aux);
-          if (a.last) {
-            // X [n, m] is the output [N, K], or its transpose
-            const int n = a.wide ? a.K : a.N, m = a.wide ? a.N : a.K;
-#pragma unroll
-            for (int h = 0; h < 4; ++h)
-              if (q < n && p + h < m) {
-                const int64_t o = (int64_t)e * a.N * a.K + (a.wide ? (int64_t)(p + h) * a.K + q : (int64_t)q * a.K + p + h);
-                a.y[o] = (uint16_t)f32_to_bf16_rne(v[h] * a.scale);
-              }
-          } else {
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              const float w = v[h] * a.out;
-              hi[h] = f32_to_f16(w);
-              lo[h] = f32_to_f16((w - f16_to_f32(hi[h])) * kLow);
-              M.xt[((int64_t)e * mp + p + h) * np + q] = (uint16_t)hi[h];
-            }
-            *reinterpret_cast<uint2*>(M.hi[a.cur ^ 1] + at) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-            *reinterpret_cast<uint2*>(M.lo[a.cur ^ 1] + at) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
-          }
+            s[h] = (int)(f32_to_bf16_rne(v[2 * h] * a.scale) | (f32_to_bf16_rne(v[2 * h + 1] * a.scale) << 16));
+          if (!a.wide && q < a.N) store_row(a, (int64_t)e * a.N + q, p, s);
         } else {
-          const int64_t me = (int64_t)e * mp;
-          if (MODE == kSquare) {
-            const uint2 o = *reinterpret_cast<const uint2*>(M.a + (me + q) * mp + p);
-            const f32x4 dp = *reinterpret_cast<const f32x4*>(M.da + me + p);
-            const float dq = M.da[me + q];
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              const float off = half_of(o, h) * a.aux;   // 0 on the diagonal
-              v[h] = p + h == q ? a.cb * dq + a.cc * (v[h] + dq * dq)
-                                : a.cb * off + a.cc * (v[h] + (dp[h] + dq) * off);
-            }
-          }
-          uint16_t* C = (MODE == kGram ? M.a : M.b);
-          float* D = (MODE == kGram ? M.da : M.db);
-          uint32_t s[4];
+          i32x4 lo;
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
-            const bool diag = p + h == q;
-            if (diag) D[me + q] = v[h];
-            s[h] = diag ? 0u : f32_to_f16(v[h] * a.out);
+            const float w0 = v[2 * h] * a.out, w1 = v[2 * h + 1] * a.out;
+            const uint32_t h0 = f32_to_f16(w0), h1 = f32_to_f16(w1);
+            s[h] = (int)(h0 | (h1 << 16));
+            lo[h] = (int)(f32_to_f16((w0 - f16_to_f32(h0)) * kLow) | (f32_to_f16((w1 - f16_to_f32(h1)) * kLow) << 16));
           }
-          *reinterpret_cast<uint2*>(C + (me + q) * mp + p) = make_uint2(s[0] | (s[1] << 16), s[2] | (s[3] << 16));
-          if (tp != tq) {
+          *reinterpret_cast<i32x4*>(M.hi[a.cur ^ 1] + at) = s;
+          *reinterpret_cast<i32x4*>(M.lo[a.cur ^ 1] + at) = lo;
+        }
+      } else {
+        if (MODE == kSquare) {
+          const i32x4 o = *reinterpret_cast<const i32x4*>(M.a + (me + q) * mp + p);
+          const float dq = M.da[me + q];
 #pragma unroll
-            for (int h = 0; h < 4; ++h) C[(me + p + h) * mp + q] = (uint16_t)s[h];
+          for (int h = 0; h < 8; ++h) {
+            const float off = half_of(o, h) * a.aux;   // 0 on the diagonal
+            v[h] = p + h == q ? a.cb * dq + a.cc * (v[h] + dq * dq)
+                              : a.cb * off + a.cc * (v[h] + (dp[h] + dq) * off);
           }
+        }
+#pragma unroll
+        for (int h = 0; h < 8; ++h)
+          if (p + h == q) {   // the diagonal stays in float32, outside
+            (MODE == kGram ? M.da : M.db)[me + q] = v[h];
+            v[h] = 0.f;
+          }
+#pragma unroll
+        for (int h = 0; h < 4; ++h) s[h] = (int)(f32_to_f16(v[2 * h] * a.out) | (f32_to_f16(v[2 * h + 1] * a.out) << 16));
+        *reinterpret_cast<i32x4*>((MODE == kGram ? M.a : M.b) + (me + q) * mp + p) = s;
+      }
+      if (turned) *reinterpret_cast<i32x4*>(chunk(r, 2 * u)) = s;
+    }
+    if (turned) {
+      lds_barrier();
+      constexpr int OC = HR / 8;   // groups of 8 rows
+#pragma unroll
+      for (int w = 0; w < U; ++w) {
+        const int o = threadIdx.x % OC, c = threadIdx.x / OC + NT / OC * w;   // rows 8 o .. + 7, column c
+        i32x4 s;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const int r = 8 * o + 2 * h;
+          const uint32_t lo = reinterpret_cast<const uint16_t*>(chunk(r, c / 8 * 2))[c % 8];
+          const uint32_t hi = reinterpret_cast<const uint16_t*>(chunk(r + 1, c / 8 * 2))[c % 8];
+          s[h] = (int)(lo | (hi << 16));
+        }
+        const int row = p0 + c, col = q0 + hf * HR + 8 * o;
+        if (MODE == kApply && a.last) {
+          if (row < a.N) store_row(a, (int64_t)e * a.N + row, col, s);
+        } else if (MODE == kApply) {
+          *reinterpret_cast<i32x4*>(M.xt + (me + row) * np + col) = s;
+        } else {
+          *reinterpret_cast<i32x4*>((MODE == kGram ? M.a : M.b) + (me + row) * mp + col) = s;
         }
       }
     }
+  }
 }
 
 template <int T, int MODE>
@@ -538,6 +638,7 @@ hipError_t launch_orthogonalize(const OrthoArgs& o, hipStream_t st) {
   a.N = o.N;
   a.K = o.K;
   a.wide = wide;
+  a.vec = o.K % 8 == 0 && ((uintptr_t)o.out & 15) == 0;
   a.scale = o.scale;
   for (int i = 0; i < o.steps; ++i) {
     const int sx = s[i][0], sa = s[i][1], sb = s[i][2];
