@@ -25,6 +25,14 @@ __device__ __forceinline__ uint32_t f32_to_bf16_rne(float f) {
   return u >> 16;
 }
 
+// Two float -> bf16 in one word (a in the low half), the same rounding, by
+// gfx950's pack conversion.
+__device__ __forceinline__ uint32_t bf16_pack2(float a, float b) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
+}
+
 // Raw buffer resource over [p, p + bytes) (32-bit data format, no stride),
 // range check clamped to 2^31 - 1 bytes.  The size is clamped with integer
 // arithmetic: a floating-point min would put the descriptor in vector

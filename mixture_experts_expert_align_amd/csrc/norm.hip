@@ -49,7 +49,7 @@ __device__ __forceinline__ void store8(void* p, int64_t i, const float (&f)[8]) 
   } else {
     i32x4 v;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = (int)(f32_to_bf16_rne(f[2 * k]) | (f32_to_bf16_rne(f[2 * k + 1]) << 16));
+    for (int k = 0; k < 4; ++k) v[k] = (int)bf16_pack2(f[2 * k], f[2 * k + 1]);
     q[0] = v;
   }
 }

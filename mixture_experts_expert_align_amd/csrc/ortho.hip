@@ -38,10 +38,6 @@ __device__ __forceinline__ uint32_t f32_to_f16(float f) {
 __device__ __forceinline__ float f16_to_f32(uint32_t u) {
   return (float)__builtin_bit_cast(_Float16, (uint16_t)u);
 }
-__device__ __forceinline__ float half_of(const i32x4& v, int h) {   // value h of 8
-  return f16_to_f32((uint32_t)v[h / 2] >> (h & 1 ? 16 : 0));
-}
-
 // 2^s
 __host__ __device__ __forceinline__ float pow2(int s) { return ldexpf(1.0f, s); }
 
@@ -63,23 +59,64 @@ struct Mats {
 
 // ------------------------------------------------------------ norm, input --
 
-// Sums of squares: kOrthoNormBlocks workgroups a matrix.
+// Sums of squares: kOrthoNormBlocks workgroups a matrix, 16 bytes a load between
+// the first and the last aligned address of the matrix, the ends by themselves.
+// (One value a load reached 1.2 TB/s.)
 template <bool BF16>
-__global__ void __launch_bounds__(256) ortho_norm_kernel(const void* u, int64_t per, double* part) {
+__global__ void __launch_bounds__(1024) ortho_norm_kernel(const void* u, int64_t per, double* part) {
+  constexpr int EL = BF16 ? 2 : 4, V = 16 / EL;   // bytes of a value, values of a load
   const int e = blockIdx.y;
-  const int64_t base = (int64_t)e * per;
-  const int64_t step = (int64_t)gridDim.x * 256;
+  const char* base = static_cast<const char*>(u) + (int64_t)e * per * EL;
+  const int64_t head = min((int64_t)((16 - ((uintptr_t)base & 15)) & 15) / EL, per);
+  const int64_t nv = (per - head) / V;
+  auto value = [&](int64_t i) {
+    const char* p = base + i * EL;
+    return BF16 ? bf16_to_f32(*reinterpret_cast<const uint16_t*>(p)) : *reinterpret_cast<const float*>(p);
+  };
   double s = 0.0;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < per; i += step) {
-    const double v = BF16 ? bf16_to_f32(static_cast<const uint16_t*>(u)[base + i]) : static_cast<const float*>(u)[base + i];
-    s += v * v;
+  const i32x4* body = reinterpret_cast<const i32x4*>(base + head * EL);
+  const int64_t step = (int64_t)gridDim.x * 1024;
+  auto add = [&](const i32x4& x) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t w = (uint32_t)x[k];
+      const double a = __uint_as_float(BF16 ? w << 16 : w);
+      s += a * a;
+      if (BF16) {
+        const double b = __uint_as_float(w & 0xffff0000u);
+        s += b * b;
+      }
+    }
+  };
+  int64_t i = (int64_t)blockIdx.x * 1024 + threadIdx.x;
+  for (; i + 3 * step < nv; i += 4 * step) {
+    i32x4 x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = body[i + k * step];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) add(x[k]);
   }
-  __shared__ double s_v[4];
+  for (; i < nv; i += step) add(body[i]);
+  if (blockIdx.x == 0) {
+    const int64_t tail = head + nv * V;
+    if (threadIdx.x < head) {
+      const double a = value(threadIdx.x);
+      s += a * a;
+    }
+    if (tail + threadIdx.x < per) {
+      const double a = value(tail + threadIdx.x);
+      s += a * a;
+    }
+  }
+  __shared__ double s_v[16];
 #pragma unroll
   for (int d = 32; d; d >>= 1) s += __shfl_xor(s, d);
   if ((threadIdx.x & 63) == 0) s_v[threadIdx.x >> 6] = s;
   __syncthreads();
-  if (threadIdx.x == 0) part[(int64_t)e * gridDim.x + blockIdx.x] = (s_v[0] + s_v[1]) + (s_v[2] + s_v[3]);
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < 16; ++w) s += s_v[w];
+    part[(int64_t)e * gridDim.x + blockIdx.x] = s;
+  }
 }
 
 // X and X^T from U, 64 x 64 values a workgroup: U [N, K] is X (wide = 0) or X^T.
@@ -395,12 +432,21 @@ __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2
     constexpr int UR = T / 8, U = HR * UR / NT;   // units of a row; of a thread
     static_assert(U * NT == HR * UR, "units fill the threads");
     const int u = threadIdx.x % UR, p = p0 + 8 * u;
-    float dp[8];
-    if (MODE != kGram) {
-      const float* D = (MODE == kApply ? M.db : M.da) + me + p;
+    // (powers of two go into the columns' factors: a value costs a few fused
+    // operations that take float16 operands as they are; written out, with each
+    // step by itself, the arithmetic took 20000 cycles a tile of 256)
+    float kp[8];
+    if (MODE == kApply) {
+      const float f = a.aux * (a.last ? a.scale : a.out);
 #pragma unroll
-      for (int h = 0; h < 8; ++h) dp[h] = D[h];
+      for (int h = 0; h < 8; ++h) kp[h] = (a.ca + M.db[me + p + h]) * f;
+    } else if (MODE == kSquare) {
+#pragma unroll
+      for (int h = 0; h < 8; ++h) kp[h] = (a.cb + a.cc * M.da[me + p + h]) * (a.aux * a.out);
     }
+    const float k_acc = MODE == kApply ? a.in * (a.last ? a.scale : a.out)
+                        : MODE == kSquare ? a.cc * (a.in * a.out)
+                                          : a.in * a.out;
 #pragma unroll
     for (int w = 0; w < U; ++w) {
       const int r = threadIdx.x / UR + NT / UR * w, q = q0 + hf * HR + r;
@@ -409,72 +455,79 @@ __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2
       for (int c = 0; c < 2; ++c) {
         const f32x4 f = *reinterpret_cast<const f32x4*>(chunk(r, 2 * u + c));
 #pragma unroll
-        for (int h = 0; h < 4; ++h) v[4 * c + h] = f[h] * a.in;
+        for (int h = 0; h < 4; ++h) v[4 * c + h] = f[h];
       }
       i32x4 s;   // the 8 finished values, 16 bits each
       if (MODE == kApply) {
         const int64_t at = ((int64_t)e * np + q) * mp + p;
-        const i32x4 xh = *reinterpret_cast<const i32x4*>(M.hi[a.cur] + at);
-        const i32x4 xl = *reinterpret_cast<const i32x4*>(M.lo[a.cur] + at);
+        const f16x8 xh = *reinterpret_cast<const f16x8*>(M.hi[a.cur] + at);
+        const f16x8 xl = *reinterpret_cast<const f16x8*>(M.lo[a.cur] + at);
 #pragma unroll
-        for (int h = 0; h < 8; ++h)
-          v[h] += (a.ca + dp[h]) * ((half_of(xh, h) + half_of(xl, h) * (1.0f / kLow)) * a.aux);
+        for (int h = 0; h < 8; ++h) v[h] = ((float)xl[h] * (1.0f / kLow) + (float)xh[h]) * kp[h] + v[h] * k_acc;
         if (a.last) {
           // X [n, m] is the output [N, K], or its transpose
 #pragma unroll
-          for (int h = 0; h < 4; ++h)
-            s[h] = (int)(f32_to_bf16_rne(v[2 * h] * a.scale) | (f32_to_bf16_rne(v[2 * h + 1] * a.scale) << 16));
+          for (int h = 0; h < 4; ++h) s[h] = (int)bf16_pack2(v[2 * h], v[2 * h + 1]);
           if (!a.wide && q < a.N) store_row(a, (int64_t)e * a.N + q, p, s);
         } else {
-          i32x4 lo;
+          f16x8 hi, lo;
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            const float w0 = v[2 * h] * a.out, w1 = v[2 * h + 1] * a.out;
-            const uint32_t h0 = f32_to_f16(w0), h1 = f32_to_f16(w1);
-            s[h] = (int)(h0 | (h1 << 16));
-            lo[h] = (int)(f32_to_f16((w0 - f16_to_f32(h0)) * kLow) | (f32_to_f16((w1 - f16_to_f32(h1)) * kLow) << 16));
+          for (int h = 0; h < 8; ++h) {
+            hi[h] = (_Float16)v[h];
+            lo[h] = (_Float16)(v[h] * kLow - (float)hi[h] * kLow);
           }
+          s = __builtin_bit_cast(i32x4, hi);
           *reinterpret_cast<i32x4*>(M.hi[a.cur ^ 1] + at) = s;
-          *reinterpret_cast<i32x4*>(M.lo[a.cur ^ 1] + at) = lo;
+          *reinterpret_cast<f16x8*>(M.lo[a.cur ^ 1] + at) = lo;
         }
       } else {
         if (MODE == kSquare) {
-          const i32x4 o = *reinterpret_cast<const i32x4*>(M.a + (me + q) * mp + p);
-          const float dq = M.da[me + q];
+          const f16x8 o = *reinterpret_cast<const f16x8*>(M.a + (me + q) * mp + p);   // 0 on the diagonal
+          const float kq = a.cc * M.da[me + q] * (a.aux * a.out);
 #pragma unroll
-          for (int h = 0; h < 8; ++h) {
-            const float off = half_of(o, h) * a.aux;   // 0 on the diagonal
-            v[h] = p + h == q ? a.cb * dq + a.cc * (v[h] + dq * dq)
-                              : a.cb * off + a.cc * (v[h] + (dp[h] + dq) * off);
-          }
+          for (int h = 0; h < 8; ++h) v[h] = (float)o[h] * (kp[h] + kq) + v[h] * k_acc;
+        } else {
+#pragma unroll
+          for (int h = 0; h < 8; ++h) v[h] *= k_acc;
         }
+        if (tp == tq) {   // the diagonal stays in float32, outside
 #pragma unroll
-        for (int h = 0; h < 8; ++h)
-          if (p + h == q) {   // the diagonal stays in float32, outside
-            (MODE == kGram ? M.da : M.db)[me + q] = v[h];
-            v[h] = 0.f;
-          }
+          for (int h = 0; h < 8; ++h)
+            if (p + h == q) {
+              const float back = 1.0f / a.out, d = MODE == kSquare ? M.da[me + q] : 0.f;
+              (MODE == kGram ? M.da : M.db)[me + q] = v[h] * back + (MODE == kSquare ? d * (a.cb + a.cc * d) : 0.f);
+              v[h] = 0.f;
+            }
+        }
+        f16x8 c;
 #pragma unroll
-        for (int h = 0; h < 4; ++h) s[h] = (int)(f32_to_f16(v[2 * h] * a.out) | (f32_to_f16(v[2 * h + 1] * a.out) << 16));
+        for (int h = 0; h < 8; ++h) c[h] = (_Float16)v[h];
+        s = __builtin_bit_cast(i32x4, c);
         *reinterpret_cast<i32x4*>((MODE == kGram ? M.a : M.b) + (me + q) * mp + p) = s;
       }
       if (turned) *reinterpret_cast<i32x4*>(chunk(r, 2 * u)) = s;
     }
     if (turned) {
       lds_barrier();
-      constexpr int OC = HR / 8;   // groups of 8 rows
+      // columns, 8 rows of one a lane: a group of 16 lanes reads 16 columns of 4
+      // rows transposed (lane L: row L / 4, columns 4 (L % 4) .. + 3; received:
+      // column L of the 4 rows), the wave 32 rows of the 16 columns
+      constexpr int UC = HR / 32 * (T / 16) / NW;   // such blocks of a wave
+      static_assert(UC * NW * 32 * 16 == HR * T, "blocks fill the waves");
+      const int L16 = lane & 15, grp = lane >> 4;
 #pragma unroll
-      for (int w = 0; w < U; ++w) {
-        const int o = threadIdx.x % OC, c = threadIdx.x / OC + NT / OC * w;   // rows 8 o .. + 7, column c
-        i32x4 s;
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const int r = 8 * o + 2 * h;
-          const uint32_t lo = reinterpret_cast<const uint16_t*>(chunk(r, c / 8 * 2))[c % 8];
-          const uint32_t hi = reinterpret_cast<const uint16_t*>(chunk(r + 1, c / 8 * 2))[c % 8];
-          s[h] = (int)(lo | (hi << 16));
-        }
-        const int row = p0 + c, col = q0 + hf * HR + 8 * o;
+      for (int w = 0; w < UC; ++w) {
+        const int b = wave + NW * w, c0 = b / (HR / 32) * 16, r0 = b % (HR / 32) * 32 + 8 * grp;
+        const int c = c0 + 4 * (L16 & 3), r = r0 + (L16 >> 2);
+        const uint32_t a0 = (uint32_t)(uintptr_t)(lds_void*)(reinterpret_cast<uint16_t*>(chunk(r, c / 8 * 2)) + c % 8);
+        const uint32_t a1 = (uint32_t)(uintptr_t)(lds_void*)(reinterpret_cast<uint16_t*>(chunk(r + 4, c / 8 * 2)) + c % 8);
+        tile::v4i16 f[2];
+        asm volatile("ds_read_b64_tr_b16 %0, %2\n\tds_read_b64_tr_b16 %1, %3\n\ts_waitcnt lgkmcnt(0)"
+                     : "=&v"(f[0]), "=&v"(f[1])
+                     : "v"(a0), "v"(a1)
+                     : "memory");
+        const i32x4 s = __builtin_bit_cast(i32x4, f);
+        const int row = p0 + c0 + L16, col = q0 + hf * HR + r0;
         if (MODE == kApply && a.last) {
           if (row < a.N) store_row(a, (int64_t)e * a.N + row, col, s);
         } else if (MODE == kApply) {
@@ -619,9 +672,9 @@ hipError_t launch_orthogonalize(const OrthoArgs& o, hipStream_t st) {
   {
     const dim3 g(kOrthoNormBlocks, (unsigned)o.E);
     if (o.bf16)
-      hipLaunchKernelGGL(ortho_norm_kernel<true>, g, dim3(256), 0, st, o.update, per, M.part);
+      hipLaunchKernelGGL(ortho_norm_kernel<true>, g, dim3(1024), 0, st, o.update, per, M.part);
     else
-      hipLaunchKernelGGL(ortho_norm_kernel<false>, g, dim3(256), 0, st, o.update, per, M.part);
+      hipLaunchKernelGGL(ortho_norm_kernel<false>, g, dim3(1024), 0, st, o.update, per, M.part);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const dim3 gi((unsigned)(o.E * (L.np / 64) * (L.mp / 64)));
     const float sc = pow2(s[0][0]);
