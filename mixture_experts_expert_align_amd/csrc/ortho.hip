@@ -414,6 +414,28 @@ __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2
   const bool turned = MODE == kApply ? !a.last || a.wide : tp != tq;
 #pragma unroll
   for (int hf = 0; hf < T / HR; ++hf) {
+    constexpr int UR = T / 8, U = HR * UR / NT;   // units of a row; of a thread
+    static_assert(U * NT == HR * UR, "units fill the threads");
+    const int u = threadIdx.x % UR, p = p0 + 8 * u;
+    auto unit_row = [&](int w) { return (int)threadIdx.x / UR + NT / UR * w; };
+    // what is read besides, all of it requested before the rows are written (a
+    // load behind another unit's stores would wait for each in turn)
+    f16x8 x1[U], x2[MODE == kApply ? U : 1];
+    float xq[MODE == kSquare ? U : 1];
+    if (MODE != kGram) {
+#pragma unroll
+      for (int w = 0; w < U; ++w) {
+        const int q = q0 + hf * HR + unit_row(w);
+        if constexpr (MODE == kApply) {
+          const int64_t at = ((int64_t)e * np + q) * mp + p;
+          x1[w] = *reinterpret_cast<const f16x8*>(M.hi[a.cur] + at);
+          x2[w] = *reinterpret_cast<const f16x8*>(M.lo[a.cur] + at);
+        } else {
+          x1[w] = *reinterpret_cast<const f16x8*>(M.a + (me + q) * mp + p);   // 0 on the diagonal
+          xq[w] = M.da[me + q];
+        }
+      }
+    }
     lds_barrier();
     // acc[i][j][4 g + h]: p = 32 (wi TI + i) + 8 g + 4 (lane / 32) + h,
     // q = 32 (wj TJ + j) + lane % 32
@@ -429,9 +451,6 @@ __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2
               (f32x4){acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
     }
     lds_barrier();
-    constexpr int UR = T / 8, U = HR * UR / NT;   // units of a row; of a thread
-    static_assert(U * NT == HR * UR, "units fill the threads");
-    const int u = threadIdx.x % UR, p = p0 + 8 * u;
     // (powers of two go into the columns' factors: a value costs a few fused
     // operations that take float16 operands as they are; written out, with each
     // step by itself, the arithmetic took 20000 cycles a tile of 256)
@@ -449,7 +468,7 @@ __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2
                                           : a.in * a.out;
 #pragma unroll
     for (int w = 0; w < U; ++w) {
-      const int r = threadIdx.x / UR + NT / UR * w, q = q0 + hf * HR + r;
+      const int r = unit_row(w), q = q0 + hf * HR + r;
       float v[8];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -460,10 +479,8 @@ __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2
       i32x4 s;   // the 8 finished values, 16 bits each
       if (MODE == kApply) {
         const int64_t at = ((int64_t)e * np + q) * mp + p;
-        const f16x8 xh = *reinterpret_cast<const f16x8*>(M.hi[a.cur] + at);
-        const f16x8 xl = *reinterpret_cast<const f16x8*>(M.lo[a.cur] + at);
 #pragma unroll
-        for (int h = 0; h < 8; ++h) v[h] = ((float)xl[h] * (1.0f / kLow) + (float)xh[h]) * kp[h] + v[h] * k_acc;
+        for (int h = 0; h < 8; ++h) v[h] = ((float)x2[w][h] * (1.0f / kLow) + (float)x1[w][h]) * kp[h] + v[h] * k_acc;
         if (a.last) {
           // X [n, m] is the output [N, K], or its transpose
 #pragma unroll
@@ -482,10 +499,9 @@ __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2
         }
       } else {
         if (MODE == kSquare) {
-          const f16x8 o = *reinterpret_cast<const f16x8*>(M.a + (me + q) * mp + p);   // 0 on the diagonal
-          const float kq = a.cc * M.da[me + q] * (a.aux * a.out);
+          const float kq = a.cc * xq[w] * (a.aux * a.out);
 #pragma unroll
-          for (int h = 0; h < 8; ++h) v[h] = (float)o[h] * (kp[h] + kq) + v[h] * k_acc;
+          for (int h = 0; h < 8; ++h) v[h] = (float)x1[w][h] * (kp[h] + kq) + v[h] * k_acc;
         } else {
 #pragma unroll
           for (int h = 0; h < 8; ++h) v[h] *= k_acc;
@@ -494,7 +510,7 @@ __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2
 #pragma unroll
           for (int h = 0; h < 8; ++h)
             if (p + h == q) {
-              const float back = 1.0f / a.out, d = MODE == kSquare ? M.da[me + q] : 0.f;
+              const float back = 1.0f / a.out, d = MODE == kSquare ? xq[MODE == kSquare ? w : 0] : 0.f;
               (MODE == kGram ? M.da : M.db)[me + q] = v[h] * back + (MODE == kSquare ? d * (a.cb + a.cc * d) : 0.f);
               v[h] = 0.f;
             }
