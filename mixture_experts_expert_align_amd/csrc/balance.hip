@@ -28,18 +28,18 @@ constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr float kLog2e = 1.44269504088896341f;
 
 // Maximum and sums over the token's LANES lanes, the same bits in each: every
-// step adds two values that the two lanes hold in either order.
-template <int CTRL>
-__device__ __forceinline__ float dpp_f32(float v) {
-  return __uint_as_float(dpp_u32<CTRL, 0xf>(__float_as_uint(v)));
+// step combines two values that the two lanes hold in either order.
+template <int CTRL, class T>
+__device__ __forceinline__ T dpp_of(T v) {
+  return __builtin_bit_cast(T, dpp_u32<CTRL, 0xf>(__builtin_bit_cast(uint32_t, v)));
 }
-template <int LANES, class F>
-__device__ __forceinline__ float lanes_all(float v, F f) {
+template <int LANES, class T, class F>
+__device__ __forceinline__ T lanes_all(T v, F f) {
   static_assert(LANES == 16 || LANES == 64, "a row of 16 lanes, or the wave");
-  v = f(v, dpp_f32<0x128>(v));   // rotations within the row by 8, 4, 2, 1
-  v = f(v, dpp_f32<0x124>(v));
-  v = f(v, dpp_f32<0x122>(v));
-  v = f(v, dpp_f32<0x121>(v));
+  v = f(v, dpp_of<0x128>(v));   // rotations within the row by 8, 4, 2, 1
+  v = f(v, dpp_of<0x124>(v));
+  v = f(v, dpp_of<0x122>(v));
+  v = f(v, dpp_of<0x121>(v));
   if (LANES == 64) {
     v = f(v, __shfl_xor(v, 16));
     v = f(v, __shfl_xor(v, 32));
@@ -51,67 +51,117 @@ __device__ __forceinline__ float lanes_max(float v) {
   return lanes_all<LANES>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 template <int LANES>
+__device__ __forceinline__ int lanes_max(int v) {
+  return lanes_all<LANES>(v, [](int a, int b) { return max(a, b); });
+}
+template <int LANES>
 __device__ __forceinline__ float lanes_sum(float v) {
   return lanes_all<LANES>(v, [](float a, float b) { return a + b; });
 }
 
-// Logits of a token: expert c + LANES i in l[i]; -inf for one that cannot be chosen.
-template <int LANES, int NV, bool BF16>
-__device__ __forceinline__ void token_logits(const BalanceArgs& a, int64_t t, int c, float (&l)[NV]) {
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = c + LANES * i;
-    float v = -INFINITY;
-    if (e < a.E) {
-      v = BF16 ? bf16_to_f32(static_cast<const uint16_t*>(a.logits)[t * a.ld + e])
-               : static_cast<const float*>(a.logits)[t * a.ld + e];
-      if (a.add_bias) v += a.bias[e];
-    }
-    l[i] = v > -INFINITY ? fmaxf(fminf(v, FLT_MAX), -FLT_MAX) : -INFINITY;
-  }
-}
+// A token's E values over LANES lanes: lane c holds VEC consecutive experts
+// from VEC (c + LANES i) on, NV values in all, loaded VEC at a time.
+template <int LANES_, int NV_, int VEC_, bool BF16_>
+struct Shape {
+  static constexpr int LANES = LANES_, NV = NV_, VEC = VEC_, NI = NV / VEC;
+  static constexpr bool BF16 = BF16_;
+  static constexpr int EL = BF16 ? 2 : 4, W = VEC * EL >= 4 ? VEC * EL / 4 : 1;   // words of a load
+  static_assert(NI * VEC == NV, "whole loads");
+  static __device__ __forceinline__ int expert(int c, int i) { return VEC * (c + LANES * i); }
+};
 
-// Scores: p[i] of l[i], 0 where it is -inf; returns the largest logit.  The
-// sigmoids are taken times e^-min(top, 0), which their quotient does not see
-// and which keeps them from all underflowing.
-template <int LANES, int NV>
-__device__ __forceinline__ float token_scores(bool sigmoid, const float (&l)[NV], float (&p)[NV]) {
-  float top = l[0];
+template <class S>
+struct Raw {
+  uint32_t w[S::NI][S::W];
+  __device__ __forceinline__ void clear() {   // -inf: what lies past E
 #pragma unroll
-  for (int i = 1; i < NV; ++i) top = fmaxf(top, l[i]);
-  top = lanes_max<LANES>(top);
-  const float shift = sigmoid ? fminf(top, 0.f) : top;
+    for (int i = 0; i < S::NI; ++i)
+#pragma unroll
+      for (int k = 0; k < S::W; ++k) w[i][k] = S::BF16 ? 0xff80ff80u : 0xff800000u;
+  }
+  __device__ __forceinline__ void load(const void* row, int E, int c) {
+    const char* p = static_cast<const char*>(row);
+#pragma unroll
+    for (int i = 0; i < S::NI; ++i) {
+      const int e = S::expert(c, i);
+      if (e < E) {
+        if constexpr (S::VEC * S::EL == 2) w[i][0] = *reinterpret_cast<const uint16_t*>(p + 2 * e);
+        else __builtin_memcpy(w[i], __builtin_assume_aligned(p + (int64_t)S::EL * e, 4 * S::W), 4 * S::W);
+      }
+    }
+  }
+  // value k of load i
+  __device__ __forceinline__ float get(int i, int k) const {
+    if constexpr (!S::BF16) return __uint_as_float(w[i][k]);
+    return __uint_as_float(k & 1 ? w[i][k / 2] & 0xffff0000u : w[i][k / 2] << 16);
+  }
+};
+
+// The token's logits (plus a bias, LDS), its scores before their division by the
+// returned sum, and the largest logit.  Nothing is done about special values
+// until they show: with a NaN, a +inf or no expert at all the sum is not a
+// positive number, and a sigmoid's whole row may underflow where none is
+// positive; then, and only then, the row is taken again with the logits that
+// compete (-inf for one that cannot be chosen, +inf as the largest float32) and
+// sigmoids times e^-min(top, 0), which their quotient does not see.
+template <class S>
+__device__ __forceinline__ float token_scores(const Raw<S>& r, int c, bool add, const float* bias, bool sigmoid,
+                                              float (&l)[S::NV], float (&p)[S::NV], float& top) {
+  top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < S::NI; ++i)
+#pragma unroll
+    for (int k = 0; k < S::VEC; ++k) l[S::VEC * i + k] = r.get(i, k);
+  if (add) {
+#pragma unroll
+    for (int i = 0; i < S::NI; ++i)
+#pragma unroll
+      for (int k = 0; k < S::VEC; ++k) l[S::VEC * i + k] += bias[S::expert(c, i) + k];
+  }
+#pragma unroll
+  for (int i = 0; i < S::NV; ++i) top = fmaxf(top, l[i]);
+  top = lanes_max<S::LANES>(top);
   float s = 0.f;
+  if (!sigmoid) {
+    // one fused operation: the rounding of top log2(e) is common to the row, and
+    // the quotient does not see it
+    const float m = -top * kLog2e;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    float v = 0.f;
-    if (l[i] > -INFINITY) {
-      if (!sigmoid)
-        v = __builtin_amdgcn_exp2f((l[i] - shift) * kLog2e);
-      else if (l[i] > 0.f)
-        v = 1.0f / (1.0f + __builtin_amdgcn_exp2f(-l[i] * kLog2e));
-      else
-        v = __builtin_amdgcn_exp2f((l[i] - shift) * kLog2e) / (1.0f + __builtin_amdgcn_exp2f(l[i] * kLog2e));
+    for (int i = 0; i < S::NV; ++i) {
+      p[i] = __builtin_amdgcn_exp2f(fmaf(l[i], kLog2e, m));
+      s += p[i];
     }
-    p[i] = v;
-    s += v;
-  }
-  s = lanes_sum<LANES>(s);
-  const float inv = s > 0.f ? 1.0f / s : 0.f;
+  } else {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) p[i] *= inv;
-  return top;
-}
-
-// Whether one of the token's ids names an expert; the same in all its lanes.
-template <int LANES>
-__device__ __forceinline__ bool token_counts(const BalanceArgs& a, int64_t t, int c) {
-  float any = 0.f;
-  for (int j = c; j < a.topk; j += LANES) {
-    const int id = a.ids[t * a.topk + j];
-    if (id >= 0 && id < a.E) any = 1.f;
+    for (int i = 0; i < S::NV; ++i) {
+      // 1 / (1 + e^-l), or e^l / (1 + e^l) below 0: no overflow in either
+      const float e = __builtin_amdgcn_exp2f(-fabsf(l[i]) * kLog2e);
+      p[i] = (l[i] > 0.f ? 1.0f : e) * __builtin_amdgcn_rcpf(1.0f + e);
+      s += p[i];
+    }
   }
-  return lanes_max<LANES>(any) > 0.f;
+  s = lanes_sum<S::LANES>(s);
+  // (decided by the token, not by its wave: its bits are its own)
+  if (s > 0.f && s < INFINITY && fabsf(top) < 1e30f && (!sigmoid || top > 0.f)) return s;
+  top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < S::NV; ++i) {
+    l[i] = l[i] > -INFINITY ? fmaxf(fminf(l[i], FLT_MAX), -FLT_MAX) : -INFINITY;
+    top = fmaxf(top, l[i]);
+  }
+  top = lanes_max<S::LANES>(top);
+  const float shift = top == -INFINITY ? 0.f : sigmoid ? fminf(top, 0.f) : top;
+  s = 0.f;
+#pragma unroll
+  for (int i = 0; i < S::NV; ++i) {
+    p[i] = __builtin_amdgcn_exp2f((l[i] - shift) * kLog2e);   // (0 for -inf)
+    if (sigmoid) {
+      const float d = 1.0f + __builtin_amdgcn_exp2f(-fabsf(l[i]) * kLog2e);
+      p[i] = (l[i] > 0.f ? 1.0f : p[i]) * __builtin_amdgcn_rcpf(d);
+    }
+    s += p[i];
+  }
+  return lanes_sum<S::LANES>(s);
 }
 
 // Offset i of the sequences, within [0, M] whatever the array holds.
@@ -121,27 +171,39 @@ __device__ __forceinline__ int64_t seq_offset(const BalanceArgs& a, int i) {
 }
 
 // The last sequence that starts at or before token t, or -1: the one t is in,
-// if it is in any.
+// if it is in any.  64 of the sequences are looked at together; t is the same
+// in all lanes, which are all here.
 __device__ __forceinline__ int seq_of(const BalanceArgs& a, int64_t t) {
-  int lo = -1, hi = a.S - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (seq_offset(a, mid) <= t) lo = mid; else hi = mid - 1;
+  int lo = -1, n = a.S;                          // it is lo or one of the n behind it
+  while (n > 0) {
+    const int step = (n + 63) / 64, i = step * (int)__lane_id();
+    const int c = __popcll(__ballot(i < n && seq_offset(a, min(lo + 1 + i, a.S)) <= t));
+    if (c == 0) break;
+    lo += 1 + step * (c - 1);
+    n = min(step - 1, n - 1 - step * (c - 1));
   }
   return lo;
 }
 
-template <int LANES, int NV, bool BF16>
+template <class S>
+__device__ __forceinline__ const void* token_row(const BalanceArgs& a, int64_t t) {
+  return static_cast<const char*>(a.logits) + t * a.ld * S::EL;
+}
+
+template <class S>
 __global__ void __launch_bounds__(kThreads) balance_tokens_kernel(BalanceArgs a) {
+  constexpr int LANES = S::LANES, NE = LANES * S::NV;
   constexpr int TOK = kThreads / LANES;          // tokens at a time
-  __shared__ float s_p[kWaves][LANES * NV];
-  __shared__ int s_c[LANES * NV];
+  __shared__ float s_p[kWaves][NE];
+  __shared__ float s_b[NE];
+  __shared__ int s_c[NE];
   __shared__ int s_t;
   const int tid = threadIdx.x, c = tid % LANES, wave = tid >> 6;
   const int64_t first = (int64_t)blockIdx.x * a.chunk;
   const int64_t last = min(first + a.chunk, a.M);
   if (blockIdx.x == 0)
     for (int s = tid; s < a.S; s += kThreads) a.done[s] = 0;
+  for (int e = tid; e < NE; e += kThreads) s_b[e] = a.add_bias && e < a.E ? a.bias[e] : 0.f;
   for (int64_t at = first; at < last;) {
     const int s = seq_of(a, at);
     if (s < 0) {                                 // before the first sequence
@@ -150,42 +212,57 @@ __global__ void __launch_bounds__(kThreads) balance_tokens_kernel(BalanceArgs a)
     }
     const int64_t end = min(seq_offset(a, s + 1), last);
     if (end <= at) break;                        // behind the last sequence
-    for (int e = tid; e < LANES * NV; e += kThreads) s_c[e] = 0;
+    Raw<S> raw;
+    raw.clear();
+    int id = -1;
+    // past the last token: that one again, not counted
+    auto load = [&](int64_t t0) {
+      const int64_t in = min(t0 + tid / LANES, end - 1);
+      raw.load(token_row<S>(a, in), a.E, c);
+      if (c < a.topk) id = a.ids[in * a.topk + c];
+    };
+    load(at);
+    for (int e = tid; e < NE; e += kThreads) s_c[e] = 0;
     if (tid == 0) s_t = 0;
     __syncthreads();
-    float acc[NV];
+    float acc[S::NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) acc[i] = 0.f;
+    for (int i = 0; i < S::NV; ++i) acc[i] = 0.f;
     int n = 0;
     for (int64_t t0 = at; t0 < end; t0 += TOK) {
       const int64_t t = t0 + tid / LANES;
-      const int64_t in = min(t, end - 1);        // past the last token: that one again, not counted
-      float l[NV], p[NV];
-      token_logits<LANES, NV, BF16>(a, in, c, l);
-      token_scores<LANES, NV>(a.sigmoid, l, p);
-      bool any = false;
-      for (int j = c; j < a.topk; j += LANES) {
-        const int id = a.ids[in * a.topk + j];
-        if (id >= 0 && id < a.E) {
+      float l[S::NV], p[S::NV], top;
+      bool any = id >= 0 && id < a.E;
+      if (any && t < end) atomicAdd(&s_c[id], 1);
+      for (int j = c + LANES; j < a.topk; j += LANES) {
+        const int64_t in = min(t, end - 1);
+        const int more = a.ids[in * a.topk + j];
+        if (more >= 0 && more < a.E) {
           any = true;
-          if (t < end) atomicAdd(&s_c[id], 1);
+          if (t < end) atomicAdd(&s_c[more], 1);
         }
       }
-      const bool on = t < end && lanes_max<LANES>(any ? 1.f : 0.f) > 0.f;
+      const Raw<S> now = raw;
+      if (t0 + TOK < end) load(t0 + TOK);
+      const float sum = token_scores<S>(now, c, a.add_bias, s_b, a.sigmoid, l, p, top);
+      const bool on = lanes_max<LANES>(t < end && any ? 1 : 0) != 0;
       n += on;
+      const float f = on && sum > 0.f ? 1.0f / sum : 0.f;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) acc[i] += on ? p[i] : 0.f;
+      for (int i = 0; i < S::NV; ++i) acc[i] += p[i] * f;
     }
     if (LANES == 16) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
+      for (int i = 0; i < S::NV; ++i) {
         acc[i] += __shfl_xor(acc[i], 16);
         acc[i] += __shfl_xor(acc[i], 32);
       }
     }
     if ((tid & 63) < LANES) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) s_p[wave][c + LANES * i] = acc[i];
+      for (int i = 0; i < S::NI; ++i)
+#pragma unroll
+        for (int k = 0; k < S::VEC; ++k) s_p[wave][S::expert(c, i) + k] = acc[S::VEC * i + k];
     }
     if (c == 0) atomicAdd(&s_t, n);
     __syncthreads();
@@ -194,8 +271,7 @@ __global__ void __launch_bounds__(kThreads) balance_tokens_kernel(BalanceArgs a)
       float v = 0.f;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) v += s_p[w][e];
-      a.psum[slot * a.E + e] = v;
-      a.csum[slot * a.E + e] = s_c[e];
+      a.part[slot * a.E + e] = make_int2((int)__float_as_uint(v), s_c[e]);
     }
     if (tid == 0) a.tsum[slot] = s_t;
     __syncthreads();
@@ -203,182 +279,265 @@ __global__ void __launch_bounds__(kThreads) balance_tokens_kernel(BalanceArgs a)
   }
 }
 
-// Workgroup (sequence, block of its experts): the waves share the sequence's slots.
-constexpr int kSumWaves = 16;
-
+// Workgroup (sequence, block of its experts): 16 experts a row of lanes, the
+// rows of all waves sharing the sequence's slots.
+template <int kSumWaves>
 __global__ void __launch_bounds__(64 * kSumWaves) balance_sums_kernel(BalanceArgs a) {
-  __shared__ double s_p[kSumWaves][kBalanceExperts];
-  __shared__ int s_c[kSumWaves][kBalanceExperts];
+  constexpr int kSumRows = 4 * kSumWaves;
+  static_assert(kBalanceExperts == 16, "a row of lanes");
+  __shared__ double s_p[kSumRows][kBalanceExperts];
+  __shared__ int s_c[kSumRows][kBalanceExperts];
   __shared__ int s_t[kSumWaves];
   const int nb = (a.E + kBalanceExperts - 1) / kBalanceExperts;
   const int s = blockIdx.x / nb, b = blockIdx.x % nb;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int e = b * kBalanceExperts + lane;
+  const int col = threadIdx.x % kBalanceExperts, row = threadIdx.x / kBalanceExperts;
+  const int e = b * kBalanceExperts + col;
   const int64_t lo = seq_offset(a, s), hi = seq_offset(a, s + 1);
   double p = 0.0;
   int c = 0, t = 0;
   if (lo < hi) {
-    const int64_t i1 = (hi - 1) / a.chunk;
-    for (int64_t i = lo / a.chunk + wave; i <= i1; i += kSumWaves) {
-      const int64_t slot = i + s;
-      if (e < a.E) {
-        p += (double)a.psum[slot * a.E + e];
-        c += a.csum[slot * a.E + e];
+    const int64_t i0 = lo / a.chunk, i1 = (hi - 1) / a.chunk;
+    if (e < a.E) {
+#pragma unroll 8
+      for (int64_t i = i0 + row; i <= i1; i += kSumRows) {
+        const int2 v = a.part[(i + s) * a.E + e];
+        p += (double)__uint_as_float((uint32_t)v.x);
+        c += v.y;
       }
-      t += a.tsum[slot];
     }
+    for (int64_t i = i0 + threadIdx.x; i <= i1; i += 64 * kSumWaves) t += a.tsum[i + s];
   }
-  s_p[wave][lane] = p;
-  s_c[wave][lane] = c;
-  if (lane == 0) s_t[wave] = t;
+  for (int d = 32; d; d >>= 1) t += __shfl_xor(t, d);
+  s_p[row][col] = p;
+  s_c[row][col] = c;
+  if ((threadIdx.x & 63) == 0) s_t[threadIdx.x >> 6] = t;
   __syncthreads();
-  if (wave != 0) return;
+  if (threadIdx.x >= 64) return;
+  // lane (row, col): a quarter of the rows, then their sum
   p = 0.0, c = 0, t = 0;
-  for (int w = 0; w < kSumWaves; ++w) {
-    p += s_p[w][lane];
-    c += s_c[w][lane];
-    t += s_t[w];
+#pragma unroll
+  for (int w = 0; w < kSumRows / 4; ++w) {
+    p += s_p[w * 4 + row][col];
+    c += s_c[w * 4 + row][col];
   }
+#pragma unroll
+  for (int d = 16; d < 64; d *= 2) {
+    p += __shfl_xor(p, d);
+    c += __shfl_xor(c, d);
+  }
+#pragma unroll
+  for (int w = 0; w < kSumWaves; ++w) t += s_t[w];
   const double mean = t > 0 ? p / t : 0.0;
-  if (e < a.E) {
+  const bool mine = row == 0 && e < a.E;
+  if (mine) {
     a.counts[(int64_t)s * a.E + e] = c;
     a.probs[(int64_t)s * a.E + e] = (float)mean;
   }
-  if (b == 0 && lane == 0) a.tokens[s] = t;
-  const double part = wave_sum_f64(e < a.E ? mean * c : 0.0);
+  if (b == 0 && threadIdx.x == 0) a.tokens[s] = t;
+  const double part = wave_sum_f64(mine ? mean * c : 0.0);
   const double scale = t > 0 ? (double)a.E / ((double)a.topk * t) : 0.0;
   if (nb == 1) {
-    if (lane == 0) a.loss[s] = (float)(part * scale);
+    if (threadIdx.x == 0) a.loss[s] = (float)(part * scale);
     return;
   }
-  // the last of the sequence's workgroups adds their parts, in their order
-  if (lane == 0) {
-    __hip_atomic_store(a.lpart + (int64_t)s * nb + b, part, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (__hip_atomic_fetch_add(a.done + s, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == nb - 1) {
-      double sum = 0.0;
-      for (int i = 0; i < nb; ++i)
-        sum += __hip_atomic_load(a.lpart + (int64_t)s * nb + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      a.loss[s] = (float)(sum * scale);
-    }
+  // the last of the sequence's workgroups adds their parts, in a fixed order; each
+  // part is where all can read it before its workgroup is counted
+  int done = 0;
+  double* parts = a.lpart + (int64_t)s * nb;
+  if (threadIdx.x == 0) {
+    __hip_atomic_store(parts + b, part, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    wait_vm<0>();
+    done = __hip_atomic_fetch_add(a.done + s, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
+  if (__builtin_amdgcn_readfirstlane(done) != nb - 1) return;
+  double sum = 0.0;
+  for (int i = threadIdx.x; i < nb; i += 64)
+    sum += __hip_atomic_load(parts + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  sum = wave_sum_f64(sum);
+  if (threadIdx.x == 0) a.loss[s] = (float)(sum * scale);
 }
 
-template <int LANES, int NV, bool BF16>
+template <class S>
 __global__ void __launch_bounds__(kThreads) balance_backward_kernel(BalanceArgs a) {
-  constexpr int TOK = kThreads / LANES;
+  constexpr int LANES = S::LANES, TOK = kThreads / LANES, NE = LANES * S::NV;
+  __shared__ float s_b[NE];
   const int c = threadIdx.x % LANES;
-  const int64_t t = a.t0 + (int64_t)blockIdx.x * TOK + threadIdx.x / LANES;
+  const int64_t first = a.t0 + (int64_t)blockIdx.x * TOK;
+  const int64_t t = first + threadIdx.x / LANES;
   const int64_t in = min(t, a.M - 1);            // past the last token: that one again, not stored
-  const int s = seq_of(a, in);
-  const bool on = token_counts<LANES>(a, in, c) && s >= 0 && in < seq_offset(a, s + 1);
-  if (a.accumulate && !on) return;               // (no barrier below)
-  float d[NV];
-  if (on) {
-    float l[NV], p[NV];
-    token_logits<LANES, NV, BF16>(a, in, c, l);
-    const float top = token_scores<LANES, NV>(a.sigmoid, l, p);
-    const int32_t* cnt = a.counts_in + (int64_t)s * a.E;
-    int ci[NV];
-    float best = -1.f;                           // the position of the best expert
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = c + LANES * i;
-      ci[i] = e < a.E ? cnt[e] : 0;
-      if (l[i] == top) best = (float)e;
+  Raw<S> raw;
+  raw.clear();
+  raw.load(token_row<S>(a, in), a.E, c);
+  bool any = false;
+  for (int j = c; j < a.topk; j += LANES) {
+    const int id = a.ids[in * a.topk + j];
+    any |= id >= 0 && id < a.E;
+  }
+  if (a.add_bias) {
+    for (int e = threadIdx.x; e < NE; e += kThreads) s_b[e] = e < a.E ? a.bias[e] : 0.f;
+    __syncthreads();
+  }
+  // the first token's sequence, or one of the next few, or that of a search by itself
+  int s = seq_of(a, min(first, a.M - 1));
+  if (LANES < 64 && a.S > 1) {
+    int k = 0;
+    while (k < 4 && s + 1 < a.S && seq_offset(a, s + 1) <= in) ++s, ++k;
+    if (k == 4) {
+      int lo = s, hi = a.S - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (seq_offset(a, mid) <= in) lo = mid; else hi = mid - 1;
+      }
+      s = lo;
     }
-    best = lanes_max<LANES>(best);
-    const int ref = best >= 0.f && best < (float)a.E ? cnt[(int)best] : 0;
+  } else if (a.S > 1) {
+    s = seq_of(a, in);
+  }
+  const bool on = lanes_max<LANES>(any ? 1 : 0) != 0 && s >= 0 && in < seq_offset(a, s + 1);
+  if (t >= a.M || (a.accumulate && !on)) return;   // whole tokens; no barrier below
+  float d[S::NV];
+  if (on) {
+    const int32_t* cnt = a.counts_in + (int64_t)s * a.E;
+    int ci[S::NV];
+#pragma unroll
+    for (int i = 0; i < S::NI; ++i) {
+      constexpr int B = S::VEC >= 4 ? 16 : 4;   // by_alignment has seen to it
+#pragma unroll
+      for (int k = 0; k < S::VEC; ++k) ci[S::VEC * i + k] = 0;
+      if (S::expert(c, i) < a.E)
+        __builtin_memcpy(ci + S::VEC * i, __builtin_assume_aligned(cnt + S::expert(c, i), B), 4 * S::VEC);
+    }
+    const double T = a.tokens_in[s];
+    const float k = T > 0 ? (float)((double)a.dloss[s] * a.E / ((double)a.topk * T * T)) : 0.f;
+    float l[S::NV], p[S::NV], top;
+    const float sum = token_scores<S>(raw, c, a.add_bias, s_b, a.sigmoid, l, p, top);
+    const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+    int ref = -1;                                // the best expert's count (of several, the largest)
+#pragma unroll
+    for (int i = 0; i < S::NV; ++i) ref = max(ref, l[i] == top ? ci[i] : -1);
+    ref = lanes_max<LANES>(ref);
     float dot = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
+    for (int i = 0; i < S::NV; ++i) {
+      p[i] *= inv;
       d[i] = (float)(ci[i] - ref);
       dot += p[i] * d[i];
     }
     dot = lanes_sum<LANES>(dot);
-    const double T = a.tokens_in[s];
-    const float k = T > 0 ? (float)((double)a.dloss[s] * a.E / ((double)a.topk * T * T)) : 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      d[i] = l[i] > -INFINITY ? k * (p[i] * (d[i] - dot)) : 0.f;
-      if (a.sigmoid && l[i] > -INFINITY) d[i] /= 1.0f + __builtin_amdgcn_exp2f(l[i] * kLog2e);
+    for (int i = 0; i < S::NV; ++i) {
+      d[i] = k * (p[i] * (d[i] - dot));   // p is 0 where l is -inf
+      if (a.sigmoid) d[i] *= __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(l[i] * kLog2e));
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) d[i] = 0.f;
+    for (int i = 0; i < S::NV; ++i) d[i] = 0.f;
   }
-  if (t >= a.M) return;
+  char* out = static_cast<char*>(a.dlogits) + t * a.dld * S::EL;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = c + LANES * i;
+  for (int i = 0; i < S::NI; ++i) {
+    const int e = S::expert(c, i);
     if (e >= a.E) continue;
-    if (BF16) {
-      uint16_t* o = static_cast<uint16_t*>(a.dlogits) + t * a.dld + e;
-      *o = (uint16_t)f32_to_bf16_rne(a.accumulate ? bf16_to_f32(*o) + d[i] : d[i]);
-    } else {
-      float* o = static_cast<float*>(a.dlogits) + t * a.dld + e;
-      *o = a.accumulate ? *o + d[i] : d[i];
+    char* o = out + (int64_t)S::EL * e;
+    uint32_t w[S::W];
+    if (a.accumulate) {
+      if constexpr (S::VEC * S::EL == 2) w[0] = *reinterpret_cast<uint16_t*>(o);
+      else __builtin_memcpy(w, __builtin_assume_aligned(o, 4 * S::W), 4 * S::W);
+#pragma unroll
+      for (int k = 0; k < S::VEC; ++k) {
+        const uint32_t u = S::BF16 ? (k & 1 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16) : w[k];
+        d[S::VEC * i + k] += __uint_as_float(u);
+      }
     }
+    if constexpr (!S::BF16) {
+#pragma unroll
+      for (int k = 0; k < S::VEC; ++k) w[k] = __float_as_uint(d[S::VEC * i + k]);
+    } else if constexpr (S::VEC == 1) {
+      w[0] = bf16_pack2(d[i], 0.f);
+    } else {
+#pragma unroll
+      for (int k = 0; k < S::VEC / 2; ++k) w[k] = bf16_pack2(d[S::VEC * i + 2 * k], d[S::VEC * i + 2 * k + 1]);
+    }
+    if constexpr (S::VEC * S::EL == 2) *reinterpret_cast<uint16_t*>(o) = (uint16_t)w[0];
+    else __builtin_memcpy(__builtin_assume_aligned(o, 4 * S::W), w, 4 * S::W);
   }
 }
 
-template <int LANES, int NV>
-hipError_t launch_tokens(const BalanceArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)(a.nchunk > 0 ? a.nchunk : 1)), block(kThreads);
-  if (a.bf16)
-    hipLaunchKernelGGL((balance_tokens_kernel<LANES, NV, true>), grid, block, 0, s, a);
-  else
-    hipLaunchKernelGGL((balance_tokens_kernel<LANES, NV, false>), grid, block, 0, s, a);
-  return hipGetLastError();
-}
+struct Forward {
+  template <class S>
+  static hipError_t go(const BalanceArgs& a, hipStream_t s) {
+    hipLaunchKernelGGL(balance_tokens_kernel<S>, dim3((unsigned)(a.nchunk > 0 ? a.nchunk : 1)), dim3(kThreads), 0, s,
+                       a);
+    return hipGetLastError();
+  }
+};
 
 // Tokens of a launch: it takes fewer than 2^32 threads, up to 64 to a token.
 constexpr int64_t kLaunchTokens = 1 << 25;
 
-template <int LANES, int NV>
-hipError_t launch_backward(BalanceArgs a, hipStream_t s) {
-  constexpr int TOK = kThreads / LANES;
-  hipError_t e = hipSuccess;
-  for (a.t0 = 0; a.t0 < a.M && e == hipSuccess; a.t0 += kLaunchTokens) {
-    const int64_t n = a.M - a.t0 < kLaunchTokens ? a.M - a.t0 : kLaunchTokens;
-    const dim3 grid((unsigned)((n + TOK - 1) / TOK)), block(kThreads);
-    if (a.bf16)
-      hipLaunchKernelGGL((balance_backward_kernel<LANES, NV, true>), grid, block, 0, s, a);
-    else
-      hipLaunchKernelGGL((balance_backward_kernel<LANES, NV, false>), grid, block, 0, s, a);
-    e = hipGetLastError();
+struct Backward {
+  template <class S>
+  static hipError_t go(BalanceArgs a, hipStream_t s) {
+    constexpr int TOK = kThreads / S::LANES;
+    hipError_t e = hipSuccess;
+    for (a.t0 = 0; a.t0 < a.M && e == hipSuccess; a.t0 += kLaunchTokens) {
+      const int64_t n = a.M - a.t0 < kLaunchTokens ? a.M - a.t0 : kLaunchTokens;
+      hipLaunchKernelGGL(balance_backward_kernel<S>, dim3((unsigned)((n + TOK - 1) / TOK)), dim3(kThreads), 0, s, a);
+      e = hipGetLastError();
+    }
+    return e;
   }
-  return e;
+};
+
+// VEC values of EL bytes a load where every row allows it.
+template <class L, int LANES, int NV, int VEC, bool BF16>
+hipError_t by_alignment(const BalanceArgs& a, hipStream_t s) {
+  if constexpr (VEC > 1) {
+    constexpr uintptr_t B = VEC * (BF16 ? 2 : 4);
+    const bool ok = a.E % VEC == 0 && a.ld % VEC == 0 && a.dld % VEC == 0 && (uintptr_t)a.logits % B == 0 &&
+                    (uintptr_t)a.dlogits % B == 0 && (VEC < 4 || (uintptr_t)a.counts_in % 16 == 0);
+    if (ok) return L::template go<Shape<LANES, NV, VEC, BF16>>(a, s);
+  }
+  return L::template go<Shape<LANES, NV, 1, BF16>>(a, s);
+}
+
+template <class L, int LANES, int NV>
+hipError_t by_type(const BalanceArgs& a, hipStream_t s) {
+  return a.bf16 ? by_alignment<L, LANES, NV, (NV < 8 ? NV : 8), true>(a, s)
+                : by_alignment<L, LANES, NV, (NV < 4 ? NV : 4), false>(a, s);
+}
+
+// 16 lanes a token for up to 512 experts, a wave for more.
+template <class L>
+hipError_t by_experts(const BalanceArgs& a, hipStream_t s) {
+  if (a.E <= 16) return by_type<L, 16, 1>(a, s);
+  if (a.E <= 64) return by_type<L, 16, 4>(a, s);
+  if (a.E <= 128) return by_type<L, 16, 8>(a, s);
+  if (a.E <= 256) return by_type<L, 16, 16>(a, s);
+  if (a.E <= 512) return by_type<L, 16, 32>(a, s);
+  return by_type<L, 64, 32>(a, s);
 }
 
 }  // namespace
 
-// Tokens of a workgroup of the first launch: at most 512 workgroups.
+// Tokens of a workgroup of the first launch: at most 1024 workgroups.
 int32_t balance_chunk(int64_t M) {
-  const int64_t c = ((M + 511) / 512 + 15) / 16 * 16;
+  const int64_t c = ((M + 1023) / 1024 + 15) / 16 * 16;
   return (int32_t)(c < 32 ? 32 : c);
 }
 
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
-  hipError_t e;
-  if (a.E <= 16) e = launch_tokens<16, 1>(a, s);
-  else if (a.E <= 64) e = launch_tokens<16, 4>(a, s);
-  else if (a.E <= 128) e = launch_tokens<16, 8>(a, s);
-  else if (a.E <= 256) e = launch_tokens<64, 4>(a, s);
-  else if (a.E <= 512) e = launch_tokens<64, 8>(a, s);
-  else e = launch_tokens<64, 32>(a, s);
+  const hipError_t e = by_experts<Forward>(a, s);
   if (e != hipSuccess) return e;
-  const dim3 grid((unsigned)((a.E + kBalanceExperts - 1) / kBalanceExperts * a.S));
-  hipLaunchKernelGGL(balance_sums_kernel, grid, dim3(64 * kSumWaves), 0, s, a);
+  const int64_t nb = (a.E + kBalanceExperts - 1) / kBalanceExperts;
+  const dim3 grid((unsigned)(nb * a.S));
+  if (a.nchunk / a.S >= 64)
+    hipLaunchKernelGGL(balance_sums_kernel<16>, grid, dim3(1024), 0, s, a);
+  else
+    hipLaunchKernelGGL(balance_sums_kernel<4>, grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
-hipError_t launch_balance_backward(const BalanceArgs& a, hipStream_t s) {
-  if (a.E <= 16) return launch_backward<16, 1>(a, s);
-  if (a.E <= 64) return launch_backward<16, 4>(a, s);
-  if (a.E <= 128) return launch_backward<16, 8>(a, s);
-  if (a.E <= 256) return launch_backward<64, 4>(a, s);
-  if (a.E <= 512) return launch_backward<64, 8>(a, s);
-  return launch_backward<64, 32>(a, s);
-}
+hipError_t launch_balance_backward(const BalanceArgs& a, hipStream_t s) { return by_experts<Backward>(a, s); }
 
 }  // namespace moe

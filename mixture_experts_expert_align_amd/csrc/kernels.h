@@ -318,7 +318,7 @@ hipError_t launch_tile_lora_bf16(const LoraArgs& a, const uint16_t* v, const uin
 
 // -------------------------------------------------------------- balance ----
 // Counts, balance loss and its gradient (balance.hip).
-constexpr int kBalanceExperts = 64;      // experts a workgroup of the second launch sums
+constexpr int kBalanceExperts = 16;      // experts a workgroup of the second launch sums
 
 struct BalanceArgs {
   int64_t M;
@@ -335,8 +335,7 @@ struct BalanceArgs {
   float* probs;                // [S, E]
   // workspace; a slot is a (chunk of tokens, sequence) pair that meet: chunk + sequence
   int32_t chunk, nchunk;       // tokens of a workgroup of the first launch; their number
-  float* psum;                 // [nchunk + S][E] sums of p
-  int32_t* csum;               // [nchunk + S][E] routes
+  int2* part;                  // [nchunk + S][E] sums of p (float bits) and routes
   int32_t* tsum;               // [nchunk + S] tokens that count
   double* lpart;               // [S][blocks of kBalanceExperts]
   int32_t* done;               // [S]

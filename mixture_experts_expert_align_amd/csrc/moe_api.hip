@@ -988,7 +988,7 @@ int moe_lora_wgrad(const moe_lora_problem* p, const void* x, const void* dy, con
 constexpr int64_t kBalanceMaxS = 65536;
 
 struct BalanceLayout {
-  int64_t psum, csum, tsum, lpart, done, end;
+  int64_t part, tsum, lpart, done, end;
 };
 
 static bool balance_layout(const moe_router* r, int64_t M, int64_t S, BalanceLayout* L) {
@@ -1002,8 +1002,7 @@ static bool balance_layout(const moe_router* r, int64_t M, int64_t S, BalanceLay
     return o;
   };
   L->lpart = take(8 * S * ((r->E + kBalanceExperts - 1) / kBalanceExperts));
-  L->psum = take(4 * slots * r->E);
-  L->csum = take(4 * slots * r->E);
+  L->part = take(8 * slots * r->E);
   L->tsum = take(4 * slots);
   L->done = take(4 * S);
   L->end = at;
@@ -1052,8 +1051,7 @@ int moe_balance_loss(const moe_router* r, int64_t M, int64_t S, const void* logi
   b.probs = probs;
   b.chunk = balance_chunk(M);
   b.nchunk = (int32_t)((M + b.chunk - 1) / b.chunk);
-  b.psum = at<float>(ws, L.psum);
-  b.csum = at<int32_t>(ws, L.csum);
+  b.part = at<int2>(ws, L.part);
   b.tsum = at<int32_t>(ws, L.tsum);
   b.lpart = at<double>(ws, L.lpart);
   b.done = at<int32_t>(ws, L.done);
