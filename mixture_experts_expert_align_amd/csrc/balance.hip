@@ -104,9 +104,11 @@ struct Raw {
 // positive; then, and only then, the row is taken again with the logits that
 // compete (-inf for one that cannot be chosen, +inf as the largest float32) and
 // sigmoids times e^-min(top, 0), which their quotient does not see.
-template <class S>
+// REST: also 1 - sigmoid in q, without cancellation (1 without sigmoids).
+template <class S, bool REST>
 __device__ __forceinline__ float token_scores(const Raw<S>& r, int c, bool add, const float* bias, bool sigmoid,
-                                              float (&l)[S::NV], float (&p)[S::NV], float& top) {
+                                              float (&l)[S::NV], float (&p)[S::NV], float (&q)[REST ? S::NV : 1],
+                                              float& top) {
   top = -INFINITY;
 #pragma unroll
   for (int i = 0; i < S::NI; ++i)
@@ -130,13 +132,16 @@ __device__ __forceinline__ float token_scores(const Raw<S>& r, int c, bool add, 
     for (int i = 0; i < S::NV; ++i) {
       p[i] = __builtin_amdgcn_exp2f(fmaf(l[i], kLog2e, m));
       s += p[i];
+      if (REST) q[REST ? i : 0] = 1.f;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < S::NV; ++i) {
       // 1 / (1 + e^-l), or e^l / (1 + e^l) below 0: no overflow in either
       const float e = __builtin_amdgcn_exp2f(-fabsf(l[i]) * kLog2e);
-      p[i] = (l[i] > 0.f ? 1.0f : e) * __builtin_amdgcn_rcpf(1.0f + e);
+      const float d = __builtin_amdgcn_rcpf(1.0f + e);
+      p[i] = (l[i] > 0.f ? 1.0f : e) * d;
+      if (REST) q[REST ? i : 0] = (l[i] > 0.f ? e : 1.0f) * d;
       s += p[i];
     }
   }
@@ -156,8 +161,9 @@ __device__ __forceinline__ float token_scores(const Raw<S>& r, int c, bool add, 
   for (int i = 0; i < S::NV; ++i) {
     p[i] = __builtin_amdgcn_exp2f((l[i] - shift) * kLog2e);   // (0 for -inf)
     if (sigmoid) {
-      const float d = 1.0f + __builtin_amdgcn_exp2f(-fabsf(l[i]) * kLog2e);
-      p[i] = (l[i] > 0.f ? 1.0f : p[i]) * __builtin_amdgcn_rcpf(d);
+      const float e = __builtin_amdgcn_exp2f(-fabsf(l[i]) * kLog2e), d = __builtin_amdgcn_rcpf(1.0f + e);
+      p[i] = (l[i] > 0.f ? 1.0f : p[i]) * d;
+      if (REST) q[REST ? i : 0] = (l[i] > 0.f ? e : 1.0f) * d;
     }
     s += p[i];
   }
@@ -204,53 +210,44 @@ __global__ void __launch_bounds__(kThreads) balance_tokens_kernel(BalanceArgs a)
   if (blockIdx.x == 0)
     for (int s = tid; s < a.S; s += kThreads) a.done[s] = 0;
   for (int e = tid; e < NE; e += kThreads) s_b[e] = a.add_bias && e < a.E ? a.bias[e] : 0.f;
-  for (int64_t at = first; at < last;) {
-    const int s = seq_of(a, at);
-    if (s < 0) {                                 // before the first sequence
-      at = min(max(seq_offset(a, 0), at + 1), last);
-      continue;
+  // logits and first ids of the tokens t0 .. t0 + TOK - 1 (past the last token:
+  // that one again, not counted), requested before the sequences are looked up
+  Raw<S> raw;
+  raw.clear();
+  int id = -1;
+  auto load = [&](int64_t t0) {
+    const int64_t in = min(t0 + tid / LANES, last - 1);
+    raw.load(token_row<S>(a, in), a.E, c);
+    if (c < a.topk) id = a.ids[in * a.topk + c];
+  };
+  if (first >= last) return;                     // no tokens at all
+  load(first);
+  // the sequence at hand, its tokens [from, to) up to the chunk's end; between
+  // sequences from is the chunk's end
+  int s;
+  int64_t from, to;
+  auto enter = [&](int64_t at) {
+    s = seq_of(a, at);
+    from = s < 0 ? last : seq_offset(a, s);
+    to = s < 0 ? seq_offset(a, 0) : seq_offset(a, s + 1);
+    if (to <= at) {                              // behind the last sequence, or offsets in no order
+      to = s < 0 ? at + 1 : last;
+      from = last;
     }
-    const int64_t end = min(seq_offset(a, s + 1), last);
-    if (end <= at) break;                        // behind the last sequence
-    Raw<S> raw;
-    raw.clear();
-    int id = -1;
-    // past the last token: that one again, not counted
-    auto load = [&](int64_t t0) {
-      const int64_t in = min(t0 + tid / LANES, end - 1);
-      raw.load(token_row<S>(a, in), a.E, c);
-      if (c < a.topk) id = a.ids[in * a.topk + c];
-    };
-    load(at);
+    to = min(to, last);
+  };
+  enter(first);
+  float acc[S::NV];
+  int n = 0;
+  auto clear = [&]() {
     for (int e = tid; e < NE; e += kThreads) s_c[e] = 0;
     if (tid == 0) s_t = 0;
-    __syncthreads();
-    float acc[S::NV];
 #pragma unroll
     for (int i = 0; i < S::NV; ++i) acc[i] = 0.f;
-    int n = 0;
-    for (int64_t t0 = at; t0 < end; t0 += TOK) {
-      const int64_t t = t0 + tid / LANES;
-      float l[S::NV], p[S::NV], top;
-      bool any = id >= 0 && id < a.E;
-      if (any && t < end) atomicAdd(&s_c[id], 1);
-      for (int j = c + LANES; j < a.topk; j += LANES) {
-        const int64_t in = min(t, end - 1);
-        const int more = a.ids[in * a.topk + j];
-        if (more >= 0 && more < a.E) {
-          any = true;
-          if (t < end) atomicAdd(&s_c[more], 1);
-        }
-      }
-      const Raw<S> now = raw;
-      if (t0 + TOK < end) load(t0 + TOK);
-      const float sum = token_scores<S>(now, c, a.add_bias, s_b, a.sigmoid, l, p, top);
-      const bool on = lanes_max<LANES>(t < end && any ? 1 : 0) != 0;
-      n += on;
-      const float f = on && sum > 0.f ? 1.0f / sum : 0.f;
-#pragma unroll
-      for (int i = 0; i < S::NV; ++i) acc[i] += p[i] * f;
-    }
+    n = 0;
+    __syncthreads();
+  };
+  auto flush = [&]() {
     if (LANES == 16) {
 #pragma unroll
       for (int i = 0; i < S::NV; ++i) {
@@ -275,13 +272,49 @@ __global__ void __launch_bounds__(kThreads) balance_tokens_kernel(BalanceArgs a)
     }
     if (tid == 0) a.tsum[slot] = s_t;
     __syncthreads();
-    at = end;
+  };
+  clear();
+  for (int64_t t0 = first; t0 < last; t0 += TOK) {
+    const int64_t t = t0 + tid / LANES, next = min(t0 + TOK, last);
+    const Raw<S> now = raw;
+    const int now_id = id;
+    if (next < last) load(next);
+    float l[S::NV], p[S::NV], q[1], top;
+    const float sum = token_scores<S, false>(now, c, a.add_bias, s_b, a.sigmoid, l, p, q, top);
+    const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+    for (;;) {
+      // the tokens of this group that are in the sequence
+      const bool in = t >= from && t < to;
+      bool any = in && now_id >= 0 && now_id < a.E;
+      if (any) atomicAdd(&s_c[now_id], 1);
+      if (in)
+        for (int j = c + LANES; j < a.topk; j += LANES) {
+          const int more = a.ids[t * a.topk + j];
+          if (more >= 0 && more < a.E) {
+            any = true;
+            atomicAdd(&s_c[more], 1);
+          }
+        }
+      const bool on = lanes_max<LANES>(any ? 1 : 0) != 0;
+      n += on;
+      const float f = on ? inv : 0.f;
+#pragma unroll
+      for (int i = 0; i < S::NV; ++i) acc[i] += p[i] * f;
+      if (to > next || to == last) break;        // goes on in the next group, or the chunk ends
+      const bool some = from < to, group = to < next;
+      if (some) flush();
+      enter(to);
+      if (some) clear();
+      if (!group) break;
+    }
   }
+  if (from < to) flush();
 }
 
 // Workgroup (sequence, block of its experts): 16 experts a row of lanes, the
 // rows of all waves sharing the sequence's slots.
-template <int kSumWaves>
+constexpr int kSumWaves = 16;
+
 __global__ void __launch_bounds__(64 * kSumWaves) balance_sums_kernel(BalanceArgs a) {
   constexpr int kSumRows = 4 * kSumWaves;
   static_assert(kBalanceExperts == 16, "a row of lanes");
@@ -409,8 +442,8 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(BalanceArgs 
     }
     const double T = a.tokens_in[s];
     const float k = T > 0 ? (float)((double)a.dloss[s] * a.E / ((double)a.topk * T * T)) : 0.f;
-    float l[S::NV], p[S::NV], top;
-    const float sum = token_scores<S>(raw, c, a.add_bias, s_b, a.sigmoid, l, p, top);
+    float l[S::NV], p[S::NV], q[S::NV], top;
+    const float sum = token_scores<S, true>(raw, c, a.add_bias, s_b, a.sigmoid, l, p, q, top);
     const float inv = sum > 0.f ? 1.0f / sum : 0.f;
     int ref = -1;                                // the best expert's count (of several, the largest)
 #pragma unroll
@@ -427,7 +460,7 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(BalanceArgs 
 #pragma unroll
     for (int i = 0; i < S::NV; ++i) {
       d[i] = k * (p[i] * (d[i] - dot));   // p is 0 where l is -inf
-      if (a.sigmoid) d[i] *= __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(l[i] * kLog2e));
+      if (a.sigmoid) d[i] *= q[i];
     }
   } else {
 #pragma unroll
@@ -520,21 +553,19 @@ hipError_t by_experts(const BalanceArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// Tokens of a workgroup of the first launch: at most 1024 workgroups.
+// Tokens of a workgroup of the first launch: at most 512 workgroups, whose parts
+// the second has to add (65536 x 256, both launches: 512 workgroups 20.6 us, 1024
+// 21.5, 2048 26.2), of 16 tokens at least (8192 x 128: 10.9 us, of 32 12.1).
 int32_t balance_chunk(int64_t M) {
-  const int64_t c = ((M + 1023) / 1024 + 15) / 16 * 16;
-  return (int32_t)(c < 32 ? 32 : c);
+  const int64_t c = ((M + 511) / 512 + 15) / 16 * 16;
+  return (int32_t)(c < 16 ? 16 : c);
 }
 
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
   const hipError_t e = by_experts<Forward>(a, s);
   if (e != hipSuccess) return e;
   const int64_t nb = (a.E + kBalanceExperts - 1) / kBalanceExperts;
-  const dim3 grid((unsigned)(nb * a.S));
-  if (a.nchunk / a.S >= 64)
-    hipLaunchKernelGGL(balance_sums_kernel<16>, grid, dim3(1024), 0, s, a);
-  else
-    hipLaunchKernelGGL(balance_sums_kernel<4>, grid, dim3(256), 0, s, a);
+  hipLaunchKernelGGL(balance_sums_kernel, dim3((unsigned)(nb * a.S)), dim3(64 * kSumWaves), 0, s, a);
   return hipGetLastError();
 }
 
