@@ -14,7 +14,8 @@
 // consecutive tokens, LANES lanes a token, and writes for each sequence that
 // it meets the sums of p, the routes and the tokens that count, into slot
 // chunk + sequence (both only grow along the tokens, so every pair that meets
-// has a slot of its own).  In the second a workgroup adds the slots of one
+// has a slot of its own).  (Few tokens: one workgroup, which finishes the
+// sequences itself.)  In the second a workgroup adds the slots of one
 // sequence, kBalanceExperts experts of it, and the last of a sequence's
 // workgroups the loss.  Floats are added in a fixed order, over a chunk's
 // tokens in float32, over the chunks in float64.
@@ -204,39 +205,50 @@ __global__ void __launch_bounds__(kThreads) balance_tokens_kernel(BalanceArgs a)
   __shared__ float s_b[NE];
   __shared__ int s_c[NE];
   __shared__ int s_t;
+  __shared__ double s_l[kWaves];
   const int tid = threadIdx.x, c = tid % LANES, wave = tid >> 6;
   const int64_t first = (int64_t)blockIdx.x * a.chunk;
-  const int64_t last = min(first + a.chunk, a.M);
-  if (blockIdx.x == 0)
+  const int last = (int)min((int64_t)a.chunk, a.M - first);   // tokens, counted from the chunk's first below
+  if (a.one) {                                   // there is no second launch; sequences without tokens
+    for (int64_t i = tid; i < (int64_t)a.S * a.E; i += kThreads) {
+      a.counts[i] = 0;
+      a.probs[i] = 0.f;
+    }
+    for (int s = tid; s < a.S; s += kThreads) {
+      a.loss[s] = 0.f;
+      a.tokens[s] = 0;
+    }
+  } else if (blockIdx.x == 0) {
     for (int s = tid; s < a.S; s += kThreads) a.done[s] = 0;
+  }
   for (int e = tid; e < NE; e += kThreads) s_b[e] = a.add_bias && e < a.E ? a.bias[e] : 0.f;
   // logits and first ids of the tokens t0 .. t0 + TOK - 1 (past the last token:
   // that one again, not counted), requested before the sequences are looked up
   Raw<S> raw;
   raw.clear();
   int id = -1;
-  auto load = [&](int64_t t0) {
-    const int64_t in = min(t0 + tid / LANES, last - 1);
+  auto load = [&](int t0) {
+    const int64_t in = first + min(t0 + tid / LANES, last - 1);
     raw.load(token_row<S>(a, in), a.E, c);
     if (c < a.topk) id = a.ids[in * a.topk + c];
   };
-  if (first >= last) return;                     // no tokens at all
-  load(first);
+  if (last <= 0) return;                         // no tokens at all
+  load(0);
   // the sequence at hand, its tokens [from, to) up to the chunk's end; between
   // sequences from is the chunk's end
   int s;
-  int64_t from, to;
-  auto enter = [&](int64_t at) {
-    s = seq_of(a, at);
-    from = s < 0 ? last : seq_offset(a, s);
-    to = s < 0 ? seq_offset(a, 0) : seq_offset(a, s + 1);
+  int from, to;
+  auto in_chunk = [&](int64_t t) { return (int)min(max(t - first, (int64_t)-1), (int64_t)last); };
+  auto enter = [&](int at) {
+    s = seq_of(a, first + at);
+    from = s < 0 ? last : in_chunk(seq_offset(a, s));
+    to = in_chunk(s < 0 ? seq_offset(a, 0) : seq_offset(a, s + 1));
     if (to <= at) {                              // behind the last sequence, or offsets in no order
       to = s < 0 ? at + 1 : last;
       from = last;
     }
-    to = min(to, last);
   };
-  enter(first);
+  enter(0);
   float acc[S::NV];
   int n = 0;
   auto clear = [&]() {
@@ -264,24 +276,44 @@ __global__ void __launch_bounds__(kThreads) balance_tokens_kernel(BalanceArgs a)
     if (c == 0) atomicAdd(&s_t, n);
     __syncthreads();
     const int64_t slot = (int64_t)blockIdx.x + s;
+    double loss = 0.0;
+    const int T = s_t;
     for (int e = tid; e < a.E; e += kThreads) {
       float v = 0.f;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) v += s_p[w][e];
-      a.part[slot * a.E + e] = make_int2((int)__float_as_uint(v), s_c[e]);
+      if (!a.one) {
+        a.part[slot * a.E + e] = make_int2((int)__float_as_uint(v), s_c[e]);
+      } else if (T > 0) {
+        const double mean = (double)v / T;
+        a.counts[(int64_t)s * a.E + e] = s_c[e];
+        a.probs[(int64_t)s * a.E + e] = (float)mean;
+        loss += mean * s_c[e];
+      }
     }
-    if (tid == 0) a.tsum[slot] = s_t;
+    if (a.one) {
+      loss = wave_sum_f64(loss);
+      if ((tid & 63) == 0) s_l[wave] = loss;
+      __syncthreads();
+      if (tid == 0 && T > 0) {
+        for (int w = 1; w < kWaves; ++w) loss += s_l[w];
+        a.tokens[s] = T;
+        a.loss[s] = (float)(loss * ((double)a.E / ((double)a.topk * T)));
+      }
+    } else if (tid == 0) {
+      a.tsum[slot] = T;
+    }
     __syncthreads();
   };
   clear();
-  for (int64_t t0 = first; t0 < last; t0 += TOK) {
-    const int64_t t = t0 + tid / LANES, next = min(t0 + TOK, last);
+  for (int t0 = 0; t0 < last; t0 += TOK) {
+    const int t = t0 + tid / LANES, next = min(t0 + TOK, last);
     const Raw<S> now = raw;
     const int now_id = id;
     if (next < last) load(next);
     float l[S::NV], p[S::NV], q[1], top;
     const float sum = token_scores<S, false>(now, c, a.add_bias, s_b, a.sigmoid, l, p, q, top);
-    const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+    const float inv = sum > 0.f ? __builtin_amdgcn_rcpf(sum) : 0.f;
     for (;;) {
       // the tokens of this group that are in the sequence
       const bool in = t >= from && t < to;
@@ -289,7 +321,7 @@ __global__ void __launch_bounds__(kThreads) balance_tokens_kernel(BalanceArgs a)
       if (any) atomicAdd(&s_c[now_id], 1);
       if (in)
         for (int j = c + LANES; j < a.topk; j += LANES) {
-          const int more = a.ids[t * a.topk + j];
+          const int more = a.ids[(first + t) * a.topk + j];
           if (more >= 0 && more < a.E) {
             any = true;
             atomicAdd(&s_c[more], 1);
@@ -444,7 +476,7 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(BalanceArgs 
     const float k = T > 0 ? (float)((double)a.dloss[s] * a.E / ((double)a.topk * T * T)) : 0.f;
     float l[S::NV], p[S::NV], q[S::NV], top;
     const float sum = token_scores<S, true>(raw, c, a.add_bias, s_b, a.sigmoid, l, p, q, top);
-    const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+    const float inv = sum > 0.f ? __builtin_amdgcn_rcpf(sum) : 0.f;
     int ref = -1;                                // the best expert's count (of several, the largest)
 #pragma unroll
     for (int i = 0; i < S::NV; ++i) ref = max(ref, l[i] == top ? ci[i] : -1);
@@ -556,14 +588,22 @@ hipError_t by_experts(const BalanceArgs& a, hipStream_t s) {
 // Tokens of a workgroup of the first launch: at most 512 workgroups, whose parts
 // the second has to add (65536 x 256, both launches: 512 workgroups 20.6 us, 1024
 // 21.5, 2048 26.2), of 16 tokens at least (8192 x 128: 10.9 us, of 32 12.1).
-int32_t balance_chunk(int64_t M) {
+// Up to four rounds of a workgroup's tokens are left to one workgroup (64 x 8,
+// loss and gradient, host included: SMALL_ONE us, in two launches 19.5).
+static int64_t one_workgroup(int64_t E) { return 4 * (kThreads / (E <= 512 ? 16 : 64)); }
+
+int32_t balance_chunk(int64_t M, int64_t E) {
+  if (M <= one_workgroup(E)) return (int32_t)one_workgroup(E);
   const int64_t c = ((M + 511) / 512 + 15) / 16 * 16;
   return (int32_t)(c < 16 ? 16 : c);
 }
 
+// One workgroup also clears the outputs of all sequences: not too many of them.
+bool balance_one(int64_t M, int64_t E, int64_t S) { return M <= one_workgroup(E) && S * E <= 8192; }
+
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
   const hipError_t e = by_experts<Forward>(a, s);
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || a.one) return e;
   const int64_t nb = (a.E + kBalanceExperts - 1) / kBalanceExperts;
   hipLaunchKernelGGL(balance_sums_kernel, dim3((unsigned)(nb * a.S)), dim3(64 * kSumWaves), 0, s, a);
   return hipGetLastError();

@@ -335,6 +335,7 @@ struct BalanceArgs {
   float* probs;                // [S, E]
   // workspace; a slot is a (chunk of tokens, sequence) pair that meet: chunk + sequence
   int32_t chunk, nchunk;       // tokens of a workgroup of the first launch; their number
+  int32_t one;                 // one workgroup, one launch
   int2* part;                  // [nchunk + S][E] sums of p (float bits) and routes
   int32_t* tsum;               // [nchunk + S] tokens that count
   double* lpart;               // [S][blocks of kBalanceExperts]
@@ -349,7 +350,8 @@ struct BalanceArgs {
   int64_t t0;                  // set by the launcher: first token of a launch
 };
 
-int32_t balance_chunk(int64_t M);
+int32_t balance_chunk(int64_t M, int64_t E);
+bool balance_one(int64_t M, int64_t E, int64_t S);
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t s);
 hipError_t launch_balance_backward(const BalanceArgs& a, hipStream_t s);
 

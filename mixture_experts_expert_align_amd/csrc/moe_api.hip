@@ -994,7 +994,7 @@ struct BalanceLayout {
 static bool balance_layout(const moe_router* r, int64_t M, int64_t S, BalanceLayout* L) {
   RouterArgs a;
   if (!router_args(r, &a) || M < 0 || M * r->topk >= (1ll << 31) || S < 1 || S > kBalanceMaxS) return false;
-  const int64_t chunk = balance_chunk(M), slots = (M + chunk - 1) / chunk + S;
+  const int64_t chunk = balance_chunk(M, r->E), slots = (M + chunk - 1) / chunk + S;
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t o = at;
@@ -1049,7 +1049,8 @@ int moe_balance_loss(const moe_router* r, int64_t M, int64_t S, const void* logi
   b.counts = counts;
   b.tokens = tokens;
   b.probs = probs;
-  b.chunk = balance_chunk(M);
+  b.chunk = balance_chunk(M, r->E);
+  b.one = balance_one(M, r->E, S);
   b.nchunk = (int32_t)((M + b.chunk - 1) / b.chunk);
   b.part = at<int2>(ws, L.part);
   b.tsum = at<int32_t>(ws, L.tsum);
