@@ -20,6 +20,7 @@
 // workgroups the loss.  Floats are added in a fixed order, over a chunk's
 // tokens in float32, over the chunks in float64.
 #include "kernels.h"
+#include "lanes.h"
 #include "route_device.h"
 
 namespace moe {
@@ -27,38 +28,6 @@ namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr float kLog2e = 1.44269504088896341f;
-
-// Maximum and sums over the token's LANES lanes, the same bits in each: every
-// step combines two values that the two lanes hold in either order.
-template <int CTRL, class T>
-__device__ __forceinline__ T dpp_of(T v) {
-  return __builtin_bit_cast(T, dpp_u32<CTRL, 0xf>(__builtin_bit_cast(uint32_t, v)));
-}
-template <int LANES, class T, class F>
-__device__ __forceinline__ T lanes_all(T v, F f) {
-  static_assert(LANES == 16 || LANES == 64, "a row of 16 lanes, or the wave");
-  v = f(v, dpp_of<0x128>(v));   // rotations within the row by 8, 4, 2, 1
-  v = f(v, dpp_of<0x124>(v));
-  v = f(v, dpp_of<0x122>(v));
-  v = f(v, dpp_of<0x121>(v));
-  if (LANES == 64) {
-    v = f(v, __shfl_xor(v, 16));
-    v = f(v, __shfl_xor(v, 32));
-  }
-  return v;
-}
-template <int LANES>
-__device__ __forceinline__ float lanes_max(float v) {
-  return lanes_all<LANES>(v, [](float a, float b) { return fmaxf(a, b); });
-}
-template <int LANES>
-__device__ __forceinline__ int lanes_max(int v) {
-  return lanes_all<LANES>(v, [](int a, int b) { return max(a, b); });
-}
-template <int LANES>
-__device__ __forceinline__ float lanes_sum(float v) {
-  return lanes_all<LANES>(v, [](float a, float b) { return a + b; });
-}
 
 // A token's E values over LANES lanes: lane c holds VEC consecutive experts
 // from VEC (c + LANES i) on, NV values in all, loaded VEC at a time.
@@ -589,7 +558,7 @@ hipError_t by_experts(const BalanceArgs& a, hipStream_t s) {
 // the second has to add (65536 x 256, both launches: 512 workgroups 20.6 us, 1024
 // 21.5, 2048 26.2), of 16 tokens at least (8192 x 128: 10.9 us, of 32 12.1).
 // Up to four rounds of a workgroup's tokens are left to one workgroup (64 x 8,
-// loss and gradient, host included: SMALL_ONE us, in two launches 19.5).
+// loss and gradient, host included: 16.8 us, in two launches 19.5).
 static int64_t one_workgroup(int64_t E) { return 4 * (kThreads / (E <= 512 ? 16 : 64)); }
 
 int32_t balance_chunk(int64_t M, int64_t E) {

@@ -11,6 +11,7 @@
 // loads its next row while it works on this one.
 #include "device_common.h"
 #include "kernels.h"
+#include "lanes.h"
 
 namespace moe {
 namespace {
@@ -77,23 +78,21 @@ __device__ __forceinline__ void weights8(const void* p, bool bf16, int i, float 
 // wave that writes one again has passed the next row's barrier, so every wave
 // has read it.
 template <int TPR, int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], float (*s)[N]) {
+__device__ __forceinline__ void row_sums(float (&v)[N], float (*s)[TPR / 64]) {
 #pragma unroll
-  for (int n = 0; n < N; ++n)
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) v[n] += __shfl_xor(v[n], d);
+  for (int n = 0; n < N; ++n) v[n] = lanes_sum<64>(v[n]);
   if constexpr (TPR > 64) {
     const int wave = threadIdx.x >> 6;
     if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-      for (int n = 0; n < N; ++n) s[wave][n] = v[n];
+      for (int n = 0; n < N; ++n) s[n][wave] = v[n];
     }
     lds_barrier();
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      v[n] = s[0][n];
+      v[n] = s[n][0];
 #pragma unroll
-      for (int w = 1; w < TPR / 64; ++w) v[n] += s[w][n];
+      for (int w = 1; w < TPR / 64; ++w) v[n] += s[n][w];
     }
   }
 }
@@ -106,7 +105,7 @@ constexpr int threads_of() {
 template <bool XF, int TPR, int NC>
 __global__ void __launch_bounds__(threads_of<TPR>()) norm_forward_kernel(NormArgs a) {
   constexpr int RW = threads_of<TPR>() / TPR;   // rows of a workgroup at a time
-  __shared__ float s_b[2][TPR / 64][1], s_x[2][TPR / 64][1];
+  __shared__ __attribute__((aligned(16))) float s_b[2][1][TPR / 64], s_x[2][1][TPR / 64];
   const int c0 = threadIdx.x % TPR;
   const bool block = a.block != nullptr, post = a.w_post != nullptr, pre = a.w_pre != nullptr;
   float wu[NC][8], wh[NC][8];                   // w_post times the channels' gate; w_pre
@@ -161,7 +160,7 @@ __global__ void __launch_bounds__(threads_of<TPR>()) norm_forward_kernel(NormArg
 #pragma unroll
           for (int q = 0; q < 8; ++q) v[0] += u[j][q] * u[j][q];
         row_sums<TPR, 1>(v, s_b[odd]);
-        scale = 1.0f / sqrtf(v[0] * inv_k + a.eps);
+        scale = __builtin_amdgcn_rsqf(v[0] * inv_k + a.eps);
       }
       if (a.gate_kind == 2) scale *= static_cast<const float*>(a.gate)[r];
 #pragma unroll
@@ -180,7 +179,7 @@ __global__ void __launch_bounds__(threads_of<TPR>()) norm_forward_kernel(NormArg
 #pragma unroll
         for (int q = 0; q < 8; ++q) v[0] += y[j][q] * y[j][q];
       row_sums<TPR, 1>(v, s_x[odd]);
-      const float rx = 1.0f / sqrtf(v[0] * inv_k + a.eps);
+      const float rx = __builtin_amdgcn_rsqf(v[0] * inv_k + a.eps);
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
         const int k = 8 * (c0 + TPR * j);
@@ -198,15 +197,41 @@ __global__ void __launch_bounds__(threads_of<TPR>()) norm_forward_kernel(NormArg
 template <bool XF, int TPR, int NC>
 __global__ void __launch_bounds__(threads_of<TPR>()) norm_backward_kernel(NormArgs a) {
   constexpr int NT = threads_of<TPR>(), RW = NT / TPR;
-  __shared__ float s_1[2][TPR / 64][3], s_2[2][TPR / 64][1];
+  __shared__ __attribute__((aligned(16))) float s_1[2][3][TPR / 64], s_2[2][1][TPR / 64];
   const int c0 = threadIdx.x % TPR;
   const bool block = a.block != nullptr, post = a.w_post != nullptr, pre = a.w_pre != nullptr;
-  float wu[NC][8], wh[NC][8], qu[NC][8], qh[NC][8];
+  // four chunks a thread (K past 8192): the sums go to LDS, and no second row
+  // waits, for want of registers
+  constexpr bool kKeep = NC <= 2;
+  __shared__ f32x4 s_acc[kKeep ? 1 : 4 * NC][kKeep ? 1 : TPR];
+  float qu[kKeep ? NC : 1][8], qh[kKeep ? NC : 1][8];
+  // sums of chunk j += v: of dh n (which 0) or of d (b rb) (1)
+  auto add = [&](int j, int which, const float (&v)[8]) {
+    if constexpr (kKeep) {
+      float(&q)[8] = which ? qu[j] : qh[j];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) q[k] += v[k];
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        f32x4& q = s_acc[4 * j + 2 * which + h][c0];
+        q = (f32x4){q[0] + v[4 * h], q[1] + v[4 * h + 1], q[2] + v[4 * h + 2], q[3] + v[4 * h + 3]};
+      }
+    }
+  };
+  float wu[NC][8], wh[NC][8];                   // as in the forward; 0 past K
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
     const int k = 8 * (c0 + TPR * j);
+    if constexpr (!kKeep) {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) qu[j][q] = qh[j][q] = wu[j][q] = wh[j][q] = 0.f;
+      for (int q = 0; q < 4; ++q) s_acc[4 * j + q][c0] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      wu[j][q] = wh[j][q] = 0.f;
+      if constexpr (kKeep) qu[j][q] = qh[j][q] = 0.f;
+    }
     if (k >= a.K) continue;
     weights8(a.w_post, a.wbf16, k, wu[j]);
     weights8(a.w_pre, a.wbf16, k, wh[j]);
@@ -218,32 +243,43 @@ __global__ void __launch_bounds__(threads_of<TPR>()) norm_backward_kernel(NormAr
     }
   }
   const float inv_k = 1.0f / (float)a.K;
-  Raw8<XF> x[NC], dy[NC];
-  Raw8<false> b[NC], dh[NC];
+  struct Row {
+    Raw8<XF> x[NC], dy[NC];
+    Raw8<false> b[NC], dh[NC];
+  };
+  Row next;
   auto load = [&](int64_t r) {
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const int k = 8 * (c0 + TPR * j);
-      x[j].zero();
-      dy[j].zero();
-      b[j].zero();
-      dh[j].zero();
+      next.x[j].zero();
+      next.dy[j].zero();
+      next.b[j].zero();
+      next.dh[j].zero();
       if (k < a.K && r < a.M) {
-        if (pre) x[j].load(a.x, r * a.K + k);
-        if (a.dx_out) dy[j].load(a.dx_out, r * a.K + k);
-        if (block) b[j].load(a.block, r * a.K + k);
-        if (pre) dh[j].load(a.dh, r * a.K + k);
+        if (pre) next.x[j].load(a.x, r * a.K + k);
+        if (a.dx_out) next.dy[j].load(a.dx_out, r * a.K + k);
+        if (block) next.b[j].load(a.block, r * a.K + k);
+        if (pre) next.dh[j].load(a.dh, r * a.K + k);
       }
     }
   };
   const int64_t step = (int64_t)gridDim.x * RW;
   int odd = 0;
-  for (int64_t r = (int64_t)blockIdx.x * RW + threadIdx.x / TPR; r < a.M; r += step, odd ^= 1) {
-    load(r);
+  int64_t r = (int64_t)blockIdx.x * RW + threadIdx.x / TPR;
+  if (kKeep) load(r);
+  for (; r < a.M; r += step, odd ^= 1) {
+    if (!kKeep) load(r);
+    const Row now = next;
+    if (kKeep) load(r + step);
+    const auto& x = now.x;
+    const auto& dy = now.dy;
+    const auto& b = now.b;
+    const auto& dh = now.dh;
     // mean squares of x' and b, and the product of w_pre dh with x'
     float v[3] = {0.f, 0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < NC; ++j)
+    for (int j = 0; j < NC; ++j) {
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         const float xv = x[j].get(q), bv = b[j].get(q);
@@ -251,9 +287,10 @@ __global__ void __launch_bounds__(threads_of<TPR>()) norm_backward_kernel(NormAr
         v[1] += wh[j][q] * dh[j].get(q) * xv;
         v[2] += bv * bv;
       }
+    }
     row_sums<TPR, 3>(v, s_1[odd]);
-    const float rx = pre ? 1.0f / sqrtf(v[0] * inv_k + a.eps) : 0.f;
-    const float rb = post ? 1.0f / sqrtf(v[2] * inv_k + a.eps) : 1.f;
+    const float rx = pre ? __builtin_amdgcn_rsqf(v[0] * inv_k + a.eps) : 0.f;
+    const float rb = post ? __builtin_amdgcn_rsqf(v[2] * inv_k + a.eps) : 1.f;
     const float gate = a.gate_kind == 2 ? static_cast<const float*>(a.gate)[r] : 1.f;
     const float mx = v[1] * inv_k * rx;           // mean of w_pre dh n
     float d[NC][8];
@@ -261,22 +298,22 @@ __global__ void __launch_bounds__(threads_of<TPR>()) norm_backward_kernel(NormAr
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const int k = 8 * (c0 + TPR * j);
-      float o[8];
+      float o[8], ah[8], au[8];
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         const float xv = x[j].get(q), bv = b[j].get(q), hv = dh[j].get(q);
         float e = dy[j].get(q);
-        if (pre) {
-          const float n = xv * rx;
-          e += rx * (wh[j][q] * hv - n * mx);
-          qh[j][q] += hv * n;
-        }
+        const float n = xv * rx;             // (without w_pre: rx is 0, and so are x' and dh here)
+        e += rx * (wh[j][q] * hv - n * mx);
+        ah[q] = hv * n;
         o[q] = block ? a.res_scale * e : e;
-        qu[j][q] += gate * e * (bv * rb);
+        au[q] = gate * e * (bv * rb);
         e *= wu[j][q];
         w[0] += e * bv;
         d[j][q] = e;
       }
+      add(j, 0, ah);
+      add(j, 1, au);
       if (k < a.K) store8<XF>(a.dx, r * a.K + k, o);
     }
     if (!block) continue;
@@ -300,8 +337,14 @@ __global__ void __launch_bounds__(threads_of<TPR>()) norm_backward_kernel(NormAr
     for (int j = 0; j < NC; ++j) {
       const int k = 8 * (c0 + TPR * j);
       if (k >= a.K) continue;
-      store8<true>(part, k, qh[j]);
-      store8<true>(part, a.K + k, qu[j]);
+      if constexpr (kKeep) {
+        store8<true>(part, k, qh[j]);
+        store8<true>(part, a.K + k, qu[j]);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+          *reinterpret_cast<f32x4*>(part + (h / 2) * a.K + k + 4 * (h % 2)) = s_acc[4 * j + h][c0];
+      }
     }
   } else {
     __shared__ float s_q[RW][2][8 * TPR * NC];
@@ -332,8 +375,10 @@ __global__ void __launch_bounds__(64 * kJoinWaves) norm_join_kernel(NormArgs a, 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int i = blockIdx.x * 64 + lane;
   float v = 0.f;
-  if (i < 2 * a.K)
+  if (i < 2 * a.K) {
+#pragma unroll 8
     for (int p = wave; p < nparts; p += kJoinWaves) v += a.part[(int64_t)p * 2 * a.K + i];
+  }
   s_v[wave][lane] = v;
   __syncthreads();
   if (wave != 0 || i >= 2 * a.K) return;
@@ -376,7 +421,7 @@ hipError_t forward_of(const NormArgs& a, hipStream_t s) {
 }
 
 // Threads of a row in the backward, by K.
-int backward_tpr(int64_t K) { return K <= 1024 ? 64 : K <= 4096 ? 256 : K <= 8192 ? 512 : 1024; }
+int backward_tpr(int64_t K) { return K <= 1024 ? 64 : K <= 4096 ? 256 : 512; }
 
 template <bool XF, int TPR, int NC>
 hipError_t backward(const NormArgs& a, int blocks, hipStream_t s) {
@@ -397,16 +442,20 @@ hipError_t backward_of(const NormArgs& a, int blocks, hipStream_t s) {
   if (a.K <= 2048) return backward<XF, 256, 1>(a, blocks, s);
   if (a.K <= 4096) return backward<XF, 256, 2>(a, blocks, s);
   if (a.K <= 8192) return backward<XF, 512, 2>(a, blocks, s);
-  return backward<XF, 1024, 2>(a, blocks, s);
+  return backward<XF, 512, 4>(a, blocks, s);
 }
 
 }  // namespace
 
-// Workgroups of the backward, each with sums of its own: two a CU at most.
+// Workgroups of the backward, each with sums of its own that are added afterwards:
+// what is resident at once, one of 512 threads or two of 256 a CU (8192 x 4096
+// bf16: 512 workgroups 87 us, 256 104, 768 102; 8192 x 6144, whose rows take 512
+// threads: 256 workgroups 142 us, 512 146, 128 233).
 int32_t norm_backward_blocks(int64_t M, int64_t K) {
   const int tpr = backward_tpr(K), rw = tpr < 256 ? 256 / tpr : 1;
   const int64_t rows = (M + rw - 1) / rw;
-  return (int32_t)(rows < 512 ? rows : 512);
+  const int64_t most = tpr <= 256 ? 512 : 256;
+  return (int32_t)(rows < most ? rows : most);
 }
 
 hipError_t launch_block_norm(const NormArgs& a, hipStream_t s) {
