@@ -577,6 +577,285 @@ hipError_t product(const StepArgs& a, int T, hipStream_t s) {
   return launch_product<64, MODE>(a, s);
 }
 
+// ----------------------------------------------------------------- narrow --
+// m <= 64: a launch a step.  Every workgroup of a matrix adds the workgroups'
+// parts of A, squares it and forms B by itself, in LDS, applies B to its rows of
+// X and leaves its part of the next A.  The three products by themselves are
+// chains of launches of a few microseconds each, and A's a single tile with all
+// of n to add (4096 x 64: 18 of a step's 27 us).
+
+constexpr int kNarrow = 64;       // m, padded
+constexpr int kNarrowRows = 128;  // rows of a round: 32 a wave
+
+struct NarrowArgs {
+  int32_t E, N, K, wide, n, m;
+  int32_t W, rows;        // workgroups of a matrix; rows of one, a multiple of kNarrowRows
+  const void* u;
+  const double* part;     // sums of squares
+  double eps;
+  float first;            // 2^ of the first X's scale
+  uint16_t* hi;           // X [E][W rows][64], two pieces, updated in place
+  uint16_t* lo;
+  const float* gin;       // parts of A [E][W][64][64], of the stored X's products
+  float* gout;
+  int32_t last;
+  float ca, cb, cc;
+  float to_a, sa, from_sa, sb, from_b, from_x, out;   // scales, as in StepArgs
+  float scale;
+  uint16_t* y;
+};
+
+enum Narrow { kNarrowInput = 0, kNarrowInputBf16 = 1, kNarrowStep = 2 };
+
+// Lanes l and l + 32 hold 8 values each of 16 in a row, the first and the last 8, as
+// loaded; or, as a product leaves them, values 0 .. 3 and 8 .. 11, and 4 .. 7 and 12 ..
+// 15.  One to the other, either way.
+__device__ __forceinline__ void halves_to_groups(i32x4& v) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const auto r = __builtin_amdgcn_permlane32_swap((uint32_t)v[k], (uint32_t)v[2 + k], false, false);
+    v[k] = (int)r[0];
+    v[2 + k] = (int)r[1];
+  }
+}
+
+// Two transposed fragments (columns j0 .. + 31) of two slices of 16 rows, c0 and c0 +
+// 16, of a round's rows, and the same for columns k0 .. + 31: reads and their wait in
+// one statement (the builtins wait for the stores in flight as well).
+__device__ __forceinline__ void narrow_frags(const uint16_t* s, int j0, int k0, int c0, int lane, f16x8 (&f)[4]) {
+  const int gq = lane >> 4, L = lane & 15;
+  uint32_t ad[8];
+  tile::v4i16 v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int j = (i & 1 ? k0 : j0) + 16 * (gq & 1) + 4 * (L & 3);
+    const int c = c0 + 16 * (i >> 1) + 8 * (gq >> 1) + (L >> 2);
+    ad[2 * i] = (uint32_t)(uintptr_t)(tile::lds_v4i16*)(s + tile::wt_off_n<64>(c, j));
+    ad[2 * i + 1] = (uint32_t)(uintptr_t)(tile::lds_v4i16*)(s + tile::wt_off_n<64>(c + 4, j));
+  }
+  asm volatile("ds_read_b64_tr_b16 %0, %8\n\tds_read_b64_tr_b16 %1, %9\n\tds_read_b64_tr_b16 %2, %10\n\t"
+               "ds_read_b64_tr_b16 %3, %11\n\tds_read_b64_tr_b16 %4, %12\n\tds_read_b64_tr_b16 %5, %13\n\t"
+               "ds_read_b64_tr_b16 %6, %14\n\tds_read_b64_tr_b16 %7, %15\n\ts_waitcnt lgkmcnt(0)"
+               : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]), "=&v"(v[6]), "=&v"(v[7])
+               : "v"(ad[0]), "v"(ad[1]), "v"(ad[2]), "v"(ad[3]), "v"(ad[4]), "v"(ad[5]), "v"(ad[6]), "v"(ad[7])
+               : "memory");
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const tile::v4i16 v8[2] = {v[2 * i], v[2 * i + 1]};
+    f[i] = __builtin_bit_cast(f16x8, v8);
+  }
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(256) ortho_narrow_kernel(NarrowArgs a) {
+  __shared__ __attribute__((aligned(16))) uint16_t s_o[kNarrow * kNarrow], s_b[kNarrow * kNarrow];
+  __shared__ __attribute__((aligned(16))) uint16_t s_x[kNarrowRows * kNarrow];
+  __shared__ __attribute__((aligned(16))) float s_d[kNarrow], s_e[kNarrow];
+  const int e = blockIdx.x / a.W, wg = blockIdx.x % a.W;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wi = wave >> 1, wj = wave & 1, l32 = lane & 31, up = lane >> 5;
+  auto frag = [&](const uint16_t* s, int row, int st) {
+    return *reinterpret_cast<const f16x8*>(s + tile::lds_off<64>(row, 2 * st + up));
+  };
+  // A round: row t of the lane in two pieces, 16-byte loads (x: also the product's
+  // operand: columns 16 st + 8 up .. + 7 of it), or as the update's values (u: 4 g + h
+  // of [i] is column 32 i + 8 g + 4 up + h, as in the product).  Requested a round
+  // ahead, the first before anything else.
+  const int tl = 32 * wave + l32;
+  const int64_t row0 = (int64_t)wg * a.rows + tl;
+  const int64_t x0 = ((int64_t)e * a.W * a.rows + row0) * kNarrow;
+  i32x4 x[4], xl[4];
+  float u[2][16];
+  auto request = [&](int rb) {
+    if constexpr (MODE == kNarrowStep) {
+      const int64_t at = x0 + (int64_t)rb * kNarrow + 8 * up;
+#pragma unroll
+      for (int st = 0; st < 4; ++st) {
+        x[st] = *reinterpret_cast<const i32x4*>(a.hi + at + 16 * st);
+        xl[st] = *reinterpret_cast<const i32x4*>(a.lo + at + 16 * st);
+      }
+    } else {
+      // (past the matrix: its last value, not taken)
+      const int64_t base = (int64_t)e * a.N * a.K, tc = min(row0 + rb, (int64_t)a.n - 1);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int pc = min(32 * i + 8 * (k / 4) + 4 * up + k % 4, a.m - 1);
+          const int64_t o = base + (a.wide ? (int64_t)pc * a.K + tc : tc * a.K + pc);
+          u[i][k] = MODE == kNarrowInputBf16 ? bf16_to_f32(static_cast<const uint16_t*>(a.u)[o])
+                                             : static_cast<const float*>(a.u)[o];
+        }
+    }
+  };
+  request(0);
+  double f = 0.0;
+  if constexpr (MODE != kNarrowStep) {
+    double s = a.part[(int64_t)e * kOrthoNormBlocks + lane];
+#pragma unroll
+    for (int d = 32; d; d >>= 1) s += __shfl_xor(s, d);
+    f = a.first / (sqrt(s) + a.eps);
+  } else {
+    // A: thread t holds columns 4 (t % 16) .. + 3 of the rows t / 16 + 16 i; four
+    // parts are requested together (past the last: that one again, not added)
+    const int c = 4 * (threadIdx.x % 16), r0 = threadIdx.x / 16;
+    f32x4 v[4] = {};
+    const float* g = a.gin + (int64_t)e * a.W * (kNarrow * kNarrow) + r0 * kNarrow + c;
+    for (int w = 0; w < a.W; w += 4) {
+      f32x4 part[4][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          part[k][i] = *reinterpret_cast<const f32x4*>(g + min(w + k, a.W - 1) * (kNarrow * kNarrow) + 16 * i * kNarrow);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (w + k < a.W) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] += part[k][i];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = r0 + 16 * i, k = r - c;   // the diagonal is value k of this thread, if 0 <= k < 4
+      uint32_t o[4];
+      float d = 0.f;
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const float w = v[i][h] * a.to_a;
+        d = k == h ? w : d;
+        o[h] = f32_to_f16(k == h ? 0.f : w * a.sa);
+      }
+      if ((unsigned)k < 4u) s_d[r] = d;
+      *reinterpret_cast<uint2*>(s_o + tile::lds_off<64>(r, c / 8) + c % 8) =
+          make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+    }
+    lds_barrier();
+    // B: wave (wi, wj) the tile of 32 p by 32 q
+    f32x16 acc = {};
+#pragma unroll
+    for (int st = 0; st < 4; ++st)
+      acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(frag(s_o, 32 * wi + l32, st), frag(s_o, 32 * wj + l32, st), acc, 0,
+                                                   0, 0);
+    const int q = 32 * wj + l32;
+    const float dq = s_d[q], sq = a.from_sa * a.from_sa;
+#pragma unroll
+    for (int g4 = 0; g4 < 4; ++g4) {
+      const int p = 32 * wi + 8 * g4 + 4 * up;
+      const uint2 o = *reinterpret_cast<const uint2*>(s_o + tile::lds_off<64>(q, p / 8) + p % 8);
+      const f32x4 dp = *reinterpret_cast<const f32x4*>(s_d + p);
+      uint32_t b[4];
+      float diag = 0.f;
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const float off = f16_to_f32((h & 2 ? o.y : o.x) >> (h & 1 ? 16 : 0)) * a.from_sa;   // 0 on the diagonal
+        const float oo = acc[4 * g4 + h] * sq;
+        diag = p + h == q ? oo : diag;
+        b[h] = f32_to_f16(p + h == q ? 0.f : (a.cb * off + a.cc * (oo + (dp[h] + dq) * off)) * a.sb);
+      }
+      if ((unsigned)(q - p) < 4u) s_e[q] = a.ca + (a.cb * dq + a.cc * (diag + dq * dq));
+      *reinterpret_cast<uint2*>(s_b + tile::lds_off<64>(q, p / 8) + p % 8) =
+          make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
+    }
+    lds_barrier();
+  }
+  f32x16 gram = {};
+  for (int rb = 0; rb < a.rows; rb += kNarrowRows) {
+    const int64_t t = row0 + rb, at = x0 + (int64_t)rb * kNarrow;
+    float val[2][16];
+    if constexpr (MODE == kNarrowStep) {
+      f32x16 acc[2] = {};
+#pragma unroll
+      for (int st = 0; st < 4; ++st)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(frag(s_b, 32 * i + l32, st),
+                                                          __builtin_bit_cast(f16x8, x[st]), acc[i], 0, 0, 0);
+#pragma unroll
+      for (int st = 0; st < 4; ++st) {
+        halves_to_groups(x[st]);
+        halves_to_groups(xl[st]);
+        const f16x8 h = __builtin_bit_cast(f16x8, x[st]), l = __builtin_bit_cast(f16x8, xl[st]);
+#pragma unroll
+        for (int g2 = 0; g2 < 2; ++g2) {
+          const int i = st / 2, g4 = 2 * (st % 2) + g2;
+          const f32x4 se = *reinterpret_cast<const f32x4*>(s_e + 16 * st + 8 * g2 + 4 * up);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float v = (float)l[4 * g2 + k] * (1.0f / kLow) + (float)h[4 * g2 + k];
+            val[i][4 * g4 + k] = (se[k] * a.from_x * v + acc[i][4 * g4 + k] * a.from_b) * a.out;
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const bool in = t < a.n && 32 * i + 8 * (k / 4) + 4 * up + k % 4 < a.m;
+          val[i][k] = in ? (float)(u[i][k] * f) : 0.f;
+        }
+    }
+    if (rb + kNarrowRows < a.rows) request(rb + kNarrowRows);
+    if (MODE == kNarrowStep && a.last) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int p = 32 * i + 8 * (k / 4) + 4 * up + k % 4;
+          if (t < a.n && p < a.m)
+            a.y[(int64_t)e * a.N * a.K + (a.wide ? (int64_t)p * a.K + t : t * a.K + p)] =
+                (uint16_t)f32_to_bf16_rne(val[i][k] * a.scale);
+        }
+      continue;
+    }
+#pragma unroll
+    for (int st = 0; st < 4; ++st) {
+      f16x8 hi, lo;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float v = val[st / 2][8 * (st % 2) + k];
+        hi[k] = (_Float16)v;
+        lo[k] = (_Float16)(v * kLow - (float)hi[k] * kLow);
+      }
+      i32x4 h = __builtin_bit_cast(i32x4, hi), l = __builtin_bit_cast(i32x4, lo);
+#pragma unroll
+      for (int g2 = 0; g2 < 2; ++g2)
+        *reinterpret_cast<int2*>(s_x + tile::wt_off_n<64>(tl, 16 * st + 8 * g2 + 4 * up)) = make_int2(h[2 * g2], h[2 * g2 + 1]);
+      halves_to_groups(h);
+      halves_to_groups(l);
+      *reinterpret_cast<i32x4*>(a.hi + at + 16 * st + 8 * up) = h;
+      *reinterpret_cast<i32x4*>(a.lo + at + 16 * st + 8 * up) = l;
+    }
+    lds_barrier();
+#pragma unroll
+    for (int st = 0; st < kNarrowRows / 16; st += 2) {
+      f16x8 fr[4];
+      narrow_frags(s_x, 32 * wi, 32 * wj, 16 * st, lane, fr);
+      gram = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr[0], fr[1], gram, 0, 0, 0);
+      gram = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr[2], fr[3], gram, 0, 0, 0);
+    }
+    lds_barrier();
+  }
+  if (MODE == kNarrowStep && a.last) return;
+  float* g = a.gout + ((int64_t)e * a.W + wg) * (kNarrow * kNarrow) + (32 * wj + l32) * kNarrow + 32 * wi + 4 * up;
+#pragma unroll
+  for (int g4 = 0; g4 < 4; ++g4)
+    *reinterpret_cast<f32x4*>(g + 8 * g4) =
+        (f32x4){gram[4 * g4], gram[4 * g4 + 1], gram[4 * g4 + 2], gram[4 * g4 + 3]};
+}
+
+// Rows of a workgroup: 256, or what leaves 16 workgroups, whose parts of A each of
+// them adds.
+int64_t narrow_rows(int64_t n) {
+  const int64_t r = (n + 15) / 16;
+  const int64_t rows = (r + kNarrowRows - 1) / kNarrowRows * kNarrowRows;
+  if (n <= kNarrowRows) return kNarrowRows;
+  return rows < 2 * kNarrowRows ? 2 * kNarrowRows : rows;
+}
+
 // What m and n are padded to: tiles of 256 where they fill the CUs and the
 // padding costs little.
 int tile_of(int64_t E, int64_t n, int64_t m) {
@@ -588,16 +867,13 @@ int tile_of(int64_t E, int64_t n, int64_t m) {
 }
 
 struct Layout {
-  int T;
-  int64_t np, mp, hi[2], lo[2], xt, a, b, da, db, part, end;
+  int T;                  // 0: narrow
+  int64_t np, mp, W, hi[2], lo[2], xt, a, b, da, db, part, end;
 };
 
 Layout layout(int64_t E, int64_t N, int64_t K) {
-  Layout L;
+  Layout L{};
   const int64_t n = N >= K ? N : K, m = N >= K ? K : N;
-  L.T = tile_of(E, n, m);
-  L.np = (n + L.T - 1) / L.T * L.T;
-  L.mp = (m + L.T - 1) / L.T * L.T;
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t o = at;
@@ -605,6 +881,21 @@ Layout layout(int64_t E, int64_t N, int64_t K) {
     return o;
   };
   L.part = take(8 * E * kOrthoNormBlocks);
+  if (m <= kNarrow) {
+    const int64_t rows = narrow_rows(n);
+    L.W = (n + rows - 1) / rows;
+    L.np = L.W * rows;
+    L.mp = kNarrow;
+    L.hi[0] = take(2 * E * L.np * L.mp);
+    L.lo[0] = take(2 * E * L.np * L.mp);
+    L.a = take(4 * E * L.W * L.mp * L.mp);   // parts of A, of this step and of the next
+    L.b = take(4 * E * L.W * L.mp * L.mp);
+    L.end = at;
+    return L;
+  }
+  L.T = tile_of(E, n, m);
+  L.np = (n + L.T - 1) / L.T * L.T;
+  L.mp = (m + L.T - 1) / L.T * L.T;
   for (int i = 0; i < 2; ++i) {
     L.hi[i] = take(2 * E * L.np * L.mp);
     L.lo[i] = take(2 * E * L.np * L.mp);
@@ -662,17 +953,76 @@ bool ortho_scales(const OrthoArgs& o, int32_t (*s)[3]) {
   return u <= 4096.0;
 }
 
+static hipError_t launch_narrow(const OrthoArgs& o, const ortho::Layout& L, const int32_t (*s)[3], hipStream_t st) {
+  using namespace ortho;
+  char* ws = static_cast<char*>(o.ws);
+  NarrowArgs a{};
+  a.E = o.E;
+  a.N = o.N;
+  a.K = o.K;
+  a.wide = o.N < o.K;
+  a.n = a.wide ? o.K : o.N;
+  a.m = a.wide ? o.N : o.K;
+  a.W = (int32_t)L.W;
+  a.rows = (int32_t)(L.np / L.W);
+  a.u = o.update;
+  a.part = reinterpret_cast<const double*>(ws + L.part);
+  a.eps = o.eps;
+  a.first = pow2(s[0][0]);
+  a.hi = reinterpret_cast<uint16_t*>(ws + L.hi[0]);
+  a.lo = reinterpret_cast<uint16_t*>(ws + L.lo[0]);
+  a.scale = o.scale;
+  a.y = o.out;
+  float* g[2] = {reinterpret_cast<float*>(ws + L.a), reinterpret_cast<float*>(ws + L.b)};
+  a.gout = g[0];
+  const dim3 grid((unsigned)(o.E * L.W)), block(256);
+  if (o.bf16)
+    hipLaunchKernelGGL(ortho_narrow_kernel<kNarrowInputBf16>, grid, block, 0, st, a);
+  else
+    hipLaunchKernelGGL(ortho_narrow_kernel<kNarrowInput>, grid, block, 0, st, a);
+  hipError_t e = hipGetLastError();
+  for (int i = 0; i < o.steps && e == hipSuccess; ++i) {
+    a.gin = g[i & 1];
+    a.gout = g[(i & 1) ^ 1];
+    a.last = i + 1 == o.steps;
+    a.ca = o.coef[i][0];
+    a.cb = o.coef[i][1];
+    a.cc = o.coef[i][2];
+    a.to_a = pow2(-2 * s[i][0]);
+    a.sa = pow2(s[i][1]);
+    a.from_sa = pow2(-s[i][1]);
+    a.sb = pow2(s[i][2]);
+    a.from_b = pow2(-s[i][0] - s[i][2]);
+    a.from_x = pow2(-s[i][0]);
+    a.out = a.last ? 1.0f : pow2(s[i + 1][0]);
+    hipLaunchKernelGGL(ortho_narrow_kernel<kNarrowStep>, grid, block, 0, st, a);
+    e = hipGetLastError();
+  }
+  return e;
+}
+
 hipError_t launch_orthogonalize(const OrthoArgs& o, hipStream_t st) {
   using namespace ortho;
   const Layout L = layout(o.E, o.N, o.K);
   int32_t s[kOrthoMaxSteps][3];
   if (!ortho_scales(o, s)) return hipErrorInvalidValue;
   char* ws = static_cast<char*>(o.ws);
+  const int wide = o.N < o.K;
+  const int64_t per = (int64_t)o.N * o.K;
+  double* part = reinterpret_cast<double*>(ws + L.part);
+  const dim3 gn(kOrthoNormBlocks, (unsigned)o.E);
+  if (o.bf16)
+    hipLaunchKernelGGL(ortho_norm_kernel<true>, gn, dim3(1024), 0, st, o.update, per, part);
+  else
+    hipLaunchKernelGGL(ortho_norm_kernel<false>, gn, dim3(1024), 0, st, o.update, per, part);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (L.T == 0) return launch_narrow(o, L, s, st);
   Mats M{};
   M.E = o.E;
   M.np = (int32_t)L.np;
   M.mp = (int32_t)L.mp;
-  M.part = reinterpret_cast<double*>(ws + L.part);
+  M.part = part;
   for (int i = 0; i < 2; ++i) {
     M.hi[i] = reinterpret_cast<uint16_t*>(ws + L.hi[i]);
     M.lo[i] = reinterpret_cast<uint16_t*>(ws + L.lo[i]);
@@ -682,16 +1032,7 @@ hipError_t launch_orthogonalize(const OrthoArgs& o, hipStream_t st) {
   M.b = reinterpret_cast<uint16_t*>(ws + L.b);
   M.da = reinterpret_cast<float*>(ws + L.da);
   M.db = reinterpret_cast<float*>(ws + L.db);
-  const int wide = o.N < o.K;
-  const int64_t per = (int64_t)o.N * o.K;
-  hipError_t e;
   {
-    const dim3 g(kOrthoNormBlocks, (unsigned)o.E);
-    if (o.bf16)
-      hipLaunchKernelGGL(ortho_norm_kernel<true>, g, dim3(1024), 0, st, o.update, per, M.part);
-    else
-      hipLaunchKernelGGL(ortho_norm_kernel<false>, g, dim3(1024), 0, st, o.update, per, M.part);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
     const dim3 gi((unsigned)(o.E * (L.np / 64) * (L.mp / 64)));
     const float sc = pow2(s[0][0]);
     if (o.bf16)
