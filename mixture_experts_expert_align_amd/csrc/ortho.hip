@@ -55,6 +55,9 @@ struct Mats {
   uint16_t* b;           // of B
   float* da;             // diagonals [mp]
   float* db;
+  float* gpart;          // [E][tiles of 64 of A][splits][64][64]: sums over parts of n
+  int32_t* gdone;        // [E][tiles]: how many of them are there, 0 between the steps
+  int32_t gtiles;        // E tiles
 };
 
 // ------------------------------------------------------------ norm, input --
@@ -156,6 +159,7 @@ __global__ void __launch_bounds__(256) ortho_input_kernel(const void* u, int N, 
       M.lo[0][at + (int64_t)r * mp + c] = (uint16_t)f32_to_f16((v - f16_to_f32(h)) * kLow);
     }
   }
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < M.gtiles; i += (int64_t)gridDim.x * 256) M.gdone[i] = 0;
   __syncthreads();
   for (int i = wave; i < 64; i += 4) {
     const int r = c0 + i, c = r0 + lane;   // of the transpose
@@ -188,6 +192,7 @@ struct StepArgs {
   float scale;
   int32_t chunk;          // consecutive tiles of an XCD
   int64_t total;          // tiles
+  int32_t splits;         // kGram, tiles of 64: workgroups that share a tile's contraction
 };
 
 // Tile of C: T x T, waves WI (along p) x WJ (along q) of TI x TJ MFMA tiles.
@@ -238,8 +243,11 @@ __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2
   const int np = M.np, mp = M.mp;
   // block b runs on XCD b % 8: runs of `chunk` tiles go to one XCD
   const int64_t kx = blockIdx.x / tile::NXCD;
-  const int64_t tl = ((kx / a.chunk) * tile::NXCD + blockIdx.x % tile::NXCD) * a.chunk + kx % a.chunk;
+  int64_t tl = ((kx / a.chunk) * tile::NXCD + blockIdx.x % tile::NXCD) * a.chunk + kx % a.chunk;
   if (tl >= a.total) return;
+  constexpr bool kSplit = MODE == kGram && T == 64;   // may share a tile
+  const int sp = kSplit ? (int)(tl % a.splits) : 0;
+  if (kSplit) tl /= a.splits;
   const int nm = mp / T;
   int e, tp, tq;
   if (MODE == kApply) {
@@ -283,7 +291,9 @@ __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2
     Q = M.hi[a.cur] + (int64_t)e * np * mp;
     qrows = np;
   }
-  const int nk = kd / kBK;
+  const int ns = kd / kBK;                    // slices; this workgroup's: nk from k0 on
+  const int k0 = kSplit ? (int)((int64_t)ns * sp / a.splits) : 0;
+  const int nk = kSplit ? (int)((int64_t)ns * (sp + 1) / a.splits) - k0 : ns;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wi = wave / WJ, wj = wave % WJ;
@@ -302,13 +312,13 @@ __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2
   auto issue_p = [&](int kt) {
     uint16_t* slot = pbase + (kt % 3) * kSlot;
 #pragma unroll
-    for (int i = 0; i < L; ++i) lds_load16(pr, slot + (wave + NW * i) * 512, op[i], kt * kBK * 2);
+    for (int i = 0; i < L; ++i) lds_load16(pr, slot + (wave + NW * i) * 512, op[i], (k0 + kt) * kBK * 2);
     issue_order();
   };
   auto issue_q = [&](int kt) {
     uint16_t* slot = qbase + (kt % 2) * kSlot;
 #pragma unroll
-    for (int i = 0; i < L; ++i) lds_load16(qr, slot + (wave + NW * i) * 512, oq[i], kt * kBK * 2);
+    for (int i = 0; i < L; ++i) lds_load16(qr, slot + (wave + NW * i) * 512, oq[i], (k0 + kt) * kBK * 2);
     issue_order();
   };
 
@@ -451,6 +461,55 @@ __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2
               (f32x4){acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
     }
     lds_barrier();
+    if constexpr (kSplit) {
+      // the tile's sums over its share of n; the last workgroup of the tile adds all of
+      // them, in their order, and goes on alone.  A part is where all can read it
+      // before its workgroup is counted.
+      if (a.splits > 1) {
+        constexpr int kCoherent = 16;   // sc1: past the XCD's own L2, to where all XCDs read
+        const __amdgpu_buffer_rsrc_t pr4 = buffer_rsrc(M.gpart + tl * a.splits * (T * T), (int64_t)a.splits * T * T * 4);
+        int* const s_last = reinterpret_cast<int*>(smem + 4 * kSlot);
+        uint32_t place[U];
+#pragma unroll
+        for (int w = 0; w < U; ++w) {
+          place[w] = (uint32_t)(unit_row(w) * T + 8 * u) * 4;
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            __builtin_amdgcn_raw_buffer_store_b128(*reinterpret_cast<const i32x4*>(chunk(unit_row(w), 2 * u + c)), pr4,
+                                                   place[w] + 16 * c, sp * T * T * 4, kCoherent);
+        }
+        wait_vm<0>();
+        lds_barrier();
+        if (threadIdx.x == 0)
+          *s_last = __hip_atomic_fetch_add(M.gdone + tl, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == a.splits - 1;
+        lds_barrier();
+        if (!*s_last) return;
+        if (threadIdx.x == 0) M.gdone[tl] = 0;
+        f32x4 sum[U][2] = {};
+        for (int s = 0; s < a.splits; s += 4) {
+          i32x4 part[4][U][2];   // past the last part: beyond the buffer, zeros
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int w = 0; w < U; ++w)
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                part[k][w][c] = __builtin_amdgcn_raw_buffer_load_b128(pr4, place[w] + 16 * c + (uint32_t)(s + k) * (T * T * 4),
+                                                                      0, kCoherent);
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int w = 0; w < U; ++w)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) sum[w][c] += __builtin_bit_cast(f32x4, part[k][w][c]);
+        }
+#pragma unroll
+        for (int w = 0; w < U; ++w)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) *reinterpret_cast<f32x4*>(chunk(unit_row(w), 2 * u + c)) = sum[w][c];
+      }
+    }
     // (powers of two go into the columns' factors: a value costs a few fused
     // operations that take float16 operands as they are; written out, with each
     // step by itself, the arithmetic took 20000 cycles a tile of 256)
@@ -559,7 +618,7 @@ __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2
 template <int T, int MODE>
 hipError_t launch_product(StepArgs a, hipStream_t s) {
   const int64_t nm = a.M.mp / T, nn = a.M.np / T;
-  a.total = a.M.E * (MODE == kApply ? nm * nn : nm * (nm + 1) / 2);
+  a.total = a.M.E * (MODE == kApply ? nm * nn : nm * (nm + 1) / 2) * (MODE == kGram && T == 64 ? a.splits : 1);
   // few tiles are dealt evenly, many in runs of 32, a tile for each CU of an XCD
   const int64_t even = (a.total + tile::NXCD - 1) / tile::NXCD;
   a.chunk = (int32_t)(even < tile::kXcdChunk ? even : tile::kXcdChunk);
@@ -581,8 +640,11 @@ hipError_t product(const StepArgs& a, int T, hipStream_t s) {
 // m <= 64: a launch a step.  Every workgroup of a matrix adds the workgroups'
 // parts of A, squares it and forms B by itself, in LDS, applies B to its rows of
 // X and leaves its part of the next A.  The three products by themselves are
-// chains of launches of a few microseconds each, and A's a single tile with all
-// of n to add (4096 x 64: 18 of a step's 27 us).
+// chains of launches of a few microseconds each, and A's a few tiles with all
+// of n to add (4096 x 64: 18 of a step's 27 us, in one launch 11).
+
+// (For m <= 128 the same, with two halves of columns and twice the threads, took 15
+// us a step and more, the three launches 13.)
 
 constexpr int kNarrow = 64;       // m, padded
 constexpr int kNarrowRows = 128;  // rows of a round: 32 a wave
@@ -619,73 +681,91 @@ __device__ __forceinline__ void halves_to_groups(i32x4& v) {
   }
 }
 
-// Two transposed fragments (columns j0 .. + 31) of two slices of 16 rows, c0 and c0 +
-// 16, of a round's rows, and the same for columns k0 .. + 31: reads and their wait in
-// one statement (the builtins wait for the stores in flight as well).
-__device__ __forceinline__ void narrow_frags(const uint16_t* s, int j0, int k0, int c0, int lane, f16x8 (&f)[4]) {
+// Transposed fragments of a round's rows (columns j .. + 31 of the 16 rows from 16 ST
+// on) for two column starts j: a lane's first read of the round's first 16 rows is at
+// a[.][0], its second, 4 rows further, at a[.][1]; 16 rows further the swizzle is the
+// same, so that a slice is a constant offset.  Reads and their wait in one statement
+// (the builtins wait for the stores in flight as well).
+__device__ __forceinline__ void narrow_places(const uint16_t* s, const int (&j)[2], int lane, uint32_t (&a)[2][2]) {
   const int gq = lane >> 4, L = lane & 15;
-  uint32_t ad[8];
-  tile::v4i16 v[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int j = (i & 1 ? k0 : j0) + 16 * (gq & 1) + 4 * (L & 3);
-    const int c = c0 + 16 * (i >> 1) + 8 * (gq >> 1) + (L >> 2);
-    ad[2 * i] = (uint32_t)(uintptr_t)(tile::lds_v4i16*)(s + tile::wt_off_n<64>(c, j));
-    ad[2 * i + 1] = (uint32_t)(uintptr_t)(tile::lds_v4i16*)(s + tile::wt_off_n<64>(c + 4, j));
-  }
-  asm volatile("ds_read_b64_tr_b16 %0, %8\n\tds_read_b64_tr_b16 %1, %9\n\tds_read_b64_tr_b16 %2, %10\n\t"
-               "ds_read_b64_tr_b16 %3, %11\n\tds_read_b64_tr_b16 %4, %12\n\tds_read_b64_tr_b16 %5, %13\n\t"
-               "ds_read_b64_tr_b16 %6, %14\n\tds_read_b64_tr_b16 %7, %15\n\ts_waitcnt lgkmcnt(0)"
-               : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]), "=&v"(v[6]), "=&v"(v[7])
-               : "v"(ad[0]), "v"(ad[1]), "v"(ad[2]), "v"(ad[3]), "v"(ad[4]), "v"(ad[5]), "v"(ad[6]), "v"(ad[7])
-               : "memory");
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const tile::v4i16 v8[2] = {v[2 * i], v[2 * i + 1]};
-    f[i] = __builtin_bit_cast(f16x8, v8);
+    for (int h = 0; h < 2; ++h)
+      a[i][h] = (uint32_t)(uintptr_t)(tile::lds_v4i16*)(
+          s + tile::wt_off_n<kNarrow>(8 * (gq >> 1) + (L >> 2) + 4 * h, j[i] + 16 * (gq & 1) + 4 * (L & 3)));
+}
+
+// acc += the products of the two fragments over slices ST .. of a round.
+template <int ST>
+__device__ __forceinline__ void narrow_gram(const uint32_t (&a)[2][2], f32x16& acc) {
+  if constexpr (ST < kNarrowRows / 16) {
+    tile::v4i16 v[4];
+    asm volatile("ds_read_b64_tr_b16 %0, %4 offset:%8\n\tds_read_b64_tr_b16 %1, %5 offset:%8\n\t"
+                 "ds_read_b64_tr_b16 %2, %6 offset:%8\n\tds_read_b64_tr_b16 %3, %7 offset:%8\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
+                 : "v"(a[0][0]), "v"(a[0][1]), "v"(a[1][0]), "v"(a[1][1]), "n"(ST * 16 * kNarrow * 2)
+                 : "memory");
+    f16x8 f[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const tile::v4i16 v8[2] = {v[2 * i], v[2 * i + 1]};
+      f[i] = __builtin_bit_cast(f16x8, v8);
+    }
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[0], f[1], acc, 0, 0, 0);
+    narrow_gram<ST + 1>(a, acc);
   }
 }
 
 template <int MODE>
 __global__ void __launch_bounds__(256) ortho_narrow_kernel(NarrowArgs a) {
-  __shared__ __attribute__((aligned(16))) uint16_t s_o[kNarrow * kNarrow], s_b[kNarrow * kNarrow];
-  __shared__ __attribute__((aligned(16))) uint16_t s_x[kNarrowRows * kNarrow];
-  __shared__ __attribute__((aligned(16))) float s_d[kNarrow], s_e[kNarrow];
+  constexpr int MP = kNarrow, SQ = MP * MP;
+  constexpr int NK = MP / 16;       // MFMA steps along m
+  __shared__ __attribute__((aligned(16))) uint16_t s_o[MODE == kNarrowStep ? SQ : 8], s_b[MODE == kNarrowStep ? SQ : 8];
+  __shared__ __attribute__((aligned(16))) uint16_t s_x[kNarrowRows * MP];
+  __shared__ __attribute__((aligned(16))) float s_d[MP], s_e[MP];
   const int e = blockIdx.x / a.W, wg = blockIdx.x % a.W;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wi = wave >> 1, wj = wave & 1, l32 = lane & 31, up = lane >> 5;
   auto frag = [&](const uint16_t* s, int row, int st) {
-    return *reinterpret_cast<const f16x8*>(s + tile::lds_off<64>(row, 2 * st + up));
+    return *reinterpret_cast<const f16x8*>(s + tile::lds_off<MP>(row, 2 * st + up));
   };
-  // A round: row t of the lane in two pieces, 16-byte loads (x: also the product's
-  // operand: columns 16 st + 8 up .. + 7 of it), or as the update's values (u: 4 g + h
-  // of [i] is column 32 i + 8 g + 4 up + h, as in the product).  Requested a round
-  // ahead, the first before anything else.
+  // A round: row t of the lane in two pieces, columns 16 st + 8 up .. + 7, 16-byte loads
+  // (x: also the product's operand); or the update's values (u: 4 g + h of [i] is column
+  // 32 i + 8 g + 4 up + h, as in the product).  Requested a round ahead, the first
+  // before anything else.
   const int tl = 32 * wave + l32;
   const int64_t row0 = (int64_t)wg * a.rows + tl;
-  const int64_t x0 = ((int64_t)e * a.W * a.rows + row0) * kNarrow;
-  i32x4 x[4], xl[4];
+  const int64_t x0 = ((int64_t)e * a.W * a.rows + row0) * MP;
+  i32x4 x[NK], xl[NK];
   float u[2][16];
   auto request = [&](int rb) {
     if constexpr (MODE == kNarrowStep) {
-      const int64_t at = x0 + (int64_t)rb * kNarrow + 8 * up;
+      const int64_t at = x0 + (int64_t)rb * MP + 8 * up;
 #pragma unroll
-      for (int st = 0; st < 4; ++st) {
+      for (int st = 0; st < NK; ++st) {
         x[st] = *reinterpret_cast<const i32x4*>(a.hi + at + 16 * st);
         xl[st] = *reinterpret_cast<const i32x4*>(a.lo + at + 16 * st);
       }
     } else {
-      // (past the matrix: its last value, not taken)
-      const int64_t base = (int64_t)e * a.N * a.K, tc = min(row0 + rb, (int64_t)a.n - 1);
+      // past the matrix: an offset past the buffer, which gives 0
+      constexpr int EL = MODE == kNarrowInputBf16 ? 2 : 4;
+      const int64_t per = (int64_t)a.N * a.K * EL;
+      const __amdgpu_buffer_rsrc_t r = buffer_rsrc(static_cast<const char*>(a.u) + e * per, per);
+      const int t = (int)(row0 + rb);
+      const uint32_t vo = (uint32_t)(a.wide ? 4 * up * a.K + t : t * a.K + 4 * up) * EL;
+      const int step = (a.wide ? a.K : 1) * EL;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-          const int pc = min(32 * i + 8 * (k / 4) + 4 * up + k % 4, a.m - 1);
-          const int64_t o = base + (a.wide ? (int64_t)pc * a.K + tc : tc * a.K + pc);
-          u[i][k] = MODE == kNarrowInputBf16 ? bf16_to_f32(static_cast<const uint16_t*>(a.u)[o])
-                                             : static_cast<const float*>(a.u)[o];
+          const int p = 32 * i + 8 * (k / 4) + k % 4;
+          const uint32_t o = t < a.n && p + 4 * up < a.m ? vo : 0x80000000u;
+          if constexpr (EL == 2)
+            u[i][k] = bf16_to_f32((uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, o, p * step, 0));
+          else
+            u[i][k] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, o, p * step, 0));
         }
     }
   };
@@ -697,29 +777,30 @@ __global__ void __launch_bounds__(256) ortho_narrow_kernel(NarrowArgs a) {
     for (int d = 32; d; d >>= 1) s += __shfl_xor(s, d);
     f = a.first / (sqrt(s) + a.eps);
   } else {
-    // A: thread t holds columns 4 (t % 16) .. + 3 of the rows t / 16 + 16 i; four
+    // A: a thread holds 4 columns from c on of every RS-th row from r0 on; some
     // parts are requested together (past the last: that one again, not added)
-    const int c = 4 * (threadIdx.x % 16), r0 = threadIdx.x / 16;
-    f32x4 v[4] = {};
-    const float* g = a.gin + (int64_t)e * a.W * (kNarrow * kNarrow) + r0 * kNarrow + c;
-    for (int w = 0; w < a.W; w += 4) {
-      f32x4 part[4][4];
+    constexpr int RS = 256 / (MP / 4), NI = MP / RS, AHEAD = 16 / NI;
+    const int c = 4 * (threadIdx.x % (MP / 4)), r0 = threadIdx.x / (MP / 4);
+    f32x4 v[NI] = {};
+    const float* g = a.gin + (int64_t)e * a.W * SQ + r0 * MP + c;
+    for (int w = 0; w < a.W; w += AHEAD) {
+      f32x4 part[AHEAD][NI];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < AHEAD; ++k)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          part[k][i] = *reinterpret_cast<const f32x4*>(g + min(w + k, a.W - 1) * (kNarrow * kNarrow) + 16 * i * kNarrow);
+        for (int i = 0; i < NI; ++i)
+          part[k][i] = *reinterpret_cast<const f32x4*>(g + (int64_t)min(w + k, a.W - 1) * SQ + RS * i * MP);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < AHEAD; ++k)
         if (w + k < a.W) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] += part[k][i];
+          for (int i = 0; i < NI; ++i) v[i] += part[k][i];
         }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = r0 + 16 * i, k = r - c;   // the diagonal is value k of this thread, if 0 <= k < 4
+    for (int i = 0; i < NI; ++i) {
+      const int r = r0 + RS * i, k = r - c;   // the diagonal is value k of this thread, if 0 <= k < 4
       uint32_t o[4];
       float d = 0.f;
 #pragma unroll
@@ -729,22 +810,23 @@ __global__ void __launch_bounds__(256) ortho_narrow_kernel(NarrowArgs a) {
         o[h] = f32_to_f16(k == h ? 0.f : w * a.sa);
       }
       if ((unsigned)k < 4u) s_d[r] = d;
-      *reinterpret_cast<uint2*>(s_o + tile::lds_off<64>(r, c / 8) + c % 8) =
+      *reinterpret_cast<uint2*>(s_o + tile::lds_off<MP>(r, c / 8) + c % 8) =
           make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
     }
     lds_barrier();
     // B: wave (wi, wj) the tile of 32 p by 32 q
     f32x16 acc = {};
 #pragma unroll
-    for (int st = 0; st < 4; ++st)
+    for (int st = 0; st < NK; ++st)
       acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(frag(s_o, 32 * wi + l32, st), frag(s_o, 32 * wj + l32, st), acc, 0,
                                                    0, 0);
+    const float sq = a.from_sa * a.from_sa;
     const int q = 32 * wj + l32;
-    const float dq = s_d[q], sq = a.from_sa * a.from_sa;
+    const float dq = s_d[q];
 #pragma unroll
     for (int g4 = 0; g4 < 4; ++g4) {
       const int p = 32 * wi + 8 * g4 + 4 * up;
-      const uint2 o = *reinterpret_cast<const uint2*>(s_o + tile::lds_off<64>(q, p / 8) + p % 8);
+      const uint2 o = *reinterpret_cast<const uint2*>(s_o + tile::lds_off<MP>(q, p / 8) + p % 8);
       const f32x4 dp = *reinterpret_cast<const f32x4*>(s_d + p);
       uint32_t b[4];
       float diag = 0.f;
@@ -756,19 +838,21 @@ __global__ void __launch_bounds__(256) ortho_narrow_kernel(NarrowArgs a) {
         b[h] = f32_to_f16(p + h == q ? 0.f : (a.cb * off + a.cc * (oo + (dp[h] + dq) * off)) * a.sb);
       }
       if ((unsigned)(q - p) < 4u) s_e[q] = a.ca + (a.cb * dq + a.cc * (diag + dq * dq));
-      *reinterpret_cast<uint2*>(s_b + tile::lds_off<64>(q, p / 8) + p % 8) =
+      *reinterpret_cast<uint2*>(s_b + tile::lds_off<MP>(q, p / 8) + p % 8) =
           make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
     }
     lds_barrier();
   }
   f32x16 gram = {};
+  uint32_t places[2][2];
+  narrow_places(s_x, {32 * wi, 32 * wj}, lane, places);
   for (int rb = 0; rb < a.rows; rb += kNarrowRows) {
-    const int64_t t = row0 + rb, at = x0 + (int64_t)rb * kNarrow;
+    const int64_t t = row0 + rb, at = x0 + (int64_t)rb * MP;
     float val[2][16];
     if constexpr (MODE == kNarrowStep) {
       f32x16 acc[2] = {};
 #pragma unroll
-      for (int st = 0; st < 4; ++st)
+      for (int st = 0; st < NK; ++st)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(frag(s_b, 32 * i + l32, st),
@@ -793,21 +877,26 @@ __global__ void __launch_bounds__(256) ortho_narrow_kernel(NarrowArgs a) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const bool in = t < a.n && 32 * i + 8 * (k / 4) + 4 * up + k % 4 < a.m;
-          val[i][k] = in ? (float)(u[i][k] * f) : 0.f;
-        }
+        for (int k = 0; k < 16; ++k) val[i][k] = (float)(u[i][k] * f);
     }
     if (rb + kNarrowRows < a.rows) request(rb + kNarrowRows);
     if (MODE == kNarrowStep && a.last) {
+      // past the matrix: an offset past the buffer, which stores nothing
+      const int64_t per = (int64_t)a.N * a.K;
+      const __amdgpu_buffer_rsrc_t r = buffer_rsrc(a.y + e * per, per * 2);
+      const uint32_t vo = (uint32_t)(a.wide ? 4 * up * a.K + (int)t : (int)t * a.K + 4 * up) * 2;
+      const int step = (a.wide ? a.K : 1) * 2;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int p = 32 * i + 8 * (k / 4) + 4 * up + k % 4;
-          if (t < a.n && p < a.m)
-            a.y[(int64_t)e * a.N * a.K + (a.wide ? (int64_t)p * a.K + t : t * a.K + p)] =
-                (uint16_t)f32_to_bf16_rne(val[i][k] * a.scale);
+        for (int k = 0; k < 16; k += 2) {
+          const uint32_t w = bf16_pack2(val[i][k] * a.scale, val[i][k + 1] * a.scale);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int p = 32 * i + 8 * (k / 4) + (k + h) % 4;
+            const uint32_t o = t < a.n && p + 4 * up < a.m ? vo : 0x80000000u;
+            __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(w >> (16 * h)), r, o, p * step, 0);
+          }
         }
       continue;
     }
@@ -823,34 +912,30 @@ __global__ void __launch_bounds__(256) ortho_narrow_kernel(NarrowArgs a) {
       i32x4 h = __builtin_bit_cast(i32x4, hi), l = __builtin_bit_cast(i32x4, lo);
 #pragma unroll
       for (int g2 = 0; g2 < 2; ++g2)
-        *reinterpret_cast<int2*>(s_x + tile::wt_off_n<64>(tl, 16 * st + 8 * g2 + 4 * up)) = make_int2(h[2 * g2], h[2 * g2 + 1]);
+        *reinterpret_cast<int2*>(s_x + tile::wt_off_n<MP>(tl, 16 * st + 8 * g2 + 4 * up)) =
+            make_int2(h[2 * g2], h[2 * g2 + 1]);
       halves_to_groups(h);
       halves_to_groups(l);
       *reinterpret_cast<i32x4*>(a.hi + at + 16 * st + 8 * up) = h;
       *reinterpret_cast<i32x4*>(a.lo + at + 16 * st + 8 * up) = l;
     }
     lds_barrier();
-#pragma unroll
-    for (int st = 0; st < kNarrowRows / 16; st += 2) {
-      f16x8 fr[4];
-      narrow_frags(s_x, 32 * wi, 32 * wj, 16 * st, lane, fr);
-      gram = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr[0], fr[1], gram, 0, 0, 0);
-      gram = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr[2], fr[3], gram, 0, 0, 0);
-    }
+    narrow_gram<0>(places, gram);
     lds_barrier();
   }
   if (MODE == kNarrowStep && a.last) return;
-  float* g = a.gout + ((int64_t)e * a.W + wg) * (kNarrow * kNarrow) + (32 * wj + l32) * kNarrow + 32 * wi + 4 * up;
+  float* g = a.gout + ((int64_t)e * a.W + wg) * SQ;
 #pragma unroll
   for (int g4 = 0; g4 < 4; ++g4)
-    *reinterpret_cast<f32x4*>(g + 8 * g4) =
+    *reinterpret_cast<f32x4*>(g + (32 * wj + l32) * MP + 32 * wi + 8 * g4 + 4 * up) =
         (f32x4){gram[4 * g4], gram[4 * g4 + 1], gram[4 * g4 + 2], gram[4 * g4 + 3]};
 }
 
-// Rows of a workgroup: 256, or what leaves 16 workgroups, whose parts of A each of
-// them adds.
-int64_t narrow_rows(int64_t n) {
-  const int64_t r = (n + 15) / 16;
+// Rows of a workgroup: two rounds, or what leaves 16 workgroups (whose parts of A
+// each of them adds) and not many more than there are CUs.
+int64_t narrow_rows(int64_t E, int64_t n) {
+  const int64_t by_cus = (256 + E - 1) / E, W = by_cus < 16 ? by_cus : 16;
+  const int64_t r = (n + W - 1) / W;
   const int64_t rows = (r + kNarrowRows - 1) / kNarrowRows * kNarrowRows;
   if (n <= kNarrowRows) return kNarrowRows;
   return rows < 2 * kNarrowRows ? 2 * kNarrowRows : rows;
@@ -866,9 +951,28 @@ int tile_of(int64_t E, int64_t n, int64_t m) {
   return 64;
 }
 
+// Tiles of the symmetric products: as large as the padding allows and half the CUs
+// have one of (32 of 512 x 2048: 96 tiles of 256 956 us, 320 of 128 905; 4 of 1024 x
+// 2048: 144 tiles of 128 379 us, of 64 387).
+int symmetric_tile(int64_t E, int64_t mp, int most) {
+  int T = most;
+  while (T > 64 && E * (mp / T) * (mp / T + 1) / 2 < 128) T /= 2;
+  return T;
+}
+
+// Workgroups that share the contraction of a tile of A, of 8 slices at least and three
+// of them (128 x 4096: 8 of them 109 us, one 172; 512 x 2048: 4 134, one 155; but two
+// for 1000 x 1000 170, one 165; of 4 slices 512 x 2048 155).
+int gram_splits(int64_t E, int64_t np, int64_t mp) {
+  const int64_t tiles = E * (mp / 64) * (mp / 64 + 1) / 2, by_cus = 512 / tiles, by_slices = np / kBK / 8;
+  const int64_t s = by_cus < by_slices ? by_cus : by_slices;
+  return (int)(s < 3 ? 1 : s > 16 ? 16 : s);
+}
+
 struct Layout {
   int T;                  // 0: narrow
-  int64_t np, mp, W, hi[2], lo[2], xt, a, b, da, db, part, end;
+  int Ts, splits;         // tiles of the symmetric products; of A, if 64
+  int64_t np, mp, W, hi[2], lo[2], xt, a, b, da, db, part, gpart, gdone, end;
 };
 
 Layout layout(int64_t E, int64_t N, int64_t K) {
@@ -882,10 +986,10 @@ Layout layout(int64_t E, int64_t N, int64_t K) {
   };
   L.part = take(8 * E * kOrthoNormBlocks);
   if (m <= kNarrow) {
-    const int64_t rows = narrow_rows(n);
+    L.mp = kNarrow;
+    const int64_t rows = narrow_rows(E, n);
     L.W = (n + rows - 1) / rows;
     L.np = L.W * rows;
-    L.mp = kNarrow;
     L.hi[0] = take(2 * E * L.np * L.mp);
     L.lo[0] = take(2 * E * L.np * L.mp);
     L.a = take(4 * E * L.W * L.mp * L.mp);   // parts of A, of this step and of the next
@@ -896,6 +1000,8 @@ Layout layout(int64_t E, int64_t N, int64_t K) {
   L.T = tile_of(E, n, m);
   L.np = (n + L.T - 1) / L.T * L.T;
   L.mp = (m + L.T - 1) / L.T * L.T;
+  L.Ts = symmetric_tile(E, L.mp, L.T);
+  L.splits = L.Ts == 64 ? gram_splits(E, L.np, L.mp) : 1;
   for (int i = 0; i < 2; ++i) {
     L.hi[i] = take(2 * E * L.np * L.mp);
     L.lo[i] = take(2 * E * L.np * L.mp);
@@ -905,6 +1011,11 @@ Layout layout(int64_t E, int64_t N, int64_t K) {
   L.b = take(2 * E * L.mp * L.mp);
   L.da = take(4 * E * L.mp);
   L.db = take(4 * E * L.mp);
+  if (L.splits > 1) {
+    const int64_t tiles = E * (L.mp / 64) * (L.mp / 64 + 1) / 2;
+    L.gpart = take(4 * tiles * L.splits * 64 * 64);
+    L.gdone = take(4 * tiles);
+  }
   L.end = at;
   return L;
 }
@@ -1032,6 +1143,11 @@ hipError_t launch_orthogonalize(const OrthoArgs& o, hipStream_t st) {
   M.b = reinterpret_cast<uint16_t*>(ws + L.b);
   M.da = reinterpret_cast<float*>(ws + L.da);
   M.db = reinterpret_cast<float*>(ws + L.db);
+  if (L.splits > 1) {
+    M.gpart = reinterpret_cast<float*>(ws + L.gpart);
+    M.gdone = reinterpret_cast<int32_t*>(ws + L.gdone);
+    M.gtiles = (int32_t)(o.E * (L.mp / 64) * (L.mp / 64 + 1) / 2);
+  }
   {
     const dim3 gi((unsigned)(o.E * (L.np / 64) * (L.mp / 64)));
     const float sc = pow2(s[0][0]);
@@ -1050,6 +1166,7 @@ hipError_t launch_orthogonalize(const OrthoArgs& o, hipStream_t st) {
   a.wide = wide;
   a.vec = o.K % 8 == 0 && ((uintptr_t)o.out & 15) == 0;
   a.scale = o.scale;
+  a.splits = L.splits;
   for (int i = 0; i < o.steps; ++i) {
     const int sx = s[i][0], sa = s[i][1], sb = s[i][2];
     a.cur = i & 1;
@@ -1059,11 +1176,11 @@ hipError_t launch_orthogonalize(const OrthoArgs& o, hipStream_t st) {
     a.cc = o.coef[i][2];
     a.in = pow2(-2 * sx);
     a.out = pow2(sa);
-    if ((e = product<kGram>(a, L.T, st)) != hipSuccess) return e;
+    if ((e = product<kGram>(a, L.Ts, st)) != hipSuccess) return e;
     a.in = pow2(-2 * sa);
     a.out = pow2(sb);
     a.aux = pow2(-sa);
-    if ((e = product<kSquare>(a, L.T, st)) != hipSuccess) return e;
+    if ((e = product<kSquare>(a, L.Ts, st)) != hipSuccess) return e;
     a.in = pow2(-sx - sb);
     a.out = a.last ? 1.0f : pow2(s[i + 1][0]);
     a.aux = pow2(-sx);

@@ -204,3 +204,43 @@ def test_same_bits_again_and_on_another_stream():
         _, b, _ = run(u)
     torch.cuda.synchronize()
     assert np.array_equal(a, b)
+
+
+@gpu
+@pytest.mark.parametrize("E,N,K", [(1, 130, 4100), (2, 3001, 200), (1, 70, 1600), (3, 65, 2000), (40, 33, 700),
+                                   (300, 20, 40)])
+def test_long_contractions_and_many_narrow_matrices(E, N, K):
+    """A's tiles shared by several workgroups; narrow matrices with several workgroups each, or one."""
+    u, got, p = run(np.stack([matrix("gauss", N, K, s) for s in range(E)]))
+    for e in (0, E // 2, E - 1):
+        check(u[e], got[e], p, e)
+    _, again, _ = run(u)
+    assert np.array_equal(got, again)
+
+
+@gpu
+def test_workspace_serves_one_problem_after_another():
+    """Its contents do not matter: problems of different sizes in turn, on one workspace, give the bits they
+    give alone, and so do two streams with a workspace each."""
+    shapes = [(1, 128, 4096), (2, 64, 300), (1, 128, 4096), (3, 200, 256), (1, 130, 4100)]
+    probs, ins, want = [], [], []
+    for i, (E, N, K) in enumerate(shapes):
+        p = moe.make_ortho_problem(E, N, K)
+        t = torch.from_numpy(np.stack([matrix("gauss", N, K, 10 * i + s) for s in range(E)])).float().cuda()
+        out = torch.empty(t.shape, dtype=torch.bfloat16, device="cuda")
+        moe.moe_orthogonalize(p, t, out, moe.allocate_ortho_workspace(p))
+        probs.append(p), ins.append(t), want.append(out)
+    size = max(moe.moe_ortho_ws_bytes(p) for p in probs)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = []
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+            for p, t in zip(probs, ins):
+                out = torch.empty(t.shape, dtype=torch.bfloat16, device="cuda")
+                moe.moe_orthogonalize(p, t, out, ws)
+                outs.append((out, ws))
+    torch.cuda.synchronize()
+    for i, (out, _) in enumerate(outs):
+        assert torch.equal(out, want[i % len(want)])
