@@ -140,23 +140,27 @@ __global__ void __launch_bounds__(256) ortho_input_kernel(const void* u, int N, 
 #pragma unroll
   for (int d = 32; d; d >>= 1) s += __shfl_xor(s, d);
   const double f = scale / (sqrt(s) + eps);
-  // the pieces in U's own order
+  // the pieces in U's own order; all values requested before the first is stored
   const int64_t base = (int64_t)e * N * K;
   const int64_t at = (int64_t)e * np * mp;
-  for (int i = wave; i < 64; i += 4) {
-    const int r = r0 + i, c = c0 + lane;
-    float v = 0.f;
-    if (r < N && c < K) {
-      const int64_t p = base + (int64_t)r * K + c;
-      v = (float)((BF16 ? bf16_to_f32(static_cast<const uint16_t*>(u)[p]) : static_cast<const float*>(u)[p]) * f);
-    }
-    s_v[i][lane] = v;
-    const uint32_t h = f32_to_f16(v);
+  float v[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const int r = min(r0 + wave + 4 * k, N - 1), c = min(c0 + lane, K - 1);   // past the matrix: not taken
+    const int64_t p = base + (int64_t)r * K + c;
+    v[k] = BF16 ? bf16_to_f32(static_cast<const uint16_t*>(u)[p]) : static_cast<const float*>(u)[p];
+  }
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const int i = wave + 4 * k, r = r0 + i, c = c0 + lane;
+    const float x = r < N && c < K ? (float)(v[k] * f) : 0.f;
+    s_v[i][lane] = x;
+    const uint32_t h = f32_to_f16(x);
     if (wide) {
       M.xt[at + (int64_t)r * np + c] = (uint16_t)h;
     } else {
       M.hi[0][at + (int64_t)r * mp + c] = (uint16_t)h;
-      M.lo[0][at + (int64_t)r * mp + c] = (uint16_t)f32_to_f16((v - f16_to_f32(h)) * kLow);
+      M.lo[0][at + (int64_t)r * mp + c] = (uint16_t)f32_to_f16((x - f16_to_f32(h)) * kLow);
     }
   }
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < M.gtiles; i += (int64_t)gridDim.x * 256) M.gdone[i] = 0;
