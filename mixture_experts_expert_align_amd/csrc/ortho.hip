@@ -945,23 +945,41 @@ int64_t narrow_rows(int64_t E, int64_t n) {
   return rows < 2 * kNarrowRows ? 2 * kNarrowRows : rows;
 }
 
-// What m and n are padded to: tiles of 256 where they fill the CUs and the
-// padding costs little.
-int tile_of(int64_t E, int64_t n, int64_t m) {
-  for (int T = 256; T > 64; T /= 2) {
-    const int64_t nm = (m + T - 1) / T, nn = (n + T - 1) / T;
-    if (E * nm * nn >= 192 && nm * T <= m + m / 8) return T;
-  }
-  return 64;
+// Time of a slice of `tiles` tiles of T over 256 CUs, in that of a tile of 256 alone on
+// its CU (1.3 us): a smaller tile has room for 2 or 4 on a CU and costs more for its
+// size.  (16 of 1536 x 4096, the products for A: 336 tiles of 256 240 us, 1248 of 128
+// 201, 4992 of 64 309; 8 of 4096 x 6144: 1088 of 256 827 us, 4224 of 128 866; X B of
+// the latter: 3072 of 256 1523 us, 12288 of 128 1895.)
+double slice_time(int T, int64_t tiles) {
+  const double q = (double)((tiles + 255) / 256);
+  if (T == 256) return q;
+  const double alone = T == 128 ? 0.35 : 0.2, each = T == 128 ? 0.295 : 0.13;
+  return q * each > alone ? q * each : alone;
 }
 
-// Tiles of the symmetric products: as large as the padding allows and half the CUs
-// have one of (32 of 512 x 2048: 96 tiles of 256 956 us, 320 of 128 905; 4 of 1024 x
-// 2048: 144 tiles of 128 379 us, of 64 387).
+// What m and n are padded to, and the tiles of X B.
+int tile_of(int64_t E, int64_t n, int64_t m) {
+  int best = 0;
+  double least = 0.0;
+  for (int T = 64; T <= 256; T *= 2) {
+    const int64_t nm = (m + T - 1) / T, nn = (n + T - 1) / T;
+    const double time = slice_time(T, E * nm * nn) * (double)(nm * T);
+    if (best == 0 || time < least) {
+      best = T;
+      least = time;
+    }
+  }
+  return best;
+}
+
+// Tiles of the symmetric products, as the padding allows.
 int symmetric_tile(int64_t E, int64_t mp, int most) {
-  int T = most;
-  while (T > 64 && E * (mp / T) * (mp / T + 1) / 2 < 128) T /= 2;
-  return T;
+  int best = 64;
+  for (int T = 128; T <= most; T *= 2) {
+    auto time = [&](int t) { return slice_time(t, E * (mp / t) * (mp / t + 1) / 2); };
+    if (time(T) < time(best)) best = T;
+  }
+  return best;
 }
 
 // Workgroups that share the contraction of a tile of A, of 8 slices at least and three
