@@ -631,8 +631,10 @@ int moe_lora_wgrad(const moe_lora_problem* p, const void* x, const void* dy, con
  * and 0 throughout for T_s = 0.  The choice is held fixed: no gradient passes
  * through the counts.  groups, topk_groups, renormalize, scale and a bias for
  * the choice only (MOE_ROUTE_BIAS_SELECT: pass bias as for moe_route_topk) play
- * no part.  Everything is computed in float32, sums over many tokens in
- * float64, in a fixed order: the same bits on every run.
+ * no part (with MOE_ROUTE_BIAS_LOGIT the bias's gradient is dlogits' column sum).
+ * Computed in float32, sums over many tokens in float64, in a fixed order: the
+ * same bits on every run of the same call (operands aligned otherwise may be read
+ * in another order, which the last bits of a row's sum can show).
  * ------------------------------------------------------------------------- */
 
 /* Bytes of moe_balance_loss's workspace for M tokens in S sequences; -1 for
@@ -750,8 +752,9 @@ int moe_block_norm_backward(const moe_norm_problem* p, const void* x_out, const 
  * off-diagonal parts, all scaled by powers of two to float16's range; the norm
  * is summed in float64.  With five steps of (3.4445, -4.775, 2.0315) the result
  * is within 2e-3 of the exact one (2-norm, relative) before its rounding to
- * bf16 for matrices of Gaussian, low-rank and decaying spectra.  A matrix with
- * a NaN or an infinity gives NaN in all of its own out; a zero matrix gives
+ * bf16 for matrices of Gaussian, low-rank and decaying spectra; what eps (or a
+ * value beside far larger ones) leaves below 2^-48 in X counts as 0.  A matrix
+ * with a NaN or an infinity gives NaN in all of its own out; a zero matrix gives
  * zeros.
  * ------------------------------------------------------------------------- */
 #define MOE_ORTHO_MAX_STEPS 16

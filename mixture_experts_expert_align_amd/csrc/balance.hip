@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(64 * kSumWaves) balance_sums_kernel(BalanceArg
   __shared__ int s_c[kSumRows][kBalanceExperts];
   __shared__ int s_t[kSumWaves];
   const int nb = (a.E + kBalanceExperts - 1) / kBalanceExperts;
-  const int s = blockIdx.x / nb, b = blockIdx.x % nb;
+  const int s = a.s0 + (int)(blockIdx.x / nb), b = blockIdx.x % nb;
   const int col = threadIdx.x % kBalanceExperts, row = threadIdx.x / kBalanceExperts;
   const int e = b * kBalanceExperts + col;
   const int64_t lo = seq_offset(a, s), hi = seq_offset(a, s + 1);
@@ -556,7 +556,8 @@ hipError_t by_experts(const BalanceArgs& a, hipStream_t s) {
 
 // Tokens of a workgroup of the first launch: at most 512 workgroups, whose parts
 // the second has to add (65536 x 256, both launches: 512 workgroups 20.6 us, 1024
-// 21.5, 2048 26.2), of 16 tokens at least (8192 x 128: 10.9 us, of 32 12.1).
+// 21.5, 2048 26.2), of 16 tokens at least (8192 x 128: 10.9 us, of 32 12.1), and of
+// 4096 at most, whatever their number, since a chunk is summed in float32.
 // Up to four rounds of a workgroup's tokens are left to one workgroup (64 x 8,
 // loss and gradient, host included: 16.8 us, in two launches 19.5).
 static int64_t one_workgroup(int64_t E) { return 4 * (kThreads / (E <= 512 ? 16 : 64)); }
@@ -564,18 +565,24 @@ static int64_t one_workgroup(int64_t E) { return 4 * (kThreads / (E <= 512 ? 16 
 int32_t balance_chunk(int64_t M, int64_t E) {
   if (M <= one_workgroup(E)) return (int32_t)one_workgroup(E);
   const int64_t c = ((M + 511) / 512 + 15) / 16 * 16;
-  return (int32_t)(c < 16 ? 16 : c);
+  return (int32_t)(c < 16 ? 16 : c > 4096 ? 4096 : c);
 }
 
 // One workgroup also clears the outputs of all sequences: not too many of them.
 bool balance_one(int64_t M, int64_t E, int64_t S) { return M <= one_workgroup(E) && S * E <= 8192; }
 
-hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
-  const hipError_t e = by_experts<Forward>(a, s);
+hipError_t launch_balance(BalanceArgs a, hipStream_t s) {
+  hipError_t e = by_experts<Forward>(a, s);
   if (e != hipSuccess || a.one) return e;
-  const int64_t nb = (a.E + kBalanceExperts - 1) / kBalanceExperts;
-  hipLaunchKernelGGL(balance_sums_kernel, dim3((unsigned)(nb * a.S)), dim3(64 * kSumWaves), 0, s, a);
-  return hipGetLastError();
+  // whole sequences, and fewer than 2^32 threads, to a launch
+  const int64_t nb = (a.E + kBalanceExperts - 1) / kBalanceExperts, most = (1 << 21) / nb, S = a.S;
+  for (int64_t s0 = 0; s0 < S && e == hipSuccess; s0 += most) {
+    a.s0 = (int32_t)s0;
+    const int64_t n = S - s0 < most ? S - s0 : most;
+    hipLaunchKernelGGL(balance_sums_kernel, dim3((unsigned)(nb * n)), dim3(64 * kSumWaves), 0, s, a);
+    e = hipGetLastError();
+  }
+  return e;
 }
 
 hipError_t launch_balance_backward(const BalanceArgs& a, hipStream_t s) { return by_experts<Backward>(a, s); }

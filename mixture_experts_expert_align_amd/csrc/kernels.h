@@ -347,12 +347,13 @@ struct BalanceArgs {
   void* dlogits;
   int64_t dld;
   int32_t accumulate;
-  int64_t t0;                  // set by the launcher: first token of a launch
+  int64_t t0;                  // set by the launcher: first token of a launch,
+  int32_t s0;                  // first sequence of a launch
 };
 
 int32_t balance_chunk(int64_t M, int64_t E);
 bool balance_one(int64_t M, int64_t E, int64_t S);
-hipError_t launch_balance(const BalanceArgs& a, hipStream_t s);
+hipError_t launch_balance(BalanceArgs a, hipStream_t s);
 hipError_t launch_balance_backward(const BalanceArgs& a, hipStream_t s);
 
 // ----------------------------------------------------------------- norm ----

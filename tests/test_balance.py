@@ -273,3 +273,118 @@ def test_sequences_do_not_see_each_other():
     for x, y in zip(a[:4], b[:4]):
         assert np.array_equal(x[1:], y[1:])
     assert torch.equal(a[4][90:], b[4][90:])
+
+
+@gpu
+def test_many_empty_sequences():
+    """More sequences than one workgroup clears by itself, nearly all of them empty."""
+    l, ids, _ = make(50, 16, 2, 1, torch.float32, 17)
+    off = np.sort(np.concatenate([[0], np.repeat([3, 20, 47], 300), [50]])).astype(np.int32)
+    check(l, ids, off)
+    l, ids, _ = make(700, 16, 2, 1, torch.bfloat16, 18)
+    off = np.sort(np.concatenate([[0], np.repeat([1, 2, 350, 699], 200), [700]])).astype(np.int32)
+    check(l, ids, off, "sigmoid")
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E", [64, 128])
+def test_operands_off_the_wide_alignment(dtype, E):
+    """Logits, gradient or counts aligned to their elements only, each against 64 bits.  A lane then holds
+    other experts of the row, so a row's sum is added in another order: each result is within the bounds of
+    `balance` (whose sum of up to 38 steps holds for any order), and two need not be the same bits."""
+    l, ids, _ = make(40, E, 3, 1, dtype, 19)
+    dloss = np.ones(1, np.float32)
+    lh = l.float().cpu().numpy().astype(np.float64)
+    rl, rc, rt, rp, tol = balance(lh, ids, [0, 40], "softmax")
+    tol = tol + rp * U24 * (48 / 4 + 10) + 1e-37
+    rd, bound = balance_backward(lh, ids, [0, 40], "softmax", rc, rt, dloss.astype(np.float64))
+    bound = bound + (2.0 ** -8 if dtype == torch.bfloat16 else U24) * np.abs(rd)
+
+    def right(result):
+        loss, counts, tokens, probs, dl = result
+        assert np.array_equal(counts, rc) and np.array_equal(tokens, rt)
+        assert np.all(np.abs(probs - rp) <= tol)
+        assert np.all(np.abs(loss - rl) <= E / (3 * rt) * (rc * tol).sum(1) + 2 * U24 * np.abs(rl))
+        gradient(dl)
+
+    def gradient(dl):
+        assert np.all(np.abs(dl.float().cpu().numpy().astype(np.float64) - rd) <= bound)
+
+    def shifted(t):
+        b = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+        v = b[1:].view(t.shape)
+        v.copy_(t)
+        return v
+    want = run(l, ids, [0, 40], "softmax", dloss=dloss)
+    right(want)
+    off = shifted(l)
+    first = run(off, ids, [0, 40], "softmax", dloss=dloss)
+    right(first)
+    again = run(off, ids, [0, 40], "softmax", dloss=dloss)     # the same call again: the same bits
+    assert all(np.array_equal(a, b) for a, b in zip(first[:4], again[:4])) and torch.equal(first[4], again[4])
+    gradient(run(l, ids, [0, 40], "softmax", dloss=dloss, dl=shifted(torch.empty_like(l)))[4])
+    r = moe.make_router(E, 3)
+    i32 = torch.from_numpy(want[1].astype(np.int32)).cuda()
+    dl = torch.empty_like(l)
+    moe.moe_balance_loss_backward(r, l, torch.from_numpy(ids).cuda(), shifted(i32),
+                                  torch.from_numpy(want[2].astype(np.int32)).cuda(), torch.ones(1, device="cuda"), dl)
+    gradient(dl)
+
+
+@gpu
+def test_more_sequences_than_one_launch_takes():
+    """65536 sequences of 2048 experts: 2^33 threads' worth of sums; three sequences hold the tokens."""
+    E, topk, S, M, full = 2048, 2, 65536, 24, [0, 20000, 65535]
+    l, ids, _ = make(M, E, topk, 1, torch.bfloat16, 23)
+    ends = [0, 9, 10, M]
+    off = np.zeros(S + 1, np.int32)
+    for i, s in enumerate(full):
+        off[s + 1:] = ends[i + 1]
+    lh = l.float().cpu().numpy().astype(np.float64)
+    rl, rc, rt, rp, tol = balance(lh, ids, ends, "softmax")
+    tol = tol + rp * U24 * (48 / 4 + 10) + 1e-37
+    r = moe.make_router(E, topk)
+    d_ids, d_off = torch.from_numpy(ids).cuda(), torch.from_numpy(off).cuda()
+    loss, tokens = torch.full((S,), 7.0, device="cuda"), torch.full((S,), 77, dtype=torch.int32, device="cuda")
+    counts = torch.full((S, E), 77, dtype=torch.int32, device="cuda")
+    probs = torch.full((S, E), 7.0, device="cuda")
+    moe.moe_balance_loss(r, l, d_ids, loss, counts, tokens, probs, moe.allocate_balance_workspace(r, M, S),
+                         seq_offsets=d_off)
+    assert np.array_equal(counts[full].cpu().numpy(), rc) and np.array_equal(tokens[full].cpu().numpy(), rt)
+    assert np.all(np.abs(probs[full].double().cpu().numpy() - rp) <= tol)
+    per = E / (topk * rt)
+    assert np.all(np.abs(loss[full].double().cpu().numpy() - rl) <= per * (rc * tol).sum(1) + 2 * U24 * np.abs(rl))
+    dl = torch.full_like(l, float("nan"))
+    moe.moe_balance_loss_backward(r, l, d_ids, counts, tokens, torch.ones(S, device="cuda"), dl, seq_offsets=d_off)
+    rd, bound = balance_backward(lh, ids, ends, "softmax", rc, rt, np.ones(3))
+    assert np.all(np.abs(dl.double().cpu().numpy() - rd) <= bound + 2.0 ** -8 * np.abs(rd))
+    for t in (loss, tokens, counts, probs):    # the empty ones
+        t[full] = 0
+        assert not t.any()
+
+
+@gpu
+def test_more_tokens_than_one_launch_takes():
+    """2^25 + 3 tokens of two experts: the ends of the gradient, and the sums."""
+    M = (1 << 25) + 3
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    l = torch.randn(M, 2, generator=g, device="cuda")
+    ids = (torch.rand(M, 1, generator=g, device="cuda") < 0.3).to(torch.int32)
+    r = moe.make_router(2, 1)
+    loss, tokens = torch.empty(1, device="cuda"), torch.empty(1, dtype=torch.int32, device="cuda")
+    counts, probs = torch.empty(1, 2, dtype=torch.int32, device="cuda"), torch.empty(1, 2, device="cuda")
+    moe.moe_balance_loss(r, l, ids, loss, counts, tokens, probs, moe.allocate_balance_workspace(r, M))
+    one = ids.sum(dtype=torch.int64).item()
+    assert tokens.item() == M and counts[0].tolist() == [M - one, one]
+    mean = torch.softmax(l.double(), 1).mean(0)
+    # 56 half steps of a score, and of a chunk's 4096 tokens 4096 / 4 + 8 more
+    assert ((probs[0].double() - mean).abs() <= (80 + 4096 / 4 + 10) * U24 * mean).all()
+    dl = torch.empty_like(l)
+    moe.moe_balance_loss_backward(r, l, ids, counts, tokens, torch.ones(1, device="cuda"), dl)
+    for s in (slice(0, 5), slice((1 << 25) - 4, M)):
+        p = torch.softmax(l[s].double(), 1)
+        c = counts[0].double()
+        want = 2.0 / M ** 2 * p * (c - (c * p).sum(1, keepdim=True))
+        assert ((dl[s].double() - want).abs() <= 300 * U24 * (2.0 / M ** 2 * p * (c[0] - c[1]).abs())).all()
