@@ -312,3 +312,10 @@ def test_offsets_past_32_bits():
     _, _, r, e = norm_forward(f64(x[-3:]), None, None, 1.0, np.ones(K), 1e-6, 1.0)
     within(h[-3:], r, e, 2.0 ** -8)
     assert not h[:100].any() and not h[70000:70100].any()
+
+
+@gpu
+@pytest.mark.parametrize("M,K", [(600, 16384), (530, 9000)])
+def test_many_long_rows(M, K):
+    check(M, K, gate="channel", seed=M)
+    check(M, K, torch.float32, torch.bfloat16, gate="token", seed=M + 1)

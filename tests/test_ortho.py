@@ -244,3 +244,21 @@ def test_workspace_serves_one_problem_after_another():
     torch.cuda.synchronize()
     for i, (out, _) in enumerate(outs):
         assert torch.equal(out, want[i % len(want)])
+
+
+@gpu
+@pytest.mark.parametrize("E,N,K", [(2, 64, 40), (2, 40, 64), (2, 96, 200), (2, 200, 96), (1, 32768, 8), (1, 3, 32768),
+                                   (2000, 3, 2)])
+def test_out_and_update_aligned_to_their_elements(E, N, K):
+    for dtype in (torch.float32, torch.bfloat16):
+        u = np.stack([matrix("gauss", N, K, s % 7) for s in range(E)])
+        t, want, p = run(u, dtype)
+        src = torch.empty(t.size + 1, dtype=dtype, device="cuda")[1:].view(E, N, K)
+        src.copy_(torch.from_numpy(t))
+        buf = torch.full((t.size + 66,), 3.0, dtype=torch.bfloat16, device="cuda")
+        out = buf[1:1 + t.size].view(E, N, K)
+        moe.moe_orthogonalize(p, src, out, moe.allocate_ortho_workspace(p))
+        assert np.array_equal(out.double().cpu().numpy(), want)
+        assert buf[0] == 3 and (buf[1 + t.size:] == 3).all()
+    for e in (0, E - 1):
+        check(t[e], want[e], p, e)
