@@ -690,7 +690,7 @@ typedef struct moe_norm_problem {
   int32_t x_dtype;      /* x, x' and their gradients: 0 float32, 1 bf16        */
   int32_t w_dtype;      /* w_post, w_pre and a gate per channel: 0 float32, 1 bf16 */
   int32_t gate_kind;    /* MOE_GATE_*                                          */
-  float eps;            /* > 0, finite                                         */
+  float eps;            /* 2^-126 or more, finite                              */
   float res_scale;      /* finite                                              */
 } moe_norm_problem;
 

@@ -1090,7 +1090,8 @@ static int norm_ok(const moe_norm_problem* p) {
   if (!p || p->M < 0 || p->M >= (1ll << 31) || p->K <= 0) return MOE_EINVAL;
   if ((p->x_dtype != 0 && p->x_dtype != 1) || (p->w_dtype != 0 && p->w_dtype != 1)) return MOE_EINVAL;
   if (p->gate_kind < MOE_GATE_NONE || p->gate_kind > MOE_GATE_TOKEN) return MOE_EINVAL;
-  if (!(p->eps > 0.0f) || !finite_f32(p->eps) || !finite_f32(p->res_scale)) return MOE_EINVAL;
+  // (the kernels' reciprocal square root takes a subnormal value as 0)
+  if (!(p->eps >= 0x1p-126f) || !finite_f32(p->eps) || !finite_f32(p->res_scale)) return MOE_EINVAL;
   if (p->K % 8 || p->K > kNormMaxK) return MOE_EUNSUPPORTED;
   return MOE_OK;
 }

@@ -957,7 +957,7 @@ int64_t narrow_rows(int64_t E, int64_t n) {
 // its CU (1.3 us): a smaller tile has room for 2 or 4 on a CU and costs more for its
 // size.  (16 of 1536 x 4096, the products for A: 336 tiles of 256 240 us, 1248 of 128
 // 201, 4992 of 64 309; 8 of 4096 x 6144: 1088 of 256 827 us, 4224 of 128 866; X B of
-// the latter: 3072 of 256 1523 us, 12288 of 128 1895.)
+// the latter in tiles of 256 1523 us, of 128 1895.)
 double slice_time(int T, int64_t tiles) {
   const double q = (double)((tiles + 255) / 256);
   if (T == 256) return q;

@@ -319,3 +319,27 @@ def test_offsets_past_32_bits():
 def test_many_long_rows(M, K):
     check(M, K, gate="channel", seed=M)
     check(M, K, torch.float32, torch.bfloat16, gate="token", seed=M + 1)
+
+
+def test_subnormal_eps_is_refused():
+    p = moe.make_norm_problem(4, 64)
+    # 8 bytes a column and workgroup; one takes all four rows
+    for eps, st in ((2.0 ** -127, -1), (1e-45, -1), (2.0 ** -126, 8 * 64)):
+        p.eps = eps
+        assert moe.load_library().moe_block_norm_ws_bytes(ctypes.byref(p)) == st
+
+
+@gpu
+def test_zero_rows_at_the_least_eps():
+    """1 / rms is 2^63 there, and 0 stays 0 in the results and the gradients."""
+    M, K = 3, 64
+    p = moe.make_norm_problem(M, K, x_dtype=torch.float32, eps=2.0 ** -126)
+    z, b = torch.zeros(M, K, device="cuda"), torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    w, x_out, h = torch.ones(K, device="cuda"), torch.full_like(z, 7.0), torch.full_like(b, 7.0)
+    moe.moe_block_norm(p, z, x_out, b, w, None, w, h)
+    assert not x_out.any() and not h.any()
+    dx, db = torch.full_like(z, 7.0), torch.full_like(b, 7.0)
+    dw = [torch.full_like(w, 7.0) for _ in range(2)]
+    moe.moe_block_norm_backward(p, x_out, z, dx, moe.allocate_norm_workspace(p), block=b, w_post=w, w_pre=w, dh=b,
+                                dblock=db, dw_post=dw[0], dw_pre=dw[1])
+    assert not any(t.any() for t in (dx, db, *dw))

@@ -262,3 +262,17 @@ def test_out_and_update_aligned_to_their_elements(E, N, K):
         assert buf[0] == 3 and (buf[1 + t.size:] == 3).all()
     for e in (0, E - 1):
         check(t[e], want[e], p, e)
+
+
+@gpu
+@pytest.mark.parametrize("E,N,K", [(4, 40, 700), (4, 700, 40), (4, 1, 5), (4, 3, 1), (20, 520, 640), (30, 1024, 600)])
+def test_not_finite_in_each_path(E, N, K):
+    """The one-launch steps, and the tiles of 64 and more: NaN in all of a bad matrix, none beside it."""
+    u = np.stack([matrix("gauss", N, K, s) for s in range(E)])
+    u[1, N - 1, 0] = np.nan
+    u[2, 0, K - 1] = -np.inf
+    for dtype in (torch.float32, torch.bfloat16):
+        x, got, p = run(u, dtype)
+        assert np.isnan(got[1]).all() and np.isnan(got[2]).all()
+        for e in (0, 3, E - 1):
+            check(x[e], got[e], p, e)
