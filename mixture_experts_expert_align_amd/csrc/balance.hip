@@ -415,9 +415,10 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(BalanceArgs 
     for (int e = threadIdx.x; e < NE; e += kThreads) s_b[e] = e < a.E ? a.bias[e] : 0.f;
     __syncthreads();
   }
-  // the first token's sequence, or one of the next few, or that of a search by itself
+  // the first token's sequence (-1: it lies before them all), or one of the next few, or
+  // that of a search by itself
   int s = seq_of(a, min(first, a.M - 1));
-  if (LANES < 64 && a.S > 1) {
+  if (LANES < 64 && a.offsets) {
     int k = 0;
     while (k < 4 && s + 1 < a.S && seq_offset(a, s + 1) <= in) ++s, ++k;
     if (k == 4) {
@@ -428,7 +429,7 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(BalanceArgs 
       }
       s = lo;
     }
-  } else if (a.S > 1) {
+  } else if (a.offsets) {
     s = seq_of(a, in);
   }
   const bool on = lanes_max<LANES>(any ? 1 : 0) != 0 && s >= 0 && in < seq_offset(a, s + 1);
