@@ -74,7 +74,8 @@ struct Raw {
 // The token's logits (plus a bias, LDS), its scores before their division by the
 // returned sum, and the largest logit.  Nothing is done about special values
 // until they show: with a NaN, a +inf or no expert at all the sum is not a
-// positive number, and a sigmoid's whole row may underflow where none is
+// positive number, past 2^29 the products with log2(e) are off by more than
+// exponentials hold, and a sigmoid's whole row may underflow where none is
 // positive; then, and only then, the row is taken again with the logits that
 // compete (-inf for one that cannot be chosen, +inf as the largest float32) and
 // sigmoids times e^-min(top, 0), which their quotient does not see.
@@ -120,8 +121,10 @@ __device__ __forceinline__ float token_scores(const Raw<S>& r, int c, bool add, 
     }
   }
   s = lanes_sum<S::LANES>(s);
-  // (decided by the token, not by its wave: its bits are its own)
-  if (s > 0.f && s < INFINITY && fabsf(top) < 1e30f && (!sigmoid || top > 0.f)) return s;
+  // (decided by the token, not by its wave: its bits are its own.  Under 2^29 the
+  // rounding of top log2(e) is 2^5 at most, so the sum lies between 2^-32 and 2^43 and
+  // has a reciprocal; at 2 10^9 it reached 2^127, whose reciprocal is subnormal, taken as 0)
+  if (s > 0.f && s < INFINITY && fabsf(top) < 0x1p29f && (!sigmoid || top > 0.f)) return s;
   top = -INFINITY;
 #pragma unroll
   for (int i = 0; i < S::NV; ++i) {

@@ -38,3 +38,27 @@ def test_one_sequence_that_begins_inside_a_workgroup(E, dtype, scoring):
         else:   # one rounding of the sum; the addend there is not rounded
             err = (got.double() - base.double() - plain.double()).abs()
             assert (err <= 2.0 ** -8 * (got.double().abs() + plain.double().abs()) + 1e-37).all()
+
+
+@gpu
+@pytest.mark.parametrize("E", [8, 100, 600])
+def test_logits_of_a_billion_and_more(E):
+    """Rows of equal or nearly equal logits t: the float32 product of t and log2(e) is off by 2^-24 of itself,
+    up to 2^6 at 10^9 and 2^8 at 5 10^9, which must not meet an exponential's range.  A token a sequence, so
+    probs are its scores."""
+    top = [-2.06e9, -2.68e9, -6.19e9, -10.94e9, 5.58e9, 7.81e9, 14.79e9, -1e9, -1e10, 1e12, -1e29, 1e30, 3e38, -1e37,
+           2.0 ** 29, -2.0 ** 29, 2.0 ** 31, -2.0 ** 31, 3e8]
+    M = 2 * len(top)
+    l = np.repeat(np.array(top, np.float32), 2)[:, None] * np.ones((M, E), np.float32)
+    l[1::2, 1:] = -np.inf if E == 100 else -3e38      # every other row: one expert, the others far below
+    ids = np.stack([np.arange(M) % E, (np.arange(M) + 3) % E], 1).astype(np.int32)
+    dloss = np.ones(M, np.float32)
+    ref, _ = scores(l.astype(np.float64), "softmax")
+    loss, counts, tokens, probs, dl = run(torch.from_numpy(l).cuda(), ids, list(range(M + 1)), "softmax", dloss=dloss)
+    assert (tokens == 1).all() and (counts.sum(1) == 2).all()
+    # equal logits, equal scores: 56 half steps for the exponential, the sum and the quotient
+    assert np.all(np.abs(probs - ref) <= 56 * U24 * ref), np.abs(probs / np.maximum(ref, 1e-30) - 1).max()
+    assert np.all(np.abs(loss - E / 2 * (counts * ref).sum(1)) <= E / 2 * 60 * U24 * (counts * ref).sum(1))
+    want = E / 2 * ref * (counts - (counts * ref).sum(1, keepdims=True))
+    # |c - dot| and dot are at most 1 here: 56 half steps of p each, 44 of the sum, 10 of the rest
+    assert np.all(np.abs(dl.double().cpu().numpy() - want) <= E / 2 * ref * 2 * (56 + 56 + 44 + 10) * U24)
