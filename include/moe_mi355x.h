@@ -727,8 +727,9 @@ int64_t moe_block_norm_ws_bytes(const moe_norm_problem* p);
  * float32 [K] or [M]; each of the three may be NULL (not wanted) and must be
  * where its operand is.  accumulate = 0 writes the sums over the tokens (dw_pre,
  * dw_post, dgate per channel; +0.0 for M = 0), 1 adds the finished sums; a
- * gate's gradient per token is always written.  Sums in float32 in a fixed
- * order.  dx_out and w_pre must not both be NULL.  ws: device,
+ * gate's gradient per token is always written.  Sums over the tokens in float32
+ * over at most 512 rows (128 in turn, 4 side by side) and in float64 over those, in
+ * a fixed order.  dx_out and w_pre must not both be NULL.  ws: device,
  * moe_block_norm_ws_bytes, 16-byte aligned, contents of no matter; calls that
  * share it must not overlap.  Other outputs must not overlap inputs.  Errors as
  * for moe_block_norm. */

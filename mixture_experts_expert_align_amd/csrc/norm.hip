@@ -372,14 +372,15 @@ __global__ void __launch_bounds__(threads_of<TPR>()) norm_backward_kernel(NormAr
   }
 }
 
-// The workgroups' sums: 64 columns a workgroup, its waves sharing the parts.
+// The workgroups' sums, added in float64 (their number grows with M): 64 columns a
+// workgroup, its waves sharing the parts.
 constexpr int kJoinWaves = 16;
 
 __global__ void __launch_bounds__(64 * kJoinWaves) norm_join_kernel(NormArgs a, int nparts) {
-  __shared__ float s_v[kJoinWaves][64];
+  __shared__ double s_v[kJoinWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int i = blockIdx.x * 64 + lane;
-  float v = 0.f;
+  double v = 0.0;
   if (i < 2 * a.K) {
 #pragma unroll 8
     for (int p = wave; p < nparts; p += kJoinWaves) v += a.part[(int64_t)p * 2 * a.K + i];
@@ -387,10 +388,11 @@ __global__ void __launch_bounds__(64 * kJoinWaves) norm_join_kernel(NormArgs a, 
   s_v[wave][lane] = v;
   __syncthreads();
   if (wave != 0 || i >= 2 * a.K) return;
-  v = 0.f;
+  v = 0.0;
 #pragma unroll
   for (int w = 0; w < kJoinWaves; ++w) v += s_v[w][lane];
-  auto put = [&](float* out, int k, float f) {
+  auto put = [&](float* out, int k, double d) {
+    const float f = (float)d;
     if (out) out[k] = a.accumulate ? out[k] + f : f;
   };
   auto weight = [&](const void* p, int k) {
@@ -455,12 +457,17 @@ hipError_t backward_of(const NormArgs& a, int blocks, hipStream_t s) {
 // Workgroups of the backward, each with sums of its own that are added afterwards:
 // what is resident at once, one of 512 threads or two of 256 a CU (8192 x 4096
 // bf16: 512 workgroups 90 us, 256 107, 768 101; 8192 x 6144, whose rows take 512
-// threads: 256 workgroups 128 us, 512 134, 128 207).
+// threads: 256 workgroups 128 us, 512 134, 128 207).  A workgroup adds its rows in
+// float32, whose rounding may be off in one direction throughout (equal rows): n in
+// turn by up to n / 2 half steps of the sum.  So none takes more than kRun; past that
+// there are more rounds of workgroups (of 64 instead of 128 in turn 17000 x 6144 took
+// 259 us, not 248).
 int32_t norm_backward_blocks(int64_t M, int64_t K) {
+  constexpr int64_t kRun = 128;
   const int tpr = backward_tpr(K), rw = tpr < 256 ? 256 / tpr : 1;
   const int64_t rows = (M + rw - 1) / rw;
   const int64_t most = tpr <= 256 ? 512 : 256;
-  return (int32_t)(rows < most ? rows : most);
+  return (int32_t)(rows < most ? rows : (rows + most * kRun - 1) / (most * kRun) * most);
 }
 
 hipError_t launch_block_norm(const NormArgs& a, hipStream_t s) {

@@ -62,3 +62,24 @@ def test_logits_of_a_billion_and_more(E):
     want = E / 2 * ref * (counts - (counts * ref).sum(1, keepdims=True))
     # |c - dot| and dot are at most 1 here: 56 half steps of p each, 44 of the sum, 10 of the rest
     assert np.all(np.abs(dl.double().cpu().numpy() - want) <= E / 2 * ref * 2 * (56 + 56 + 44 + 10) * U24)
+
+
+@gpu
+@pytest.mark.parametrize("M,K,gate", [(1 << 20, 64, "channel"), (1 << 18, 1032, "none"), (1 << 16, 4104, "channel"),
+                                      (1 << 16, 9000, "none")])
+def test_sums_over_many_equal_rows(M, K, gate):
+    """Every row adds the same term, so a run of n float32 additions can be off in one direction by half a step of
+    the sum each, n / 2 half steps of the last.  The bound is block_refs' 100 half steps, whatever M."""
+    o = operands(1, K, torch.bfloat16, torch.float32, gate, True, True, K)
+    p = moe.make_norm_problem(M, K, gate_kind=GATE[gate])
+    rows = {n: o[n].expand(M, K).contiguous() for n in ("x", "block", "dx_out", "dh")}
+    sums = {n: torch.empty(K, device="cuda") for n in ("dw_post", "dw_pre") + (("dgate",) if gate != "none" else ())}
+    dx, db = torch.empty_like(rows["x"]), torch.empty_like(rows["x"])
+    moe.moe_block_norm_backward(p, rows["x"], rows["dx_out"], dx, moe.allocate_norm_workspace(p), rows["block"],
+                                o["w_post"], o["gate"], o["w_pre"], rows["dh"], db, **sums)
+    ref = norm_backward(f64(o["x"]), f64(o["block"]), f64(o["w_post"]), gate64(o, gate), f64(o["w_pre"]),
+                        f64(o["dx_out"]), f64(o["dh"]), p.eps, p.res_scale)
+    for n, got in sums.items():
+        want, err = ref["dgate_channel" if n == "dgate" else n]
+        within(got, M * want, M * err, 2.0 ** -24, n)
+    assert (dx == dx[0]).all() and (db == db[0]).all()
