@@ -699,8 +699,8 @@ typedef struct moe_norm_problem {
 void moe_block_struct_sizes(int64_t* norm, int64_t* ortho);
 
 /* x [M, K]: device, x_dtype; block [M, K]: device bf16 or NULL; w_post [K], NULL
- * without a norm behind the block; gate: NULL exactly when gate_kind is NONE,
- * device w_dtype [K] or float32 [M]; w_pre [K] and h [M, K] (device bf16): both
+ * without a norm behind the block; gate: NULL exactly when gate_kind is NONE
+ * (one per token may also be with M = 0), device w_dtype [K] or float32 [M]; w_pre [K] and h [M, K] (device bf16): both
  * or neither; x_out [M, K]: device, x_dtype, may be x itself, NULL exactly when
  * block is.  block NULL needs w_pre, no w_post and MOE_GATE_NONE (res_scale is
  * not applied).  16-byte alignment for all but a gate per token (4).  M = 0

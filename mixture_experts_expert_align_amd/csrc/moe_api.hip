@@ -1102,7 +1102,8 @@ static bool optional16(const void* q) { return ((uintptr_t)q & 15) == 0; }
 // What forward and backward ask of the weights and the gate alike.
 static bool norm_weights(const moe_norm_problem* p, const void* w_post, const void* gate, const void* w_pre) {
   if (!optional16(w_post) || !optional16(w_pre)) return false;
-  if ((p->gate_kind == MOE_GATE_NONE) != (gate == nullptr)) return false;
+  const bool empty = p->gate_kind == MOE_GATE_TOKEN && p->M == 0;   // a gate of no elements may be null
+  if (!empty && (p->gate_kind == MOE_GATE_NONE) != (gate == nullptr)) return false;
   return ((uintptr_t)gate & (p->gate_kind == MOE_GATE_TOKEN ? 3 : 15)) == 0;
 }
 
@@ -1155,7 +1156,8 @@ int moe_block_norm_backward(const moe_norm_problem* p, const void* x_out, const 
   if (st != MOE_OK) return st;
   const bool rows = p->M > 0;
   if (!norm_weights(p, w_post, gate, w_pre) || (accumulate != 0 && accumulate != 1) || !optional16(dw_post) || !optional16(dw_pre) || !aligned16(ws) ||
-      (dw_post && !w_post) || (dw_pre && !w_pre) || (dgate && !gate) || ((uintptr_t)dgate & 3))
+      (dw_post && !w_post) || (dw_pre && !w_pre) || (dgate && p->gate_kind == MOE_GATE_NONE) ||
+      ((uintptr_t)dgate & 3))
     return MOE_EINVAL;
   if (rows && (!norm_block(block, w_post, gate, w_pre) || !aligned16(x_out) || !aligned16(dx) ||
                !optional16(dblock) || !optional16(dx_out) || !optional16(dh) ||

@@ -83,3 +83,36 @@ def test_sums_over_many_equal_rows(M, K, gate):
         want, err = ref["dgate_channel" if n == "dgate" else n]
         within(got, M * want, M * err, 2.0 ** -24, n)
     assert (dx == dx[0]).all() and (db == db[0]).all()
+
+
+@gpu
+def test_no_tokens_with_a_gate_per_token():
+    """An empty gate has no address; the sums are written, or left by accumulate."""
+    K = 520
+    p = moe.make_norm_problem(0, K, gate_kind=moe.GATE_TOKEN)
+    none = torch.empty(0, K, dtype=torch.bfloat16, device="cuda")
+    w, empty = torch.ones(K, device="cuda"), torch.empty(0, device="cuda")
+    ws = moe.allocate_norm_workspace(p)
+    moe.moe_block_norm(p, none, none, none, w, empty, w, none)
+    for dgate in (empty, None):
+        s = [torch.full((K,), -0.0, device="cuda") for _ in range(2)]
+        moe.moe_block_norm_backward(p, none, none, none, ws, none, w, empty, w, none, none, s[0], dgate, s[1])
+        assert all(not t.any() and not torch.signbit(t).any() for t in s)
+        s = [torch.full((K,), 2.5, device="cuda") for _ in range(2)]
+        moe.moe_block_norm_backward(p, none, none, none, ws, none, w, empty, w, none, none, s[0], dgate, s[1],
+                                    accumulate=True)
+        assert all((t == 2.5).all() for t in s)
+
+
+def test_a_gate_per_token_is_asked_for_where_there_are_tokens():
+    lib, a = moe.load_library(), 4096
+    p = moe.make_norm_problem(4, 64, gate_kind=moe.GATE_TOKEN)
+    assert lib.moe_block_norm(ctypes.byref(p), a, a, a, None, a, a, a, None) == moe.MOE_EINVAL
+    args = [a, a, a, None, a, a, a, a, a, a, None, a, 0, a, None]
+    assert lib.moe_block_norm_backward(ctypes.byref(p), *args) == moe.MOE_EINVAL
+    # without tokens too, a gate's gradient per channel needs the gate, and a gate needs its kind
+    p = moe.make_norm_problem(0, 64, gate_kind=moe.GATE_CHANNEL)
+    assert lib.moe_block_norm_backward(ctypes.byref(p), *args) == moe.MOE_EINVAL
+    p = moe.make_norm_problem(0, 64)
+    args[3] = a
+    assert lib.moe_block_norm_backward(ctypes.byref(p), *args) == moe.MOE_EINVAL
