@@ -116,3 +116,25 @@ def test_a_gate_per_token_is_asked_for_where_there_are_tokens():
     p = moe.make_norm_problem(0, 64)
     args[3] = a
     assert lib.moe_block_norm_backward(ctypes.byref(p), *args) == moe.MOE_EINVAL
+
+
+@gpu
+@pytest.mark.parametrize("M,E", [(100, 12), (1500, 12), (700, 600)])
+def test_malformed_offsets_write_nothing_past_workspace_or_gradient(M, E):
+    """Offsets that descend or leave [0, M], in one launch and in two: the slots that depend on them stay within the
+    workspace, the gradient within its rows."""
+    l, ids, _ = make(M, E, 2, 1, torch.float32, 13)
+    r, dev_ids = moe.make_router(E, 2), torch.from_numpy(ids).cuda()
+    for off in ([0, M - 10, M // 5, M], [-5, 30, 2 * M, 10 * M], [M, 0, M, 0], [1 << 30, -(1 << 30), 5, M // 2],
+                [M // 2, -(1 << 31), (1 << 31) - 1, 0]):
+        o = torch.tensor(off, dtype=torch.int32, device="cuda")
+        ws = torch.full((moe.moe_balance_ws_bytes(r, M, 3) + 4096,), 255, dtype=torch.uint8, device="cuda")
+        f = torch.full((2, 4, E), 7.0, device="cuda")
+        n = torch.full((2, 4, E), 77, dtype=torch.int32, device="cuda")
+        loss, probs, tokens, counts = f[0, :3, 0].contiguous(), f[1, :3], n[0, :3, 0].contiguous(), n[1, :3]
+        grad = torch.full((M + 2, E), 7.0, device="cuda")
+        moe.moe_balance_loss(r, l, dev_ids, loss, counts, tokens, probs, ws, seq_offsets=o)
+        moe.moe_balance_loss_backward(r, l, dev_ids, counts, tokens, torch.ones(3, device="cuda"), grad[1:M + 1],
+                                      seq_offsets=o)
+        assert (ws[-4096:] == 255).all() and (f[1, 3] == 7).all() and (n[1, 3] == 77).all()
+        assert (grad[0] == 7).all() and (grad[M + 1] == 7).all()
