@@ -796,9 +796,10 @@ _FLOATS = (torch.float32, torch.bfloat16)      # by dtype code
 
 
 def moe_block_norm_ws_bytes(problem: MoeNormProblem) -> int:
-    v = load_library().moe_block_norm_ws_bytes(ctypes.byref(problem))
-    if v < 0:
-        raise MoeError("moe_block_norm_ws_bytes", MOE_EINVAL)
+    lib = load_library()
+    v = lib.moe_block_norm_ws_bytes(ctypes.byref(problem))
+    if v < 0:   # refused, and so by the call itself, before it looks at its operands
+        raise MoeError("moe_block_norm_ws_bytes", lib.moe_block_norm(ctypes.byref(problem), *[None] * 8))
     return v
 
 
@@ -865,9 +866,10 @@ def make_ortho_problem(E, N, K, dtype=torch.float32, steps=5, coef=MUON_COEF, ep
 
 
 def moe_ortho_ws_bytes(problem: MoeOrthoProblem) -> int:
-    v = load_library().moe_ortho_ws_bytes(ctypes.byref(problem))
-    if v < 0:
-        raise MoeError("moe_ortho_ws_bytes", MOE_EINVAL)
+    lib = load_library()
+    v = lib.moe_ortho_ws_bytes(ctypes.byref(problem))
+    if v < 0:   # refused, and so by the call itself, before it looks at its operands
+        raise MoeError("moe_ortho_ws_bytes", lib.moe_orthogonalize(ctypes.byref(problem), *[None] * 4))
     return v
 
 

@@ -138,3 +138,16 @@ def test_malformed_offsets_write_nothing_past_workspace_or_gradient(M, E):
                                       seq_offsets=o)
         assert (ws[-4096:] == 255).all() and (f[1, 3] == 7).all() and (n[1, 3] == 77).all()
         assert (grad[0] == 7).all() and (grad[M + 1] == 7).all()
+
+
+def test_workspace_sizes_of_refused_problems_name_the_reason():
+    for call, p, status in ((moe.moe_block_norm_ws_bytes, moe.make_norm_problem(4, 60), moe.MOE_EUNSUPPORTED),
+                            (moe.moe_block_norm_ws_bytes, moe.make_norm_problem(4, 1 << 20), moe.MOE_EUNSUPPORTED),
+                            (moe.moe_block_norm_ws_bytes, moe.make_norm_problem(-1, 64), moe.MOE_EINVAL),
+                            (moe.moe_ortho_ws_bytes, moe.make_ortho_problem(1, 40000, 8), moe.MOE_EUNSUPPORTED),
+                            (moe.moe_ortho_ws_bytes, moe.make_ortho_problem(1, 8, 8, coef=(1e9, 0, 0)),
+                             moe.MOE_EUNSUPPORTED),
+                            (moe.moe_ortho_ws_bytes, moe.make_ortho_problem(0, 8, 8), moe.MOE_EINVAL)):
+        with pytest.raises(moe.MoeError) as e:
+            call(p)
+        assert e.value.status == status
