@@ -655,6 +655,12 @@ hipError_t product(const StepArgs& a, int T, hipStream_t s) {
 // X and leaves its part of the next A.  The three products by themselves are
 // chains of launches of a few microseconds each, and A's a few tiles with all
 // of n to add (4096 x 64: 18 of a step's 27 us, in one launch 11).
+//
+// Here X and B enter all products in two pieces (the product of two second pieces is
+// left out): with the first piece alone the rounding of a few strong directions
+// reached the weak ones, at up to 4e-2 of the result (n x 2 to n x 64, r singular
+// values of 1, the others 1e-2 to 1e-5); so it is 1.4e-3.  64 x 4096: 66.5 us with
+// the first pieces, 71.3 with both in X B, 75.6 in A too.
 
 // (For m <= 128 the same, with two halves of columns and twice the threads, took 15
 // us a step and more, the three launches 13.)
@@ -709,24 +715,32 @@ __device__ __forceinline__ void narrow_places(const uint16_t* s, const int (&j)[
           s + tile::wt_off_n<kNarrow>(8 * (gq >> 1) + (L >> 2) + 4 * h, j[i] + 16 * (gq & 1) + 4 * (L & 3)));
 }
 
-// acc += the products of the two fragments over slices ST .. of a round.
+// acc += the products of the two fragments over slices ST .. of a round, low += those with
+// a second piece, which lies a round behind the first, at kLow times their value.
 template <int ST>
-__device__ __forceinline__ void narrow_gram(const uint32_t (&a)[2][2], f32x16& acc) {
+__device__ __forceinline__ void narrow_gram(const uint32_t (&a)[2][2], f32x16& acc, f32x16& low) {
   if constexpr (ST < kNarrowRows / 16) {
-    tile::v4i16 v[4];
-    asm volatile("ds_read_b64_tr_b16 %0, %4 offset:%8\n\tds_read_b64_tr_b16 %1, %5 offset:%8\n\t"
-                 "ds_read_b64_tr_b16 %2, %6 offset:%8\n\tds_read_b64_tr_b16 %3, %7 offset:%8\n\ts_waitcnt lgkmcnt(0)"
-                 : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
-                 : "v"(a[0][0]), "v"(a[0][1]), "v"(a[1][0]), "v"(a[1][1]), "n"(ST * 16 * kNarrow * 2)
+    tile::v4i16 v[8];
+    constexpr int at = ST * 16 * kNarrow * 2;
+    asm volatile("ds_read_b64_tr_b16 %0, %8 offset:%12\n\tds_read_b64_tr_b16 %1, %9 offset:%12\n\t"
+                 "ds_read_b64_tr_b16 %2, %10 offset:%12\n\tds_read_b64_tr_b16 %3, %11 offset:%12\n\t"
+                 "ds_read_b64_tr_b16 %4, %8 offset:%13\n\tds_read_b64_tr_b16 %5, %9 offset:%13\n\t"
+                 "ds_read_b64_tr_b16 %6, %10 offset:%13\n\tds_read_b64_tr_b16 %7, %11 offset:%13\n\t"
+                 "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]), "=&v"(v[6]),
+                   "=&v"(v[7])
+                 : "v"(a[0][0]), "v"(a[0][1]), "v"(a[1][0]), "v"(a[1][1]), "n"(at), "n"(at + kNarrowRows * kNarrow * 2)
                  : "memory");
-    f16x8 f[2];
+    f16x8 f[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       const tile::v4i16 v8[2] = {v[2 * i], v[2 * i + 1]};
       f[i] = __builtin_bit_cast(f16x8, v8);
     }
     acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[0], f[1], acc, 0, 0, 0);
-    narrow_gram<ST + 1>(a, acc);
+    low = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[2], f[1], low, 0, 0, 0);
+    low = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[0], f[3], low, 0, 0, 0);
+    narrow_gram<ST + 1>(a, acc, low);
   }
 }
 
@@ -734,8 +748,9 @@ template <int MODE>
 __global__ void __launch_bounds__(256) ortho_narrow_kernel(NarrowArgs a) {
   constexpr int MP = kNarrow, SQ = MP * MP;
   constexpr int NK = MP / 16;       // MFMA steps along m
-  __shared__ __attribute__((aligned(16))) uint16_t s_o[MODE == kNarrowStep ? SQ : 8], s_b[MODE == kNarrowStep ? SQ : 8];
-  __shared__ __attribute__((aligned(16))) uint16_t s_x[kNarrowRows * MP];
+  __shared__ __attribute__((aligned(16))) uint16_t s_o[MODE == kNarrowStep ? SQ : 8], s_b[MODE == kNarrowStep ? SQ : 8],
+      s_bl[MODE == kNarrowStep ? SQ : 8];   // B's second piece
+  __shared__ __attribute__((aligned(16))) uint16_t s_x[2 * kNarrowRows * MP];   // both pieces
   __shared__ __attribute__((aligned(16))) float s_d[MP], s_e[MP];
   const int e = blockIdx.x / a.W, wg = blockIdx.x % a.W;
   const int lane = threadIdx.x & 63;
@@ -841,35 +856,50 @@ __global__ void __launch_bounds__(256) ortho_narrow_kernel(NarrowArgs a) {
       const int p = 32 * wi + 8 * g4 + 4 * up;
       const uint2 o = *reinterpret_cast<const uint2*>(s_o + tile::lds_off<MP>(q, p / 8) + p % 8);
       const f32x4 dp = *reinterpret_cast<const f32x4*>(s_d + p);
-      uint32_t b[4];
+      uint32_t b[4], bl[4];
       float diag = 0.f;
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
         const float off = f16_to_f32((h & 2 ? o.y : o.x) >> (h & 1 ? 16 : 0)) * a.from_sa;   // 0 on the diagonal
         const float oo = acc[4 * g4 + h] * sq;
         diag = p + h == q ? oo : diag;
-        b[h] = f32_to_f16(p + h == q ? 0.f : (a.cb * off + a.cc * (oo + (dp[h] + dq) * off)) * a.sb);
+        const float v = p + h == q ? 0.f : (a.cb * off + a.cc * (oo + (dp[h] + dq) * off)) * a.sb;
+        b[h] = f32_to_f16(v);
+        bl[h] = f32_to_f16((v - f16_to_f32(b[h])) * kLow);
       }
       if ((unsigned)(q - p) < 4u) s_e[q] = a.ca + (a.cb * dq + a.cc * (diag + dq * dq));
       *reinterpret_cast<uint2*>(s_b + tile::lds_off<MP>(q, p / 8) + p % 8) =
           make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
+      *reinterpret_cast<uint2*>(s_bl + tile::lds_off<MP>(q, p / 8) + p % 8) =
+          make_uint2(bl[0] | (bl[1] << 16), bl[2] | (bl[3] << 16));
     }
     lds_barrier();
   }
-  f32x16 gram = {};
+  f32x16 gram = {}, gram_low = {};
   uint32_t places[2][2];
   narrow_places(s_x, {32 * wi, 32 * wj}, lane, places);
   for (int rb = 0; rb < a.rows; rb += kNarrowRows) {
     const int64_t t = row0 + rb, at = x0 + (int64_t)rb * MP;
     float val[2][16];
     if constexpr (MODE == kNarrowStep) {
+      // X B in pieces: both products with a second piece, at kLow times their value, then
+      // the one of the first
       f32x16 acc[2] = {};
+      auto add = [&](const uint16_t* s_p, const i32x4(&xp)[NK]) {
 #pragma unroll
-      for (int st = 0; st < NK; ++st)
+        for (int st = 0; st < NK; ++st)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(frag(s_b, 32 * i + l32, st),
-                                                          __builtin_bit_cast(f16x8, x[st]), acc[i], 0, 0, 0);
+          for (int i = 0; i < 2; ++i)
+            acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(frag(s_p, 32 * i + l32, st),
+                                                            __builtin_bit_cast(f16x8, xp[st]), acc[i], 0, 0, 0);
+      };
+      add(s_bl, x);
+      add(s_b, xl);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) acc[i][k] *= 1.0f / kLow;
+      add(s_b, x);
 #pragma unroll
       for (int st = 0; st < 4; ++st) {
         halves_to_groups(x[st]);
@@ -924,16 +954,18 @@ __global__ void __launch_bounds__(256) ortho_narrow_kernel(NarrowArgs a) {
       }
       i32x4 h = __builtin_bit_cast(i32x4, hi), l = __builtin_bit_cast(i32x4, lo);
 #pragma unroll
-      for (int g2 = 0; g2 < 2; ++g2)
-        *reinterpret_cast<int2*>(s_x + tile::wt_off_n<MP>(tl, 16 * st + 8 * g2 + 4 * up)) =
-            make_int2(h[2 * g2], h[2 * g2 + 1]);
+      for (int g2 = 0; g2 < 2; ++g2) {
+        uint16_t* const place = s_x + tile::wt_off_n<MP>(tl, 16 * st + 8 * g2 + 4 * up);
+        *reinterpret_cast<int2*>(place) = make_int2(h[2 * g2], h[2 * g2 + 1]);
+        *reinterpret_cast<int2*>(place + kNarrowRows * MP) = make_int2(l[2 * g2], l[2 * g2 + 1]);
+      }
       halves_to_groups(h);
       halves_to_groups(l);
       *reinterpret_cast<i32x4*>(a.hi + at + 16 * st + 8 * up) = h;
       *reinterpret_cast<i32x4*>(a.lo + at + 16 * st + 8 * up) = l;
     }
     lds_barrier();
-    narrow_gram<0>(places, gram);
+    narrow_gram<0>(places, gram, gram_low);
     lds_barrier();
   }
   if (MODE == kNarrowStep && a.last) return;
@@ -941,7 +973,9 @@ __global__ void __launch_bounds__(256) ortho_narrow_kernel(NarrowArgs a) {
 #pragma unroll
   for (int g4 = 0; g4 < 4; ++g4)
     *reinterpret_cast<f32x4*>(g + (32 * wj + l32) * MP + 32 * wi + 8 * g4 + 4 * up) =
-        (f32x4){gram[4 * g4], gram[4 * g4 + 1], gram[4 * g4 + 2], gram[4 * g4 + 3]};
+        (f32x4){gram[4 * g4] + gram_low[4 * g4] * (1.0f / kLow), gram[4 * g4 + 1] + gram_low[4 * g4 + 1] * (1.0f / kLow),
+                gram[4 * g4 + 2] + gram_low[4 * g4 + 2] * (1.0f / kLow),
+                gram[4 * g4 + 3] + gram_low[4 * g4 + 3] * (1.0f / kLow)};
 }
 
 // Rows of a workgroup: two rounds, or what leaves 16 workgroups (whose parts of A
