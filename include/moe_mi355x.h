@@ -748,12 +748,15 @@ int moe_block_norm_backward(const moe_norm_problem* p, const void* x_out, const 
  *   out = scale X
  *
  * Products of float16 operands summed in float32 in a fixed order (the same
- * bits on every run).  X is kept in two float16 pieces (22 bits), the
+ * bits on every run).  X is kept in two float16 pieces (22 bits; both enter X B
+ * where min(N, K) is at most 512, and A where it is at most 64), the
  * diagonals of A and of b A + c A^2 in float32 beside their float16
  * off-diagonal parts, all scaled by powers of two to float16's range; the norm
  * is summed in float64.  With five steps of (3.4445, -4.775, 2.0315) the result
  * is within 2e-3 of the exact one (2-norm, relative) before its rounding to
- * bf16 for matrices of Gaussian, low-rank and decaying spectra; what eps (or a
+ * bf16, for matrices of Gaussian and decaying spectra and for strong directions
+ * over others of any size; steps that multiply small differences of singular
+ * values multiply rounding errors with them.  What eps (or a
  * value beside far larger ones) leaves below 2^-48 in X counts as 0.  A matrix
  * with a NaN or an infinity gives NaN in all of its own out; a zero matrix gives
  * zeros.

@@ -12,13 +12,15 @@
 // about a each time, and what rounding adds in its direction with it, so bf16
 // operands (8 bits) leave errors of 1 to 9%.  Here operands are float16 (11
 // bits), scaled by powers of two to its range; the term a X takes X in two
-// pieces, float16 and the rest in float16 times 2^11 (22 bits); and the
-// diagonals of A and B, which hold most of them where X is near orthogonal,
-// stay in float32 outside the products:
+// pieces, float16 and the rest in float16 times 2^11 (22 bits), and so do X B up to
+// m = 512 and, up to m = 64, also X^T X, and X B with B in two pieces too (the
+// smaller m, the more one entry's rounding counts); and the diagonals of A and B, which hold most of them where X is near
+// orthogonal, stay in float32 outside the products:
 //   A = D + O, A^2 = O O + D O + O D + D^2,  X (a I + B) = X (a I + D_B) + X O_B.
-// What is left is 1e-4 to 1.4e-3 of the result (2-norm; Gaussian, low-rank and
-// decaying spectra, 256 x 256 to 4096 x 64, 5 steps), under the 1.7e-3 of its
-// rounding to bf16.
+// What is left of 5 steps' result is (2-norm, relative; Gaussian matrices, decaying
+// spectra, and r singular values of 1 over others of 3e-2 to 1e-5, the worst of
+// all) up to 1.4e-3 for m up to 64, 1.1e-3 up to 512 and 2e-3 past it, a worst
+// case about as large as the rounding to bf16 that follows (1.7e-3).
 //
 // Large matrices are bound by the matrix units and by what the epilogues move: 8 of
 // 4096 x 6144 take 820 us for A, 577 for B and 1524 for X B a step (1.07, 0.98 and
@@ -189,7 +191,7 @@ __global__ void __launch_bounds__(256) ortho_input_kernel(const void* u, int N, 
 
 // --------------------------------------------------------------- products --
 
-enum Product { kGram = 0, kSquare = 1, kApply = 2 };
+enum Product { kGram = 0, kSquare = 1, kApply = 2, kApplyBoth = 3 };   // both pieces of X in X B
 
 struct StepArgs {
   Mats M;
@@ -243,6 +245,7 @@ template <int T, int MODE>
 __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2 : T == 128 ? 2 : 4)
     ortho_product_kernel(StepArgs a) {
   using S = Shape<T>;
+  constexpr bool kXB = MODE == kApply || MODE == kApplyBoth, kBoth = MODE == kApplyBoth;
   constexpr int WI = S::WI, WJ = S::WJ, TI = S::TI, TJ = S::TJ, NW = WI * WJ;
   static_assert(32 * WI * TI == T && 32 * WJ * TJ == T, "the waves cover the tile");
   constexpr int kSlot = T * kBK;          // uint16 elements
@@ -263,7 +266,7 @@ __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2
   if (kSplit) tl /= a.splits;
   const int nm = mp / T;
   int e, tp, tq;
-  if (MODE == kApply) {
+  if (kXB) {
     // bands of kBand rows of tiles, column by column: 32 tiles in a row read 4
     // row tiles of X and 8 of B
     const int nn = np / T, per = nn * nm;
@@ -306,12 +309,15 @@ __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2
   }
   const int ns = kd / kBK;                    // slices; this workgroup's: nk from k0 on
   const int k0 = kSplit ? (int)((int64_t)ns * sp / a.splits) : 0;
-  const int nk = kSplit ? (int)((int64_t)ns * (sp + 1) / a.splits) - k0 : ns;
+  const int nk = kSplit ? (int)((int64_t)ns * (sp + 1) / a.splits) - k0 : kBoth ? 2 * ns : ns;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wi = wave / WJ, wj = wave % WJ;
   const __amdgpu_buffer_rsrc_t pr = buffer_rsrc(P, (int64_t)mp * kd * 2);
   const __amdgpu_buffer_rsrc_t qr = buffer_rsrc(Q, qrows * kd * 2);
+  // both pieces: X's second, kLow times its value, in the first ns slices
+  const __amdgpu_buffer_rsrc_t q2 = kBoth ? buffer_rsrc(M.lo[a.cur] + (int64_t)e * np * mp, qrows * kd * 2) : qr;
+  auto column = [&](int kt) { return (kBoth && kt >= ns ? kt - ns : k0 + kt) * kBK * 2; };
   // load i of this wave: slot rows 8 (wave + NW i) .. +7, lane l -> row l / 8,
   // physical chunk l % 8 (lds_off's swizzle: logical chunk ^ (row / 2) % 8)
   uint32_t op[L], oq[L];
@@ -325,13 +331,14 @@ __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2
   auto issue_p = [&](int kt) {
     uint16_t* slot = pbase + (kt % 3) * kSlot;
 #pragma unroll
-    for (int i = 0; i < L; ++i) lds_load16(pr, slot + (wave + NW * i) * 512, op[i], (k0 + kt) * kBK * 2);
+    for (int i = 0; i < L; ++i) lds_load16(pr, slot + (wave + NW * i) * 512, op[i], column(kt));
     issue_order();
   };
   auto issue_q = [&](int kt) {
     uint16_t* slot = qbase + (kt % 2) * kSlot;
 #pragma unroll
-    for (int i = 0; i < L; ++i) lds_load16(qr, slot + (wave + NW * i) * 512, oq[i], (k0 + kt) * kBK * 2);
+    for (int i = 0; i < L; ++i)
+      lds_load16(kBoth && kt < ns ? q2 : qr, slot + (wave + NW * i) * 512, oq[i], column(kt));
     issue_order();
   };
 
@@ -386,6 +393,14 @@ __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2
   // slice kt; F 1: slice kt+2 exists, 0: only kt+1, -1: kt is the last
   auto slice = [&](int kt, auto mode) {
     constexpr int F = decltype(mode)::value;
+    if (kBoth && kt == ns) {   // (all products of the slices before are in)
+#pragma unroll
+      for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int j = 0; j < TJ; ++j)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) acc[i][j][r] *= 1.0f / kLow;
+    }
 #pragma unroll
     for (int st = 0; st + 1 < NSTEP; ++st) {
       // (P's loads have a slice more to arrive than Q's: issued later, they leave
@@ -434,7 +449,7 @@ __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2
     return stage + r * T + ((((c >> 1) ^ ((r ^ (r >> 3)) & SW)) + (c & 1) * (CH / 2)) << 2);
   };
   const int64_t me = (int64_t)e * mp;
-  const bool turned = MODE == kApply ? !a.last || a.wide : tp != tq;
+  const bool turned = kXB ? !a.last || a.wide : tp != tq;
 #pragma unroll
   for (int hf = 0; hf < T / HR; ++hf) {
     constexpr int UR = T / 8, U = HR * UR / NT;   // units of a row; of a thread
@@ -443,13 +458,13 @@ __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2
     auto unit_row = [&](int w) { return (int)threadIdx.x / UR + NT / UR * w; };
     // what is read besides, all of it requested before the rows are written (a
     // load behind another unit's stores would wait for each in turn)
-    f16x8 x1[U], x2[MODE == kApply ? U : 1];
+    f16x8 x1[U], x2[kXB ? U : 1];
     float xq[MODE == kSquare ? U : 1];
     if (MODE != kGram) {
 #pragma unroll
       for (int w = 0; w < U; ++w) {
         const int q = q0 + hf * HR + unit_row(w);
-        if constexpr (MODE == kApply) {
+        if constexpr (kXB) {
           const int64_t at = ((int64_t)e * np + q) * mp + p;
           x1[w] = *reinterpret_cast<const f16x8*>(M.hi[a.cur] + at);
           x2[w] = *reinterpret_cast<const f16x8*>(M.lo[a.cur] + at);
@@ -527,7 +542,7 @@ __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2
     // operations that take float16 operands as they are; written out, with each
     // step by itself, the arithmetic took 20000 cycles a tile of 256)
     float kp[8];
-    if (MODE == kApply) {
+    if (kXB) {
       const float f = a.aux * (a.last ? a.scale : a.out);
 #pragma unroll
       for (int h = 0; h < 8; ++h) kp[h] = (a.ca + M.db[me + p + h]) * f;
@@ -535,7 +550,7 @@ __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2
 #pragma unroll
       for (int h = 0; h < 8; ++h) kp[h] = (a.cb + a.cc * M.da[me + p + h]) * (a.aux * a.out);
     }
-    const float k_acc = MODE == kApply ? a.in * (a.last ? a.scale : a.out)
+    const float k_acc = kXB ? a.in * (a.last ? a.scale : a.out)
                         : MODE == kSquare ? a.cc * (a.in * a.out)
                                           : a.in * a.out;
 #pragma unroll
@@ -549,7 +564,7 @@ __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2
         for (int h = 0; h < 4; ++h) v[4 * c + h] = f[h];
       }
       i32x4 s;   // the 8 finished values, 16 bits each
-      if (MODE == kApply) {
+      if (kXB) {
         const int64_t at = ((int64_t)e * np + q) * mp + p;
 #pragma unroll
         for (int h = 0; h < 8; ++h) v[h] = ((float)x2[w][h] * (1.0f / kLow) + (float)x1[w][h]) * kp[h] + v[h] * k_acc;
@@ -616,9 +631,9 @@ __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2
                      : "memory");
         const i32x4 s = __builtin_bit_cast(i32x4, f);
         const int row = p0 + c0 + L16, col = q0 + hf * HR + r0;
-        if (MODE == kApply && a.last) {
+        if (kXB && a.last) {
           if (row < a.N) store_row(a, (int64_t)e * a.N + row, col, s);
-        } else if (MODE == kApply) {
+        } else if (kXB) {
           *reinterpret_cast<i32x4*>(M.xt + (me + row) * np + col) = s;
         } else {
           *reinterpret_cast<i32x4*>((MODE == kGram ? M.a : M.b) + (me + row) * mp + col) = s;
@@ -631,7 +646,7 @@ __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2
 template <int T, int MODE>
 hipError_t launch_product(StepArgs a, hipStream_t s) {
   const int64_t nm = a.M.mp / T, nn = a.M.np / T;
-  a.total = a.M.E * (MODE == kApply ? nm * nn : nm * (nm + 1) / 2) * (MODE == kGram && T == 64 ? a.splits : 1);
+  a.total = a.M.E * (MODE >= kApply ? nm * nn : nm * (nm + 1) / 2) * (MODE == kGram && T == 64 ? a.splits : 1);
   // few tiles are dealt evenly, many in runs of 32, a tile for each CU of an XCD
   const int64_t even = (a.total + tile::NXCD - 1) / tile::NXCD;
   a.chunk = (int32_t)(even < tile::kXcdChunk ? even : tile::kXcdChunk);
@@ -1034,9 +1049,18 @@ int gram_splits(int64_t E, int64_t np, int64_t mp) {
   return (int)(s < 3 ? 1 : s > 16 ? 16 : s);
 }
 
+// Matrices up to this m take both pieces of X in X B.  With the first alone the
+// rounding of a few strong directions that reaches the weak ones is up to 4.4e-3 of
+// the result for 4096 x 128 (spectra as above), 2.8e-3 for 4096 x 256, 1.9e-3 for
+// 2048 x 512 and 4096 x 513, 1.2e-3 for 1024 x 1024; with both 1.1e-3 and less.  8 of 256 x 512: 85.8
+// us with the first piece, 91.5 with both; 32 of 512 x 2048 835 and 929, 64 of 256 x 4096
+// 1254 and 1319.
+constexpr int64_t kBothMost = 512;
+
 struct Layout {
   int T;                  // 0: narrow
   int Ts, splits;         // tiles of the symmetric products; of A, if 64
+  bool both;              // both pieces of X in X B
   int64_t np, mp, W, hi[2], lo[2], xt, a, b, da, db, part, gpart, gdone, end;
 };
 
@@ -1063,6 +1087,7 @@ Layout layout(int64_t E, int64_t N, int64_t K) {
     return L;
   }
   L.T = tile_of(E, n, m);
+  L.both = m <= kBothMost;
   L.np = (n + L.T - 1) / L.T * L.T;
   L.mp = (m + L.T - 1) / L.T * L.T;
   L.Ts = symmetric_tile(E, L.mp, L.T);
@@ -1249,7 +1274,7 @@ hipError_t launch_orthogonalize(const OrthoArgs& o, hipStream_t st) {
     a.in = pow2(-sx - sb);
     a.out = a.last ? 1.0f : pow2(s[i + 1][0]);
     a.aux = pow2(-sx);
-    if ((e = product<kApply>(a, L.T, st)) != hipSuccess) return e;
+    if ((e = L.both ? product<kApplyBoth>(a, L.T, st) : product<kApply>(a, L.T, st)) != hipSuccess) return e;
   }
   return hipSuccess;
 }

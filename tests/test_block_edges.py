@@ -196,3 +196,10 @@ def test_a_few_strong_directions_of_a_narrow_matrix(n, m):
     """Singular values far below others: what rounding adds in a strong direction must not reach the weak ones.
     Within the 2e-3 that the interface states (64-bit evaluations with the kernel's roundings leave up to 1.4e-3)."""
     a_few_strong_directions(n, m)
+
+
+@gpu
+@pytest.mark.parametrize("n,m", [(65, 65), (1024, 96), (96, 1000), (2048, 128), (256, 256), (260, 1030), (1536, 384),
+                                 (700, 512), (1024, 520), (768, 768)])
+def test_a_few_strong_directions(n, m):
+    a_few_strong_directions(n, m)
