@@ -1135,16 +1135,16 @@ bool ortho_scales(const OrthoArgs& o, int32_t (*s)[3]) {
         most = fmax(most, g(sqrt(y)));
       }
     };
-    if (c != 0.0) {
-      const double d = 9 * b * b - 20 * a * c;
-      if (d >= 0.0) {
-        at((-3 * b + sqrt(d)) / (10 * c));
-        at((-3 * b - sqrt(d)) / (10 * c));
-      }
-      at(-b / (2 * c));
-    } else if (b != 0.0) {
-      at(-a / (3 * b));
+    // (the root whose numerator does not cancel, and the other by their product: for
+    // c = 0 too, and where c is so small that the two of a numerator would be one
+    // number; a division by 0 leaves nothing inside)
+    const double d = 9 * b * b - 20 * a * c;
+    if (d >= 0.0) {
+      const double q = -(3 * b + copysign(sqrt(d), b)) / 2;
+      at(q / (5 * c));
+      at(a / q);
     }
+    at(-b / (2 * c));
     s[i][0] = power(u);
     s[i][1] = power(u * u);
     s[i][2] = power(most);

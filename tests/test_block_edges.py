@@ -203,3 +203,15 @@ def test_a_few_strong_directions_of_a_narrow_matrix(n, m):
                                  (700, 512), (1024, 520), (768, 768)])
 def test_a_few_strong_directions(n, m):
     a_few_strong_directions(n, m)
+
+
+@gpu
+@pytest.mark.parametrize("N,K", [(96, 40), (130, 200)])
+@pytest.mark.parametrize("coef", [(3.0, -3.0, 1e-20), (3.0, -3.0, -1e-20), (2.0, -2.0, 1e-30), (2.0, 1e-25, 1e-30),
+                                  (1.5, -0.5, 1e-18)])
+def test_coefficients_beside_far_larger_ones(coef, N, K):
+    """The largest value that a singular value can take lies at a root of a + 3 b y + 5 c y^2, whose usual formula
+    cancels for small c: a bound that misses it scales X past float16's range."""
+    u, got, p = ortho_run(np.stack([few_strong(N, K, 3, 0.5, s) for s in range(2)]), coef=[coef] * 2)
+    for e in range(2):
+        ortho_check(u[e], got[e], p, e)
