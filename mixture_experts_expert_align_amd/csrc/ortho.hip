@@ -543,16 +543,13 @@ __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2
     // step by itself, the arithmetic took 20000 cycles a tile of 256)
     float kp[8];
     if (kXB) {
-      const float f = a.aux * (a.last ? a.scale : a.out);
 #pragma unroll
-      for (int h = 0; h < 8; ++h) kp[h] = (a.ca + M.db[me + p + h]) * f;
+      for (int h = 0; h < 8; ++h) kp[h] = (a.ca + M.db[me + p + h]) * (a.aux * a.out);
     } else if (MODE == kSquare) {
 #pragma unroll
       for (int h = 0; h < 8; ++h) kp[h] = (a.cb + a.cc * M.da[me + p + h]) * (a.aux * a.out);
     }
-    const float k_acc = kXB ? a.in * (a.last ? a.scale : a.out)
-                        : MODE == kSquare ? a.cc * (a.in * a.out)
-                                          : a.in * a.out;
+    const float k_acc = MODE == kSquare ? a.cc * (a.in * a.out) : a.in * a.out;
 #pragma unroll
     for (int w = 0; w < U; ++w) {
       const int r = unit_row(w), q = q0 + hf * HR + r;
@@ -569,9 +566,10 @@ __global__ void __launch_bounds__(64 * Shape<T>::WI * Shape<T>::WJ, T == 256 ? 2
 #pragma unroll
         for (int h = 0; h < 8; ++h) v[h] = ((float)x2[w][h] * (1.0f / kLow) + (float)x1[w][h]) * kp[h] + v[h] * k_acc;
         if (a.last) {
-          // X [n, m] is the output [N, K], or its transpose
+          // X [n, m] is the output [N, K], or its transpose.  (The scale by itself: times
+          // the powers of two above a small one would be subnormal.)
 #pragma unroll
-          for (int h = 0; h < 4; ++h) s[h] = (int)bf16_pack2(v[2 * h], v[2 * h + 1]);
+          for (int h = 0; h < 4; ++h) s[h] = (int)bf16_pack2(v[2 * h] * a.scale, v[2 * h + 1] * a.scale);
           if (!a.wide && q < a.N) store_row(a, (int64_t)e * a.N + q, p, s);
         } else {
           f16x8 hi, lo;

@@ -215,3 +215,18 @@ def test_coefficients_beside_far_larger_ones(coef, N, K):
     u, got, p = ortho_run(np.stack([few_strong(N, K, 3, 0.5, s) for s in range(2)]), coef=[coef] * 2)
     for e in range(2):
         ortho_check(u[e], got[e], p, e)
+
+
+@gpu
+@pytest.mark.parametrize("N,K", [(40, 64), (96, 66), (66, 200), (300, 400)])
+@pytest.mark.parametrize("scale", [1e-37, -2e-37, 1e37, 2e38])
+def test_scales_at_the_ends_of_float32(scale, N, K):
+    """Values near 1 in blocks of 2 x 2, so that the result is a normal number wherever it is not 0: the scale meets
+    X itself, not the powers of two that the products carry."""
+    u = np.zeros((2, N, K))
+    g = np.random.default_rng(N + K)
+    for i in range(0, min(N, K) - 1, 2):
+        u[:, i:i + 2, i:i + 2] = np.eye(2) + 0.6 * g.uniform(-1, 1, (2, 2, 2))
+    u, got, p = ortho_run(u, scale=scale)
+    for e in range(2):
+        ortho_check(u[e], got[e], p, e)
