@@ -677,8 +677,8 @@ int moe_balance_loss_backward(const moe_router* r, int64_t M, int64_t S, const v
  *
  * with rms(v) = sqrt(mean of v^2 + eps), gate none (1), one per channel [K] or
  * one per token [M].  Computed in float32; x' and h are each rounded once, h
- * from the x' before its rounding.  (Squares past the largest float32, values
- * beyond 1.8e19 in magnitude, make a row's rms infinite.)  One call serves the
+ * from the x' before its rounding.  (A row whose squares add up past the largest
+ * float32, values of 1.8e19 / sqrt(K) throughout, has an infinite rms here.)  One call serves the
  * first norm of a model (block NULL), every junction between two blocks, and
  * the last block's output (w_pre NULL).
  * ------------------------------------------------------------------------- */

@@ -549,7 +549,10 @@ hipError_t by_type(const BalanceArgs& a, hipStream_t s) {
                 : by_alignment<L, LANES, NV, (NV < 4 ? NV : 4), false>(a, s);
 }
 
-// 16 lanes a token for up to 512 experts, a wave for more.
+// 16 lanes a token for up to 512 experts, a wave for more.  (At 512 experts in bf16, 16
+// lanes and a wave of 8 values a lane, from a graph: 65536 tokens 25.0 and 35.1 us, their
+// gradient 31.6 and 36.4; 16381 tokens 20.8 and 20.4, 12.3 and 13.2; 4096 tokens 11.9 and
+// 11.9, 5.2 and 4.9.)
 template <class L>
 hipError_t by_experts(const BalanceArgs& a, hipStream_t s) {
   if (a.E <= 16) return by_type<L, 16, 1>(a, s);
