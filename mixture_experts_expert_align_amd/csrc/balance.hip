@@ -21,7 +21,7 @@
 // tokens in float32, over the chunks in float64.
 //
 // Bound by latency more than by bytes: 65536 x 256 bf16 is 36 MB, read in 14 us
-// (2.5 TB/s), and 8 us of sums; 16381 x 512 (sigmoid, 13 sequences) takes 15 and 9
+// (2.5 TB/s), and 8 us of sums; 16381 x 512 (sigmoid, 13 sequences) takes 14 and 9
 // us and its gradient, 34 MB, 14; 8192 x 128 float32 5, 6 and 5 us.
 #include "kernels.h"
 #include "lanes.h"

@@ -23,13 +23,14 @@
 // case about as large as the rounding to bf16 that follows (1.7e-3).
 //
 // Large matrices are bound by the matrix units and by what the epilogues move: 8 of
-// 4096 x 6144 take 820 us for A, 577 for B and 1524 for X B a step (1.07, 0.98 and
-// 1.08 PFLOP/s of what the tiles compute).  A tile of X B is 1.4 us a slice and 37
+// 4096 x 6144 take 841 us for A, 593 for B and 1555 for X B a step (1.04, 0.96 and
+// 1.06 PFLOP/s of what the tiles compute; 820, 577 and 1524 on another card), A and B
+// 7 to 8% of them in a last round that fills a quarter of the CUs.  A tile of X B is 1.4 us a slice and 37
 // us besides, in which 650 KB of X come and go; workgroups that start at different
 // times, requests a slice earlier, tiles of 128 (11% slower) and tiles of two
 // products in one launch (9 to 17%) did not shorten it.
 // Small ones are bound by the latency of three dependent launches a step (8 of 256 x
-// 512: 5.7, 4.7 and 6.0 us), m <= 64 of one (64 x 4096: 11.5 us).
+// 512: 5.6, 4.6 and 7.1 us), m <= 64 of one (64 x 4096: 13.4 us).
 #include <math.h>
 
 #include <type_traits>
