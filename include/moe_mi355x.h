@@ -678,9 +678,9 @@ int moe_balance_loss_backward(const moe_router* r, int64_t M, int64_t S, const v
  * with rms(v) = sqrt(mean of v^2 + eps), gate none (1), one per channel [K] or
  * one per token [M].  Computed in float32; x' and h are each rounded once, h
  * from the x' before its rounding.  (A row whose squares add up past the largest
- * float32, values of 1.8e19 / sqrt(K) throughout, has an infinite rms here.)  One call serves the
- * first norm of a model (block NULL), every junction between two blocks, and
- * the last block's output (w_pre NULL).
+ * float32, values of 1.8e19 / sqrt(K) throughout, has an infinite rms here.)  One
+ * call serves the first norm of a model (block NULL), every junction between two
+ * blocks, and the last block's output (w_pre NULL).
  * ------------------------------------------------------------------------- */
 enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2 };
 
@@ -700,8 +700,8 @@ void moe_block_struct_sizes(int64_t* norm, int64_t* ortho);
 
 /* x [M, K]: device, x_dtype; block [M, K]: device bf16 or NULL; w_post [K], NULL
  * without a norm behind the block; gate: NULL exactly when gate_kind is NONE
- * (one per token may also be with M = 0), device w_dtype [K] or float32 [M]; w_pre [K] and h [M, K] (device bf16): both
- * or neither; x_out [M, K]: device, x_dtype, may be x itself, NULL exactly when
+ * (one per token may also be with M = 0), device w_dtype [K] or float32 [M]; w_pre
+ * [K] and h [M, K] (device bf16): both or neither; x_out [M, K]: device, x_dtype, may be x itself, NULL exactly when
  * block is.  block NULL needs w_pre, no w_post and MOE_GATE_NONE (res_scale is
  * not applied).  16-byte alignment for all but a gate per token (4).  M = 0
  * enqueues nothing.  MOE_EINVAL: a bad field, a null or misaligned pointer, a

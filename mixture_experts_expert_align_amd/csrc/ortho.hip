@@ -14,8 +14,9 @@
 // bits), scaled by powers of two to its range; the term a X takes X in two
 // pieces, float16 and the rest in float16 times 2^11 (22 bits), and so do X B up to
 // m = 512 and, up to m = 64, also X^T X, and X B with B in two pieces too (the
-// smaller m, the more one entry's rounding counts); and the diagonals of A and B, which hold most of them where X is near
-// orthogonal, stay in float32 outside the products:
+// smaller m, the more one entry's rounding counts); and the diagonals of A and B,
+// which hold most of them where X is near orthogonal, stay in float32 outside the
+// products:
 //   A = D + O, A^2 = O O + D O + O D + D^2,  X (a I + B) = X (a I + D_B) + X O_B.
 // What is left of 5 steps' result is (2-norm, relative; Gaussian matrices, decaying
 // spectra, and r singular values of 1 over others of 3e-2 to 1e-5, the worst of
@@ -25,10 +26,10 @@
 // Large matrices are bound by the matrix units and by what the epilogues move: 8 of
 // 4096 x 6144 take 841 us for A, 593 for B and 1555 for X B a step (1.04, 0.96 and
 // 1.06 PFLOP/s of what the tiles compute; 820, 577 and 1524 on another card), A and B
-// 7 to 8% of them in a last round that fills a quarter of the CUs.  A tile of X B is 1.4 us a slice and 37
-// us besides, in which 650 KB of X come and go; workgroups that start at different
-// times, requests a slice earlier, tiles of 128 (11% slower) and tiles of two
-// products in one launch (9 to 17%) did not shorten it.
+// 7 to 8% of the whole in a last round that fills a quarter of the CUs.  A tile of X B
+// is 1.4 us a slice and 37 us besides, in which 650 KB of X come and go; workgroups
+// that start at different times, requests a slice earlier, tiles of 128 (11% slower)
+// and tiles of two products in one launch (9 to 17%) did not shorten it.
 // Small ones are bound by the latency of three dependent launches a step (8 of 256 x
 // 512: 5.6, 4.6 and 7.1 us), m <= 64 of one (64 x 4096: 13.4 us).
 #include <math.h>
@@ -670,11 +671,11 @@ hipError_t product(const StepArgs& a, int T, hipStream_t s) {
 // chains of launches of a few microseconds each, and A's a few tiles with all
 // of n to add (4096 x 64: 18 of a step's 27 us, in one launch 11).
 //
-// Here X and B enter all products in two pieces (the product of two second pieces is
-// left out): with the first piece alone the rounding of a few strong directions
-// reached the weak ones, at up to 4e-2 of the result (n x 2 to n x 64, r singular
-// values of 1, the others 1e-2 to 1e-5); so it is 1.4e-3.  64 x 4096: 66.5 us with
-// the first pieces, 71.3 with both in X B, 75.6 in A too.
+// Here X enters A and X B in two pieces, and B the latter (the product of two second
+// pieces is left out): with the first pieces alone the rounding of a few strong
+// directions reached the weak ones, at up to 4e-2 of the result (n x 2 to n x 64, r
+// singular values of 1, the others 1e-2 to 1e-5); so it is 1.4e-3.  64 x 4096: 66.5 us
+// with the first pieces, 71.3 with both in X B, 75.6 with both in A too.
 
 // (For m <= 128 the same, with two halves of columns and twice the threads, took 15
 // us a step and more, the three launches 13.)
@@ -987,7 +988,8 @@ __global__ void __launch_bounds__(256) ortho_narrow_kernel(NarrowArgs a) {
 #pragma unroll
   for (int g4 = 0; g4 < 4; ++g4)
     *reinterpret_cast<f32x4*>(g + (32 * wj + l32) * MP + 32 * wi + 8 * g4 + 4 * up) =
-        (f32x4){gram[4 * g4] + gram_low[4 * g4] * (1.0f / kLow), gram[4 * g4 + 1] + gram_low[4 * g4 + 1] * (1.0f / kLow),
+        (f32x4){gram[4 * g4] + gram_low[4 * g4] * (1.0f / kLow),
+                gram[4 * g4 + 1] + gram_low[4 * g4 + 1] * (1.0f / kLow),
                 gram[4 * g4 + 2] + gram_low[4 * g4 + 2] * (1.0f / kLow),
                 gram[4 * g4 + 3] + gram_low[4 * g4 + 3] * (1.0f / kLow)};
 }
@@ -1050,10 +1052,10 @@ int gram_splits(int64_t E, int64_t np, int64_t mp) {
 
 // Matrices up to this m take both pieces of X in X B.  With the first alone the
 // rounding of a few strong directions that reaches the weak ones is up to 4.4e-3 of
-// the result for 4096 x 128 (spectra as above), 2.8e-3 for 4096 x 256, 1.9e-3 for
-// 2048 x 512 and 4096 x 513, 1.2e-3 for 1024 x 1024; with both 1.1e-3 and less.  8 of 256 x 512: 85.8
-// us with the first piece, 91.5 with both; 32 of 512 x 2048 835 and 929, 64 of 256 x 4096
-// 1254 and 1319.
+// the result for 4096 x 128 (spectra as above), 2.8e-3 for 4096 x 256, 2e-3 for
+// 4096 x 513, 1.2e-3 for 1024 x 1024; with both 1.1e-3 and less.  8 of 256 x 512: 85.8
+// us with the first piece, 91.5 with both; 32 of 512 x 2048 835 and 929, 64 of 256 x
+// 4096 1254 and 1319.
 constexpr int64_t kBothMost = 512;
 
 struct Layout {

@@ -191,7 +191,8 @@ def a_few_strong_directions(n, m):
 
 
 @gpu
-@pytest.mark.parametrize("n,m", [(64, 2), (2, 2), (64, 5), (5, 5), (6, 7), (9, 9), (17, 16), (1000, 12), (16, 300), (1024, 32), (4096, 64), (64, 64)])
+@pytest.mark.parametrize("n,m", [(64, 2), (2, 2), (64, 5), (5, 5), (6, 7), (9, 9), (17, 16), (1000, 12),
+                                 (16, 300), (1024, 32), (4096, 64), (64, 64)])
 def test_a_few_strong_directions_of_a_narrow_matrix(n, m):
     """Singular values far below others: what rounding adds in a strong direction must not reach the weak ones.
     Within the 2e-3 that the interface states (64-bit evaluations with the kernel's roundings leave up to 1.4e-3)."""
